@@ -413,12 +413,20 @@ def prepare(case, seed):
 
 # ---------------------------------------------------------------- plain forms
 
+def _half(x):
+    """float64 -> fp16 in one rounding (torch's own conversion goes through float32 and rounds twice): a float32
+    rounded to odd keeps what the second rounding needs to know."""
+    f = x.float()
+    f = torch.where(f.double().abs() > x.abs(), torch.nextafter(f, torch.zeros_like(f)), f)
+    return (f.view(torch.int32) | (f.double() != x).int()).view(torch.float32).half()
+
+
 def _plain_encode(x, bits):
     """Rows (float64) -> blocks: y = R x / ||x|| in 64 bits, compared in float32."""
     n = x.norm(dim=-1, keepdim=True)
     y = torch.where(n > 0, (x @ _rotation(torch.float64).T) / n.clamp_min(1e-300), 0.0)
     codes = torch.bucketize(y.float(), _bounds(bits), right=True, out_int32=True).to(torch.uint8)
-    return _pack(codes, n.squeeze(-1), bits)
+    return _pack(codes, _half(n.squeeze(-1)), bits)
 
 
 def _plain_decode(blocks, bits):
@@ -619,7 +627,8 @@ def _exact_quantised(x, bits):
     for b in _levels(bits)[1].tolist():
         code += y >= b
     c = torch.from_numpy(_levels(bits)[0]).cuda().double()[code]
-    return _exact_butterfly(c) * sign * norm.half().double() / math.sqrt(D)
+    step = torch.exp2(torch.floor(torch.log2(norm.clamp_min(2.0**-14))) - 10)      # spacing of fp16 at the norm
+    return _exact_butterfly(c) * sign * (torch.round(norm / step) * step) / math.sqrt(D)
 
 
 def exact(case, seed):
