@@ -468,6 +468,159 @@ int tq_attn_decode_d(const void *q, int q_dtype, const uint8_t *k_blocks, const 
                      int Hkv, int T_cap, int T, int head_dim, float scale, const float *R, float *out,
                      void *workspace, size_t workspace_bytes, void *stream);
 
+/* ---- Rotary positions and quantise-on-insert of a decode step or prompt chunk
+ * (the pages insert keys that their model has already rotated: [spec]
+ * Integration Points; these calls take the rotation along). */
+
+typedef enum { TQ_ROPE_HALF = 0, TQ_ROPE_ADJACENT = 1 } tq_rope_style;
+
+/* Rotary positions of one to three axes (time, height, width of an image or
+ * video token).  The first rot_dim elements of a head form rot_dim / 2 pairs:
+ * pair i is elements (i, i + rot_dim / 2) (TQ_ROPE_HALF) or (2i, 2i + 1)
+ * (TQ_ROPE_ADJACENT); it turns by position[axis[i]] times its frequency.
+ * turn[i] is the frequency in 2^-64 turns per position (modulo one turn), so
+ * angles of far positions are exact.  Travels by value, like tq_codebook. */
+typedef struct {
+    int head_dim;        /* 128 */
+    int rot_dim;         /* 32, 64, 96 or 128 */
+    int style;
+    int axes;            /* 1, 2 or 3 */
+    uint8_t axis[64];
+    uint64_t turn[64];
+} tq_rope;
+
+/* Fill *out: pair i has the frequency base^(-2 i / rot_dim) radians.  Axis a
+ * takes sections[a] pairs (axes entries, together rot_dim / 2): one section
+ * after the other, or (interleaved) pair i goes to axis i % axes while i <
+ * axes * sections[i % axes], the pairs left over to axis 0.  Host only.
+ * Errors: TQ_ERR_ARG (NULL, base <= 1, sections that do not add up),
+ * TQ_ERR_UNSUPPORTED. */
+int tq_rope_load(int head_dim, int rot_dim, double base, int style, int axes, const int *sections, int interleaved,
+                 tq_rope *out);
+
+/* Replace the frequencies of a loaded rope by freqs[rot_dim / 2] (radians per
+ * position, at most 1024 in size): scaled or extended contexts.  Host only.
+ * Errors: TQ_ERR_ARG, TQ_ERR_UNSUPPORTED. */
+int tq_rope_set_freqs(tq_rope *rope, const double *freqs);
+
+/* Rotate the heads of n_tok tokens: pair (a, b) of angle t becomes (a cos t -
+ * b sin t, b cos t + a sin t), in float32, rounded once to dtype; elements
+ * from rot_dim on are copied.
+ *   x, out   device rows of 128 elements of dtype (TQ_F32 / TQ_BF16 /
+ *            TQ_F16); head h of token n at n * tok_stride + h * head_stride
+ *            elements (strides times the element size multiples of 16, bases
+ *            16-byte aligned).  out may be x itself with the same strides
+ *            (in place); otherwise they must not overlap.
+ *   pos      device int64: axis a of token n at pos[a * pos_axis_stride + n].
+ *            Any int64 value (positions may be negative).
+ * n_tok == 0 is a no-op.  Errors: TQ_ERR_ARG, TQ_ERR_UNSUPPORTED, TQ_ERR_ALIGN,
+ * TQ_ERR_CUDA. */
+int tq_rope_apply(const void *x, int dtype, int64_t n_tok, int heads, int64_t x_tok_stride, int64_t x_head_stride,
+                  const int64_t *pos, int64_t pos_axis_stride, const tq_rope *rope, void *out,
+                  int64_t out_tok_stride, int64_t out_head_stride, void *stream);
+
+/* Insert the keys and values of n_tok new tokens into packed caches in one
+ * launch: keys are rotated by rope (as tq_rope_apply, but kept in float32),
+ * then keys and values are encoded as by tq_encode_kv.  Codes and norms are
+ * those of the definition evaluated in double precision (y rounded once to
+ * float32 and compared with the float32 boundaries; the norm rounded once to
+ * fp16), also next to a boundary.
+ *   k, v      device rows of dtype, head h of token n at n * tok_stride + h *
+ *             head_stride elements (alignment as tq_rope_apply).  k with
+ *             k_blocks, or v with v_blocks, may be NULL (then not written).
+ *   rope      NULL: keys are taken as they are (pos is then unused).
+ *   kcb, vcb  2-, 3- or 4-bit codebooks of tq_codebook_load(128, bits).
+ *   k_blocks, v_blocks   device caches of n_blocks blocks each, 2-byte aligned.
+ *   dst       device int64: the block of head h of token n is dst[n] + h *
+ *             dst_head_stride.  [B][Hkv][T_cap]: dst = b * Hkv * T_cap + t,
+ *             stride T_cap; a pool [pages][Hkv][page]: dst = page_index * Hkv
+ *             * page + slot, stride page.  Tokens with a negative dst
+ *             (padding) and blocks past n_blocks are not written.  Two tokens
+ *             must not name the same block.
+ * n_tok == 0 is a no-op.  A row with a non-finite element stores a non-finite
+ * norm and codes 0.  Errors: TQ_ERR_ARG, TQ_ERR_UNSUPPORTED (also a codebook
+ * whose boundaries are not those of tq_codebook_load), TQ_ERR_ALIGN,
+ * TQ_ERR_CUDA. */
+int tq_insert_kv(const void *k, int64_t k_tok_stride, int64_t k_head_stride, const void *v, int64_t v_tok_stride,
+                 int64_t v_head_stride, int dtype, int64_t n_tok, int heads, const int64_t *pos,
+                 int64_t pos_axis_stride, const tq_rope *rope, const tq_codebook *kcb, const tq_codebook *vcb,
+                 tq_signs signs, uint8_t *k_blocks, uint8_t *v_blocks, int64_t n_blocks, const int64_t *dst,
+                 int64_t dst_head_stride, void *stream);
+
+/* ---- Eviction from a cache by accumulated attention weight ([serde]
+ * Limitations leaves eviction to the engine; the packed cache makes it a move
+ * of blocks).  A decode loop calls tq_attn_decode_weights instead of
+ * tq_attn_decode, and once a sequence has outgrown its budget tq_evict_select
+ * and tq_evict_compact, after which its length is new_lens[b]; positions of
+ * new tokens go on counting (blocks keep the positions they were inserted
+ * with). */
+
+/* Workspace bytes of tq_attn_decode_weights for contexts of up to T tokens on
+ * the current device (partials and, per token and query head, a score).
+ * Host only.  0 for an invalid shape. */
+size_t tq_attn_weights_workspace_bytes(int B, int Hq, int Hkv, int T);
+
+/* tq_attn_decode over packed 2/3/4-bit keys and values that also adds up
+ * every cached token's attention weight over the query heads of its KV head:
+ *   weights[b][h][t] <- decay * weights[b][h][t] + sum_g softmax(s_g)_t
+ * for t < L_b (decay 0 overwrites; weights from L_b on are left as they are).
+ *   q, k_blocks, v_blocks, seq_lens, scale, T   as tq_attn_decode.
+ *   block_table  NULL: caches [B][Hkv][T_cap] (T_cap a multiple of 8); else
+ *                device int32 [B][max_pages] and pools [pages][Hkv]
+ *                [page_tokens], page_tokens a multiple of 32, as for
+ *                tq_attn_decode_paged (T_cap unused).
+ *   weights      device float32, row (b, h) at (b * Hkv + h) *
+ *                weights_row_stride, weights_row_stride >= T.
+ *   out          device [B][Hq][128] of out_dtype (TQ_F32 / TQ_BF16 / TQ_F16).
+ *                Values enter the tensor cores in 16 bits: float32 outputs
+ *                are good to about 1e-4 of their largest element.
+ *   workspace    >= tq_attn_weights_workspace_bytes(B, Hq, Hkv, T) bytes,
+ *                16-byte aligned, clobbered; calls that overlap on the GPU
+ *                must use different workspaces.
+ * A query with non-finite scores gives NaN outputs and NaN weights.  Results
+ * do not depend on timing.  Errors: TQ_ERR_ARG, TQ_ERR_UNSUPPORTED (turboq8,
+ * Hq / Hkv > 8, page_tokens not a multiple of 32), TQ_ERR_ALIGN,
+ * TQ_ERR_WORKSPACE, TQ_ERR_CUDA. */
+int tq_attn_decode_weights(const void *q, int q_dtype, const uint8_t *k_blocks, const tq_codebook *kcb,
+                           const uint8_t *v_blocks, const tq_codebook *vcb, const int32_t *block_table, int max_pages,
+                           int page_tokens, const int32_t *seq_lens, int B, int Hq, int Hkv, int T_cap, int T,
+                           float scale, tq_signs signs, float *weights, int64_t weights_row_stride, float decay,
+                           void *out, int out_dtype, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Choose the tokens of each (sequence, KV head) that stay.  A sequence of
+ * L <= keep tokens keeps them all; of a longer one stay the first `first`,
+ * the last `last`, and of the others the keep - first - last with the largest
+ * weights (equal weights: the lower index; -0 equals +0; NaN above all).
+ *   weights   device float32, row (b, h) at (b * Hkv + h) * row_stride,
+ *             row_stride >= T; entries from L_b on are not read.
+ *   seq_lens  device int32 [B] (each clamped to [0, T]) or NULL for T.
+ *   kept      device int32 [B][Hkv][keep]: the indices in ascending order,
+ *             -1 past the last one.
+ *   new_lens  device int32 [B]: min(L_b, keep); not the seq_lens array.
+ * first + last <= keep; T <= 2^30.  No workspace.  Errors: TQ_ERR_ARG,
+ * TQ_ERR_UNSUPPORTED, TQ_ERR_ALIGN, TQ_ERR_CUDA. */
+int tq_evict_select(const float *weights, int64_t row_stride, const int32_t *seq_lens, int B, int Hkv, int T,
+                    int keep, int first, int last, int32_t *kept, int32_t *new_lens, void *stream);
+
+/* Move the kept tokens of every (sequence, KV head) together, in place:
+ * token j takes the block and weight of token kept[j], j < new_lens[b]; the
+ * blocks from new_lens[b] on are left as they are, the weights from there to
+ * T are set to 0 (a token inserted there starts from nothing).
+ *   k_blocks, v_blocks   device caches of blocks of k_block_bytes /
+ *             v_block_bytes bytes (any block format; even, at most 512),
+ *             [B][Hkv][T_cap], or with a block_table pools [num_pages][Hkv]
+ *             [page_tokens] (any page_tokens).  No page may belong to two
+ *             sequences.  v_blocks may be NULL.
+ *   weights   as for tq_attn_decode_weights, or NULL.
+ *   kept, new_lens   of tq_evict_select: ascending, kept[j] >= j.  An index
+ *             outside j .. T - 1, or a table entry outside the pool, leaves
+ *             its token where it is.
+ * Errors: TQ_ERR_ARG, TQ_ERR_UNSUPPORTED, TQ_ERR_ALIGN, TQ_ERR_CUDA. */
+int tq_evict_compact(uint8_t *k_blocks, int k_block_bytes, uint8_t *v_blocks, int v_block_bytes, float *weights,
+                     int64_t weights_row_stride, const int32_t *kept, int keep, const int32_t *new_lens,
+                     const int32_t *block_table, int max_pages, int page_tokens, int num_pages, int B, int Hkv,
+                     int T_cap, int T, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

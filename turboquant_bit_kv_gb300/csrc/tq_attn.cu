@@ -5,6 +5,7 @@
 #include <cmath>
 
 #include "tq_attn.cuh"
+#include "tq_attn_combine.cuh"
 #include "tq_attn_mma.h"
 #include "tq_internal.h"
 
@@ -153,108 +154,20 @@ __global__ void __launch_bounds__(kAttnThreads) attn_prep_mma_kernel(const __gri
     }
 }
 
-// Merge for the tensor-core kernel's partition: the slots of segment
-// j = (sequence, KV head) are the warps whose chunk ranges touch it.  One
-// CTA per (sequence, query head) of 128 x ng threads: thread d of slot
-// group g reduces output dim d over batches g, g + ng, ... of 32 slots.
-// Reading what other SMs just wrote costs a full L2 round trip, so each
-// thread issues every load of a batch at once (m and l of each slot -- the
-// same address across the group -- and its dim of acc) and only then
-// reduces, with the running max rescaled between batches; the groups run
-// their rounds side by side and meet in shared memory.  Launched as a
-// programmatic dependent of the attention kernel: its CTAs wait here until
-// that grid has finished and its writes are visible.
+// The merge (tq_attn_combine.cuh), one CTA per (sequence, query head).
+// Launched as a programmatic dependent of the attention kernel: its CTAs wait
+// here until that grid has finished and its writes are visible.
 __global__ void __launch_bounds__(kAttnThreads * kCombineMaxGroups) attn_combine_mma_kernel(
     const float *ws, MmaPlan plan, int Hq, int Hkv, int rotate_back, uint32_t s0, uint32_t s1, uint32_t s2,
     uint32_t s3, float *out) {
-    constexpr int kBatch = 32;
-    __shared__ float buf[kD];
-    __shared__ float gacc[kCombineMaxGroups][kD];
-    __shared__ float gml[kCombineMaxGroups][2];
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int d = threadIdx.x & (kD - 1), grp = threadIdx.x / kD, ng = blockDim.x / kD;
-    const int b = blockIdx.x / Hq, h = blockIdx.x % Hq;
-    const int G = Hq / Hkv;
-    const int64_t j = (int64_t)b * Hkv + h / G;
-    const int64_t first = mma_worker_of_chunk(j * plan.C, plan);
-    const int nslots = (int)(mma_worker_of_chunk((j + 1) * plan.C - 1, plan) - first + 1);
-    const float *base = ws + (int64_t)blockIdx.x * plan.Smax * kPartialFloats;
-    float M = -INFINITY, l = 0.f, acc = 0.f;
-    for (int sb = grp * kBatch; sb < nslots; sb += ng * kBatch) {
-        float mv[kBatch], lv[kBatch], xv[kBatch];
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            const bool ok = sb + i < nslots;
-            const float *ps = base + (int64_t)(sb + i) * kPartialFloats;
-            mv[i] = ok ? __ldcg(ps) : -INFINITY;
-            lv[i] = ok ? __ldcg(ps + 1) : 0.f;
-            xv[i] = ok ? __ldcg(ps + 4 + d) : 0.f;
-        }
-        float Mb = M;
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) Mb = fmaxf(Mb, mv[i]);
-        if (Mb == -INFINITY) continue;   // nothing valid so far
-        if (M != -INFINITY && Mb != M) {
-            const float c = exp2f(M - Mb);
-            l *= c;
-            acc *= c;
-        }
-        M = Mb;
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            const float w = mv[i] == -INFINITY ? 0.f : exp2f(mv[i] - M);
-            l = fmaf(w, lv[i], l);
-            acc = fmaf(w, xv[i], acc);
-        }
-    }
-    if (ng > 1) {
-        // the groups' states, rescaled to their common max (every thread of a group holds the same
-        // M and l)
-        gacc[grp][d] = acc;
-        if (d == 0) {
-            gml[grp][0] = M;
-            gml[grp][1] = l;
-        }
-        __syncthreads();
-        if (grp == 0) {
-            float Mt = -INFINITY;
-            for (int g = 0; g < ng; ++g) Mt = fmaxf(Mt, gml[g][0]);
-            l = 0.f;
-            acc = 0.f;
-            if (Mt != -INFINITY) {
-                for (int g = 0; g < ng; ++g) {
-                    const float mg = gml[g][0];
-                    const float w = mg == -INFINITY ? 0.f : exp2f(mg - Mt);
-                    l = fmaf(w, gml[g][1], l);
-                    acc = fmaf(w, gacc[g][d], acc);
-                }
-            }
-        }
-    }
-    const float o = (l > 0.f || l != l) ? acc / l : 0.f;   // a NaN l (failed copy) propagates
-    if (!rotate_back) {
-        if (grp == 0) out[(int64_t)blockIdx.x * kD + d] = o;
-        return;
-    }
-    // inverse rotation by group 0; every thread passes the same barriers
-    if (grp == 0) buf[d] = o;
-    __syncthreads();
-#pragma unroll
-    for (int L = 1; L < kD; L <<= 1) {
-        float v = 0.f, w = 0.f;
-        if (grp == 0) {
-            v = buf[d];
-            w = buf[d ^ L];
-        }
-        __syncthreads();
-        if (grp == 0) buf[d] = (d & L) ? (w - v) : (v + w);
-        __syncthreads();
-    }
-    if (grp == 0) {
-        const uint32_t sw[4] = {s0, s1, s2, s3};
-        const float v = buf[d] * 0.08838834764831845f;
-        out[(int64_t)blockIdx.x * kD + d] = ((sw[d >> 5] >> (d & 31)) & 1u) ? -v : v;
-    }
+    combine_mma(ws, plan, blockIdx.x, Hq, Hkv, rotate_back, 0.08838834764831845f, s0, s1, s2, s3,
+                [&](int d, float v) { out[(int64_t)blockIdx.x * kD + d] = v; });
+}
+
+int launch_attn_prep_mma(const AttnArgs &a, const MmaPlan &plan, int qjl, cudaStream_t st) {
+    attn_prep_mma_kernel<<<a.B * a.Hkv, kAttnThreads, 0, st>>>(a, plan, qjl);
+    return launch_status();
 }
 
 static int attn_smem_bytes(int kb, int vb) {
@@ -281,9 +194,8 @@ namespace {
 int mma_path(AttnArgs &a, int kb, int vb, bool qjl, bool packed_v, tq_signs signs, float *out, bool paged,
              cudaStream_t st) {
     MmaPlan mp = mma_plan(a.B, a.Hq, a.Hkv, a.T, kb, vb, qjl, a.G);
-    attn_prep_mma_kernel<<<a.B * a.Hkv, kAttnThreads, 0, st>>>(a, mp, qjl ? 1 : 0);
-    if (cudaGetLastError() != cudaSuccess) return TQ_ERR_CUDA;
-    int r;
+    int r = launch_attn_prep_mma(a, mp, qjl ? 1 : 0, st);
+    if (r != TQ_OK) return r;
     if (paged) {
         const int nt = a.G <= 4 ? 1 : 2;
         r = kb == 2 ? launch_attn_mma_paged_k2(a, mp, vb, nt, st)
@@ -366,6 +278,7 @@ extern "C" int tq_attn_decode(const void *q, int q_dtype, const uint8_t *k_block
     a.table = nullptr;
     a.max_pages = 0;
     a.page = 0;
+    a.scores = nullptr;
     a.q = q;
     a.q_dtype = q_dtype;
     a.k = k_blocks;
@@ -453,6 +366,7 @@ extern "C" int tq_attn_decode_paged(const void *q, int q_dtype, const uint8_t *k
         a.table = block_table;
         a.max_pages = max_pages;
         a.page = page_tokens;
+        a.scores = nullptr;
         return mma_path(a, kb, vb, false, true, signs, out, true, static_cast<cudaStream_t>(stream));
     }
     // otherwise the one-token case of the tensor-core causal attention (no workspace)

@@ -481,7 +481,10 @@ __device__ __forceinline__ int64_t paged_row0(const AttnArgs &a, int j, int t0) 
            (t0 - pg * a.page) - t0;
 }
 
-template <int KB, int VB, bool QJL, int NT, bool WIDE, bool PAGED = false>
+// SCORES: every live token's scores (log2 domain, before the softmax) are also
+// written to a.scores, from which attn_weights_kernel takes the attention
+// weights once the softmax statistics are final.
+template <int KB, int VB, bool QJL, int NT, bool WIDE, bool PAGED = false, bool SCORES = false>
 __global__ void __launch_bounds__(Cfg<KB, VB, QJL, NT, WIDE>::kThreads, Cfg<KB, VB, QJL, NT, WIDE>::kMinBlocks)
     attn_mma_kernel(const __grid_constant__ AttnArgs a, const MmaPlan plan) {
     using C = Cfg<KB, VB, QJL, NT, WIDE>;
@@ -812,6 +815,20 @@ __global__ void __launch_bounds__(Cfg<KB, VB, QJL, NT, WIDE>::kThreads, Cfg<KB, 
                     s[nt][mt][1] = tb < nvalid ? eb : -INFINITY;
                 }
             }
+            if constexpr (SCORES) {
+                // tokens' rows of G scores lie back to back: a warp's stores of one fragment row cover
+                // 8 tokens' heads in neighbouring words
+                float *sc = a.scores + ((int64_t)j * plan.C + ci) * (kMmaChunk * a.G);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    const int head = C::kH8 ? 2 * t + nt : 4 * nt + t;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int tok = g + 8 * i;
+                        if (head < a.G && tok < nvalid) __stcg(sc + tok * a.G + head, s[nt][i >> 1][i & 1]);
+                    }
+                }
+            }
             // ---- online softmax per head (max over the rows g of the warp)
             bool moved = false;
             float corr[NT];
@@ -841,8 +858,10 @@ __global__ void __launch_bounds__(Cfg<KB, VB, QJL, NT, WIDE>::kThreads, Cfg<KB, 
                 float nva = 1.f, nvb = 1.f;
                 if constexpr (!C::kRawV) {
                     constexpr float vf = VB == 8 ? 1.f / 255.f : 1.f;
-                    nva = __half2float(__ushort_as_half((unsigned short)lds_u16(vs_s + ta * C::kVBytes))) * vf;
-                    nvb = __half2float(__ushort_as_half((unsigned short)lds_u16(vs_s + tb * C::kVBytes))) * vf;
+                    // (the last 16-byte piece of a partial chunk brings in up to 15 bytes of the block behind the
+                    // sequence: its norm may be anything, NaN too, and must not meet that token's P of 0)
+                    nva = ta < nvalid ? __half2float(__ushort_as_half((unsigned short)lds_u16(vs_s + ta * C::kVBytes))) * vf : 0.f;
+                    nvb = tb < nvalid ? __half2float(__ushort_as_half((unsigned short)lds_u16(vs_s + tb * C::kVBytes))) * vf : 0.f;
                 }
                 // B fragments of P (8 x 8 blocks of token rows g / g + 8, transposed): per n-tile, or
                 // (kH8) index 0: the hi parts of the 8 heads, 1: the lo parts
@@ -850,9 +869,16 @@ __global__ void __launch_bounds__(Cfg<KB, VB, QJL, NT, WIDE>::kThreads, Cfg<KB, 
                 float pa[NT], pb[NT];
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    const float mm = mrun[nt];
-                    pa[nt] = mm == -INFINITY ? 0.f : exp2f(s[nt][mt][0] - mm);
-                    pb[nt] = mm == -INFINITY ? 0.f : exp2f(s[nt][mt][1] - mm);
+                    if constexpr (SCORES) {
+                        // no finite score so far: scores are -inf (P 0) or NaN (which stays NaN)
+                        const float mm = mrun[nt] == -INFINITY ? 0.f : mrun[nt];
+                        pa[nt] = exp2f(s[nt][mt][0] - mm);
+                        pb[nt] = exp2f(s[nt][mt][1] - mm);
+                    } else {
+                        const float mm = mrun[nt];
+                        pa[nt] = mm == -INFINITY ? 0.f : exp2f(s[nt][mt][0] - mm);
+                        pb[nt] = mm == -INFINITY ? 0.f : exp2f(s[nt][mt][1] - mm);
+                    }
                     lrun[nt] += pa[nt] + pb[nt];
                 }
                 if constexpr (C::kH8) {
@@ -969,13 +995,13 @@ __global__ void __launch_bounds__(Cfg<KB, VB, QJL, NT, WIDE>::kThreads, Cfg<KB, 
     }
 }
 
-template <int KB, int VB, bool QJL, int NT, bool WIDE, bool PAGED = false>
+template <int KB, int VB, bool QJL, int NT, bool WIDE, bool PAGED = false, bool SCORES = false>
 int launch_cfg_w(const AttnArgs &a, MmaPlan &plan, cudaStream_t st) {
     static_assert(!QJL || NT == 1, "the QJL term covers up to 4 query heads per KV head");
     static_assert(!(QJL && PAGED), "paged caches hold packed keys and values only");
     using C = Cfg<KB, VB, QJL, NT, WIDE>;
     static int done[64] = {0};
-    if (set_smem_limit((const void *)attn_mma_kernel<KB, VB, QJL, NT, WIDE, PAGED>, C::kSmemTotal, done) != TQ_OK)
+    if (set_smem_limit((const void *)attn_mma_kernel<KB, VB, QJL, NT, WIDE, PAGED, SCORES>, C::kSmemTotal, done) != TQ_OK)
         return TQ_ERR_CUDA;
     // a programmatic dependent of the query-prep kernel: its prologue (first copies, tables) overlaps it
     cudaLaunchConfig_t cfg = {};
@@ -988,18 +1014,18 @@ int launch_cfg_w(const AttnArgs &a, MmaPlan &plan, cudaStream_t st) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, attn_mma_kernel<KB, VB, QJL, NT, WIDE, PAGED>, a, plan) != cudaSuccess)
+    if (cudaLaunchKernelEx(&cfg, attn_mma_kernel<KB, VB, QJL, NT, WIDE, PAGED, SCORES>, a, plan) != cudaSuccess)
         return TQ_ERR_CUDA;
     return launch_status();
 }
 
 // Only 2-bit values with one n-tile have a narrow (12-warp) variant.
-template <int KB, int VB, bool QJL, int NT, bool PAGED = false>
+template <int KB, int VB, bool QJL, int NT, bool PAGED = false, bool SCORES = false>
 int launch_cfg(const AttnArgs &a, MmaPlan &plan, cudaStream_t st) {
     if constexpr (VB == 2 && NT == 1) {
-        if (!plan.wide) return launch_cfg_w<KB, VB, QJL, NT, false, PAGED>(a, plan, st);
+        if (!plan.wide) return launch_cfg_w<KB, VB, QJL, NT, false, PAGED, SCORES>(a, plan, st);
     }
-    return launch_cfg_w<KB, VB, QJL, NT, true, PAGED>(a, plan, st);
+    return launch_cfg_w<KB, VB, QJL, NT, true, PAGED, SCORES>(a, plan, st);
 }
 
 template <int KB, int VB, bool QJL, int NT>

@@ -53,6 +53,9 @@ int wait_failed_attn_k2(unsigned *v, bool clear);
 int wait_failed_attn_k3(unsigned *v, bool clear);
 int wait_failed_attn_k4(unsigned *v, bool clear);
 int wait_failed_attn_k8(unsigned *v, bool clear);
+int wait_failed_attn_k2w(unsigned *v, bool clear);
+int wait_failed_attn_k3w(unsigned *v, bool clear);
+int wait_failed_attn_k4w(unsigned *v, bool clear);
 int wait_failed_prefill(unsigned *v, bool clear);
 int wait_failed_headdim(unsigned *v, bool clear);
 

@@ -30,6 +30,11 @@ class tq_signs(ctypes.Structure):
     _fields_ = [("w", ctypes.c_uint32 * 4)]
 
 
+class tq_rope(ctypes.Structure):
+    _fields_ = [("head_dim", ctypes.c_int), ("rot_dim", ctypes.c_int), ("style", ctypes.c_int),
+                ("axes", ctypes.c_int), ("axis", ctypes.c_uint8 * 64), ("turn", ctypes.c_uint64 * 64)]
+
+
 class TQError(RuntimeError):
     def __init__(self, status, what):
         super().__init__("%s: %s (status %d)" % (what, tq_status_string(status), status))
@@ -91,6 +96,20 @@ def lib():
         L.tq_attn_workspace_bytes_d.restype = sz
         L.tq_attn_decode_d.argtypes = [vp, c_int, vp, cbp, vp, cbp, vp, c_int, c_int, c_int, c_int, c_int, c_int,
                                        ctypes.c_float, vp, vp, vp, sz, vp]
+        rp = ctypes.POINTER(tq_rope)
+        L.tq_rope_load.argtypes = [c_int, c_int, ctypes.c_double, c_int, c_int, ctypes.POINTER(c_int), c_int, rp]
+        L.tq_rope_set_freqs.argtypes = [rp, ctypes.POINTER(ctypes.c_double)]
+        L.tq_rope_apply.argtypes = [vp, c_int, i64, c_int, i64, i64, vp, i64, rp, vp, i64, i64, vp]
+        L.tq_insert_kv.argtypes = [vp, i64, i64, vp, i64, i64, c_int, i64, c_int, vp, i64, rp, cbp, cbp, tq_signs, vp,
+                                   vp, i64, vp, i64, vp]
+        L.tq_attn_weights_workspace_bytes.argtypes = [c_int] * 4
+        L.tq_attn_weights_workspace_bytes.restype = sz
+        L.tq_attn_decode_weights.argtypes = [vp, c_int, vp, cbp, vp, cbp, vp, c_int, c_int, vp, c_int, c_int, c_int,
+                                             c_int, c_int, ctypes.c_float, tq_signs, vp, i64, ctypes.c_float, vp,
+                                             c_int, vp, sz, vp]
+        L.tq_evict_select.argtypes = [vp, i64, vp, c_int, c_int, c_int, c_int, c_int, c_int, vp, vp, vp]
+        L.tq_evict_compact.argtypes = [vp, c_int, vp, c_int, vp, i64, vp, c_int, vp, vp, c_int, c_int, c_int, c_int,
+                                       c_int, c_int, c_int, vp]
         _lib = L
     return _lib
 
@@ -377,3 +396,211 @@ def tq_attn_decode_d(q, k_blocks, kcb, v_blocks, vcb, R, out, workspace, T, scal
                                   _ptr(R), _ptr(out), _ptr(workspace), workspace.numel() * workspace.element_size(),
                                   _stream(stream)), "tq_attn_decode_d")
     return out
+
+
+# ---- rotary positions, quantise-on-insert of new tokens, eviction by attention weight
+
+TQ_ROPE_HALF, TQ_ROPE_ADJACENT = 0, 1
+
+
+class _On:
+    """Checks that the tensors of a call are CUDA tensors of one device and makes that device current."""
+
+    def __init__(self, what, *tensors):
+        dev = None
+        for t in tensors:
+            if t is None:
+                continue
+            if not t.is_cuda:
+                raise ValueError("%s: CUDA tensors expected" % what)
+            if dev is None:
+                dev = t.device
+            elif t.device != dev:
+                raise ValueError("%s: tensors on different devices" % what)
+        self.dev, self.guard = dev, None
+
+    def __enter__(self):
+        if self.dev is not None and self.dev.index != torch.cuda.current_device():
+            self.guard = torch.cuda.device(self.dev)
+            self.guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def _need(ok, what):
+    if not ok:
+        raise ValueError(what)
+
+
+def tq_rope_load(rot_dim=128, base=10000.0, style=TQ_ROPE_HALF, sections=None, interleaved=False, head_dim=128):
+    """Rotary positions; ``sections``: pairs of each axis (default: one axis)."""
+    sections = [rot_dim // 2] if sections is None else [int(n) for n in sections]
+    r = tq_rope()
+    _check(lib().tq_rope_load(head_dim, rot_dim, float(base), style, len(sections),
+                              (ctypes.c_int * max(1, len(sections)))(*sections), 1 if interleaved else 0,
+                              ctypes.byref(r)), "tq_rope_load")
+    return r
+
+
+def tq_rope_set_freqs(rope, freqs):
+    """Replace the frequencies (radians per position) of the rope's pairs."""
+    freqs = [float(f) for f in freqs]
+    _need(len(freqs) == rope.rot_dim // 2, "tq_rope_set_freqs: one frequency per pair expected")
+    _check(lib().tq_rope_set_freqs(ctypes.byref(rope), (ctypes.c_double * len(freqs))(*freqs)), "tq_rope_set_freqs")
+    return rope
+
+
+def _heads(x, what):
+    """(tokens, heads, token stride, head stride) of rows [n, heads, 128]."""
+    _need(x.dim() == 3 and x.shape[2] == 128 and x.stride(2) == 1, "%s: [tokens, heads, 128] expected" % what)
+    return x.shape[0], x.shape[1], x.stride(0), x.stride(1)
+
+
+def _positions(pos, rope, n, what):
+    """(pointer, axis stride) of positions [n] or [axes, n]."""
+    _need(pos.dtype == torch.int64, "%s: int64 positions expected" % what)
+    _need((pos.dim() == 1 and rope.axes == 1 and pos.shape[0] == n) or
+          (pos.dim() == 2 and tuple(pos.shape) == (rope.axes, n)), "%s: positions [axes, tokens] expected" % what)
+    _need(n <= 1 or pos.stride(-1) == 1, "%s: positions of an axis must be contiguous" % what)
+    return _ptr(pos), pos.stride(0) if pos.dim() == 2 else 0
+
+
+def tq_rope_apply(x, pos, rope, out, stream=None):
+    """Rotate heads x [n, heads, 128] into out (same shape and dtype; out may
+    be x).  pos int64 [axes, n] (or [n] for one axis)."""
+    n, heads, xt, xh = _heads(x, "tq_rope_apply")
+    _, _, ot, oh = _heads(out, "tq_rope_apply")
+    _need(out.shape == x.shape and out.dtype == x.dtype, "tq_rope_apply: out must have the shape and dtype of x")
+    p, pa = _positions(pos, rope, n, "tq_rope_apply")
+    with _On("tq_rope_apply", x, pos, out):
+        _check(lib().tq_rope_apply(_ptr(x), _dtype(x), n, heads, xt, xh, p, pa, ctypes.byref(rope), _ptr(out), ot, oh,
+                                   _stream(stream)), "tq_rope_apply")
+    return out
+
+
+def tq_insert_kv(k, v, pos, rope, kcb, vcb, signs, k_blocks, v_blocks, dst, dst_head_stride, stream=None):
+    """Rotate keys k [n, Hkv, 128] (rope None: as they are), quantise keys and
+    values v [n, Hkv, 128] and write them into the caches (uint8, last dim the
+    block): the block of head h of token n is number dst[n] + h *
+    dst_head_stride; tokens of negative dst are skipped.  k with k_blocks, or v
+    with v_blocks, may be None."""
+    x = k if k is not None else v
+    _need(x is not None, "tq_insert_kv: no rows")
+    n, heads, _, _ = _heads(x, "tq_insert_kv")
+    _need(dst.dtype == torch.int64 and dst.dim() == 1 and dst.shape[0] == n and dst.is_contiguous(),
+          "tq_insert_kv: dst int64 [tokens] expected")
+    strides, blocks = [], None
+    for rows, cache, cb in ((k, k_blocks, kcb), (v, v_blocks, vcb)):
+        _need((rows is None) == (cache is None), "tq_insert_kv: rows and their blocks come together")
+        if rows is None:
+            strides.append((0, 0))
+            continue
+        m, hh, st, sh = _heads(rows, "tq_insert_kv")
+        _need((m, hh) == (n, heads) and rows.dtype == x.dtype, "tq_insert_kv: k and v of one shape and dtype expected")
+        size = tq_block_bytes(cb.bits)
+        _need(cache.dtype == torch.uint8 and cache.is_contiguous() and cache.dim() >= 1 and cache.shape[-1] == size,
+              "tq_insert_kv: contiguous uint8 blocks of %d bytes expected" % size)
+        _need(blocks is None or cache.numel() // size == blocks, "tq_insert_kv: caches of different sizes")
+        blocks = cache.numel() // size
+        strides.append((st, sh))
+    p, pa = (None, 0) if rope is None or k is None else _positions(pos, rope, n, "tq_insert_kv")
+    with _On("tq_insert_kv", k, v, pos if p is not None else None, k_blocks, v_blocks, dst):
+        _check(lib().tq_insert_kv(_ptr(k), strides[0][0], strides[0][1], _ptr(v), strides[1][0], strides[1][1],
+                                  _dtype(x), n, heads, p, pa, None if p is None else ctypes.byref(rope),
+                                  None if kcb is None else ctypes.byref(kcb), None if vcb is None else ctypes.byref(vcb),
+                                  signs, _ptr(k_blocks), _ptr(v_blocks), blocks, _ptr(dst), dst_head_stride,
+                                  _stream(stream)), "tq_insert_kv")
+
+
+def tq_attn_weights_workspace_bytes(B, Hq, Hkv, T):
+    return int(lib().tq_attn_weights_workspace_bytes(B, Hq, Hkv, T))
+
+
+def _table(block_table, B, what):
+    if block_table is None:
+        return None, 0
+    _need(block_table.dtype == torch.int32 and block_table.dim() == 2 and block_table.shape[0] == B and
+          block_table.is_contiguous(), "%s: block_table int32 [B, max_pages] expected" % what)
+    return _ptr(block_table), block_table.shape[1]
+
+
+def _weights(w, B, Hkv, T, what):
+    """Row stride of accumulators [B, Hkv, >= T]."""
+    _need(w.dtype == torch.float32 and w.dim() == 3 and w.shape[0] == B and w.shape[1] == Hkv and w.shape[2] >= T and
+          w.stride(2) == 1 and (B == 1 or Hkv == 1 or w.stride(0) == Hkv * w.stride(1)),
+          "%s: weights float32 [B, Hkv, >= T] expected" % what)
+    return w.stride(1) if Hkv > 1 or B == 1 else w.stride(0)
+
+
+def _lens(t, B, what):
+    _need(t is None or (t.dtype == torch.int32 and t.dim() == 1 and t.shape[0] == B and t.is_contiguous()),
+          "%s: lengths int32 [B] expected" % what)
+
+
+def _cache(t, cb, B, paged, what):
+    """(Hkv, tokens of a sequence or page) of caches [B or pages, Hkv, tokens, bytes]."""
+    _need(t.dtype == torch.uint8 and t.dim() == 4 and t.is_contiguous() and (paged or t.shape[0] == B) and
+          (cb is None or t.shape[3] == tq_block_bytes(cb.bits)), "%s: contiguous packed blocks expected" % what)
+    return t.shape[1], t.shape[2]
+
+
+def tq_attn_decode_weights(q, k_blocks, kcb, v_blocks, vcb, weights, out, workspace, T, scale, signs, seq_lens=None,
+                           block_table=None, decay=1.0, stream=None):
+    """Decode attention that adds each cached token's attention weight to
+    weights float32 [B, Hkv, >= T].  q [B, Hq, 128]; caches [B, Hkv, T_cap,
+    bytes], or with a block_table int32 [B, max_pages] pools [pages, Hkv,
+    page, bytes]; out [B, Hq, 128] float32, bfloat16 or float16."""
+    what = "tq_attn_decode_weights"
+    _need(q.dim() == 3 and q.shape[2] == 128 and q.is_contiguous(), "%s: contiguous q [B, Hq, 128] expected" % what)
+    B, Hq, _ = q.shape
+    Hkv, unit = _cache(k_blocks, kcb, B, block_table is not None, what)
+    _need(_cache(v_blocks, vcb, B, block_table is not None, what) == (Hkv, unit), "%s: caches of one shape expected" % what)
+    _need(out.shape == q.shape and out.is_contiguous(), "%s: contiguous out of q's shape expected" % what)
+    _lens(seq_lens, B, what)
+    stride = _weights(weights, B, Hkv, T, what)
+    table, pages = _table(block_table, B, what)
+    with _On(what, q, k_blocks, v_blocks, weights, out, workspace, seq_lens, block_table):
+        _check(lib().tq_attn_decode_weights(_ptr(q), _dtype(q), _ptr(k_blocks), ctypes.byref(kcb), _ptr(v_blocks),
+                                            ctypes.byref(vcb), table, pages, unit, _ptr(seq_lens), B, Hq, Hkv, unit, T,
+                                            scale, signs, _ptr(weights), stride, decay, _ptr(out), _dtype(out),
+                                            _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                            _stream(stream)), what)
+    return out
+
+
+def tq_evict_select(weights, kept, new_lens, T, first, last, seq_lens=None, stream=None):
+    """The tokens that stay: kept int32 [B, Hkv, keep] (ascending, -1 past the
+    last), new_lens int32 [B]."""
+    what = "tq_evict_select"
+    _need(kept.dtype == torch.int32 and kept.dim() == 3 and kept.is_contiguous(), "%s: kept int32 [B, Hkv, keep] expected" % what)
+    B, Hkv, keep = kept.shape
+    _need(new_lens is not None, "%s: new_lens expected" % what)
+    _lens(new_lens, B, what)
+    _lens(seq_lens, B, what)
+    stride = _weights(weights, B, Hkv, T, what)
+    with _On(what, weights, kept, new_lens, seq_lens):
+        _check(lib().tq_evict_select(_ptr(weights), stride, _ptr(seq_lens), B, Hkv, T, keep, first, last, _ptr(kept),
+                                     _ptr(new_lens), _stream(stream)), what)
+    return kept
+
+
+def tq_evict_compact(k_blocks, v_blocks, kept, new_lens, T, weights=None, block_table=None, stream=None):
+    """Move the kept tokens together in place: caches (and pools) as for
+    tq_attn_decode_weights, of any block format; v_blocks may be None."""
+    what = "tq_evict_compact"
+    _need(kept.dtype == torch.int32 and kept.dim() == 3 and kept.is_contiguous(), "%s: kept int32 [B, Hkv, keep] expected" % what)
+    B, Hkv, keep = kept.shape
+    _need(new_lens is not None, "%s: new_lens expected" % what)
+    _lens(new_lens, B, what)
+    table, pages = _table(block_table, B, what)
+    h, unit = _cache(k_blocks, None, B, table is not None, what)
+    _need(h == Hkv and (v_blocks is None or (_cache(v_blocks, None, B, table is not None, what) == (h, unit) and
+                                             v_blocks.shape[0] == k_blocks.shape[0])), "%s: caches of one shape expected" % what)
+    stride = 0 if weights is None else _weights(weights, B, Hkv, T, what)
+    with _On(what, k_blocks, v_blocks, kept, new_lens, weights, block_table):
+        _check(lib().tq_evict_compact(_ptr(k_blocks), k_blocks.shape[3], _ptr(v_blocks),
+                                      0 if v_blocks is None else v_blocks.shape[3], _ptr(weights), stride, _ptr(kept),
+                                      keep, _ptr(new_lens), table, pages, unit, k_blocks.shape[0], B, Hkv, unit, T,
+                                      _stream(stream)), what)
