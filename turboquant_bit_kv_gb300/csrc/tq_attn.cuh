@@ -45,7 +45,7 @@ struct AttnArgs {
     // table[b * max_pages + t / page] of pools [pages][Hkv][page]; page a multiple of 32
     const int32_t *table;
     int max_pages, page;
-    float *scores;           // [B * Hkv][chunks * 32][G] log2-domain scores (the kernels that keep them only)
+    float *scores;           // [B * Hkv][chunks][G][32] log2-domain scores (the kernels that keep them only)
 };
 
 __host__ __device__ inline int attn_tiles(int T) { return (T + kTT - 1) / kTT; }

@@ -816,8 +816,8 @@ __global__ void __launch_bounds__(Cfg<KB, VB, QJL, NT, WIDE>::kThreads, Cfg<KB, 
                 }
             }
             if constexpr (SCORES) {
-                // tokens' rows of G scores lie back to back: a warp's stores of one fragment row cover
-                // 8 tokens' heads in neighbouring words
+                // per chunk G rows of 32 tokens: a warp's store of one fragment row fills 32-byte pieces of
+                // 4 rows
                 float *sc = a.scores + ((int64_t)j * plan.C + ci) * (kMmaChunk * a.G);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
@@ -825,7 +825,7 @@ __global__ void __launch_bounds__(Cfg<KB, VB, QJL, NT, WIDE>::kThreads, Cfg<KB, 
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int tok = g + 8 * i;
-                        if (head < a.G && tok < nvalid) __stcg(sc + tok * a.G + head, s[nt][i >> 1][i & 1]);
+                        if (head < a.G) __stcg(sc + head * kMmaChunk + tok, s[nt][i >> 1][i & 1]);
                     }
                 }
             }

@@ -52,7 +52,7 @@ struct WeightsArgs {
 // CTAs [0, B Hq): the merge of one (sequence, query head).  The rest: the
 // weights of kMergeTokens tokens of one segment (sequence, KV head): the
 // final maximum and sum of its heads, one warp per head over the segment's
-// slots, then a token per thread.
+// slots, then a chunk of 32 tokens per warp at a time.
 __global__ void __launch_bounds__(kAttnThreads * kCombineMaxGroups) attn_weights_kernel(
     const __grid_constant__ WeightsArgs a, const __grid_constant__ MmaPlan plan) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -105,13 +105,23 @@ __global__ void __launch_bounds__(kAttnThreads * kCombineMaxGroups) attn_weights
         }
     }
     __syncthreads();
-    const float *sc = a.scores + j * plan.C * (kMmaChunk * a.G);
-    float *w = a.weights + j * a.w_stride;
+    // a warp takes a chunk of 32 tokens at a time: G rows of 32 scores, one coalesced load each
     const int end = min(t0 + kMergeTokens, L);
-    for (int t = t0 + threadIdx.x; t < end; t += blockDim.x) {
+    float *w = a.weights + j * a.w_stride;
+    const float *sc = a.scores + j * plan.C * (kMmaChunk * a.G) + lane;
+    for (int c = t0 / kMmaChunk + warp; c * kMmaChunk < end; c += nw) {
+        const float *row = sc + (int64_t)c * (kMmaChunk * a.G);
+        const int t = c * kMmaChunk + lane;
+        const bool in = t < end;
+        float s[8], old = 0.f;
+#pragma unroll
+        for (int g = 0; g < 8; ++g) s[g] = g < a.G ? __ldcs(row + g * kMmaChunk) : 0.f;
+        if (in && a.decay != 0.f) old = __ldcs(w + t) * a.decay;
         float p = 0.f;
-        for (int g = 0; g < a.G; ++g) p = fmaf(exp2f(__ldcg(sc + (int64_t)t * a.G + g) - ml[g][0]), ml[g][1], p);
-        w[t] = a.decay == 0.f ? p : fmaf(a.decay, w[t], p);
+#pragma unroll
+        for (int g = 0; g < 8; ++g)
+            if (g < a.G) p = fmaf(exp2f(s[g] - ml[g][0]), ml[g][1], p);
+        if (in) w[t] = old + p;
     }
 }
 

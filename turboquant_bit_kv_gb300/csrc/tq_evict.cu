@@ -17,11 +17,11 @@ namespace cg = cooperative_groups;
 namespace tq {
 namespace {
 
-constexpr int kSelThreads = 512;
+constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kSelCached = 40 * 1024;      // keys of a CTA's chunk held in shared memory (160 KB)
-constexpr int kSelChunk = 8192;            // keys a CTA gets before a row takes more CTAs
+constexpr int kSelChunk = 20 * 1024;       // keys a CTA gets before a row takes more CTAs
 constexpr int kMaxCluster = 8;             // portable cluster size
 
 // ---- selection
@@ -112,8 +112,12 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
                     }
                     in = ranked(i) && (r == 0 || (k >> (shift[r] + width[r])) == prefix);
                 }
-                // one add for the lanes that share the first such lane's digit (ties and zeros are common)
                 const uint32_t d = (k >> shift[r]) & ((1u << width[r]) - 1u);
+                if (r > 0) {   // few keys share the higher digits
+                    if (in) atomicAdd(&s.hist[r][d], 1u);
+                    continue;
+                }
+                // one add for the lanes that share the first such lane's digit (ties and zeros are common)
                 const uint32_t live = __ballot_sync(0xffffffffu, in);
                 if (live) {
                     const uint32_t lead = __shfl_sync(0xffffffffu, d, __ffs(live) - 1);
@@ -123,10 +127,10 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
                 }
             }
             cl.sync();
-            // the row's histogram, from the top: thread t holds bins of digits top - 4 t .. top - 4 t - 3
+            // the row's histogram, from the top: thread t holds the bins of digits top - 2 t and top - 2 t - 1
             constexpr int kPer = kBins / kSelThreads;
             const int bins = 1 << width[r];
-            uint32_t cnt[kPer] = {0, 0, 0, 0}, sum = 0;
+            uint32_t cnt[kPer] = {}, sum = 0;
 #pragma unroll
             for (int e = 0; e < kPer; ++e) {
                 const int at = bins - 1 - (tid * kPer + e);
@@ -143,8 +147,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
             }
             if (lane == 31) s.part[warp] = inc;
             __syncthreads();
-            uint32_t before = inc - sum;
-            for (int p = 0; p < warp; ++p) before += s.part[p];
+            uint32_t before = inc - sum + warp_sum(lane < warp ? s.part[lane] : 0u);
             if (before < m && before + sum >= m) {   // exactly one thread
                 uint32_t acc = before;
 #pragma unroll
@@ -186,10 +189,9 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
         s.equal[warp] = equal;
     }
     __syncthreads();
-    if (tid < 2) {
-        uint32_t t = 0;
-        for (int p = 0; p < kSelWarps; ++p) t += tid == 0 ? s.above[p] : s.equal[p];
-        s.sums[tid] = t;
+    if (warp < 2) {
+        const uint32_t t = warp_sum(warp == 0 ? s.above[lane] : s.equal[lane]);
+        if (lane == 0) s.sums[warp] = t;
     }
     cl.sync();
     uint32_t na = 0, ne = 0;   // tokens of either class before this warp's piece
@@ -198,10 +200,9 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
         na += o[0];
         ne += o[1];
     }
-    for (int p = 0; p < warp; ++p) {
-        na += s.above[p];
-        ne += s.equal[p];
-    }
+    static_assert(kSelWarps == 32, "a lane per warp");
+    na += warp_sum(lane < warp ? s.above[lane] : 0u);
+    ne += warp_sum(lane < warp ? s.equal[lane] : 0u);
     for (int i0 = p0; i0 < p1; i0 += 32) {
         const int i = i0 + lane;
         const int c = i < p1 ? cls(i) : 0;
@@ -218,36 +219,45 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
 // ---- compaction
 //
 // Token j of a row takes the block of token kept[j] >= j (ascending), in
-// place.  The row goes by in steps of (CTAs x kMovTile) tokens: a step's
-// blocks are read into registers, the cluster meets, and the step's blocks
-// are written.  A block that a step writes lies at or below every source of
-// the following steps (kept[j] >= j), so the only order to keep is "all reads
-// of a step before its writes": the next step's reads are already on their
-// way when the cluster meets.  Every kept block is read once and written
-// once; blocks that stay where they are are not touched.  Blocks are 2-byte
-// aligned (34, 50, 66 ... bytes), so they move in half words, neighbouring
-// threads taking neighbouring half words.
-constexpr int kMovThreads = 512;
-constexpr int kMovTile = 64;               // tokens of a CTA and step
-constexpr int kMovMaxHalf = 256;           // half words of a K and a V block together
-constexpr int kMovPer = 16;                // half words a thread holds
+// place.  The row goes by in steps of (CTAs x tile) tokens: a step's blocks
+// are read into shared memory, the cluster meets, and the step's blocks are
+// written.  A block that a step writes lies at or below every source of the
+// following steps (kept[j] >= j), so the only order to keep is "all reads of
+// a step before its writes".  Every kept block is read once and written once;
+// tiles in which nothing moves are left alone.
+//
+// Blocks of 34, 50, 66 ... bytes start at any even address.  WIDE (cache and
+// pages multiples of 8 tokens, so that eight blocks are a multiple of 16
+// bytes; aligned bases): a block is read as the aligned 16-byte pieces that
+// it lies in, with the bytes around it, and written as part of a group of
+// eight blocks that starts and ends on a 16-byte boundary, its pieces put
+// together from half words in shared memory.  Otherwise half words are
+// read and written one by one.
+constexpr int kMovThreads = 256;
+constexpr int kMovSmem = 56 * 1024;        // four CTAs per SM: enough reads in flight
+constexpr int kMovMaxBytes = 512;          // of a block
 
 struct MovArgs {
     uint8_t *blocks[2];
     float *weights;
     const int32_t *kept, *new_lens, *table;
     int64_t w_stride;
-    int half[2];                           // half words of a block
-    uint32_t inv[2];                       // ceil(2^21 / half)
+    int bytes[2];                          // of a block (0: no such cache)
+    int pieces[2];                         // 16-byte pieces that a block may lie in
+    int pitch[2];                          // shared-memory bytes of a token
+    uint32_t inv_half[2], inv_piece[2];    // ceil(2^32 / n) of the half words of a block, the pieces
     int Hkv, T, T_cap, keep, max_pages, page, num_pages, tile;
 };
 
-struct MovShared {
-    int64_t src[2][kMovTile], dst[2][kMovTile];   // slots of the step's tokens; src < 0: stays
-};
+__device__ __forceinline__ int div_by(uint32_t p, uint32_t inv) { return inv ? (int)__umulhi(p, inv) : (int)p; }
 
-__global__ void __launch_bounds__(kMovThreads) compact_kernel(const __grid_constant__ MovArgs a) {
-    __shared__ MovShared s;
+template <bool WIDE>
+__global__ void __launch_bounds__(kMovThreads, 4) compact_kernel(const __grid_constant__ MovArgs a) {
+    extern __shared__ __align__(16) uint8_t mov_smem[];
+    int64_t *src = reinterpret_cast<int64_t *>(mov_smem);      // [tile] source slot
+    int64_t *dst = src + a.tile;                               // [tile] own slot, -1: not in the pool
+    uint8_t *stage0 = reinterpret_cast<uint8_t *>(dst + a.tile);
+    float *sw = reinterpret_cast<float *>(stage0 + (size_t)a.tile * (a.pitch[0] + a.pitch[1]));
     cg::cluster_group cl = cg::this_cluster();
     const int tid = threadIdx.x, C = (int)cl.num_blocks(), rank = (int)cl.block_rank();
     const int64_t row = blockIdx.x / C;
@@ -267,71 +277,116 @@ __global__ void __launch_bounds__(kMovThreads) compact_kernel(const __grid_const
         if (id < 0 || id >= a.num_pages) return -1;
         return ((int64_t)id * a.Hkv + h) * a.page + (t - pg * a.page);
     };
-    uint16_t cur[2][kMovPer], nxt[2][kMovPer];
-    float wcur = 0.f, wnxt = 0.f;
-    // slots of step t's tokens into buffer t & 1, then its half words into registers
-    auto load = [&](int t, uint16_t (&v)[2][kMovPer], float &wv) {
+    for (int t = 0; t < steps; ++t) {
         const int base = t * per + rank * a.tile;
-        if (tid < a.tile) {
-            const int j = base + tid;
-            int64_t from = -1, to = -1;
-            if (j < n) {
-                const int src = kept[j];
-                if (src > j && src < a.T) {
-                    from = slot(src);
-                    to = slot(j);
-                    if (to < 0) from = -1;
-                    if (w) wv = w[src];
+        const int cnt = max(0, min(a.tile, n - base));
+        const bool moves = cnt > 0 && kept[base + cnt - 1] != base + cnt - 1;
+        if (moves) {
+            for (int i = tid; i < cnt; i += kMovThreads) {
+                const int j = base + i;
+                int from = kept[j];
+                if (from < j || from >= a.T) from = j;   // not a place to take from: it stays
+                const int64_t own = slot(j);
+                int64_t s = from == j ? own : slot(from);
+                if (s < 0) {
+                    s = own;
+                    from = j;
                 }
+                src[i] = s;
+                dst[i] = own;
+                if (w) sw[i] = w[own < 0 ? j : from];
             }
-            s.src[t & 1][tid] = from;
-            s.dst[t & 1][tid] = to;
-        }
-        __syncthreads();
+            __syncthreads();
+            uint8_t *stage = stage0;
 #pragma unroll
-        for (int side = 0; side < 2; ++side) {
-            const int hw = a.half[side], total = a.tile * hw;
+            for (int side = 0; side < 2; ++side) {
+                const int bytes = a.bytes[side];
+                if (bytes == 0) continue;
+                const uint8_t *cache = a.blocks[side];
+                if (WIDE) {
+                    const int np = a.pieces[side], total = cnt * np;
+                    for (int p0 = tid; p0 < total; p0 += 4 * kMovThreads) {
+                        uint4 v[4];
+                        int at[4];
 #pragma unroll
-            for (int q = 0; q < kMovPer; ++q) {
-                const int p = q * kMovThreads + tid;
-                if (p < total) {
-                    const int j = (int)(((uint64_t)p * a.inv[side]) >> 21), i = p - j * hw;
-                    const int64_t from = s.src[t & 1][j];
-                    if (from >= 0)
-                        v[side][q] = reinterpret_cast<const uint16_t *>(a.blocks[side])[from * hw + i];
+                        for (int u = 0; u < 4; ++u) {
+                            const int p = p0 + u * kMovThreads;
+                            at[u] = -1;
+                            if (p < total) {
+                                const int i = div_by(p, a.inv_piece[side]), q = p - i * np;
+                                const int64_t s = src[i];
+                                if (s >= 0) {
+                                    const int64_t first = s * bytes, piece = (first >> 4) + q;
+                                    if (piece * 16 < first + bytes) {
+                                        at[u] = i * a.pitch[side] + q * 16;
+                                        v[u] = *reinterpret_cast<const uint4 *>(cache + piece * 16);
+                                    }
+                                }
+                            }
+                        }
+#pragma unroll
+                        for (int u = 0; u < 4; ++u)
+                            if (at[u] >= 0) *reinterpret_cast<uint4 *>(stage + at[u]) = v[u];
+                    }
+                } else {
+                    const int hw = bytes / 2, total = cnt * hw;
+#pragma unroll 8
+                    for (int p = tid; p < total; p += kMovThreads) {
+                        const int i = div_by(p, a.inv_half[side]), k = p - i * hw;
+                        if (src[i] >= 0)
+                            *reinterpret_cast<uint16_t *>(stage + i * a.pitch[side] + 2 * k) =
+                                reinterpret_cast<const uint16_t *>(cache)[src[i] * hw + k];
+                    }
                 }
+                stage += a.tile * a.pitch[side];
             }
         }
-    };
-    auto store = [&](int t, const uint16_t (&v)[2][kMovPer], float wv) {
+        cl.sync();   // every CTA has read its blocks of this step
+        if (moves) {
+            const uint8_t *stage = stage0;
 #pragma unroll
-        for (int side = 0; side < 2; ++side) {
-            const int hw = a.half[side], total = a.tile * hw;
+            for (int side = 0; side < 2; ++side) {
+                const int bytes = a.bytes[side], hw = bytes / 2, pitch = a.pitch[side];
+                if (bytes == 0) continue;
+                uint8_t *cache = a.blocks[side];
+                const int words = WIDE ? cnt * bytes / 16 : 0;   // whole 16-byte pieces of the tile
+                for (int x = tid; x < words; x += kMovThreads) {
+                    // piece x holds half words 8 x .. 8 x + 7 of the tile, of at most two blocks that matter
+                    const int i = div_by(8 * x, a.inv_half[side]), k = 8 * x - i * hw;
+                    const int o = (i & ~7);
+                    uint32_t v[4];
 #pragma unroll
-            for (int q = 0; q < kMovPer; ++q) {
-                const int p = q * kMovThreads + tid;
-                if (p < total) {
-                    const int j = (int)(((uint64_t)p * a.inv[side]) >> 21), i = p - j * hw;
-                    if (s.src[t & 1][j] >= 0)
-                        reinterpret_cast<uint16_t *>(a.blocks[side])[s.dst[t & 1][j] * hw + i] = v[side][q];
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t e[2];
+#pragma unroll
+                        for (int z = 0; z < 2; ++z) {
+                            int ii = i, kk = k + 2 * q + z;
+                            while (kk >= hw) {
+                                kk -= hw;
+                                ++ii;
+                            }
+                            const uint32_t skew = (uint32_t)(src[ii] * bytes) & 15u;
+                            e[z] = *reinterpret_cast<const uint16_t *>(stage + ii * pitch + skew + 2 * kk);
+                        }
+                        v[q] = e[0] | (e[1] << 16);
+                    }
+                    if (dst[o] >= 0)
+                        *reinterpret_cast<uint4 *>(cache + dst[o] * bytes + (int64_t)(8 * x - o * hw) * 2) =
+                            make_uint4(v[0], v[1], v[2], v[3]);
                 }
+                const int total = cnt * hw;
+                for (int p = words * 8 + tid; p < total; p += kMovThreads) {
+                    const int i = div_by(p, a.inv_half[side]), k = p - i * hw;
+                    const uint32_t skew = WIDE ? (uint32_t)(src[i] * bytes) & 15u : 0u;
+                    if (dst[i] >= 0)
+                        reinterpret_cast<uint16_t *>(cache)[dst[i] * hw + k] =
+                            *reinterpret_cast<const uint16_t *>(stage + i * pitch + skew + 2 * k);
+                }
+                stage += a.tile * pitch;
             }
-        }
-        const int j = t * per + rank * a.tile + tid;
-        if (w && tid < a.tile && s.src[t & 1][tid] >= 0) w[j] = wv;
-    };
-    if (steps) {
-        load(0, cur, wcur);
-        for (int t = 0; t < steps; ++t) {
-            if (t + 1 < steps) load(t + 1, nxt, wnxt);
-            cl.sync();   // every CTA has read step t (and t + 1)
-            store(t, cur, wcur);
-            __syncthreads();   // the slots of step t are rewritten by load(t + 2)
-#pragma unroll
-            for (int side = 0; side < 2; ++side)
-#pragma unroll
-                for (int q = 0; q < kMovPer; ++q) cur[side][q] = nxt[side][q];
-            wcur = wnxt;
+            if (w)
+                for (int i = tid; i < cnt; i += kMovThreads) w[base + i] = sw[i];
+            __syncthreads();   // the next step's blocks take this one's place
         }
     }
     // vacated slots start from zero again (all reads lie before the last meeting)
@@ -376,10 +431,11 @@ extern "C" int tq_evict_select(const float *weights, int64_t row_stride, const i
     if (seq_lens == new_lens) return TQ_ERR_ARG;   // other rows still read the old lengths
     if (!aligned(weights, 4) || !aligned(kept, 4) || !aligned(new_lens, 4) || !aligned(seq_lens, 4)) return TQ_ERR_ALIGN;
     const int64_t rows = (int64_t)B * Hkv;
-    // CTAs per row: a chunk of at most kSelChunk keys each, more while SMs would stay idle and a chunk
-    // keeps 1024 keys
+    // CTAs per row: a chunk of at most kSelChunk keys each; while SMs would stay idle, of 8192
     int C = 1;
-    while (C < kMaxCluster && ((T + C - 1) / C > kSelChunk || (rows * C * 2 <= sm_count() && T / (2 * C) >= 1024))) C *= 2;
+    while (C < kMaxCluster &&
+           ((T + C - 1) / C > kSelChunk || (rows * C * 2 <= sm_count() && (T + C - 1) / C > 8192)))
+        C *= 2;
     const int chunk = (T + C - 1) / C;
     SelArgs a;
     a.weights = weights;
@@ -415,7 +471,7 @@ extern "C" int tq_evict_compact(uint8_t *k_blocks, int k_block_bytes, uint8_t *v
     }
     const int vbytes = v_blocks ? v_block_bytes : 0;
     if ((k_block_bytes & 1) || (vbytes & 1)) return TQ_ERR_ALIGN;
-    if (k_block_bytes > 2 * kMovMaxHalf || vbytes > 2 * kMovMaxHalf) return TQ_ERR_UNSUPPORTED;
+    if (k_block_bytes > kMovMaxBytes || vbytes > kMovMaxBytes) return TQ_ERR_UNSUPPORTED;
     if (!aligned(k_blocks, 2) || !aligned(v_blocks, 2) || !aligned(weights, 4) || !aligned(kept, 4) ||
         !aligned(new_lens, 4) || !aligned(block_table, 4))
         return TQ_ERR_ALIGN;
@@ -427,9 +483,18 @@ extern "C" int tq_evict_compact(uint8_t *k_blocks, int k_block_bytes, uint8_t *v
     a.new_lens = new_lens;
     a.table = block_table;
     a.w_stride = weights_row_stride;
-    a.half[0] = k_block_bytes / 2;
-    a.half[1] = vbytes / 2;
-    for (int i = 0; i < 2; ++i) a.inv[i] = a.half[i] ? ((1u << 21) + a.half[i] - 1) / a.half[i] : 0;
+    const bool wide = aligned(k_blocks, 16) && aligned(v_blocks, 16) && ((block_table ? page_tokens : T_cap) & 7) == 0;
+    const int bytes[2] = {k_block_bytes, vbytes};
+    auto inverse = [](int n) { return n < 2 ? 0u : (uint32_t)(((1ull << 32) + n - 1) / n); };
+    int token = 2 * 8 + 4;   // shared memory of a token
+    for (int i = 0; i < 2; ++i) {
+        a.bytes[i] = bytes[i];
+        a.pieces[i] = bytes[i] ? (bytes[i] + 14 + 15) / 16 : 0;
+        a.pitch[i] = wide ? a.pieces[i] * 16 : bytes[i];
+        a.inv_half[i] = inverse(bytes[i] / 2);
+        a.inv_piece[i] = inverse(a.pieces[i]);
+        token += a.pitch[i];
+    }
     a.Hkv = Hkv;
     a.T = T;
     a.T_cap = T_cap;
@@ -437,13 +502,22 @@ extern "C" int tq_evict_compact(uint8_t *k_blocks, int k_block_bytes, uint8_t *v
     a.max_pages = max_pages;
     a.page = page_tokens;
     a.num_pages = num_pages;
-    // tokens of a CTA and step: as many as the threads' registers hold
-    const int widest = a.half[0] > a.half[1] ? a.half[0] : a.half[1];
-    a.tile = kMovThreads * kMovPer / widest;
-    if (a.tile > kMovTile) a.tile = kMovTile;
     const int64_t rows = (int64_t)B * Hkv;
     const int m = keep < T ? keep : T;
+    // CTAs per row: while the GPU holds more (four per SM) and each still gets 64 tokens
     int C = 1;
-    while (C < kMaxCluster && rows * C < 4 * (int64_t)sm_count() && C * a.tile < m) C *= 2;
-    return launch_cluster(compact_kernel, rows, C, kMovThreads, 0, static_cast<cudaStream_t>(stream), a);
+    while (C < kMaxCluster && rows * C < 4 * (int64_t)sm_count() && m > C * 64) C *= 2;
+    // tokens of a CTA and step: the shared memory's worth at most, the steps of equal size, groups of eight
+    const int most = (kMovSmem / token) & ~7;
+    const int steps = (m + C * most - 1) / (C * most);
+    a.tile = ((m + C * steps - 1) / (C * steps) + 7) & ~7;
+    const size_t smem = (size_t)a.tile * token;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    static int done[2][64] = {{0}};
+    if (wide) {
+        if (set_smem_limit((const void *)compact_kernel<true>, kMovSmem, done[0]) != TQ_OK) return TQ_ERR_CUDA;
+        return launch_cluster(compact_kernel<true>, rows, C, kMovThreads, smem, st, a);
+    }
+    if (set_smem_limit((const void *)compact_kernel<false>, kMovSmem, done[1]) != TQ_OK) return TQ_ERR_CUDA;
+    return launch_cluster(compact_kernel<false>, rows, C, kMovThreads, smem, st, a);
 }

@@ -162,6 +162,22 @@ __device__ __noinline__ uint32_t row_double(const uint8_t *row, const Side &sd, 
     return __half_as_ushort(__double2half(nrm));
 }
 
+// fp16 norm of a row by a whole warp, from its unrotated elements (rope keeps
+// the norm), in double precision.
+template <int DT>
+__device__ __noinline__ uint32_t norm_double(const uint8_t *row) {
+    const int lane = threadIdx.x & 31;
+    double ss = 0.0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const double v = elem_double<DT>(row, 4 * lane + i);
+        ss = fma(v, v, ss);
+    }
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
+    return __half_as_ushort(__double2half(sqrt(ss)));
+}
+
 // Rotary positions on a row in the layout of fwht_pair128: element 16 c + 8 h
 // + k is p[c & 3][k].x (c < 4) or .y.
 template <int M>
@@ -229,17 +245,19 @@ __global__ void __launch_bounds__(kThreads, 4) insert_kernel(const __grid_consta
     const int bits = sd.bits, levels = 1 << bits, bytes = 2 + 16 * bits;
     const int64_t tok = min64(tok0 + r, a.n_tok - 1);   // this thread's token
 
-    for (int i = tid; i < 128 * 16; i += kThreads) {
-        const int cell = i >> 4;
+    static_assert(kThreads == 128, "a thread per cell");
+    {
         uint32_t below = 0;
         float edge = 3.0e38f;   // a cell without a boundary: v - edge < 0 for every v
         for (int j = 0; j < levels - 1; ++j) {
             const float v = sd.b[j] * kGrid;
             const int at = (int)(__float_as_uint(v + (12582912.f + 64.f)) & 127u);
-            if (at < cell) ++below;
-            if (at == cell) edge = v;
+            if (at < tid) ++below;
+            if (at == tid) edge = v;
         }
-        sm.cells[i] = make_uint2(__float_as_uint(edge), below + 1);
+        const uint2 e = make_uint2(__float_as_uint(edge), below + 1);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) sm.cells[tid * 16 + ((i + tid) & 15)] = e;
     }
     if (sd.style != kRopeNone) {
         for (int i = tid; i < kRopePairs * kTok; i += kThreads) {
@@ -327,9 +345,9 @@ __global__ void __launch_bounds__(kThreads, 4) insert_kernel(const __grid_consta
         uint32_t w[8];
         float near = bits == 4 ? quantise<4>(p, scale, cells, w)
                                : bits == 3 ? quantise<3>(p, scale, cells, w) : quantise<2>(p, scale, cells, w);
-        const bool redo = !safe || near < kEps || near_fp16_tie_fast(nrm);
-        uint32_t todo = __ballot_sync(0xffffffffu, redo);
+        uint32_t todo = __ballot_sync(0xffffffffu, !safe || near < kEps);
         todo = (todo | (todo >> 1)) & 0x55555555u;   // either thread of a row speaks for it
+        uint32_t ties = __ballot_sync(0xffffffffu, near_fp16_tie_fast(nrm)) & 0x55555555u & ~todo;
 
         // stage the 16 blocks: half word 0 the norm, then the codes
         uint16_t *blk = stage + r * (bytes / 2);
@@ -357,6 +375,14 @@ __global__ void __launch_bounds__(kThreads, 4) insert_kernel(const __grid_consta
             }
         }
         __syncwarp();
+        while (ties) {
+            const int l = __ffs(ties) - 1, rr = l >> 1;
+            ties &= ties - 1;
+            const int64_t t = min64(tok0 + rr, a.n_tok - 1);
+            const uint32_t nb = norm_double<DT>(sd.x + t * sd.tok + head * sd.head);
+            if (lane == 0) stage[rr * (bytes / 2)] = (uint16_t)nb;
+            __syncwarp();
+        }
         while (todo) {
             const int l = __ffs(todo) - 1, rr = l >> 1;
             todo &= todo - 1;
