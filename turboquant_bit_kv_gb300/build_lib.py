@@ -19,7 +19,7 @@ SOURCES = ["tq_host.cpp", "tq_encode.cu", "tq_decode.cu", "tq_codec.cu", "tq_qjl
            "tq_headdim_mma8.cu", "tq_rope.cu", "tq_insert.cu", "tq_evict.cu",
            "tq_attn_weights.cu", "tq_attn_mma_k2w.cu", "tq_attn_mma_k3w.cu", "tq_attn_mma_k4w.cu"]
 HEADERS = ["tq_device.cuh", "tq_tc.cuh", "tq_attn.cuh", "tq_attn_mma.h", "tq_attn_mma.cuh", "tq_internal.h", "tq_headdim.cuh",
-           "tq_headdim_mma.cuh", "tq_rope.cuh", "tq_attn_combine.cuh"]
+           "tq_headdim_mma.cuh", "tq_rope.cuh", "tq_attn_combine.cuh", "tq_ff.cuh"]
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(kAttnThreads * kCombineMaxGroups) attn_combine
     const float *ws, MmaPlan plan, int Hq, int Hkv, int rotate_back, uint32_t s0, uint32_t s1, uint32_t s2,
     uint32_t s3, float *out) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    combine_mma(ws, plan, blockIdx.x, Hq, Hkv, rotate_back, 0.08838834764831845f, s0, s1, s2, s3,
+    combine_mma<32>(ws, plan, blockIdx.x, Hq, Hkv, rotate_back, 0.08838834764831845f, s0, s1, s2, s3,
                 [&](int d, float v) { out[(int64_t)blockIdx.x * kD + d] = v; });
 }
 

@@ -10,18 +10,17 @@ namespace tq {
 // Merge for the tensor-core kernel's partition, by one CTA for one (sequence,
 // query head) bh: the slots of segment j = (sequence, KV head) are the warps
 // whose chunk ranges touch it.  128 x ng threads: thread d of slot group g
-// reduces output dim d over batches g, g + ng, ... of 32 slots.  Reading what
+// reduces output dim d over batches g, g + ng, ... of kBatch slots.  Reading what
 // other SMs just wrote costs a full L2 round trip, so each thread issues
 // every load of a batch at once (m and l of each slot -- the same address
 // across the group -- and its dim of acc) and only then reduces, with the
 // running max rescaled between batches; the groups run their rounds side by
 // side and meet in shared memory.  rotate_back applies D H with the factor
 // out_scale; store(d, value) takes the output.
-template <class Store>
+template <int kBatch, class Store>
 __device__ __forceinline__ void combine_mma(const float *ws, const MmaPlan &plan, int bh, int Hq, int Hkv,
                                             int rotate_back, float out_scale, uint32_t s0, uint32_t s1, uint32_t s2,
                                             uint32_t s3, Store store) {
-    constexpr int kBatch = 32;
     __shared__ float buf[kD];
     __shared__ float gacc[kCombineMaxGroups][kD];
     __shared__ float gml[kCombineMaxGroups][2];

@@ -34,7 +34,8 @@ int launch_attn_prep_mma(const AttnArgs &a, const MmaPlan &plan, int qjl, cudaSt
 
 namespace {
 
-constexpr int kMergeTokens = 1024;   // tokens of a weights CTA
+constexpr int kMergeBatch = 16;      // slots a merging thread loads at once (one round covers 16 x groups)
+constexpr int kWeightsTokens = 1024; // tokens of a weights CTA at least
 
 struct WeightsArgs {
     const float *ws;
@@ -43,23 +44,23 @@ struct WeightsArgs {
     float *weights;
     void *out;
     int64_t w_stride;
-    int Hq, Hkv, G, T, B, parts;     // parts: weights CTAs per segment
+    int Hq, Hkv, G, T, B, parts, per;   // parts: weights CTAs per segment, of per tokens each (a multiple of 32)
     int out_dtype;
     float decay, out_scale;
     uint32_t signs[4];
 };
 
 // CTAs [0, B Hq): the merge of one (sequence, query head).  The rest: the
-// weights of kMergeTokens tokens of one segment (sequence, KV head): the
+// weights of a.per tokens of one segment (sequence, KV head): the
 // final maximum and sum of its heads, one warp per head over the segment's
 // slots, then a chunk of 32 tokens per warp at a time.
-__global__ void __launch_bounds__(kAttnThreads * kCombineMaxGroups) attn_weights_kernel(
+__global__ void __launch_bounds__(kAttnThreads * kCombineMaxGroups, 2) attn_weights_kernel(
     const __grid_constant__ WeightsArgs a, const __grid_constant__ MmaPlan plan) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int heads = a.B * a.Hq;
     if ((int)blockIdx.x < heads) {
         const int64_t at = (int64_t)blockIdx.x * kD;
-        combine_mma(a.ws, plan, blockIdx.x, a.Hq, a.Hkv, 1, a.out_scale, a.signs[0], a.signs[1], a.signs[2],
+        combine_mma<kMergeBatch>(a.ws, plan, blockIdx.x, a.Hq, a.Hkv, 1, a.out_scale, a.signs[0], a.signs[1], a.signs[2],
                     a.signs[3], [&](int d, float v) {
                         if (a.out_dtype == TQ_F32) static_cast<float *>(a.out)[at + d] = v;
                         else if (a.out_dtype == TQ_BF16) static_cast<__nv_bfloat16 *>(a.out)[at + d] = __float2bfloat16_rn(v);
@@ -70,7 +71,7 @@ __global__ void __launch_bounds__(kAttnThreads * kCombineMaxGroups) attn_weights
     __shared__ float ml[8][2];   // final maximum, 1 / sum
     const int64_t unit = blockIdx.x - heads;
     const int64_t j = unit / a.parts;
-    const int t0 = (int)(unit % a.parts) * kMergeTokens;
+    const int t0 = (int)(unit % a.parts) * a.per;
     const int b = (int)(j / a.Hkv);
     int L = a.T;
     if (a.seq_lens) {
@@ -105,23 +106,29 @@ __global__ void __launch_bounds__(kAttnThreads * kCombineMaxGroups) attn_weights
         }
     }
     __syncthreads();
-    // a warp takes a chunk of 32 tokens at a time: G rows of 32 scores, one coalesced load each
-    const int end = min(t0 + kMergeTokens, L);
+    // a warp takes two chunks of 32 tokens at a time: G rows of 32 scores each, one coalesced load a row
+    const int end = min(t0 + a.per, L);
     float *w = a.weights + j * a.w_stride;
     const float *sc = a.scores + j * plan.C * (kMmaChunk * a.G) + lane;
-    for (int c = t0 / kMmaChunk + warp; c * kMmaChunk < end; c += nw) {
-        const float *row = sc + (int64_t)c * (kMmaChunk * a.G);
-        const int t = c * kMmaChunk + lane;
-        const bool in = t < end;
-        float s[8], old = 0.f;
+    for (int c = t0 / kMmaChunk + 2 * warp; c * kMmaChunk < end; c += 2 * nw) {
+        float s[2][8], old[2] = {0.f, 0.f};
 #pragma unroll
-        for (int g = 0; g < 8; ++g) s[g] = g < a.G ? __ldcs(row + g * kMmaChunk) : 0.f;
-        if (in && a.decay != 0.f) old = __ldcs(w + t) * a.decay;
-        float p = 0.f;
+        for (int u = 0; u < 2; ++u) {
+            const int t = (c + u) * kMmaChunk + lane;
+            const float *row = sc + (int64_t)(c + u) * (kMmaChunk * a.G);
 #pragma unroll
-        for (int g = 0; g < 8; ++g)
-            if (g < a.G) p = fmaf(exp2f(s[g] - ml[g][0]), ml[g][1], p);
-        if (in) w[t] = old + p;
+            for (int g = 0; g < 8; ++g) s[u][g] = g < a.G && t < end ? __ldcs(row + g * kMmaChunk) : 0.f;
+            if (t < end && a.decay != 0.f) old[u] = __ldcs(w + t) * a.decay;
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int t = (c + u) * kMmaChunk + lane;
+            float p = 0.f;
+#pragma unroll
+            for (int g = 0; g < 8; ++g)
+                if (g < a.G) p = fmaf(exp2f(s[u][g] - ml[g][0]), ml[g][1], p);
+            if (t < end) w[t] = old[u] + p;
+        }
     }
 }
 
@@ -201,7 +208,13 @@ extern "C" int tq_attn_decode_weights(const void *q, int q_dtype, const uint8_t 
         !aligned(workspace, 16) || !aligned(weights, 4) || !aligned(seq_lens, 4) || !aligned(block_table, 4))
         return TQ_ERR_ALIGN;
     if (workspace_bytes < tq_attn_weights_workspace_bytes(B, Hq, Hkv, T)) return TQ_ERR_WORKSPACE;
-    const int parts = (T + kMergeTokens - 1) / kMergeTokens;
+    // weights CTAs per segment: about eight per SM, each of kWeightsTokens tokens at least (every one of
+    // them works out its heads' maximum and sum)
+    const int64_t segs = (int64_t)B * Hkv, wanted = ((int64_t)sm_count() * 8 + segs - 1) / segs;
+    const int most = (T + kWeightsTokens - 1) / kWeightsTokens;
+    int parts = (int)(wanted < most ? wanted : most);
+    const int per = ((T + parts - 1) / parts + kMmaChunk - 1) / kMmaChunk * kMmaChunk;
+    parts = (T + per - 1) / per;
     const int64_t grid = (int64_t)B * Hq + (int64_t)B * Hkv * parts;
     if (grid > 0x7FFFFFFF) return TQ_ERR_UNSUPPORTED;
 
@@ -254,13 +267,15 @@ extern "C" int tq_attn_decode_weights(const void *q, int q_dtype, const uint8_t 
     w.T = T;
     w.B = B;
     w.parts = parts;
+    w.per = per;
     w.out_dtype = out_dtype;
     w.decay = decay;
     w.out_scale = 0.08838834764831845f / vf;
     for (int i = 0; i < 4; ++i) w.signs[i] = signs.w[i];
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3(kAttnThreads * mma_combine_groups(plan));
+    const int groups = (plan.Smax + kMergeBatch - 1) / kMergeBatch;
+    cfg.blockDim = dim3(kAttnThreads * (groups < 1 ? 1 : (groups > kCombineMaxGroups ? kCombineMaxGroups : groups)));
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

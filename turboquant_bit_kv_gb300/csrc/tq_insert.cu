@@ -6,30 +6,52 @@
 // in between), nrm = ||x||, y = H (D x) / (sqrt(128) nrm), code_j =
 // #{i : b_i <= y_j}, block = [fp16 nrm][packed codes]; a value row the same
 // without rope.  Each row is read once and each block written once (the floor:
-// 256 + 66 bytes for a 16-bit row at 4 bits); the rotation, 7 x 128 additions
-// a row, and the quantiser, about 8 instructions an element, make instruction
-// issue the bound.
+// 256 + 66 bytes for a 16-bit row at 4 bits).  Instruction issue is what
+// bounds the kernel, and the quantiser (about 6.5 instructions an element) the
+// largest part of it.
 //
 // Layout.  A CTA takes 16 tokens and four warps; a warp takes the 16 tokens
-// of one head at a time, two threads per row (element map of fwht_pair128, in
-// which elements j and j + 64 of a row are the two halves of one packed
-// pair).  The sines and cosines of the 16 tokens are computed once per CTA
-// and shared by its heads; the sign diagonal D is folded in: the rows' sign
-// bits are flipped as they are unpacked, and the sine of a pair whose two
-// signs differ is negated.
+// of one head at a time as the 16 rows of m16n8k16 products.  Thread (g, t) =
+// (lane / 4, lane % 4) holds elements 32 c + 8 t .. + 7 (c = 0 .. 3) of rows g
+// and g + 8.  H factors over the bits of the element index: bits 0, 1, 3 and 4
+// are the k index of a product with the 16 x 16 Hadamard matrix (eight k-tiles
+// of 16 elements, +-1 operands, exact), bits 2, 5 and 6 number the k-tiles and
+// are three butterfly stages on the accumulators, which a thread holds all of:
+// the transform costs no shuffle and no shared memory.  The columns are ordered
+// so that a thread gets back the elements whose inputs it held.  Rows of 16-bit
+// elements enter as they are; rotated (or float32) rows are scaled by a power
+// of two to a norm of about 2^9 and split x = hi + lo into two fp16 parts (22
+// bits; the float32 accumulation keeps 24).
 //
-// Codes.  The quantiser works in v = 63 y: adding 1.5 * 2^23 rounds v to an
-// integer whose low 7 bits select one of 128 cells; a cell holds at most one
-// boundary b (checked on the host) and the number of boundaries below it, and
-// the sign of v - b finishes the count.  The table has 16 copies (one per
-// lane of a half warp), so the 8-byte loads meet no bank conflict.
+// The sines and cosines of the 16 tokens are computed once per CTA and shared
+// by its heads; the sign diagonal D is folded in: the rows' sign bits are
+// flipped as they are loaded, and the sine of a pair whose two signs differ is
+// negated.
+//
+// Codes.  The quantiser works in v = 63 y: adding 1.5 * 2^16 + 64.5 leaves v
+// + 64.5 with seven fraction bits in the low mantissa bits, so that one AND
+// gives the cell floor(v + 64.5) of 128 times the 128 bytes of its table row; a
+// cell holds at most one boundary b (checked on the host) and the number of
+// boundaries below it, and the sign of v - b finishes the count.  A row has 16
+// copies (one per lane of a half warp), so the 8-byte loads meet no bank
+// conflict.
 //
 // Borders.  Decisions are those of 64-bit arithmetic (y rounded once to
 // float32 and compared with the float32 boundaries), although the row is
 // transformed in float32: a row with a coordinate closer to a boundary than
-// kEps (far above the float32 error), a norm close to a rounding border of
-// fp16 or a sum of squares outside float32's safe range is taken again by its
-// whole warp in double precision (about 0.4% of rows).
+// kEps or a norm closer to a rounding border of fp16 than kTieUlps (both far
+// above the float32 error; about 0.2% of rows each) is listed, and when the CTA
+// is through its tiles the listed rows are taken again in double-float
+// arithmetic, one by each of its warps (four for their norms alone).  Rows of a
+// sum of squares outside float32's safe range go through double precision.  (The
+// double-precision pipe has one sixty-fourth of the float32 rate: on it, all
+// such rows together cost 168 of the 433 us of a prompt of 131072 tokens x 8
+// heads; in double-float but one at a time between the tiles, where three warps
+// wait for the fourth, 157 of 398.)
+//
+// CTAs are persistent, four per SM, each on keys or on values; a warp's next
+// rows are on their way to shared memory (each thread copies what it will read
+// itself) while it works on the current ones.
 #include <cmath>
 #include <cstring>
 
@@ -46,9 +68,16 @@ constexpr int kThreads = 32 * kWarps;
 constexpr float kGrid = 63.f;        // cells per unit of y
 // Distance to a boundary, in v = 63 y, below which a row is decided in double
 // precision: 2e-6 of a coordinate's standard deviation (1 / sqrt(128)).  The
-// float32 path is off by about 1.2e-7 of it (rms: rope, seven butterfly
-// stages and the scale, each half an ulp of partial sums of the row's size).
+// float32 path is off by about 1.5e-7 of it (rms: rope, the fp16 split, the
+// products' accumulation, three butterfly stages and the scale, each an ulp or
+// less of partial sums of the row's size).
 constexpr float kEps = 2e-6f * kGrid * 0.08838834764831845f;
+
+// Distance of the norm to a rounding border of fp16, in units of its last
+// float32 place.  The norm is off by about one of them (rms): nine roundings in
+// the sum of squares, halved by the root, those of the elements (independent,
+// so of little weight in the sum), and three of the root itself.
+constexpr uint32_t kTieUlps = 8;
 
 enum { kRopeNone = 0, kRopeHalf1, kRopeHalf2, kRopeHalf3, kRopeHalf4, kRopeAdjacent };
 
@@ -66,15 +95,32 @@ struct InsertArgs {
     Side side[2];           // keys, values
     const int64_t *pos, *dst;
     int64_t n_tok, pos_axis, dst_head;
-    int heads, heads_per_cta, groups;   // groups of heads per token tile
+    int units;              // of a side: (tile group, head group) pairs
+    int heads, heads_per_cta, groups;   // groups of heads per tile group
+    int tiles;              // token tiles of a CTA at once: 4, 2 or 1 for 1, 2 or more heads
+    int ctas[2];            // of each side
     uint32_t signs[4];
 };
 
+constexpr int kList = 256;               // rows to take again that a CTA can list
+constexpr uint64_t kRange = 1ull << 63;  // listed for being outside float32's safe range
+constexpr int kStage = kTok * 33 + 8;    // half words a warp stages its 16 blocks in (and the 128 values of a
+                                         // row taken again)
+
 struct Shared {
     uint2 cells[128 * 16];                    // (boundary, boundaries below + 1) x 16 copies
-    float2 cs[kRopePairs][kTok];              // (cos, sin'), sin' negated where the pair's signs differ
-    alignas(16) uint16_t stage[kWarps][kTok * 33 + 8];   // packed blocks of a warp's 16 rows
-    double2 cs64[kWarps][kRopePairs];         // a row's cos and sin (double-precision path)
+    alignas(16) uint16_t stage[kWarps][kStage];
+    uint4 in[kWarps][8][32];                  // the next rows (16-bit types), as their threads read them
+    uint4 flip[4][4];                         // sign bits of the 16-bit elements 32 c + 8 t .. + 7
+    uint64_t turn[kRopePairs];                // the rope, and whether a pair's two signs differ (bit 2 of axis)
+    uint8_t axis[kRopePairs];
+    uint64_t list[kList];                     // token * heads + head: norms from the front, rows from the back
+    int listed[2];
+    // cosines and sines (negated where the pair's two signs differ) of two
+    // neighbouring pairs, (c, c', s, s'); unit u of token n and thread t at
+    // [(u * 16 + n) * 4 + t].  Halves: unit 4 c + k holds pairs 32 c + 8 t + 2 k and the next.
+    // Adjacent: unit 2 c + k holds pairs 16 c + 4 t + 2 k and the next.  A table per token tile.
+    alignas(16) float4 cs[][8 * kTok * 4];
 };
 
 template <int DT>
@@ -83,167 +129,460 @@ struct Row {
     static constexpr int kBytes = DT == TQ_F32 ? 4 : 2;
 };
 
-// Element e of a row as a double.
+// Element e of a row.
 template <int DT>
-__device__ __forceinline__ double elem_double(const uint8_t *row, int e) {
-    if constexpr (DT == TQ_F32) return (double)reinterpret_cast<const float *>(row)[e];
+__device__ __forceinline__ float elem(const uint8_t *row, int e) {
+    if constexpr (DT == TQ_F32) return reinterpret_cast<const float *>(row)[e];
     else if constexpr (DT == TQ_BF16)
-        return (double)__uint_as_float((uint32_t)reinterpret_cast<const uint16_t *>(row)[e] << 16);
+        return __uint_as_float((uint32_t)reinterpret_cast<const uint16_t *>(row)[e] << 16);
     else
-        return (double)__half2float(reinterpret_cast<const __half *>(row)[e]);
+        return __half2float(reinterpret_cast<const __half *>(row)[e]);
 }
 
-// One row by a whole warp in double precision: lane l holds elements
-// 4 l .. 4 l + 3.  Returns the fp16 norm; code[i] is the code of element
-// 4 l + i.
-template <int DT>
-__device__ __noinline__ uint32_t row_double(const uint8_t *row, const Side &sd, const tq_rope &rope,
-                                            const InsertArgs &a, int64_t tok, double2 *cs64, uint32_t (&code)[4]) {
+// Rows taken again.  The code is kept small and in loops, values in shared
+// memory: it runs seldom, and fetching instructions that are not in a cache
+// costs more than executing them (unrolled, two rows of the same arithmetic
+// took 20 us).
+
+// Codes of elements 4 l .. 4 l + 3 (byte i of code) into a block.
+__device__ __forceinline__ void write_codes(uint8_t *block, int bits, uint32_t code, int lane) {
+    if (bits == 4) {
+        code |= code >> 4;   // bytes 0 and 2 hold two codes each
+        reinterpret_cast<uint16_t *>(block)[1 + lane] = (uint16_t)((code & 0xFFu) | ((code >> 8) & 0xFF00u));
+        return;
+    }
+    const uint32_t low = code & 0x03030303u;
+    block[2 + lane] = (uint8_t)(low | (low >> 6) | (low >> 12) | (low >> 18));
+    if (bits == 3) {
+        const uint32_t top = (code >> 2) & 0x01010101u;
+        uint32_t hi = (top | (top >> 7) | (top >> 14) | (top >> 21)) & 15u;
+        hi |= __shfl_down_sync(0xffffffffu, hi, 1) << 4;
+        if (!(lane & 1)) block[34 + lane / 2] = (uint8_t)hi;
+    }
+}
+
+// A value of either arithmetic, for the code that the two share.
+__device__ __forceinline__ double add_(double a, double b) { return a + b; }
+__device__ __forceinline__ ff add_(ff a, ff b) { return ff_add(a, b); }
+__device__ __forceinline__ double neg_(double a) { return -a; }
+__device__ __forceinline__ ff neg_(ff a) { return ff_neg(a); }
+__device__ __forceinline__ double mul_(double a, double b) { return a * b; }
+__device__ __forceinline__ ff mul_(ff a, ff b) { return ff_mul(a, b); }
+__device__ __forceinline__ double scale_(double a, float b) { return a * (double)b; }
+__device__ __forceinline__ ff scale_(ff a, float b) { return ff_scale(a, b); }
+__device__ __forceinline__ double shfl_(double a, int m) { return __shfl_xor_sync(0xffffffffu, a, m); }
+__device__ __forceinline__ ff shfl_(ff a, int m) {
+    return {__shfl_xor_sync(0xffffffffu, a.h, m), __shfl_xor_sync(0xffffffffu, a.l, m)};
+}
+__device__ __forceinline__ void load_(double &v, float x) { v = (double)x; }
+__device__ __forceinline__ void load_(ff &v, float x) { v = ff_of(x); }
+__device__ __forceinline__ void sincos_(uint64_t f, double &s, double &c) { rope_sincos_double(f, s, c); }
+__device__ __forceinline__ void sincos_(uint64_t f, ff &s, ff &c) { rope_sincos_ff(f, s, c); }
+
+// One row by a warp in the arithmetic N: H (D x) of the rotated row into
+// v[128]; the sum of the row's squares is returned.
+template <int DT, class N>
+__device__ __forceinline__ N transform_row(const uint8_t *row, const Side &sd, const tq_rope &rope, const InsertArgs &a,
+                                           int64_t tok, N *v) {
     const int lane = threadIdx.x & 31;
-    double v[4];
-    if (sd.style != kRopeNone) {
-        const int pairs = rope.rot_dim / 2;
-        for (int i = lane; i < pairs; i += 32) {
-            const int64_t t = a.pos[rope.axis[i] * a.pos_axis + tok];
-            double s, c;
-            rope_sincos_double(rope_turns(rope.turn[i], t), s, c);
-            cs64[i] = make_double2(c, s);
+    const int pairs = sd.style == kRopeNone ? 0 : rope.rot_dim / 2;
+#pragma unroll 1
+    for (int pr = lane; pr < kRopePairs; pr += 32) {
+        const bool turned = pr < pairs, half = turned && sd.style != kRopeAdjacent;
+        const int ea = half ? pr : 2 * pr, eb = half ? pr + pairs : 2 * pr + 1;
+        const float xa = elem<DT>(row, ea), xb = elem<DT>(row, eb);
+        N ra, rb;
+        load_(ra, xa);
+        load_(rb, xb);
+        if (turned) {
+            N s, c;
+            sincos_(rope_turns(rope.turn[pr], a.pos[rope.axis[pr] * a.pos_axis + tok]), s, c);
+            ra = add_(scale_(c, xa), scale_(s, -xb));
+            rb = add_(scale_(c, xb), scale_(s, xa));
         }
+        v[ea] = ra;
+        v[eb] = rb;
+    }
+    __syncwarp();
+    N ss;
+    load_(ss, 0.f);
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i) {
+        const N x = v[32 * i + lane];
+        ss = add_(ss, mul_(x, x));
+        if ((a.signs[i] >> lane) & 1u) v[32 * i + lane] = neg_(x);
+    }
+#pragma unroll 1
+    for (int m = 1; m < 32; m <<= 1) ss = add_(ss, shfl_(ss, m));
+#pragma unroll 1
+    for (int h = 1; h < kD; h <<= 1) {
         __syncwarp();
 #pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const int n = 32 * q + lane, i = ((n & ~(h - 1)) << 1) | (n & (h - 1));
+            const N x = v[i], y = v[i + h];
+            v[i] = add_(x, y);
+            v[i + h] = add_(x, neg_(y));
+        }
+    }
+    __syncwarp();
+    return ss;
+}
+
+// A row outside float32's safe range (or of zeros), in double precision.
+template <int DT>
+__device__ __noinline__ void range_row(const uint8_t *row, uint8_t *block, const Side &sd, const tq_rope &rope,
+                                       const InsertArgs &a, int64_t tok, double *v) {
+    const int lane = threadIdx.x & 31;
+    bool any = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) any |= elem<DT>(row, 4 * lane + i) != 0.f;
+    uint32_t code = 0x01010101u << (sd.bits - 1), norm = 0;
+    if (__any_sync(0xffffffffu, any)) {
+        const double nrm = sqrt(transform_row<DT, double>(row, sd, rope, a, tok, v));
+        norm = __half_as_ushort(__double2half(nrm));
+        const double f = 1.0 / (nrm * 11.313708498984761);   // sqrt(128)
+        code = 0;
+#pragma unroll 1
         for (int i = 0; i < 4; ++i) {
-            const int e = 4 * lane + i;
-            v[i] = elem_double<DT>(row, e);
-            if (e < 2 * pairs) {
-                const bool half = sd.style != kRopeAdjacent;
-                const int pr = half ? (e < pairs ? e : e - pairs) : e >> 1;
-                const bool second = half ? e >= pairs : (e & 1) != 0;
-                const int other = half ? (second ? e - pairs : e + pairs) : e ^ 1;
-                const double2 t = cs64[pr];
-                const double o = elem_double<DT>(row, other);
-                v[i] = fma(v[i], t.x, second ? o * t.y : -o * t.y);
+            const float y = (float)(v[4 * lane + i] * f);
+#pragma unroll 1
+            for (int j = 0; j < (1 << sd.bits) - 1; ++j) code += sd.b[j] <= y ? 1u << (8 * i) : 0u;
+        }
+    }
+    if (lane == 0) *reinterpret_cast<uint16_t *>(block) = (uint16_t)norm;
+    write_codes(block, sd.bits, code, lane);
+}
+
+// A row whose codes float32 does not decide, in double-float.
+template <int DT>
+__device__ __noinline__ void near_row(const uint8_t *row, uint8_t *block, const Side &sd, const tq_rope &rope,
+                                      const InsertArgs &a, int64_t tok, ff *v) {
+    const int lane = threadIdx.x & 31;
+    const ff nrm = ff_sqrt(transform_row<DT, ff>(row, sd, rope, a, tok, v));
+    if (lane == 0) *reinterpret_cast<uint16_t *>(block) = ff_half(nrm);
+    // y >= b after its rounding to float32 where v >= b' sqrt(128) nrm, b' half way to b's lower neighbour;
+    // lane j has boundary j
+    const float b = sd.b[lane < 15 ? lane : 14];
+    const uint32_t w = __float_as_uint(b);
+    const float under = b == 0.f ? 0.f : __uint_as_float(b > 0.f ? w - 1 : w + 1);
+    const ff k = ff_mul(nrm, ff_of(11.313708498984761f, (float)(11.313708498984761 - (double)11.313708498984761f)));
+    const ff mine = ff_mul(k, ff_of(b, b == 0.f ? 0.f : 0.5f * (under - b)));
+    ff x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = v[4 * lane + i];
+    uint32_t code = 0;
+#pragma unroll 1
+    for (int j = 0; j < (1 << sd.bits) - 1; ++j) {
+        const float eh = __shfl_sync(0xffffffffu, mine.h, j), el = __shfl_sync(0xffffffffu, mine.l, j);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            // (of two renormalised values the larger high part, then the larger low part)
+            code += x[i].h > eh || (x[i].h == eh && x[i].l >= el) ? 1u << (8 * i) : 0u;
+    }
+    write_codes(block, sd.bits, code, lane);
+}
+
+// Norms of four rows (rope keeps them), one per eight lanes.
+template <int DT>
+__device__ __noinline__ void norm_rows(const uint8_t *row, uint8_t *block, bool write) {
+    const int l = threadIdx.x & 7;
+    ff ss = ff_of(0.f);
+#pragma unroll 4
+    for (int i = 0; i < 16; ++i) {
+        const ff x = ff_of(elem<DT>(row, 16 * l + i));
+        ss = ff_add(ss, ff_mul(x, x));
+    }
+#pragma unroll 1
+    for (int m = 1; m < 8; m <<= 1) ss = ff_add(ss, shfl_(ss, m));
+    if (write && l == 0) *reinterpret_cast<uint16_t *>(block) = ff_half(ff_sqrt(ss));
+}
+
+// The listed rows by a warp, its share of them: of the norms list[0 .. ties)
+// four at a time from i0 * 4 on, of the others, counted from the list's end,
+// one at a time from i0 on.
+template <int DT>
+__device__ __noinline__ void take_again(const uint64_t *list, int size, int ties, int rows, int i0, int step,
+                                        const Side &sd, const tq_rope &rope, const InsertArgs &a, uint16_t *stage) {
+    auto place = [&](uint64_t entry, const uint8_t *&row, uint8_t *&block) {
+        const int64_t id = (int64_t)(entry & ~kRange), tok = id / a.heads;
+        const int head = (int)(id - tok * a.heads);
+        row = sd.x + tok * sd.tok + head * sd.head;
+        block = sd.blocks + (a.dst[tok] + head * a.dst_head) * (2 + 16 * sd.bits);
+        return tok;
+    };
+    const uint8_t *row;
+    uint8_t *block;
+    for (int i = i0; i < rows; i += step) {
+        const uint64_t entry = list[size - 1 - i];
+        const int64_t tok = place(entry, row, block);
+        if (entry & kRange) range_row<DT>(row, block, sd, rope, a, tok, reinterpret_cast<double *>(stage));
+        else near_row<DT>(row, block, sd, rope, a, tok, reinterpret_cast<ff *>(stage));
+        __syncwarp();
+    }
+    for (int i = 4 * i0; i < ties; i += 4 * step) {
+        const int q = i + ((threadIdx.x >> 3) & 3);
+        place(list[q < ties ? q : i], row, block);
+        norm_rows<DT>(row, block, q < ties);
+    }
+}
+
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+
+// (a, b) <- (a cos - b sin, b cos + a sin) for two pairs at once.
+__device__ __forceinline__ void turn2(float2 &a, float2 &b, const float4 &t) {
+    const float2 c = make_float2(t.x, t.y), s = make_float2(t.z, t.w), n = make_float2(-t.z, -t.w);
+    const float2 va = a, vb = b;
+    a = fma2(va, c, mul2(vb, n));
+    b = fma2(vb, c, mul2(va, s));
+}
+
+// A row's elements in a thread: x[c][k] holds elements 32 c + 8 t + 2 k, + 1.
+typedef float2 RowPart[4][4];
+
+// Rotary positions on a thread's part of a row; cs: the row's token in the
+// table of sines, [unit * 64].
+__device__ __forceinline__ void rope_row(RowPart &x, int style, const float4 *cs, int t) {
+    if (style == kRopeHalf4) {          // pairs (e, e + 64)
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) turn2(x[c][k], x[c + 2][k], cs[(4 * c + k) * 64]);
+    } else if (style == kRopeAdjacent) {   // pairs (e, e + 1): e even
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int k = 0; k < 4; k += 2) {
+                const float4 w = cs[(2 * c + k / 2) * 64];
+                const float2 a = x[c][k], b = x[c][k + 1];
+                x[c][k] = make_float2(fmaf(a.x, w.x, -(a.y * w.z)), fmaf(a.y, w.x, a.x * w.z));
+                x[c][k + 1] = make_float2(fmaf(b.x, w.y, -(b.y * w.w)), fmaf(b.y, w.y, b.x * w.w));
+            }
+    } else if (style == kRopeHalf2) {   // pairs (e, e + 32)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) turn2(x[0][k], x[1][k], cs[k * 64]);
+    } else if (style == kRopeHalf1) {   // pairs (e, e + 16): thread t with t ^ 2
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float4 w = cs[k * 64 - (t & 2)];   // pair index modulo 16: thread t & 1
+            float2 o;
+            o.x = __shfl_xor_sync(0xffffffffu, x[0][k].x, 2);
+            o.y = __shfl_xor_sync(0xffffffffu, x[0][k].y, 2);
+            const float2 s = (t & 2) ? make_float2(w.z, w.w) : make_float2(-w.z, -w.w);
+            x[0][k] = fma2(x[0][k], make_float2(w.x, w.y), mul2(o, s));
+        }
+    } else if (style == kRopeHalf3) {
+        // pairs (e, e + 48): the partner of chunk c's element lies in thread t ^ 2, chunk (c + 1) % 3 for
+        // t < 2, (c + 2) % 3 for the others; pair index e or e - 48
+        const bool hi = (t & 2) != 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            float2 o[3];
+#pragma unroll
+            for (int c = 0; c < 3; ++c) {
+                const float2 send = hi ? x[(c + 1) % 3][k] : x[(c + 2) % 3][k];
+                o[c].x = __shfl_xor_sync(0xffffffffu, send.x, 2);
+                o[c].y = __shfl_xor_sync(0xffffffffu, send.y, 2);
+            }
+#pragma unroll
+            for (int c = 0; c < 3; ++c) {
+                // first of its pair: chunk 0, and chunk 1 for t < 2
+                const bool second = c == 2 || (c == 1 && hi);
+                // pair 32 c' + 8 t' + 2 k: chunk 0 as it is; chunk 1: t < 2 as it is, else pair 8 (t - 2);
+                // chunk 2: t < 2 pair 8 (t + 2), else 32 + 8 (t - 2)
+                const int unit = c == 0 ? 0 : (c == 1 ? (hi ? 0 : 1) : (hi ? 1 : 0));
+                const int shift = c == 0 ? 0 : (c == 1 ? (hi ? -2 : 0) : (hi ? -2 : 2));
+                const float4 w = cs[(4 * unit + k) * 64 + shift];
+                const float2 s = second ? make_float2(w.z, w.w) : make_float2(-w.z, -w.w);
+                x[c][k] = fma2(x[c][k], make_float2(w.x, w.y), mul2(o[c], s));
             }
         }
-        __syncwarp();
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = elem_double<DT>(row, 4 * lane + i);
     }
-    double ss = 0.0;
+}
+
+template <bool BF16>
+__device__ __forceinline__ void mma16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                      uint32_t b1) {
+    if constexpr (BF16)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%0, %1, %2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%0, %1, %2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The same with the accumulator starting at zero.
+template <bool BF16>
+__device__ __forceinline__ void mma16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                            uint32_t b0, uint32_t b1) {
+    if constexpr (BF16)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%10, %10, %10, %10};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%10, %10, %10, %10};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+// Accumulators: [c][s][n-tile][4]; entries 0, 1 (row g) and 2, 3 (row g + 8)
+// are elements 32 c + 8 t + 4 s + 2 nt, + 1.
+typedef float Acc[4][2][2][4];
+
+// The butterflies over element bits 2 (s), 5 and 6 (c).
+__device__ __forceinline__ void butterflies(Acc &u) {
+    auto step = [](float (&a)[4], float (&b)[4]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) ss = fma(v[i], v[i], ss);
+        for (int i = 0; i < 4; i += 2) {
+            const float2 x = make_float2(a[i], a[i + 1]), y = make_float2(b[i], b[i + 1]);
+            const float2 p = add2(x, y), m = sub2(x, y);
+            a[i] = p.x;
+            a[i + 1] = p.y;
+            b[i] = m.x;
+            b[i + 1] = m.y;
+        }
+    };
 #pragma unroll
-    for (int m = 1; m < 32; m <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
-    const double nrm = sqrt(ss);
+    for (int nt = 0; nt < 2; ++nt) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if ((a.signs[lane >> 3] >> (4 * (lane & 7) + i)) & 1u) v[i] = -v[i];
-    const double x0 = v[0] + v[1], x1 = v[0] - v[1], x2 = v[2] + v[3], x3 = v[2] - v[3];
-    v[0] = x0 + x2;
-    v[2] = x0 - x2;
-    v[1] = x1 + x3;
-    v[3] = x1 - x3;
+        for (int c = 0; c < 4; ++c) step(u[c][0][nt], u[c][1][nt]);
 #pragma unroll
-    for (int m = 1; m < 32; m <<= 1) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const double o = __shfl_xor_sync(0xffffffffu, v[i], m);
-            v[i] = (lane & m) ? o - v[i] : v[i] + o;
+        for (int s = 0; s < 2; ++s) {
+            step(u[0][s][nt], u[1][s][nt]);
+            step(u[2][s][nt], u[3][s][nt]);
+            step(u[0][s][nt], u[2][s][nt]);
+            step(u[1][s][nt], u[3][s][nt]);
         }
     }
-    const double f = ss > 0.0 ? 1.0 / (nrm * 11.313708498984761) : 0.0;   // sqrt(128)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float y = (float)(v[i] * f);
-        uint32_t n = 0;
-        for (int j = 0; j < (1 << sd.bits) - 1; ++j) n += sd.b[j] <= y ? 1u : 0u;
-        code[i] = n;
-    }
-    return __half_as_ushort(__double2half(nrm));
 }
 
-// fp16 norm of a row by a whole warp, from its unrotated elements (rope keeps
-// the norm), in double precision.
-template <int DT>
-__device__ __noinline__ uint32_t norm_double(const uint8_t *row) {
-    const int lane = threadIdx.x & 31;
-    double ss = 0.0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const double v = elem_double<DT>(row, 4 * lane + i);
-        ss = fma(v, v, ss);
-    }
-#pragma unroll
-    for (int m = 1; m < 32; m <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
-    return __half_as_ushort(__double2half(sqrt(ss)));
-}
-
-// Rotary positions on a row in the layout of fwht_pair128: element 16 c + 8 h
-// + k is p[c & 3][k].x (c < 4) or .y.
-template <int M>
-__device__ __forceinline__ void rope_half(float2 (&p)[4][8], const float2 (*cs)[kTok], int tok, int h) {
-#pragma unroll
-    for (int c = 0; c < M; ++c)
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const float2 t = cs[16 * c + 8 * h + k][tok];
-            float &fa = c < 4 ? p[c & 3][k].x : p[c & 3][k].y;
-            float &fb = c + M < 4 ? p[(c + M) & 3][k].x : p[(c + M) & 3][k].y;
-            const float va = fa, vb = fb;
-            fa = fmaf(va, t.x, -(vb * t.y));
-            fb = fmaf(vb, t.x, va * t.y);
-        }
-}
-
-__device__ __forceinline__ void rope_adjacent(float2 (&p)[4][8], const float2 (*cs)[kTok], int tok, int h) {
-#pragma unroll
-    for (int c = 0; c < 4; ++c)
-#pragma unroll
-        for (int k = 0; k < 8; k += 2) {
-            const int i = 8 * c + 4 * h + k / 2;
-            const float2 t = cs[i][tok], u = cs[i + 32][tok];   // elements below and from 64 on
-            const float2 va = p[c][k], vb = p[c][k + 1];
-            p[c][k] = make_float2(fmaf(va.x, t.x, -(vb.x * t.y)), fmaf(va.y, u.x, -(vb.y * u.y)));
-            p[c][k + 1] = make_float2(fmaf(vb.x, t.x, va.x * t.y), fmaf(vb.y, u.x, va.y * u.y));
-        }
-}
-
-// Codes of this thread's 64 elements of a row, packed: for chunk c (0..7) and
-// element 16 c + 8 h + k the BITS-wide field k of w[c].  Returns the smallest
-// |v - b| met.
-template <int BITS>
-__device__ __forceinline__ float quantise(const float2 (&p)[4][8], float scale, const uint2 *cells, uint32_t (&w)[8]) {
+// Codes of a thread's 32 elements of row R (0: g, 1: g + 8), the BITS-wide
+// field k of w[c] element 32 c + 8 t + k.  Returns the smallest |v - b| met.
+template <int BITS, int R>
+__device__ __forceinline__ float quantise(const Acc &u, float scale, const uint8_t *cells, uint32_t lane8,
+                                          uint32_t (&w)[4]) {
     float near = 1.f;
+    const float2 s2 = make_float2(scale, scale), m2 = make_float2(98304.f + 64.5f, 98304.f + 64.5f);
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
+    for (int c = 0; c < 4; ++c) {
         uint32_t acc = 0;
 #pragma unroll
-        for (int k = 7; k >= 0; --k) {
-            const float u = c < 4 ? p[c & 3][k].x : p[c & 3][k].y;
-            const uint32_t cell = __float_as_uint(fmaf(u, scale, 12582912.f + 64.f)) & 127u;
-            const uint2 e = cells[cell * 16];
-            const float t = fmaf(u, scale, -__uint_as_float(e.x));
-            near = fminf(near, fabsf(t));
-            acc = (acc << BITS) + e.y + (uint32_t)(__float_as_int(t) >> 31);
+        for (int q = 3; q >= 0; --q) {
+            const float2 x = make_float2(u[c][q >> 1][q & 1][2 * R], u[c][q >> 1][q & 1][2 * R + 1]);
+            const float2 v = fma2(x, s2, m2);
+            const uint2 e1 = *reinterpret_cast<const uint2 *>(cells + ((__float_as_uint(v.y) & 0x3F80u) | lane8));
+            const uint2 e0 = *reinterpret_cast<const uint2 *>(cells + ((__float_as_uint(v.x) & 0x3F80u) | lane8));
+            const float t1 = fmaf(x.y, scale, -__uint_as_float(e1.x)), t0 = fmaf(x.x, scale, -__uint_as_float(e0.x));
+            near = fminf(fminf(near, fabsf(t1)), fabsf(t0));
+            acc = (acc << BITS) + e1.y + (uint32_t)(__float_as_int(t1) >> 31);
+            acc = (acc << BITS) + e0.y + (uint32_t)(__float_as_int(t0) >> 31);
         }
         w[c] = acc;
     }
     return near;
 }
 
+// Quantise and stage one row: half word 0 of its block the norm, then the codes.
+template <int BITS, int R>
+__device__ __forceinline__ float pack_row(const Acc &u, float scale, const uint8_t *cells, uint32_t lane8,
+                                          uint16_t *blk, int t) {
+    uint32_t w[4];
+    const float near = quantise<BITS, R>(u, scale, cells, lane8, w);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        if constexpr (BITS == 4) {
+            blk[1 + 8 * c + 2 * t] = (uint16_t)w[c];
+            blk[2 + 8 * c + 2 * t] = (uint16_t)(w[c] >> 16);
+        } else if constexpr (BITS == 2) {
+            blk[1 + 4 * c + t] = (uint16_t)w[c];
+        } else {
+            uint32_t lo = 0, hi = 0;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                lo |= ((w[c] >> (3 * k)) & 3u) << (2 * k);
+                hi |= ((w[c] >> (3 * k + 2)) & 1u) << k;
+            }
+            blk[1 + 4 * c + t] = (uint16_t)lo;
+            reinterpret_cast<uint8_t *>(blk)[34 + 4 * c + t] = (uint8_t)hi;
+        }
+    }
+    return near;
+}
+
+// One float2 as two fp16 parts, hi + lo.
+__device__ __forceinline__ void split2(float2 x, uint32_t &hi, uint32_t &lo) {
+    const __half2 h = __floats2half2_rn(x.x, x.y);
+    const float2 r = sub2(x, __half22float2(h));
+    const __half2 l = __floats2half2_rn(r.x, r.y);
+    hi = *reinterpret_cast<const uint32_t *>(&h);
+    lo = *reinterpret_cast<const uint32_t *>(&l);
+}
+
 template <int DT>
 __global__ void __launch_bounds__(kThreads, 4) insert_kernel(const __grid_constant__ tq_rope rope,
-                                                             const __grid_constant__ InsertArgs a, int sides, int first) {
+                                                             const __grid_constant__ InsertArgs a) {
     constexpr int NV = Row<DT>::kVecs, ES = Row<DT>::kBytes;
     extern __shared__ __align__(16) uint8_t dsmem[];
     Shared &sm = *reinterpret_cast<Shared *>(dsmem);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, h = lane & 1, r = lane >> 1;
-    const Side &sd = a.side[first + blockIdx.x % sides];
-    const int64_t unit = blockIdx.x / sides;
-    const int64_t tok0 = unit / a.groups * kTok;
-    const int head0 = (int)(unit % a.groups) * a.heads_per_cta;
-    const int bits = sd.bits, levels = 1 << bits, bytes = 2 + 16 * bits;
-    const int64_t tok = min64(tok0 + r, a.n_tok - 1);   // this thread's token
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+    const int which = (int)blockIdx.x < a.ctas[0] ? 0 : 1;
+    const Side &sd = a.side[which];
+    const int cta = blockIdx.x - (which ? a.ctas[0] : 0), step = a.ctas[which];
+    const int bits = sd.bits, levels = 1 << bits, bytes = 2 + 16 * bits, style = sd.style;
+    // the warps of a tile take its heads in turn
+    const int hw = kWarps / a.tiles, tile = warp / hw;
+
+    // rows of a unit: a tile of 16 tokens, and the heads of a group in this warp's turn
+    const bool one_group = a.groups == 1;
+    auto group_of = [&](int unit) { return one_group ? 0 : unit % a.groups; };
+    auto tile_of = [&](int unit) { return ((int64_t)(one_group ? unit : unit / a.groups) * a.tiles + tile) * kTok; };
+    auto head_of = [&](int unit) { return group_of(unit) * a.heads_per_cta + warp % hw; };
+    auto head_end = [&](int unit) { return min((group_of(unit) + 1) * a.heads_per_cta, a.heads); };
+    // the two rows of this thread: its 8 elements of chunk c at + 32 c
+    auto rows_of = [&](int64_t tok0, const uint8_t *(&p)[2]) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) p[r] = sd.x + min64(tok0 + g + 8 * r, a.n_tok - 1) * sd.tok + 8 * t * ES;
+    };
+    // copies of the rows of (rows, head) to this thread's places
+    auto fetch = [&](const uint8_t *const (&rows)[2], int head) {
+        if constexpr (DT != TQ_F32) {
+            const int64_t at = head * sd.head;
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const uint8_t *p = rows[r] + at;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) cp_async16(&sm.in[warp][4 * r + c][lane], p + 32 * c * ES);
+            }
+            cp_async_commit();
+        }
+    };
+    int unit = cta;
+    int head = 0;
+    // the next (unit, head) of this warp from (u, h) on that has rows; u past the end if none
+    auto settle = [&](int &u, int &h) {
+        while (u < a.units && (h >= head_end(u) || tile_of(u) >= a.n_tok)) {
+            u += step;
+            if (u < a.units) h = head_of(u);
+        }
+    };
+    if (unit < a.units) {
+        head = head_of(unit);
+        int u = unit;
+        int h = head;
+        settle(u, h);
+        if (u < a.units) {
+            const uint8_t *rows[2];
+            rows_of(tile_of(u), rows);
+            fetch(rows, h);
+        }
+    }
 
     static_assert(kThreads == 128, "a thread per cell");
     {
@@ -251,7 +590,7 @@ __global__ void __launch_bounds__(kThreads, 4) insert_kernel(const __grid_consta
         float edge = 3.0e38f;   // a cell without a boundary: v - edge < 0 for every v
         for (int j = 0; j < levels - 1; ++j) {
             const float v = sd.b[j] * kGrid;
-            const int at = (int)(__float_as_uint(v + (12582912.f + 64.f)) & 127u);
+            const int at = (int)floorf(v + 64.5f);
             if (at < tid) ++below;
             if (at == tid) edge = v;
         }
@@ -259,180 +598,311 @@ __global__ void __launch_bounds__(kThreads, 4) insert_kernel(const __grid_consta
 #pragma unroll
         for (int i = 0; i < 16; ++i) sm.cells[tid * 16 + ((i + tid) & 15)] = e;
     }
-    if (sd.style != kRopeNone) {
-        for (int i = tid; i < kRopePairs * kTok; i += kThreads) {
-            const int pr = i / kTok, t = i % kTok;
-            float s = 0.f, c = 1.f;
-            if (pr < rope.rot_dim / 2) {
-                const int64_t n = min64(tok0 + t, a.n_tok - 1);
-                rope_sincos(rope_turns(rope.turn[pr], a.pos[rope.axis[pr] * a.pos_axis + n]), s, c);
-                const int ea = sd.style == kRopeAdjacent ? 2 * pr : pr;
-                const int eb = sd.style == kRopeAdjacent ? ea + 1 : pr + rope.rot_dim / 2;
-                if (((a.signs[ea >> 5] >> (ea & 31)) ^ (a.signs[eb >> 5] >> (eb & 31))) & 1u) s = -s;
-            }
-            sm.cs[pr][t] = make_float2(c, s);
-        }
+    if (tid < 64) {   // word k of chunk c, thread t: elements 32 c + 8 t + 2 k, + 1
+        const int e = 2 * tid, c = e >> 5, th = (e >> 3) & 3, k = (e >> 1) & 3;
+        const uint32_t s2 = a.signs[e >> 5] >> (e & 31);
+        reinterpret_cast<uint32_t *>(&sm.flip[c][th])[k] = (s2 & 1u) << 15 | (s2 & 2u) << 30;
     }
-    __syncthreads();
+    if (tid < 2) sm.listed[tid] = 0;
+    if (tid < kRopePairs && style != kRopeNone) {
+        const int pairs = rope.rot_dim / 2;
+        const int ea = style == kRopeAdjacent ? 2 * tid : tid, eb = style == kRopeAdjacent ? ea + 1 : tid + pairs;
+        const uint32_t differ = tid < pairs ? ((a.signs[ea >> 5] >> (ea & 31)) ^ (a.signs[eb >> 5] >> (eb & 31))) & 1u : 0u;
+        // (past the rotated elements: no angle)
+        sm.turn[tid] = tid < pairs ? rope.turn[tid] : 0;
+        sm.axis[tid] = (uint8_t)((tid < pairs ? rope.axis[tid] : 0) | differ << 2);
+    }
 
-    const int64_t dst = tok0 + r < a.n_tok ? a.dst[tok] : -1;
+    // the 16 x 16 Hadamard matrix as B fragments: k = (thread t, j) in, n = (thread g / 2, j = 2 nt + g % 2)
+    // out; j = 0, 1 in b[nt][0], 2, 3 in b[nt][1]; 1.0 of the products' type
+    constexpr bool kBf = DT == TQ_BF16;
+    const bool direct = DT != TQ_F32 && style == kRopeNone;
+    uint32_t bf[2][2];
+    {
+        const uint32_t one = direct && kBf ? 0x3F80u : 0x3C00u;
+        const int tt = __popc(t & (g >> 1));
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const int jo = 2 * nt + (g & 1);
+                const uint32_t n0 = (tt + __popc((2 * q) & jo)) & 1, n1 = (tt + __popc((2 * q + 1) & jo)) & 1;
+                bf[nt][q] = (one | n0 << 15) | (one | n1 << 15) << 16;
+            }
+    }
     uint16_t *stage = sm.stage[warp];
-    const uint2 *cells = sm.cells + (lane & 15);
-    const int head_end = min(head0 + a.heads_per_cta, a.heads);
-    for (int head = head0 + warp; head < head_end; head += kWarps) {
-        const uint8_t *row = sd.x + tok * sd.tok + head * sd.head;
-        uint4 raw[8][NV];
+    const uint8_t *cells = reinterpret_cast<const uint8_t *>(sm.cells);
+    const uint32_t lane8 = (lane & 15) * 8;
+
+    for (; unit < a.units; unit += step) {
+        const int64_t tok0 = tile_of(unit);
+        const int64_t my = tok0 + (lane & 15);
+        const int64_t dst = my < a.n_tok ? a.dst[my] : -1;   // of token lane % 16
+        if (style != kRopeNone) {
+            const bool adj = style == kRopeAdjacent;
+            const int64_t first = tile_of(unit) - tile * kTok;
+            const int th = tid & 3;
+            __syncthreads();   // the rope's copy is there, and the last unit's table no longer read
+            for (int v = 0; v < a.tiles; ++v) {
+                // this thread's token of the tile, and its units tid / 64, + 2, ...
+                const int64_t at = min64(first + v * kTok + ((tid >> 2) & 15), a.n_tok - 1);
+                int64_t pos[3];
 #pragma unroll
-        for (int c = 0; c < 8; ++c)
+                for (int i = 0; i < 3; ++i) pos[i] = a.pos[(i < rope.axes ? i : 0) * a.pos_axis + at];
 #pragma unroll
-            for (int i = 0; i < NV; ++i)
-                raw[c][i] = __ldcs(reinterpret_cast<const uint4 *>(row + (16 * c + 8 * h) * ES) + i);
-        float2 p[4][8];
+                for (int u = 0; u < 4; ++u) {
+                    const int unit8 = 2 * u + (tid >> 6);
+                    const int p0 = adj ? 16 * (unit8 >> 1) + 4 * th + 2 * (unit8 & 1) : 32 * (unit8 >> 2) + 8 * th + 2 * (unit8 & 3);
+                    float s[2], c[2];
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-            // elements 16 c + 8 h .. + 7: their signs are bits 16 (c & 1) + 8 h .. of word c / 2
-            const uint32_t sg = a.signs[c >> 1] >> (16 * (c & 1) + 8 * h);
-            float f[8];
+                    for (int z = 0; z < 2; ++z) {
+                        const uint32_t ax = sm.axis[p0 + z];
+                        const int64_t p = (ax & 3u) == 0 ? pos[0] : (ax & 3u) == 1 ? pos[1] : pos[2];
+                        rope_sincos(rope_turns(sm.turn[p0 + z], p), s[z], c[z]);
+                        if (ax & 4u) s[z] = -s[z];
+                    }
+                    sm.cs[v][u * 128 + tid] = make_float4(c[0], c[1], s[0], s[1]);
+                }
+            }
+        }
+        if (style != kRopeNone || unit == cta) __syncthreads();
+        const int hend = tok0 < a.n_tok ? head_end(unit) : 0;
+        const uint8_t *rows[2];
+        rows_of(tok0, rows);
+        for (head = head_of(unit); head < hend; head += hw) {
+            uint4 raw[2][4][NV];
             if constexpr (DT == TQ_F32) {
-                const uint32_t w[8] = {raw[c][0].x, raw[c][0].y, raw[c][0].z, raw[c][0].w,
-                                       raw[c][NV - 1].x, raw[c][NV - 1].y, raw[c][NV - 1].z, raw[c][NV - 1].w};
 #pragma unroll
-                for (int k = 0; k < 8; ++k) f[k] = __uint_as_float(w[k] ^ ((sg << (31 - k)) & 0x80000000u));
+                for (int r = 0; r < 2; ++r)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+#pragma unroll
+                        for (int i = 0; i < NV; ++i)
+                            raw[r][c][i] =
+                                __ldcs(reinterpret_cast<const uint4 *>(rows[r] + head * sd.head + 32 * c * ES) + i);
             } else {
-                uint32_t w[4] = {raw[c][0].x, raw[c][0].y, raw[c][0].z, raw[c][0].w};
+                cp_async_wait<0>();
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    w[k] ^= ((sg << (15 - 2 * k)) & 0x8000u) | ((sg << (30 - 2 * k)) & 0x80000000u);
-                    if constexpr (DT == TQ_BF16) {
-                        f[2 * k] = bf16_bits_lo(w[k]);
-                        f[2 * k + 1] = bf16_bits_hi(w[k]);
-                    } else {
-                        const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&w[k]));
-                        f[2 * k] = x.x;
-                        f[2 * k + 1] = x.y;
+                for (int r = 0; r < 2; ++r)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) raw[r][c][0] = sm.in[warp][4 * r + c][lane];
+                if (head + hw < hend) {
+                    fetch(rows, head + hw);
+                } else {
+                    int u = unit;
+                    int h = head + hw;
+                    settle(u, h);
+                    if (u < a.units) {
+                        const uint8_t *next[2];
+                        rows_of(tile_of(u), next);
+                        fetch(next, h);
+                    }
+                }
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const uint4 f = sm.flip[c][t];
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        raw[r][c][0].x ^= f.x;
+                        raw[r][c][0].y ^= f.y;
+                        raw[r][c][0].z ^= f.z;
+                        raw[r][c][0].w ^= f.w;
                     }
                 }
             }
+            Acc u;
+            // sums of squares of rows g and g + 8 (of the whole row after the quad's shuffles)
+            float ss[2], post[2] = {1.f, 1.f};   // (post: the inverse of a row's factor)
+            if (direct) {
+                if constexpr (DT != TQ_F32) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                if (c < 4) p[c & 3][k].x = f[k];
-                else p[c & 3][k].y = f[k];
-            }
-        }
-        switch (sd.style) {
-            case kRopeHalf4: rope_half<4>(p, sm.cs, r, h); break;
-            case kRopeHalf3: rope_half<3>(p, sm.cs, r, h); break;
-            case kRopeHalf2: rope_half<2>(p, sm.cs, r, h); break;
-            case kRopeHalf1: rope_half<1>(p, sm.cs, r, h); break;
-            case kRopeAdjacent: rope_adjacent(p, sm.cs, r, h); break;
-            default: break;
-        }
-        float2 acc2[4];
+                    for (int c = 0; c < 4; ++c)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            acc2[c] = __fmul2_rn(p[c][0], p[c][0]);
-#pragma unroll
-            for (int k = 1; k < 8; ++k) acc2[c] = __ffma2_rn(p[c][k], p[c][k], acc2[c]);
-        }
-        const float2 a01 = add2(add2(acc2[0], acc2[1]), add2(acc2[2], acc2[3]));
-        float ss = a01.x + a01.y;
-        ss += __shfl_xor_sync(0xffffffffu, ss, 1);
-        fwht_pair128(p, h ? -1.f : 1.f);
-        const float nrm = sqrtf(ss);
-        // 2^-100 .. 2^100: squares neither underflow nor overflow (false for a NaN as well)
-        const bool safe = ss >= 7.888609052210118e-31f && ss <= 1.2676506002282294e30f;
-        const float scale = kGrid * 0.08838834764831845f / nrm;
-        uint32_t w[8];
-        float near = bits == 4 ? quantise<4>(p, scale, cells, w)
-                               : bits == 3 ? quantise<3>(p, scale, cells, w) : quantise<2>(p, scale, cells, w);
-        uint32_t todo = __ballot_sync(0xffffffffu, !safe || near < kEps);
-        todo = (todo | (todo >> 1)) & 0x55555555u;   // either thread of a row speaks for it
-        uint32_t ties = __ballot_sync(0xffffffffu, near_fp16_tie_fast(nrm)) & 0x55555555u & ~todo;
-
-        // stage the 16 blocks: half word 0 the norm, then the codes
-        uint16_t *blk = stage + r * (bytes / 2);
-        if (h == 0) blk[0] = __half_as_ushort(__float2half_rn(nrm));
-        if (bits == 4) {
-#pragma unroll
-            for (int c = 0; c < 8; ++c) {
-                blk[1 + 4 * c + 2 * h] = (uint16_t)w[c];
-                blk[2 + 4 * c + 2 * h] = (uint16_t)(w[c] >> 16);
-            }
-        } else if (bits == 2) {
-#pragma unroll
-            for (int c = 0; c < 8; ++c) blk[1 + 2 * c + h] = (uint16_t)w[c];
-        } else {
-#pragma unroll
-            for (int c = 0; c < 8; ++c) {
-                uint32_t lo = 0, hi = 0;
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    lo |= ((w[c] >> (3 * k)) & 3u) << (2 * k);
-                    hi |= ((w[c] >> (3 * k + 2)) & 1u) << k;
+                        for (int nt = 0; nt < 2; ++nt) {
+                            const uint4 x = raw[0][c][0], y = raw[1][c][0];
+                            mma16_first<kBf>(u[c][0][nt], x.x, y.x, x.y, y.y, bf[nt][0], bf[nt][1]);
+                            mma16_first<kBf>(u[c][1][nt], x.z, y.z, x.w, y.w, bf[nt][0], bf[nt][1]);
+                        }
                 }
-                blk[1 + 2 * c + h] = (uint16_t)lo;
-                reinterpret_cast<uint8_t *>(blk)[34 + 2 * c + h] = (uint8_t)hi;
-            }
-        }
-        __syncwarp();
-        while (ties) {
-            const int l = __ffs(ties) - 1, rr = l >> 1;
-            ties &= ties - 1;
-            const int64_t t = min64(tok0 + rr, a.n_tok - 1);
-            const uint32_t nb = norm_double<DT>(sd.x + t * sd.tok + head * sd.head);
-            if (lane == 0) stage[rr * (bytes / 2)] = (uint16_t)nb;
-            __syncwarp();
-        }
-        while (todo) {
-            const int l = __ffs(todo) - 1, rr = l >> 1;
-            todo &= todo - 1;
-            const int64_t t = min64(tok0 + rr, a.n_tok - 1);
-            uint32_t code[4];
-            const uint32_t nb = row_double<DT>(sd.x + t * sd.tok + head * sd.head, sd, rope, a, t, sm.cs64[warp], code);
-            uint16_t *b = stage + rr * (bytes / 2);
-            if (lane == 0) b[0] = (uint16_t)nb;
-            if (bits == 4) {
-                b[1 + lane] = (uint16_t)(code[0] | (code[1] << 4) | (code[2] << 8) | (code[3] << 12));
+                // a product with the 16 x 16 matrix has 16 times the row's sum of squares
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    float2 q[4];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float2 x = make_float2(u[c][i >> 1][i & 1][2 * r], u[c][i >> 1][i & 1][2 * r + 1]);
+                            q[c] = i ? fma2(x, x, q[c]) : mul2(x, x);
+                        }
+                    q[0] = add2(add2(q[0], q[1]), add2(q[2], q[3]));
+                    ss[r] = q[0].x + q[0].y;
+                    ss[r] += __shfl_xor_sync(0xffffffffu, ss[r], 1);
+                    ss[r] += __shfl_xor_sync(0xffffffffu, ss[r], 2);
+                    ss[r] *= 0.0625f;
+                }
             } else {
-                const uint32_t lo = (code[0] & 3u) | ((code[1] & 3u) << 2) | ((code[2] & 3u) << 4) | ((code[3] & 3u) << 6);
-                reinterpret_cast<uint8_t *>(b)[2 + lane] = (uint8_t)lo;
-                if (bits == 3) {
-                    uint32_t hi = (code[0] >> 2) | ((code[1] >> 2) << 1) | ((code[2] >> 2) << 2) | ((code[3] >> 2) << 3);
-                    hi |= __shfl_down_sync(0xffffffffu, hi, 1) << 4;
-                    if (!(lane & 1)) reinterpret_cast<uint8_t *>(b)[34 + lane / 2] = (uint8_t)hi;
+                RowPart x[2];
+#pragma unroll
+                for (int r = 0; r < 2; ++r)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const uint4 v0 = raw[r][c][0], v1 = raw[r][c][NV - 1];
+                        if constexpr (DT == TQ_F32) {
+                            const uint4 f = sm.flip[c][t];
+                            const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+                            const uint32_t m[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                x[r][c][k] = make_float2(__uint_as_float(w[2 * k] ^ (m[k] << 16)),
+                                                         __uint_as_float(w[2 * k + 1] ^ (m[k] & 0x80000000u)));
+                        } else {
+                            const uint32_t w[4] = {v0.x, v0.y, v0.z, v0.w};
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                if constexpr (kBf) x[r][c][k] = make_float2(bf16_bits_lo(w[k]), bf16_bits_hi(w[k]));
+                                else x[r][c][k] = __half22float2(*reinterpret_cast<const __half2 *>(&w[k]));
+                            }
+                        }
+                    }
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    rope_row(x[r], style, sm.cs[tile] + (g + 8 * r) * 4 + t, t);
+                    float2 q[4];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) q[c] = k ? fma2(x[r][c][k], x[r][c][k], q[c]) : mul2(x[r][c][k], x[r][c][k]);
+                    q[0] = add2(add2(q[0], q[1]), add2(q[2], q[3]));
+                    ss[r] = q[0].x + q[0].y;
+                    ss[r] += __shfl_xor_sync(0xffffffffu, ss[r], 1);
+                    ss[r] += __shfl_xor_sync(0xffffffffu, ss[r], 2);
+                    // power of two that brings the norm to [2^9, 2^10.5): half the exponent of the sum of
+                    // squares (rows outside the safe range are redone, whatever comes of it here)
+                    const int e = (int)(__float_as_uint(ss[r]) >> 23) - 127;
+                    const float pre = __uint_as_float((uint32_t)(127 + 9 - (e >> 1)) << 23);
+                    post[r] = __uint_as_float((uint32_t)(127 - 9 + (e >> 1)) << 23);
+                    const float2 p2 = make_float2(pre, pre);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) x[r][i >> 2][i & 3] = mul2(x[r][i >> 2][i & 3], p2);
+                }
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) {
+                        uint32_t hi[2][2], lo[2][2];
+#pragma unroll
+                        for (int r = 0; r < 2; ++r)
+#pragma unroll
+                            for (int q = 0; q < 2; ++q) split2(x[r][c][2 * s + q], hi[r][q], lo[r][q]);
+#pragma unroll
+                        for (int nt = 0; nt < 2; ++nt) {
+                            mma16_first<false>(u[c][s][nt], hi[0][0], hi[1][0], hi[0][1], hi[1][1], bf[nt][0], bf[nt][1]);
+                            mma16<false>(u[c][s][nt], lo[0][0], lo[1][0], lo[0][1], lo[1][1], bf[nt][0], bf[nt][1]);
+                        }
+                    }
+            }
+            butterflies(u);
+            bool redo[2], tie[2];
+            float nrm[2], near[2], sc[2];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                // 1 / norm: the hardware's estimate and one Newton step (2^-23)
+                float inv;
+                asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(ss[r]));
+                inv = fmaf(inv * fmaf(-ss[r] * inv, inv, 1.f), 0.5f, inv);
+                nrm[r] = ss[r] * inv;
+                sc[r] = kGrid * 0.08838834764831845f * inv * post[r];
+                // 2^-100 .. 2^100: squares neither underflow nor overflow (false for a NaN as well)
+                redo[r] = !(ss[r] >= 7.888609052210118e-31f && ss[r] <= 1.2676506002282294e30f);
+                tie[r] = ((__float_as_uint(nrm[r]) & 0x1FFFu) - (0x1000u - kTieUlps)) <= 2 * kTieUlps ||
+                         !(nrm[r] >= 6.103515625e-05f && nrm[r] < 65504.f);   // (or outside fp16's normal range)
+            }
+            uint16_t *blkA = stage + g * (bytes / 2), *blkB = stage + (g + 8) * (bytes / 2);
+            if (t == 0) {
+                blkA[0] = __half_as_ushort(__float2half_rn(nrm[0]));
+                blkB[0] = __half_as_ushort(__float2half_rn(nrm[1]));
+            }
+            if (bits == 4) {
+                near[0] = pack_row<4, 0>(u, sc[0], cells, lane8, blkA, t);
+                near[1] = pack_row<4, 1>(u, sc[1], cells, lane8, blkB, t);
+            } else if (bits == 3) {
+                near[0] = pack_row<3, 0>(u, sc[0], cells, lane8, blkA, t);
+                near[1] = pack_row<3, 1>(u, sc[1], cells, lane8, blkB, t);
+            } else {
+                near[0] = pack_row<2, 0>(u, sc[0], cells, lane8, blkA, t);
+                near[1] = pack_row<2, 1>(u, sc[1], cells, lane8, blkB, t);
+            }
+            __syncwarp();
+
+            // store: 16 consecutive block slots at a 16-byte boundary leave as one run, else block by block
+            const int64_t slot = dst < 0 ? -1 : dst + head * a.dst_head;
+            const bool ok = slot >= 0 && slot < sd.n_blocks;
+            const int64_t slot0 = __shfl_sync(0xffffffffu, slot, 0);
+            uint8_t *out0 = sd.blocks + slot0 * bytes;
+            const bool run = __all_sync(0xffffffffu, ok && slot == slot0 + (lane & 15)) && ((uintptr_t)out0 & 15) == 0;
+            const uint32_t okm = __ballot_sync(0xffffffffu, ok);
+            if (run) {
+                for (int i = lane; i < bytes; i += 32)
+                    reinterpret_cast<uint4 *>(out0)[i] = reinterpret_cast<const uint4 *>(stage)[i];
+            } else {
+                for (int q = 0; q < kTok; ++q) {
+                    const int64_t s = __shfl_sync(0xffffffffu, slot, q);
+                    if (!((okm >> q) & 1u)) continue;
+                    uint16_t *o = reinterpret_cast<uint16_t *>(sd.blocks + s * bytes);
+                    const uint16_t *b = stage + q * (bytes / 2);
+                    for (int i = lane; i < bytes / 2; i += 32) o[i] = b[i];
+                }
+            }
+
+            // rows to take again: bits 4 g .. of a mask for rows g and g + 8 (any thread of the quad speaks for its
+            // row)
+            uint32_t todo[2], ties[2], wild[2];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                wild[r] = __ballot_sync(0xffffffffu, redo[r]);
+                uint32_t m = __ballot_sync(0xffffffffu, redo[r] || near[r] < kEps);
+                m |= m >> 1;
+                todo[r] = (m | m >> 2) & 0x11111111u;
+                ties[r] = __ballot_sync(0xffffffffu, tie[r]) & 0x11111111u;
+            }
+            if (todo[0] | todo[1] | ties[0] | ties[1]) {
+                // lane n < 16 lists row n: for its norm, or whole
+                const int bit = 4 * (lane & 7), odd = lane & 8;
+                const bool whole = ((odd ? todo[1] : todo[0]) >> bit) & 1u, tied = ((odd ? ties[1] : ties[0]) >> bit) & 1u;
+                const uint64_t entry = (uint64_t)(my * a.heads + head) |
+                                       ((((odd ? wild[1] : wild[0]) >> bit) & 1u) ? kRange : 0);
+                bool full = false;
+                if (lane < kTok && ok && (whole || tied)) {
+                    const int at = atomicAdd(&sm.listed[whole ? 1 : 0], 1);
+                    full = at >= kList / 2;
+                    if (!full) sm.list[whole ? kList - 1 - at : at] = entry;
+                }
+                // that half of the list is full (inputs of many zeros, say): at once
+                uint32_t m = __ballot_sync(0xffffffffu, full);
+                while (m) {
+                    const int q = __ffs(m) - 1;
+                    m &= m - 1;
+                    const uint64_t one = __shfl_sync(0xffffffffu, entry, q);
+                    const bool row = __shfl_sync(0xffffffffu, whole, q);
+                    __syncwarp();   // its block is written, and the staged blocks are read
+                    take_again<DT>(&one, 1, row ? 0 : 1, row ? 1 : 0, 0, 1, sd, rope, a, stage);
                 }
             }
             __syncwarp();
         }
-
-        // store: 16 consecutive block slots at a 16-byte boundary leave as one run, else block by block
-        const int64_t slot = dst < 0 ? -1 : dst + head * a.dst_head;
-        const bool ok = slot >= 0 && slot < sd.n_blocks;
-        const int64_t slot0 = __shfl_sync(0xffffffffu, slot, 0);
-        uint8_t *out0 = sd.blocks + slot0 * bytes;
-        const bool run = __all_sync(0xffffffffu, ok && slot == slot0 + r) && ((uintptr_t)out0 & 15) == 0;
-        if (run) {
-            for (int i = lane; i < bytes; i += 32)
-                reinterpret_cast<uint4 *>(out0)[i] = reinterpret_cast<const uint4 *>(stage)[i];
-        } else {
-            const uint32_t okm = __ballot_sync(0xffffffffu, ok);
-            for (int q = 0; q < kTok; ++q) {
-                if (!((okm >> (2 * q)) & 1u)) continue;
-                const int64_t s = __shfl_sync(0xffffffffu, slot, 2 * q);
-                uint16_t *o = reinterpret_cast<uint16_t *>(sd.blocks + s * bytes);
-                const uint16_t *b = stage + q * (bytes / 2);
-                for (int i = lane; i < bytes / 2; i += 32) o[i] = b[i];
-            }
-        }
-        __syncwarp();
     }
+    __syncthreads();
+    take_again<DT>(sm.list, kList, min(sm.listed[0], kList / 2), min(sm.listed[1], kList / 2), warp, kWarps, sd, rope, a,
+                   stage);
 }
 
 template <int DT>
-int launch(const tq_rope &rope, const InsertArgs &a, int sides, int first, unsigned grid, cudaStream_t st) {
+int launch(const tq_rope &rope, const InsertArgs &a, cudaStream_t st) {
+    const int smem = (int)(sizeof(Shared) + (size_t)a.tiles * sizeof(float4) * 8 * kTok * 4);
     static int done[64] = {0};
-    if (set_smem_limit((const void *)insert_kernel<DT>, (int)sizeof(Shared), done) != TQ_OK) return TQ_ERR_CUDA;
-    insert_kernel<DT><<<grid, kThreads, sizeof(Shared), st>>>(rope, a, sides, first);
+    if (set_smem_limit((const void *)insert_kernel<DT>, smem, done) != TQ_OK) return TQ_ERR_CUDA;
+    insert_kernel<DT><<<a.ctas[0] + a.ctas[1], kThreads, smem, st>>>(rope, a);
     return launch_status();
 }
 
@@ -444,9 +914,9 @@ bool cells_ok(const tq_codebook *cb) {
     for (int i = 0; i < cb->levels - 1; ++i) {
         const float v = cb->boundaries[i] * kGrid;
         if (!(std::fabs(v) < 62.f)) return false;
-        const float n = std::nearbyint(v);
-        if (std::fabs(v - n) > 0.5f - 1.f / 64.f) return false;
-        const int cell = (int)n + 64;
+        const float n = std::floor(v + 64.5f);
+        if (std::fabs(v + 64.f - n) > 0.5f - 1.f / 64.f) return false;
+        const int cell = (int)n;
         if (cell <= last) return false;
         last = cell;
     }
@@ -504,20 +974,27 @@ extern "C" int tq_insert_kv(const void *k, int64_t k_tok_stride, int64_t k_head_
     a.n_tok = n_tok;
     a.heads = heads;
     for (int i = 0; i < 4; ++i) a.signs[i] = signs.w[i];
-    const int sides = (k != nullptr) + (v != nullptr), first = k ? 0 : 1;
-    const int64_t tiles = (n_tok + kTok - 1) / kTok;
-    // all heads of a token tile in one CTA share its sines; with few tiles four heads a CTA fill more SMs
-    a.heads_per_cta = tiles * sides >= (int64_t)sm_count() * 4 ? heads : (heads < kWarps ? heads : kWarps);
+    // token tiles of a CTA: its four warps share a tile's sines, or take a tile each where heads are few
+    a.tiles = heads == 1 ? 4 : heads == 2 ? 2 : 1;
+    const int64_t tiles = (n_tok + (int64_t)kTok * a.tiles - 1) / (kTok * a.tiles);
+    const int sides = (k != nullptr) + (v != nullptr);
+    const int64_t slots = (int64_t)sm_count() * 4;
+    // with few tiles, four heads a CTA fill more SMs
+    a.heads_per_cta = heads <= kWarps || tiles * sides >= slots ? heads : kWarps;
     a.groups = (heads + a.heads_per_cta - 1) / a.heads_per_cta;
-    const int64_t grid = tiles * a.groups * sides;
-    if (grid > 0x7FFFFFFF) return TQ_ERR_UNSUPPORTED;
+    if (tiles * a.groups > 0x3FFFFFFF) return TQ_ERR_UNSUPPORTED;
+    a.units = (int)(tiles * a.groups);
+    // a rotated key costs about half as much again as a value
+    const int64_t share = sides == 1 ? slots : a.side[0].style == kRopeNone ? slots / 2 : slots * 3 / 5;
+    a.ctas[0] = k ? (int)min64(a.units, share) : 0;
+    a.ctas[1] = v ? (int)min64(a.units, k ? slots - share : slots) : 0;
     tq_rope none;
     if (!rope) std::memset(&none, 0, sizeof(none));
     const tq_rope &r = rope ? *rope : none;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     switch (dtype) {
-        case TQ_BF16: return launch<TQ_BF16>(r, a, sides, first, (unsigned)grid, st);
-        case TQ_F16: return launch<TQ_F16>(r, a, sides, first, (unsigned)grid, st);
-        default: return launch<TQ_F32>(r, a, sides, first, (unsigned)grid, st);
+        case TQ_BF16: return launch<TQ_BF16>(r, a, st);
+        case TQ_F16: return launch<TQ_F16>(r, a, st);
+        default: return launch<TQ_F32>(r, a, st);
     }
 }

@@ -12,6 +12,7 @@
 #include <stdint.h>
 
 #include "tq.h"
+#include "tq_ff.cuh"
 
 namespace tq {
 
@@ -43,9 +44,58 @@ __device__ __forceinline__ void rope_sincos(uint64_t frac, float &s, float &c) {
     c = ((q + 1u) & 2u) ? -ca : ca;
 }
 
-// The same in double precision.
+// 1 / (n (n + 1)), n = 1 .. 20.
+static __constant__ double kRopeInverse[20] = {
+    1. / 2,   1. / 6,   1. / 12,  1. / 20,  1. / 30,  1. / 42,  1. / 56,  1. / 72,  1. / 90,  1. / 110,
+    1. / 132, 1. / 156, 1. / 182, 1. / 210, 1. / 240, 1. / 272, 1. / 306, 1. / 342, 1. / 380, 1. / 420};
+
+// The same in double precision (series through x^21 and x^20, below 2^-70 of
+// their values at pi/4), in few instructions: for rare rows.
 __device__ __forceinline__ void rope_sincos_double(uint64_t frac, double &s, double &c) {
-    sincospi((double)(int64_t)frac * 1.0842021724855044e-19 /* 2^-63 */, &s, &c);
+    const uint32_t q = (uint32_t)((frac + (1ull << 61)) >> 62);
+    const double x = (double)(int64_t)(frac - ((uint64_t)q << 62)) * 3.4061215800300735e-19;   // 2 pi / 2^64
+    const double x2 = x * x;
+    // sin x / x = 1 - x2 / (2 3) (1 - x2 / (4 5) (...)), cos x = 1 - x2 / (1 2) (1 - x2 / (3 4) (...))
+    double ps = 1.0, pc = 1.0;
+#pragma unroll 1
+    for (int k = 9; k >= 0; --k) {
+        ps = fma(-x2 * kRopeInverse[2 * k + 1], ps, 1.0);
+        pc = fma(-x2 * kRopeInverse[2 * k], pc, 1.0);
+    }
+    ps *= x;
+    s = (q & 1u) ? pc : ps;
+    c = (q & 1u) ? ps : pc;
+    if (q & 2u) s = -s;
+    if ((q + 1u) & 2u) c = -c;
+}
+
+// The same in double-float arithmetic, to about 2^-34: the angle exact, the
+// series' terms through x^5 in double-float, the rest (below 2^-11) in float32.
+__device__ __forceinline__ void rope_sincos_ff(uint64_t frac, ff &s, ff &c) {
+    const uint32_t q = (uint32_t)((frac + (1ull << 61)) >> 62);
+    const int64_t r = (int64_t)(frac - ((uint64_t)q << 62));
+    const float f1 = __int2float_rn((int)(r >> 32));
+    const int64_t rest = r - ((int64_t)f1 << 32);          // below 2^40 in size
+    const float f2 = (float)(int)(rest >> 16) * 1.52587890625e-05f + (float)(int)(rest & 0xFFFF) * 2.3283064365386963e-10f;
+    // times 2 pi / 2^32, as two float32
+    const ff x = ff_mul(ff_quick(f1, f2), ff_of(1.46291807926715967e-09f, 1.46291807926715967e-09 - (double)1.46291807926715967e-09f));
+    const ff z = ff_mul(x, x);
+    // sin x = x (1 - z / 6 + z^2 / 120 - z^3 (1 / 7! - z / 9! + z^2 / 11!))
+    const float ts = z.h * z.h * z.h * fmaf(z.h, fmaf(z.h, 2.50521083854417188e-08f, -2.75573192239858907e-06f), 1.98412698412698413e-04f);
+    const ff z2 = ff_mul(z, z);
+    const ff k6 = {1.66666666666666667e-01f, (float)(1.66666666666666667e-01 - (double)1.66666666666666667e-01f)};
+    const ff k120 = {8.33333333333333333e-03f, (float)(8.33333333333333333e-03 - (double)8.33333333333333333e-03f)};
+    const ff k24 = {4.16666666666666667e-02f, (float)(4.16666666666666667e-02 - (double)4.16666666666666667e-02f)};
+    const ff one = {1.f, 0.f};
+    const ff ps = ff_mul(x, ff_add(ff_sub(one, ff_mul(z, k6)), ff_sub(ff_mul(z2, k120), ff_of(ts))));
+    // cos x = 1 - z / 2 + z^2 / 24 - z^3 (1 / 6! - z / 8! + z^2 / 10! - z^3 / 12!)
+    const float tc = z.h * z.h * z.h * fmaf(z.h, fmaf(z.h, fmaf(z.h, -2.08767569878680990e-09f, 2.75573192239858907e-07f),
+                                                      -2.48015873015873016e-05f), 1.38888888888888889e-03f);
+    const ff pc = ff_add(ff_sub(one, ff_scale(z, 0.5f)), ff_sub(ff_mul(z2, k24), ff_of(tc)));
+    s = (q & 1u) ? pc : ps;
+    c = (q & 1u) ? ps : pc;
+    if (q & 2u) s = ff_neg(s);
+    if ((q + 1u) & 2u) c = ff_neg(c);
 }
 
 // Argument check of a caller's rope (host).

@@ -123,8 +123,14 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+# the current stream's handle without building a Stream object (3 us a call on the host)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream):
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
@@ -404,29 +410,37 @@ TQ_ROPE_HALF, TQ_ROPE_ADJACENT = 0, 1
 
 
 class _On:
-    """Checks that the tensors of a call are CUDA tensors of one device and makes that device current."""
+    """Makes the device of a call's tensors current while it runs."""
 
-    def __init__(self, what, *tensors):
-        dev = None
-        for t in tensors:
-            if t is None:
-                continue
-            if not t.is_cuda:
-                raise ValueError("%s: CUDA tensors expected" % what)
-            if dev is None:
-                dev = t.device
-            elif t.device != dev:
-                raise ValueError("%s: tensors on different devices" % what)
-        self.dev, self.guard = dev, None
+    def __init__(self, dev):
+        self.guard = None if dev == torch.cuda.current_device() else torch.cuda.device(dev)
 
     def __enter__(self):
-        if self.dev is not None and self.dev.index != torch.cuda.current_device():
-            self.guard = torch.cuda.device(self.dev)
+        if self.guard is not None:
             self.guard.__enter__()
 
     def __exit__(self, *exc):
         if self.guard is not None:
             self.guard.__exit__(*exc)
+
+
+def _on(what, *tensors):
+    """The one CUDA device of the tensors (None skipped), made current."""
+    dev = -1
+    for t in tensors:
+        if t is not None:
+            d = t.get_device()
+            if d < 0:
+                raise ValueError("%s: CUDA tensors expected" % what)
+            if d != dev:
+                if dev >= 0:
+                    raise ValueError("%s: tensors on different devices" % what)
+                dev = d
+    return _On(dev)
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
 
 
 def _need(ok, what):
@@ -454,29 +468,34 @@ def tq_rope_set_freqs(rope, freqs):
 
 def _heads(x, what):
     """(tokens, heads, token stride, head stride) of rows [n, heads, 128]."""
-    _need(x.dim() == 3 and x.shape[2] == 128 and x.stride(2) == 1, "%s: [tokens, heads, 128] expected" % what)
-    return x.shape[0], x.shape[1], x.stride(0), x.stride(1)
+    shape, stride = x.shape, x.stride()
+    if len(shape) != 3 or shape[2] != 128 or stride[2] != 1:
+        raise ValueError("%s: [tokens, heads, 128] expected" % what)
+    return shape[0], shape[1], stride[0], stride[1]
 
 
-def _positions(pos, rope, n, what):
-    """(pointer, axis stride) of positions [n] or [axes, n]."""
-    _need(pos.dtype == torch.int64, "%s: int64 positions expected" % what)
-    _need((pos.dim() == 1 and rope.axes == 1 and pos.shape[0] == n) or
-          (pos.dim() == 2 and tuple(pos.shape) == (rope.axes, n)), "%s: positions [axes, tokens] expected" % what)
-    _need(n <= 1 or pos.stride(-1) == 1, "%s: positions of an axis must be contiguous" % what)
-    return _ptr(pos), pos.stride(0) if pos.dim() == 2 else 0
+def _axis_stride(pos, rope, n, what):
+    """Axis stride of positions [n] or [axes, n]."""
+    shape, stride = tuple(pos.shape), pos.stride()
+    axes = rope.axes
+    if pos.dtype != torch.int64 or not (shape == (axes, n) or (axes == 1 and shape == (n,))):
+        raise ValueError("%s: int64 positions [axes, tokens] expected" % what)
+    if n > 1 and stride[-1] != 1:
+        raise ValueError("%s: positions of an axis must be contiguous" % what)
+    return stride[0] if len(shape) == 2 else 0
 
 
 def tq_rope_apply(x, pos, rope, out, stream=None):
     """Rotate heads x [n, heads, 128] into out (same shape and dtype; out may
     be x).  pos int64 [axes, n] (or [n] for one axis)."""
     n, heads, xt, xh = _heads(x, "tq_rope_apply")
-    _, _, ot, oh = _heads(out, "tq_rope_apply")
-    _need(out.shape == x.shape and out.dtype == x.dtype, "tq_rope_apply: out must have the shape and dtype of x")
-    p, pa = _positions(pos, rope, n, "tq_rope_apply")
-    with _On("tq_rope_apply", x, pos, out):
-        _check(lib().tq_rope_apply(_ptr(x), _dtype(x), n, heads, xt, xh, p, pa, ctypes.byref(rope), _ptr(out), ot, oh,
-                                   _stream(stream)), "tq_rope_apply")
+    m, oheads, ot, oh = _heads(out, "tq_rope_apply")
+    if m != n or oheads != heads or out.dtype != x.dtype:
+        raise ValueError("tq_rope_apply: out must have the shape and dtype of x")
+    pa = _axis_stride(pos, rope, n, "tq_rope_apply")
+    with _on("tq_rope_apply", x, pos, out):
+        _check(lib().tq_rope_apply(x.data_ptr(), _dtype(x), n, heads, xt, xh, pos.data_ptr(), pa, rope, out.data_ptr(),
+                                   ot, oh, _stream(stream)), "tq_rope_apply")
     return out
 
 
@@ -486,64 +505,73 @@ def tq_insert_kv(k, v, pos, rope, kcb, vcb, signs, k_blocks, v_blocks, dst, dst_
     block): the block of head h of token n is number dst[n] + h *
     dst_head_stride; tokens of negative dst are skipped.  k with k_blocks, or v
     with v_blocks, may be None."""
+    what = "tq_insert_kv"
     x = k if k is not None else v
     _need(x is not None, "tq_insert_kv: no rows")
-    n, heads, _, _ = _heads(x, "tq_insert_kv")
-    _need(dst.dtype == torch.int64 and dst.dim() == 1 and dst.shape[0] == n and dst.is_contiguous(),
-          "tq_insert_kv: dst int64 [tokens] expected")
+    n, heads, _, _ = _heads(x, what)
+    if dst.dtype != torch.int64 or tuple(dst.shape) != (n,) or not dst.is_contiguous():
+        raise ValueError("tq_insert_kv: dst int64 [tokens] expected")
     strides, blocks = [], None
     for rows, cache, cb in ((k, k_blocks, kcb), (v, v_blocks, vcb)):
         _need((rows is None) == (cache is None), "tq_insert_kv: rows and their blocks come together")
         if rows is None:
-            strides.append((0, 0))
+            strides += [0, 0]
             continue
-        m, hh, st, sh = _heads(rows, "tq_insert_kv")
-        _need((m, hh) == (n, heads) and rows.dtype == x.dtype, "tq_insert_kv: k and v of one shape and dtype expected")
-        size = tq_block_bytes(cb.bits)
-        _need(cache.dtype == torch.uint8 and cache.is_contiguous() and cache.dim() >= 1 and cache.shape[-1] == size,
-              "tq_insert_kv: contiguous uint8 blocks of %d bytes expected" % size)
-        _need(blocks is None or cache.numel() // size == blocks, "tq_insert_kv: caches of different sizes")
-        blocks = cache.numel() // size
-        strides.append((st, sh))
-    p, pa = (None, 0) if rope is None or k is None else _positions(pos, rope, n, "tq_insert_kv")
-    with _On("tq_insert_kv", k, v, pos if p is not None else None, k_blocks, v_blocks, dst):
-        _check(lib().tq_insert_kv(_ptr(k), strides[0][0], strides[0][1], _ptr(v), strides[1][0], strides[1][1],
-                                  _dtype(x), n, heads, p, pa, None if p is None else ctypes.byref(rope),
-                                  None if kcb is None else ctypes.byref(kcb), None if vcb is None else ctypes.byref(vcb),
-                                  signs, _ptr(k_blocks), _ptr(v_blocks), blocks, _ptr(dst), dst_head_stride,
-                                  _stream(stream)), "tq_insert_kv")
+        m, hh, st, sh = _heads(rows, what)
+        if m != n or hh != heads or rows.dtype != x.dtype:
+            raise ValueError("tq_insert_kv: k and v of one shape and dtype expected")
+        size, shape = 2 + 16 * cb.bits, cache.shape
+        if cache.dtype != torch.uint8 or not cache.is_contiguous() or len(shape) == 0 or shape[-1] != size:
+            raise ValueError("tq_insert_kv: contiguous uint8 blocks of %d bytes expected" % size)
+        count = cache.numel() // size
+        if blocks is not None and count != blocks:
+            raise ValueError("tq_insert_kv: caches of different sizes")
+        blocks = count
+        strides += [st, sh]
+    turn = rope is not None and k is not None
+    pa = _axis_stride(pos, rope, n, what) if turn else 0
+    with _on(what, k, v, pos if turn else None, k_blocks, v_blocks, dst):
+        _check(lib().tq_insert_kv(_at(k), strides[0], strides[1], _at(v), strides[2], strides[3], _dtype(x), n, heads,
+                                  pos.data_ptr() if turn else None, pa, rope if turn else None, kcb, vcb, signs,
+                                  _at(k_blocks), _at(v_blocks), blocks, dst.data_ptr(), dst_head_stride,
+                                  _stream(stream)), what)
 
 
 def tq_attn_weights_workspace_bytes(B, Hq, Hkv, T):
     return int(lib().tq_attn_weights_workspace_bytes(B, Hq, Hkv, T))
 
 
-def _table(block_table, B, what):
+def _pages(block_table, B, what):
+    """Entries of a sequence in a block table int32 [B, max_pages] (0 without one)."""
     if block_table is None:
-        return None, 0
-    _need(block_table.dtype == torch.int32 and block_table.dim() == 2 and block_table.shape[0] == B and
-          block_table.is_contiguous(), "%s: block_table int32 [B, max_pages] expected" % what)
-    return _ptr(block_table), block_table.shape[1]
+        return 0
+    shape = block_table.shape
+    if block_table.dtype != torch.int32 or len(shape) != 2 or shape[0] != B or not block_table.is_contiguous():
+        raise ValueError("%s: block_table int32 [B, max_pages] expected" % what)
+    return shape[1]
 
 
-def _weights(w, B, Hkv, T, what):
+def _row_of(w, B, Hkv, T, what):
     """Row stride of accumulators [B, Hkv, >= T]."""
-    _need(w.dtype == torch.float32 and w.dim() == 3 and w.shape[0] == B and w.shape[1] == Hkv and w.shape[2] >= T and
-          w.stride(2) == 1 and (B == 1 or Hkv == 1 or w.stride(0) == Hkv * w.stride(1)),
-          "%s: weights float32 [B, Hkv, >= T] expected" % what)
-    return w.stride(1) if Hkv > 1 or B == 1 else w.stride(0)
+    shape, stride = w.shape, w.stride()
+    if (w.dtype != torch.float32 or len(shape) != 3 or shape[0] != B or shape[1] != Hkv or shape[2] < T or
+            stride[2] != 1 or (B > 1 and Hkv > 1 and stride[0] != Hkv * stride[1])):
+        raise ValueError("%s: weights float32 [B, Hkv, >= T] expected" % what)
+    return stride[1] if Hkv > 1 or B == 1 else stride[0]
 
 
 def _lens(t, B, what):
-    _need(t is None or (t.dtype == torch.int32 and t.dim() == 1 and t.shape[0] == B and t.is_contiguous()),
-          "%s: lengths int32 [B] expected" % what)
+    if t.dtype != torch.int32 or tuple(t.shape) != (B,) or not t.is_contiguous():
+        raise ValueError("%s: lengths int32 [B] expected" % what)
 
 
-def _cache(t, cb, B, paged, what):
-    """(Hkv, tokens of a sequence or page) of caches [B or pages, Hkv, tokens, bytes]."""
-    _need(t.dtype == torch.uint8 and t.dim() == 4 and t.is_contiguous() and (paged or t.shape[0] == B) and
-          (cb is None or t.shape[3] == tq_block_bytes(cb.bits)), "%s: contiguous packed blocks expected" % what)
-    return t.shape[1], t.shape[2]
+def _cache(t, size, first, what):
+    """Shape of caches [B or pages, Hkv, tokens, bytes]; size and first checked unless None."""
+    shape = t.shape
+    if (t.dtype != torch.uint8 or len(shape) != 4 or not t.is_contiguous() or
+            (first is not None and shape[0] != first) or (size is not None and shape[3] != size)):
+        raise ValueError("%s: contiguous packed blocks expected" % what)
+    return shape
 
 
 def tq_attn_decode_weights(q, k_blocks, kcb, v_blocks, vcb, weights, out, workspace, T, scale, signs, seq_lens=None,
@@ -553,36 +581,52 @@ def tq_attn_decode_weights(q, k_blocks, kcb, v_blocks, vcb, weights, out, worksp
     bytes], or with a block_table int32 [B, max_pages] pools [pages, Hkv,
     page, bytes]; out [B, Hq, 128] float32, bfloat16 or float16."""
     what = "tq_attn_decode_weights"
-    _need(q.dim() == 3 and q.shape[2] == 128 and q.is_contiguous(), "%s: contiguous q [B, Hq, 128] expected" % what)
-    B, Hq, _ = q.shape
-    Hkv, unit = _cache(k_blocks, kcb, B, block_table is not None, what)
-    _need(_cache(v_blocks, vcb, B, block_table is not None, what) == (Hkv, unit), "%s: caches of one shape expected" % what)
-    _need(out.shape == q.shape and out.is_contiguous(), "%s: contiguous out of q's shape expected" % what)
-    _lens(seq_lens, B, what)
-    stride = _weights(weights, B, Hkv, T, what)
-    table, pages = _table(block_table, B, what)
-    with _On(what, q, k_blocks, v_blocks, weights, out, workspace, seq_lens, block_table):
-        _check(lib().tq_attn_decode_weights(_ptr(q), _dtype(q), _ptr(k_blocks), ctypes.byref(kcb), _ptr(v_blocks),
-                                            ctypes.byref(vcb), table, pages, unit, _ptr(seq_lens), B, Hq, Hkv, unit, T,
-                                            scale, signs, _ptr(weights), stride, decay, _ptr(out), _dtype(out),
-                                            _ptr(workspace), workspace.numel() * workspace.element_size(),
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != 128 or not q.is_contiguous():
+        raise ValueError("%s: contiguous q [B, Hq, 128] expected" % what)
+    B, Hq = shape[0], shape[1]
+    first = B if block_table is None else None
+    ks = _cache(k_blocks, 2 + 16 * kcb.bits, first, what)
+    vs = _cache(v_blocks, 2 + 16 * vcb.bits, first, what)
+    Hkv, unit = ks[1], ks[2]
+    if ks[:3] != vs[:3]:
+        raise ValueError("%s: caches of one shape expected" % what)
+    if out.shape != shape or not out.is_contiguous():
+        raise ValueError("%s: contiguous out of q's shape expected" % what)
+    if seq_lens is not None:
+        _lens(seq_lens, B, what)
+    stride = _row_of(weights, B, Hkv, T, what)
+    pages = _pages(block_table, B, what)
+    with _on(what, q, k_blocks, v_blocks, weights, out, workspace, seq_lens, block_table):
+        _check(lib().tq_attn_decode_weights(q.data_ptr(), _dtype(q), k_blocks.data_ptr(), kcb, v_blocks.data_ptr(), vcb,
+                                            _at(block_table), pages, unit, _at(seq_lens), B, Hq, Hkv, unit, T, scale,
+                                            signs, weights.data_ptr(), stride, decay, out.data_ptr(), _dtype(out),
+                                            workspace.data_ptr(), workspace.numel() * workspace.element_size(),
                                             _stream(stream)), what)
     return out
+
+
+def _kept(kept, new_lens, what):
+    shape = kept.shape
+    if kept.dtype != torch.int32 or len(shape) != 3 or not kept.is_contiguous():
+        raise ValueError("%s: kept int32 [B, Hkv, keep] expected" % what)
+    if new_lens is None:
+        raise ValueError("%s: new_lens expected" % what)
+    _lens(new_lens, shape[0], what)
+    return shape
 
 
 def tq_evict_select(weights, kept, new_lens, T, first, last, seq_lens=None, stream=None):
     """The tokens that stay: kept int32 [B, Hkv, keep] (ascending, -1 past the
     last), new_lens int32 [B]."""
     what = "tq_evict_select"
-    _need(kept.dtype == torch.int32 and kept.dim() == 3 and kept.is_contiguous(), "%s: kept int32 [B, Hkv, keep] expected" % what)
-    B, Hkv, keep = kept.shape
-    _need(new_lens is not None, "%s: new_lens expected" % what)
-    _lens(new_lens, B, what)
-    _lens(seq_lens, B, what)
-    stride = _weights(weights, B, Hkv, T, what)
-    with _On(what, weights, kept, new_lens, seq_lens):
-        _check(lib().tq_evict_select(_ptr(weights), stride, _ptr(seq_lens), B, Hkv, T, keep, first, last, _ptr(kept),
-                                     _ptr(new_lens), _stream(stream)), what)
+    B, Hkv, keep = _kept(kept, new_lens, what)
+    if seq_lens is not None:
+        _lens(seq_lens, B, what)
+    stride = _row_of(weights, B, Hkv, T, what)
+    with _on(what, weights, kept, new_lens, seq_lens):
+        _check(lib().tq_evict_select(weights.data_ptr(), stride, _at(seq_lens), B, Hkv, T, keep, first, last,
+                                     kept.data_ptr(), new_lens.data_ptr(), _stream(stream)), what)
     return kept
 
 
@@ -590,17 +634,21 @@ def tq_evict_compact(k_blocks, v_blocks, kept, new_lens, T, weights=None, block_
     """Move the kept tokens together in place: caches (and pools) as for
     tq_attn_decode_weights, of any block format; v_blocks may be None."""
     what = "tq_evict_compact"
-    _need(kept.dtype == torch.int32 and kept.dim() == 3 and kept.is_contiguous(), "%s: kept int32 [B, Hkv, keep] expected" % what)
-    B, Hkv, keep = kept.shape
-    _need(new_lens is not None, "%s: new_lens expected" % what)
-    _lens(new_lens, B, what)
-    table, pages = _table(block_table, B, what)
-    h, unit = _cache(k_blocks, None, B, table is not None, what)
-    _need(h == Hkv and (v_blocks is None or (_cache(v_blocks, None, B, table is not None, what) == (h, unit) and
-                                             v_blocks.shape[0] == k_blocks.shape[0])), "%s: caches of one shape expected" % what)
-    stride = 0 if weights is None else _weights(weights, B, Hkv, T, what)
-    with _On(what, k_blocks, v_blocks, kept, new_lens, weights, block_table):
-        _check(lib().tq_evict_compact(_ptr(k_blocks), k_blocks.shape[3], _ptr(v_blocks),
-                                      0 if v_blocks is None else v_blocks.shape[3], _ptr(weights), stride, _ptr(kept),
-                                      keep, _ptr(new_lens), table, pages, unit, k_blocks.shape[0], B, Hkv, unit, T,
-                                      _stream(stream)), what)
+    B, Hkv, keep = _kept(kept, new_lens, what)
+    pages = _pages(block_table, B, what)
+    first = B if block_table is None else None
+    ks = _cache(k_blocks, None, first, what)
+    vbytes = 0
+    if v_blocks is not None:
+        vs = _cache(v_blocks, None, first, what)
+        if vs[:3] != ks[:3]:
+            raise ValueError("%s: caches of one shape expected" % what)
+        vbytes = vs[3]
+    if ks[1] != Hkv:
+        raise ValueError("%s: caches of kept's heads expected" % what)
+    unit = ks[2]
+    stride = 0 if weights is None else _row_of(weights, B, Hkv, T, what)
+    with _on(what, k_blocks, v_blocks, kept, new_lens, weights, block_table):
+        _check(lib().tq_evict_compact(k_blocks.data_ptr(), ks[3], _at(v_blocks), vbytes, _at(weights), stride,
+                                      kept.data_ptr(), keep, new_lens.data_ptr(), _at(block_table), pages, unit, ks[0],
+                                      B, Hkv, unit, T, _stream(stream)), what)
