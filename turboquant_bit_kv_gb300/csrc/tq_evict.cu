@@ -26,13 +26,18 @@ constexpr int kMaxCluster = 8;             // portable cluster size
 
 // ---- selection
 //
-// Of the tokens that are not kept anyway (the first, the last), the m
-// largest weights: three rounds of an 11-, 11- and 10-bit radix select on
-// order-preserving keys find the m-th largest key K exactly, every CTA of the
-// row adding up all the row's histograms by itself; then everything above K
-// stays and, of the tokens equal to K, the ones of lowest index.  Weights are
-// read from memory once (chunks beyond kSelCached keys are read again from
-// L2) and the indices written once: 4 bytes in a token, 4 out a kept one.
+// Of the tokens that are not kept anyway (the first, the last), the m largest
+// weights.  On order-preserving keys, a histogram of the top 11 bits finds the
+// bin that the m-th largest key lies in (every CTA of the row adds up all the
+// row's histograms by itself); a second pass over the keys counts what lies in
+// higher bins and lists the keys of that bin, and two more rounds of 11 and 10
+// bits over the list find the m-th largest key K itself.  Everything above K
+// stays and, of the tokens equal to K, the ones of lowest index: each warp has a
+// contiguous piece of the row's tokens and knows how many stay before it, so a
+// last pass writes the indices in order.  Weights are read from memory once
+// (chunks beyond kSelCached keys are read again from L2) and the indices
+// written once: 4 bytes in a token, 4 out a kept one.  Issue bounds it: about
+// 50 instructions per 32 keys.
 
 // Key of a weight: ascending with it as unsigned integers, -0 equal to +0,
 // every NaN above +inf.
@@ -50,19 +55,62 @@ struct SelArgs {
     int Hkv, T, keep, first, last, cached;   // cached: shared-memory keys of a CTA (0: none)
 };
 
+constexpr int kSelList = 4096;     // keys of the threshold's bin that a CTA can list
+
 struct SelShared {
     uint32_t hist[3][kBins];
+    uint32_t key[kSelList];        // listed keys, and the warps whose pieces they are of
+    uint8_t of[kSelList];
     uint32_t part[kSelWarps];
-    uint32_t found[3];             // digit of the m-th largest key, keys above it, total
-    uint32_t above[kSelWarps], equal[kSelWarps];
-    uint32_t sums[2];              // this CTA's kept-anyway or larger, and equal tokens
+    uint32_t found[2];             // digit of the m-th largest key, keys above it
+    uint32_t above[kSelWarps], equal[kSelWarps];   // per warp's piece
+    uint32_t sums[2];              // this CTA's larger and equal tokens
+    uint32_t listed;
 };
 
 __device__ __forceinline__ uint32_t warp_sum(uint32_t v) { return __reduce_add_sync(0xffffffffu, v); }
 
+// The digit (of WIDTH bits) that the m-th largest key has, from the row's
+// histograms hist of all its CTAs, and how many keys have larger ones.
+template <int WIDTH>
+__device__ __forceinline__ void find_digit(cg::cluster_group &cl, SelShared &s, uint32_t *hist, uint32_t &m,
+                                           uint32_t &prefix) {
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, C = (int)cl.num_blocks();
+    constexpr int kNum = 1 << WIDTH, kPer = kNum / kSelThreads;
+    // thread t holds the bins of digits kNum - 1 - kPer t downwards
+    uint32_t cnt[kPer], sum = 0;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) {
+        cnt[e] = 0;
+        for (int p = 0; p < C; ++p) cnt[e] += cl.map_shared_rank(hist, p)[kNum - 1 - (tid * kPer + e)];
+        sum += cnt[e];
+    }
+    uint32_t inc = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t v = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += v;
+    }
+    if (lane == 31) s.part[warp] = inc;
+    __syncthreads();
+    uint32_t before = inc - sum + warp_sum(lane < warp ? s.part[lane] : 0u);
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) {
+        if (before < m && before + cnt[e] >= m) {   // exactly one bin
+            s.found[0] = (uint32_t)(kNum - 1 - (tid * kPer + e));
+            s.found[1] = before;
+        }
+        before += cnt[e];
+    }
+    __syncthreads();
+    prefix = (prefix << WIDTH) | s.found[0];
+    m -= s.found[1];
+}
+
 __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_constant__ SelArgs a) {
     extern __shared__ __align__(16) uint32_t keys[];
     __shared__ SelShared s;
+    static_assert(kSelWarps == 32 && kSelThreads == 1024, "a lane per warp, a thread per bin of 10 bits");
     cg::cluster_group cl = cg::this_cluster();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int C = (int)cl.num_blocks(), rank = (int)cl.block_rank();
@@ -79,114 +127,97 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
         for (int i = rank * kSelThreads + tid; i < a.keep; i += C * kSelThreads) kept[i] = i < L ? i : -1;
         return;
     }
-    const float *w = a.weights + row * a.row_stride;
-    const int chunk = (L + C - 1) / C;
-    const int lo = min(rank * chunk, L), n = min(L - lo, chunk);   // this CTA's tokens lo .. lo + n - 1
-    const int first = a.first, last0 = L - a.last;                 // tokens first .. last0 - 1 are ranked
+    // kept anyway: the first and the last tokens
+    for (int i = rank * kSelThreads + tid; i < a.first; i += C * kSelThreads) kept[i] = i;
+    for (int i = rank * kSelThreads + tid; i < a.last; i += C * kSelThreads) kept[a.keep - a.last + i] = L - a.last + i;
+    uint32_t m = (uint32_t)(a.keep - a.first - a.last);   // to find among the others
+    if (m == 0) return;
+    kept += a.first;
+    // the others: tokens a.first + 0 .. R - 1, this CTA's lo .. lo + n - 1 of them, this warp's p0 .. p1 - 1
+    // of those (a multiple of 32 each)
+    const int R = L - a.first - a.last;
+    const int chunk = (R + C - 1) / C, lo = min(rank * chunk, R), n = min(R - lo, chunk);
+    const float *w = a.weights + row * a.row_stride + a.first + lo;
     const bool cached = n <= a.cached;
-    auto key = [&](int i) { return cached ? keys[i] : weight_key(__ldg(w + lo + i)); };
-    auto ranked = [&](int i) { return lo + i >= first && lo + i < last0; };
-
-    for (int i = tid; i < 3 * kBins; i += kSelThreads) (&s.hist[0][0])[i] = 0;
-    __syncthreads();
-    // keys below a prefix mask: round r counts the digits of the keys whose higher digits match
-    uint32_t prefix = 0, m = (uint32_t)(a.keep - a.first - a.last);   // the m-th largest is sought, m >= 1
-    const bool none = m == 0;
-    constexpr int shift[3] = {21, 10, 0};
-    constexpr int width[3] = {11, 11, 10};
-    if (!none) {
-#pragma unroll
-        for (int r = 0; r < 3; ++r) {
-            const int steps = (n + kSelThreads - 1) / kSelThreads;
-#pragma unroll 4
-            for (int q = 0; q < steps; ++q) {
-                const int i = q * kSelThreads + tid;
-                bool in = i < n;
-                uint32_t k = 0;
-                if (in) {
-                    if (r == 0) {
-                        k = weight_key(__ldcs(w + lo + i));
-                        if (cached) keys[i] = k;
-                    } else {
-                        k = key(i);
-                    }
-                    in = ranked(i) && (r == 0 || (k >> (shift[r] + width[r])) == prefix);
-                }
-                const uint32_t d = (k >> shift[r]) & ((1u << width[r]) - 1u);
-                if (r > 0) {   // few keys share the higher digits
-                    if (in) atomicAdd(&s.hist[r][d], 1u);
-                    continue;
-                }
-                // one add for the lanes that share the first such lane's digit (ties and zeros are common)
-                const uint32_t live = __ballot_sync(0xffffffffu, in);
-                if (live) {
-                    const uint32_t lead = __shfl_sync(0xffffffffu, d, __ffs(live) - 1);
-                    const uint32_t same = __ballot_sync(0xffffffffu, in && d == lead);
-                    if (lane == __ffs(live) - 1) atomicAdd(&s.hist[r][d], (uint32_t)__popc(same));
-                    else if (in && d != lead) atomicAdd(&s.hist[r][d], 1u);
-                }
-            }
-            cl.sync();
-            // the row's histogram, from the top: thread t holds the bins of digits top - 2 t and top - 2 t - 1
-            constexpr int kPer = kBins / kSelThreads;
-            const int bins = 1 << width[r];
-            uint32_t cnt[kPer] = {}, sum = 0;
-#pragma unroll
-            for (int e = 0; e < kPer; ++e) {
-                const int at = bins - 1 - (tid * kPer + e);
-                if (at >= 0) {
-                    for (int p = 0; p < C; ++p) cnt[e] += cl.map_shared_rank(&s.hist[r][0], p)[at];
-                }
-                sum += cnt[e];
-            }
-            uint32_t inc = sum;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const uint32_t v = __shfl_up_sync(0xffffffffu, inc, o);
-                if (lane >= o) inc += v;
-            }
-            if (lane == 31) s.part[warp] = inc;
-            __syncthreads();
-            uint32_t before = inc - sum + warp_sum(lane < warp ? s.part[lane] : 0u);
-            if (before < m && before + sum >= m) {   // exactly one thread
-                uint32_t acc = before;
-#pragma unroll
-                for (int e = 0; e < kPer; ++e) {
-                    if (acc < m && acc + cnt[e] >= m) {
-                        s.found[0] = (uint32_t)(bins - 1 - (tid * kPer + e));
-                        s.found[1] = acc;
-                    }
-                    acc += cnt[e];
-                }
-            }
-            __syncthreads();
-            prefix = (prefix << width[r]) | s.found[0];
-            m -= s.found[1];
-            __syncthreads();
-        }
-    }
-    // prefix: the threshold key; m: how many of the tokens equal to it stay (those of lowest index)
-    // class of token i: kept anyway or larger (1), equal to the threshold (2), evicted (0)
-    auto cls = [&](int i) -> int {
-        if (!ranked(i)) return 1;
-        if (none) return 0;
-        const uint32_t k = key(i);
-        return k > prefix ? 1 : (k == prefix ? 2 : 0);
-    };
-    // each warp takes a contiguous piece of the chunk, a multiple of 32 tokens
     const int piece = ((n + kSelWarps - 1) / kSelWarps + 31) & ~31;
     const int p0 = min(warp * piece, n), p1 = min(p0 + piece, n);
-    uint32_t above = 0, equal = 0;
-    for (int i = p0 + lane; i < p1; i += 32) {
-        const int c = cls(i);
-        above += c == 1;
-        equal += c == 2;
+
+    for (int i = tid; i < 3 * kBins; i += kSelThreads) (&s.hist[0][0])[i] = 0;
+    if (tid == 0) s.listed = 0;
+    __syncthreads();
+    // pass 1: keys, and the histogram of their top 11 bits
+#pragma unroll 4
+    for (int i0 = p0; i0 < p1; i0 += 32) {
+        const int i = i0 + lane;
+        const bool in = i < p1;
+        const uint32_t k = in ? weight_key(__ldcs(w + i)) : 0;
+        if (in && cached) keys[i] = k;
+        // one add for the lanes that share the first lane's digit (ties and zeros are common)
+        const uint32_t d = k >> 21, lead = __shfl_sync(0xffffffffu, d, 0);
+        const uint32_t same = __ballot_sync(0xffffffffu, in && d == lead);
+        if (lane == 0) atomicAdd(&s.hist[0][d], (uint32_t)__popc(same));
+        else if (in && d != lead) atomicAdd(&s.hist[0][d], 1u);
+    }
+    cl.sync();
+    uint32_t prefix = 0;
+    find_digit<11>(cl, s, s.hist[0], m, prefix);
+    // pass 2: keys of higher bins counted, those of the bin listed and their next digit counted
+    const uint32_t top = prefix;
+    uint32_t above = 0;
+#pragma unroll 4
+    for (int i0 = p0; i0 < p1; i0 += 32) {
+        const int i = i0 + lane;
+        const uint32_t k = i < p1 ? (cached ? keys[i] : weight_key(__ldg(w + i))) : 0;
+        above += (k >> 21) > top;
+        if (i < p1 && (k >> 21) == top) {
+            const uint32_t at = atomicAdd(&s.listed, 1u);
+            if (at < kSelList) {
+                s.key[at] = k;
+                s.of[at] = (uint8_t)warp;
+            }
+            atomicAdd(&s.hist[1][(k >> 10) & 2047u], 1u);
+        }
     }
     above = warp_sum(above);
-    equal = warp_sum(equal);
     if (lane == 0) {
         s.above[warp] = above;
-        s.equal[warp] = equal;
+        s.equal[warp] = 0;
+    }
+    cl.sync();
+    find_digit<11>(cl, s, s.hist[1], m, prefix);
+    // the last digit, over the list, or over the keys again where they did not fit
+    const uint32_t listed = s.listed;
+    const bool fits = listed <= kSelList;
+    auto key = [&](int i) { return cached ? keys[i] : weight_key(__ldg(w + i)); };
+    if (fits) {
+        for (uint32_t i = tid; i < listed; i += kSelThreads)
+            if ((s.key[i] >> 10) == prefix) atomicAdd(&s.hist[2][s.key[i] & 1023u], 1u);
+    } else {
+        for (int i = p0 + lane; i < p1; i += 32)
+            if ((key(i) >> 10) == prefix) atomicAdd(&s.hist[2][key(i) & 1023u], 1u);
+    }
+    cl.sync();
+    find_digit<10>(cl, s, s.hist[2], m, prefix);
+    // prefix: the threshold key; m: how many of the tokens equal to it stay.  The bin's keys by piece:
+    if (fits) {
+        for (uint32_t i = tid; i < listed; i += kSelThreads) {
+            const uint32_t k = s.key[i];
+            if (k > prefix) atomicAdd(&s.above[s.of[i]], 1u);
+            else if (k == prefix) atomicAdd(&s.equal[s.of[i]], 1u);
+        }
+    } else {
+        uint32_t more = 0, equal = 0;
+        for (int i = p0 + lane; i < p1; i += 32) {
+            const uint32_t k = key(i);
+            more += k > prefix && (k >> 21) == top;
+            equal += k == prefix;
+        }
+        more = warp_sum(more);
+        equal = warp_sum(equal);
+        if (lane == 0) {
+            s.above[warp] += more;
+            s.equal[warp] = equal;
+        }
     }
     __syncthreads();
     if (warp < 2) {
@@ -194,24 +225,31 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
         if (lane == 0) s.sums[warp] = t;
     }
     cl.sync();
-    uint32_t na = 0, ne = 0;   // tokens of either class before this warp's piece
+    uint32_t na = 0, ne = 0;   // larger and equal tokens before this warp's piece
     for (int p = 0; p < rank; ++p) {
         const uint32_t *o = cl.map_shared_rank(&s.sums[0], p);
         na += o[0];
         ne += o[1];
     }
-    static_assert(kSelWarps == 32, "a lane per warp");
     na += warp_sum(lane < warp ? s.above[lane] : 0u);
     ne += warp_sum(lane < warp ? s.equal[lane] : 0u);
+    const uint32_t under = (1u << lane) - 1u;
+    const int token0 = a.first + lo;
+#pragma unroll 4
     for (int i0 = p0; i0 < p1; i0 += 32) {
         const int i = i0 + lane;
-        const int c = i < p1 ? cls(i) : 0;
-        const uint32_t ma = __ballot_sync(0xffffffffu, c == 1), me = __ballot_sync(0xffffffffu, c == 2);
-        const uint32_t under = (1u << lane) - 1u;
-        const uint32_t ra = na + __popc(ma & under), re = ne + __popc(me & under);
-        if (c == 1 || (c == 2 && re < m)) kept[ra + min(re, m)] = lo + i;
+        const uint32_t k = i < p1 ? key(i) : 0;
+        const bool eq = k == prefix && i < p1;
+        const uint32_t ma = __ballot_sync(0xffffffffu, k > prefix), me = __ballot_sync(0xffffffffu, eq);
+        const uint32_t ra = na + __popc(ma & under);
+        if (me == 0) {
+            if (k > prefix) kept[ra + min(ne, m)] = token0 + i;
+        } else {
+            const uint32_t re = ne + __popc(me & under);
+            if (k > prefix || (eq && re < m)) kept[ra + min(re, m)] = token0 + i;
+            ne += __popc(me);
+        }
         na += __popc(ma);
-        ne += __popc(me);
     }
     cl.sync();   // no CTA leaves while others still read its sums
 }
@@ -230,9 +268,9 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
 // pages multiples of 8 tokens, so that eight blocks are a multiple of 16
 // bytes; aligned bases): a block is read as the aligned 16-byte pieces that
 // it lies in, with the bytes around it, and written as part of a group of
-// eight blocks that starts and ends on a 16-byte boundary, its pieces put
-// together from half words in shared memory.  Otherwise half words are
-// read and written one by one.
+// eight blocks that starts and ends on a 16-byte boundary, its 16-byte pieces
+// put together from the aligned words around them in shared memory.  Otherwise
+// (and for blocks below 16 bytes) half words are read and written one by one.
 constexpr int kMovThreads = 256;
 constexpr int kMovSmem = 56 * 1024;        // four CTAs per SM: enough reads in flight
 constexpr int kMovMaxBytes = 512;          // of a block
@@ -251,6 +289,18 @@ struct MovArgs {
 
 __device__ __forceinline__ int div_by(uint32_t p, uint32_t inv) { return inv ? (int)__umulhi(p, inv) : (int)p; }
 
+// 16 bytes at a 2-byte aligned shared-memory address.
+__device__ __forceinline__ void lds16_a2(const uint8_t *p, uint32_t (&v)[4]) {
+    const uint32_t at = (uint32_t)__cvta_generic_to_shared(p);
+    const uint32_t *w = reinterpret_cast<const uint32_t *>(p - (at & 2u));
+    const uint32_t sh = (at & 2u) * 8u;
+    uint32_t x[5];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) x[i] = w[i];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = __funnelshift_r(x[i], x[i + 1], sh);
+}
+
 template <bool WIDE>
 __global__ void __launch_bounds__(kMovThreads, 4) compact_kernel(const __grid_constant__ MovArgs a) {
     extern __shared__ __align__(16) uint8_t mov_smem[];
@@ -258,6 +308,7 @@ __global__ void __launch_bounds__(kMovThreads, 4) compact_kernel(const __grid_co
     int64_t *dst = src + a.tile;                               // [tile] own slot, -1: not in the pool
     uint8_t *stage0 = reinterpret_cast<uint8_t *>(dst + a.tile);
     float *sw = reinterpret_cast<float *>(stage0 + (size_t)a.tile * (a.pitch[0] + a.pitch[1]));
+    uint16_t *place = reinterpret_cast<uint16_t *>(sw + a.tile);   // [2][tile] where a token's block starts in the stage
     cg::cluster_group cl = cg::this_cluster();
     const int tid = threadIdx.x, C = (int)cl.num_blocks(), rank = (int)cl.block_rank();
     const int64_t row = blockIdx.x / C;
@@ -294,6 +345,10 @@ __global__ void __launch_bounds__(kMovThreads, 4) compact_kernel(const __grid_co
                 }
                 src[i] = s;
                 dst[i] = own;
+#pragma unroll
+                for (int side = 0; side < 2; ++side)
+                    place[side * a.tile + i] =
+                        (uint16_t)(i * a.pitch[side] + (WIDE ? (int)((uint32_t)s * (uint32_t)a.bytes[side] & 15u) : 0));
                 if (w) sw[i] = w[own < 0 ? j : from];
             }
             __syncthreads();
@@ -314,13 +369,11 @@ __global__ void __launch_bounds__(kMovThreads, 4) compact_kernel(const __grid_co
                             at[u] = -1;
                             if (p < total) {
                                 const int i = div_by(p, a.inv_piece[side]), q = p - i * np;
-                                const int64_t s = src[i];
-                                if (s >= 0) {
-                                    const int64_t first = s * bytes, piece = (first >> 4) + q;
-                                    if (piece * 16 < first + bytes) {
-                                        at[u] = i * a.pitch[side] + q * 16;
-                                        v[u] = *reinterpret_cast<const uint4 *>(cache + piece * 16);
-                                    }
+                                const int64_t s = src[i], first = s * bytes;
+                                const int skew = (int)(first & 15);
+                                if (s >= 0 && q * 16 < skew + bytes) {
+                                    at[u] = i * a.pitch[side] + q * 16;
+                                    v[u] = *reinterpret_cast<const uint4 *>(cache + (first - skew) + q * 16);
                                 }
                             }
                         }
@@ -346,43 +399,36 @@ __global__ void __launch_bounds__(kMovThreads, 4) compact_kernel(const __grid_co
             const uint8_t *stage = stage0;
 #pragma unroll
             for (int side = 0; side < 2; ++side) {
-                const int bytes = a.bytes[side], hw = bytes / 2, pitch = a.pitch[side];
+                const int bytes = a.bytes[side], hw = bytes / 2;
                 if (bytes == 0) continue;
                 uint8_t *cache = a.blocks[side];
+                const uint16_t *at = place + side * a.tile;
                 const int words = WIDE ? cnt * bytes / 16 : 0;   // whole 16-byte pieces of the tile
                 for (int x = tid; x < words; x += kMovThreads) {
-                    // piece x holds half words 8 x .. 8 x + 7 of the tile, of at most two blocks that matter
-                    const int i = div_by(8 * x, a.inv_half[side]), k = 8 * x - i * hw;
-                    const int o = (i & ~7);
+                    // piece x: half words 8 x .. 8 x + 7 of the tile, of block i from its k-th on, the last
+                    // 8 - r of them perhaps of the next block (blocks have 8 at least)
+                    const int i = div_by(8 * x, a.inv_half[side]), k = 8 * x - i * hw, r = hw - k, o = i & ~7;
                     uint32_t v[4];
+                    lds16_a2(stage + at[i] + 2 * k, v);
+                    if (r < 8) {
+                        uint32_t u[4];
+                        lds16_a2(stage + at[i + 1] - 2 * r, u);
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        uint32_t e[2];
-#pragma unroll
-                        for (int z = 0; z < 2; ++z) {
-                            int ii = i, kk = k + 2 * q + z;
-                            while (kk >= hw) {
-                                kk -= hw;
-                                ++ii;
-                            }
-                            const uint32_t skew = (uint32_t)(src[ii] * bytes) & 15u;
-                            e[z] = *reinterpret_cast<const uint16_t *>(stage + ii * pitch + skew + 2 * kk);
-                        }
-                        v[q] = e[0] | (e[1] << 16);
+                        for (int q = 0; q < 4; ++q)
+                            v[q] = 2 * q >= r ? u[q] : (2 * q + 1 >= r ? (v[q] & 0xFFFFu) | (u[q] & 0xFFFF0000u) : v[q]);
                     }
                     if (dst[o] >= 0)
-                        *reinterpret_cast<uint4 *>(cache + dst[o] * bytes + (int64_t)(8 * x - o * hw) * 2) =
+                        *reinterpret_cast<uint4 *>(cache + dst[o] * bytes + (8 * x - o * hw) * 2) =
                             make_uint4(v[0], v[1], v[2], v[3]);
                 }
                 const int total = cnt * hw;
                 for (int p = words * 8 + tid; p < total; p += kMovThreads) {
                     const int i = div_by(p, a.inv_half[side]), k = p - i * hw;
-                    const uint32_t skew = WIDE ? (uint32_t)(src[i] * bytes) & 15u : 0u;
                     if (dst[i] >= 0)
                         reinterpret_cast<uint16_t *>(cache)[dst[i] * hw + k] =
-                            *reinterpret_cast<const uint16_t *>(stage + i * pitch + skew + 2 * k);
+                            *reinterpret_cast<const uint16_t *>(stage + at[i] + 2 * k);
                 }
-                stage += a.tile * pitch;
+                stage += a.tile * a.pitch[side];
             }
             if (w)
                 for (int i = tid; i < cnt; i += kMovThreads) w[base + i] = sw[i];
@@ -483,10 +529,11 @@ extern "C" int tq_evict_compact(uint8_t *k_blocks, int k_block_bytes, uint8_t *v
     a.new_lens = new_lens;
     a.table = block_table;
     a.w_stride = weights_row_stride;
-    const bool wide = aligned(k_blocks, 16) && aligned(v_blocks, 16) && ((block_table ? page_tokens : T_cap) & 7) == 0;
+    const bool wide = aligned(k_blocks, 16) && aligned(v_blocks, 16) && ((block_table ? page_tokens : T_cap) & 7) == 0 &&
+                      k_block_bytes >= 16 && (vbytes == 0 || vbytes >= 16);
     const int bytes[2] = {k_block_bytes, vbytes};
     auto inverse = [](int n) { return n < 2 ? 0u : (uint32_t)(((1ull << 32) + n - 1) / n); };
-    int token = 2 * 8 + 4;   // shared memory of a token
+    int token = 2 * 8 + 4 + 2 * 2;   // shared memory of a token
     for (int i = 0; i < 2; ++i) {
         a.bytes[i] = bytes[i];
         a.pieces[i] = bytes[i] ? (bytes[i] + 14 + 15) / 16 : 0;

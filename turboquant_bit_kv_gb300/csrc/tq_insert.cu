@@ -40,7 +40,7 @@
 // float32 and compared with the float32 boundaries), although the row is
 // transformed in float32: a row with a coordinate closer to a boundary than
 // kEps or a norm closer to a rounding border of fp16 than kTieUlps (both far
-// above the float32 error; about 0.2% of rows each) is listed, and when the CTA
+// above the float32 error; about 0.1% of rows each) is listed, and when the CTA
 // is through its tiles the listed rows are taken again in double-float
 // arithmetic, one by each of its warps (four for their norms alone).  Rows of a
 // sum of squares outside float32's safe range go through double precision.  (The
@@ -66,18 +66,18 @@ constexpr int kTok = 16;             // tokens of a CTA
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr float kGrid = 63.f;        // cells per unit of y
-// Distance to a boundary, in v = 63 y, below which a row is decided in double
-// precision: 2e-6 of a coordinate's standard deviation (1 / sqrt(128)).  The
-// float32 path is off by about 1.5e-7 of it (rms: rope, the fp16 split, the
-// products' accumulation, three butterfly stages and the scale, each an ulp or
-// less of partial sums of the row's size).
-constexpr float kEps = 2e-6f * kGrid * 0.08838834764831845f;
-
+// Distance to a boundary, in v = 63 y, below which a row's codes are decided
+// again: 1.25e-6 of a coordinate's standard deviation (1 / sqrt(128)).  The
+// float32 path (rope, the fp16 split, the products' accumulation, three
+// butterfly stages and the scale, each an ulp or less of partial sums of the
+// row's size) is off by 1.1e-7 of it (rms); over 1.2e9 coordinates of keys and
+// values of all types, loud channels among them, the furthest decision it got
+// wrong lay 4.3e-7 from its boundary.
+constexpr float kEps = 1.25e-6f * kGrid * 0.08838834764831845f;
 // Distance of the norm to a rounding border of fp16, in units of its last
-// float32 place.  The norm is off by about one of them (rms): nine roundings in
-// the sum of squares, halved by the root, those of the elements (independent,
-// so of little weight in the sum), and three of the root itself.
-constexpr uint32_t kTieUlps = 8;
+// float32 place: it is off by about one of them (the furthest of the wrong
+// roundings in the same rows 1.1e-7 of the norm, two units at most).
+constexpr uint32_t kTieUlps = 5;
 
 enum { kRopeNone = 0, kRopeHalf1, kRopeHalf2, kRopeHalf3, kRopeHalf4, kRopeAdjacent };
 
