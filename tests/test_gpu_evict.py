@@ -151,6 +151,18 @@ def test_attend_lengths(tq, T, B, Hkv, page):
     run_attend(tq, B, 4 * Hkv, Hkv, T, 3, 3, page, [T + 100] + [T // 2] * (B - 1), 0.0, "bf16", "f32", T + 1)
 
 
+@pytest.mark.parametrize("B,Hkv,page", [(33, 2, 0), (70, 1, 32), (128, 1, 0)])
+def test_attend_many_sequences(tq, B, Hkv, page):
+    """Batches over 32 sequences, most of them short or empty, one long: the work is split over live chunks."""
+    rng = np.random.default_rng(B)
+    lens = [int(n) for n in rng.integers(-1, 70, B)]
+    lens[B // 2] = 700
+    lens[-1] = 1
+    run_attend(tq, B, 2 * Hkv, Hkv, 700, 4, 2, page, lens, 1.0, "bf16", "f32", B)
+    run_attend(tq, B, 5 * Hkv, Hkv, 200, 2, 3, page, [0] * (B - 1) + [7], 1.0, "bf16", "f32", B + 1)
+    run_attend(tq, B, Hkv, Hkv, 40, 3, 4, page, [0] * B, 0.5, "f16", "bf16", B + 2)
+
+
 def test_attend_matches_the_plain_decode(tq):
     """Same scores and values as tq_attn_decode: outputs agree to its tolerance, and the weights of a fresh
     accumulator add up to the group's heads."""

@@ -75,6 +75,23 @@ __global__ void __launch_bounds__(kAttnThreads) attn_prep_mma_kernel(const __gri
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int64_t j = blockIdx.x;
     const int b = (int)(j / a.Hkv), kvh = (int)(j % a.Hkv);
+    if (a.live && warp == 3) {
+        // the workers that meet this segment, from the chunks of the sequences before it and of all
+        int before = 0, all = 0;
+        for (int i = lane; i < a.B; i += 32) {
+            const int c = live_chunks(a, i);
+            all += c;
+            if (i < b) before += c;
+        }
+        before = __reduce_add_sync(0xffffffffu, before);
+        all = __reduce_add_sync(0xffffffffu, all);
+        const int c = live_chunks(a, b);
+        if (lane == 0) {
+            const int64_t total = (int64_t)all * a.Hkv, start = (int64_t)before * a.Hkv + (int64_t)kvh * c;
+            const int first = c ? live_worker(start, total, a.workers) : 0;
+            a.live[j] = make_int2(first, c ? live_worker(start + c - 1, total, a.workers) - first + 1 : 0);
+        }
+    }
     for (int h = warp; h < 8; h += 4) {
         float v[4] = {0.f, 0.f, 0.f, 0.f};
         if (h < a.G) {
@@ -161,8 +178,14 @@ __global__ void __launch_bounds__(kAttnThreads * kCombineMaxGroups) attn_combine
     const float *ws, MmaPlan plan, int Hq, int Hkv, int rotate_back, uint32_t s0, uint32_t s1, uint32_t s2,
     uint32_t s3, float *out) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    combine_mma<32>(ws, plan, blockIdx.x, Hq, Hkv, rotate_back, 0.08838834764831845f, s0, s1, s2, s3,
-                [&](int d, float v) { out[(int64_t)blockIdx.x * kD + d] = v; });
+    // the slots of segment j = (sequence, KV head) are the warps whose chunk ranges touch it
+    const int b = blockIdx.x / Hq, h = blockIdx.x % Hq;
+    const int64_t j = (int64_t)b * Hkv + h / (Hq / Hkv);
+    const int64_t first = mma_worker_of_chunk(j * plan.C, plan);
+    const int nslots = (int)(mma_worker_of_chunk((j + 1) * plan.C - 1, plan) - first + 1);
+    combine_mma<32>(ws + (int64_t)blockIdx.x * plan.Smax * kPartialFloats, kPartialFloats, nslots, rotate_back,
+                    0.08838834764831845f, s0, s1, s2, s3,
+                    [&](int d, float v) { out[(int64_t)blockIdx.x * kD + d] = v; });
 }
 
 int launch_attn_prep_mma(const AttnArgs &a, const MmaPlan &plan, int qjl, cudaStream_t st) {
@@ -279,6 +302,7 @@ extern "C" int tq_attn_decode(const void *q, int q_dtype, const uint8_t *k_block
     a.max_pages = 0;
     a.page = 0;
     a.scores = nullptr;
+    a.live = nullptr;
     a.q = q;
     a.q_dtype = q_dtype;
     a.k = k_blocks;
@@ -367,6 +391,7 @@ extern "C" int tq_attn_decode_paged(const void *q, int q_dtype, const uint8_t *k
         a.max_pages = max_pages;
         a.page = page_tokens;
         a.scores = nullptr;
+    a.live = nullptr;
         return mma_path(a, kb, vb, false, true, signs, out, true, static_cast<cudaStream_t>(stream));
     }
     // otherwise the one-token case of the tensor-core causal attention (no workspace)

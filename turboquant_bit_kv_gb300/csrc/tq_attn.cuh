@@ -45,7 +45,10 @@ struct AttnArgs {
     // table[b * max_pages + t / page] of pools [pages][Hkv][page]; page a multiple of 32
     const int32_t *table;
     int max_pages, page;
-    float *scores;           // [B * Hkv][chunks][G][32] log2-domain scores (the kernels that keep them only)
+    // the kernels that keep the scores only:
+    float *scores;           // [B * Hkv][chunks][G][32] log2-domain scores
+    int2 *live;              // [B * Hkv]: a segment's first worker, and how many workers meet it
+    int workers;
 };
 
 __host__ __device__ inline int attn_tiles(int T) { return (T + kTT - 1) / kTT; }

@@ -8,36 +8,29 @@
 namespace tq {
 
 // Merge for the tensor-core kernel's partition, by one CTA for one (sequence,
-// query head) bh: the slots of segment j = (sequence, KV head) are the warps
-// whose chunk ranges touch it.  128 x ng threads: thread d of slot group g
-// reduces output dim d over batches g, g + ng, ... of kBatch slots.  Reading what
-// other SMs just wrote costs a full L2 round trip, so each thread issues
-// every load of a batch at once (m and l of each slot -- the same address
-// across the group -- and its dim of acc) and only then reduces, with the
-// running max rescaled between batches; the groups run their rounds side by
-// side and meet in shared memory.  rotate_back applies D H with the factor
-// out_scale; store(d, value) takes the output.
+// query head): the partials at base + i * stride, i < nslots.  128 x ng
+// threads: thread d of slot group g reduces output dim d over batches g, g +
+// ng, ... of kBatch slots.  Reading what other SMs just wrote costs a full L2
+// round trip, so each thread issues every load of a batch at once (m and l of
+// each slot -- the same address across the group -- and its dim of acc) and
+// only then reduces, with the running max rescaled between batches; the groups
+// run their rounds side by side and meet in shared memory.  rotate_back applies
+// D H with the factor out_scale; store(d, value) takes the output.
 template <int kBatch, class Store>
-__device__ __forceinline__ void combine_mma(const float *ws, const MmaPlan &plan, int bh, int Hq, int Hkv,
-                                            int rotate_back, float out_scale, uint32_t s0, uint32_t s1, uint32_t s2,
-                                            uint32_t s3, Store store) {
+__device__ __forceinline__ void combine_mma(const float *base, int stride, int nslots, int rotate_back,
+                                            float out_scale, uint32_t s0, uint32_t s1, uint32_t s2, uint32_t s3,
+                                            Store store) {
     __shared__ float buf[kD];
     __shared__ float gacc[kCombineMaxGroups][kD];
     __shared__ float gml[kCombineMaxGroups][2];
     const int d = threadIdx.x & (kD - 1), grp = threadIdx.x / kD, ng = blockDim.x / kD;
-    const int b = bh / Hq, h = bh % Hq;
-    const int G = Hq / Hkv;
-    const int64_t j = (int64_t)b * Hkv + h / G;
-    const int64_t first = mma_worker_of_chunk(j * plan.C, plan);
-    const int nslots = (int)(mma_worker_of_chunk((j + 1) * plan.C - 1, plan) - first + 1);
-    const float *base = ws + (int64_t)bh * plan.Smax * kPartialFloats;
     float M = -INFINITY, l = 0.f, acc = 0.f;
     for (int sb = grp * kBatch; sb < nslots; sb += ng * kBatch) {
         float mv[kBatch], lv[kBatch], xv[kBatch];
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
             const bool ok = sb + i < nslots;
-            const float *ps = base + (int64_t)(sb + i) * kPartialFloats;
+            const float *ps = base + (int64_t)(sb + i) * stride;
             mv[i] = ok ? __ldcg(ps) : -INFINITY;
             lv[i] = ok ? __ldcg(ps + 1) : 0.f;
             xv[i] = ok ? __ldcg(ps + 4 + d) : 0.f;

@@ -481,6 +481,39 @@ __device__ __forceinline__ int64_t paged_row0(const AttnArgs &a, int j, int t0) 
            (t0 - pg * a.page) - t0;
 }
 
+// The live chunks of a warp's lanes' sequences b0 + lane, all KV heads, added
+// up to each lane's own.
+__device__ __forceinline__ int live_scan(const AttnArgs &a, int b0, int &c) {
+    const int lane = threadIdx.x & 31;
+    c = b0 + lane < a.B ? live_chunks(a, b0 + lane) : 0;
+    int inc = c * a.Hkv;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(kFull, inc, o);
+        if (lane >= o) inc += v;
+    }
+    return inc;
+}
+
+// Segment and chunk of live chunk x (a warp together), given the first 32
+// sequences' scan.
+__device__ __forceinline__ void live_place(const AttnArgs &a, int x, int inc, int c, int &j, int &chunk) {
+    for (int b0 = 0;;) {
+        const uint32_t past = __ballot_sync(kFull, inc > x);
+        if (past) {
+            const int l = __ffs(past) - 1, cb = __shfl_sync(kFull, c, l);
+            const int rem = x - (__shfl_sync(kFull, inc, l) - cb * a.Hkv), h = rem / cb;
+            j = (b0 + l) * a.Hkv + h;
+            chunk = rem - h * cb;
+            return;
+        }
+        x -= __shfl_sync(kFull, inc, 31);
+        b0 += 32;
+        if (b0 >= a.B) return;   // (not met: x is below the total)
+        inc = live_scan(a, b0, c);
+    }
+}
+
 // SCORES: every live token's scores (log2 domain, before the softmax) are also
 // written to a.scores, from which attn_weights_kernel takes the attention
 // weights once the softmax statistics are final.
@@ -508,9 +541,27 @@ __global__ void __launch_bounds__(Cfg<KB, VB, QJL, NT, WIDE>::kThreads, Cfg<KB, 
     // this warp's chunks [lo, hi) in (segment, position) order: segments j0 .. j1, from chunk cb0
     // of segment j0 to chunk ce1 (exclusive) of segment j1
     const int gw = warp * plan.P + blockIdx.x;
-    const bool active = gw < plan.W;
+    bool active = gw < plan.W;
     int j0 = 0, j1 = -1, cb0 = 0, ce1 = 0;
-    if (active) {
+    if constexpr (SCORES) {
+        if (active) {
+            int c;
+            const int inc = live_scan(a, 0, c);
+            int total = __shfl_sync(kFull, inc, 31), more = 0;
+            for (int b = 32 + lane; b < a.B; b += 32) more += live_chunks(a, b) * a.Hkv;
+            if (a.B > 32) total += __reduce_add_sync(kFull, more);
+            const int W = min(plan.W, total);
+            active = gw < W;
+            if (active) {
+                // gw total / W = gw (total / W) + gw (total % W) / W, the products below 2^31 (W <= 2^14)
+                const int q = total / W, r = total - q * W;
+                const int lo = gw * q + gw * r / W, hi = (gw + 1) * q + (gw + 1) * r / W;
+                live_place(a, lo, inc, c, j0, cb0);
+                live_place(a, hi - 1, inc, c, j1, ce1);
+                ++ce1;
+            }
+        }
+    } else if (active) {
         const int64_t lo = (int64_t)gw * plan.Ctot / plan.W, hi = ((int64_t)gw + 1) * plan.Ctot / plan.W;
         j0 = (int)(lo / plan.C);
         j1 = (int)((hi - 1) / plan.C);
@@ -952,7 +1003,7 @@ __global__ void __launch_bounds__(Cfg<KB, VB, QJL, NT, WIDE>::kThreads, Cfg<KB, 
 
         // ---- this warp's partial of segment j: fold the (hi, lo) columns (G <= 4), sum l over the rows g
         const bool ok = __all_sync(kFull, copies_ok);
-        const int slot = (int)(gw - mma_worker_of_chunk((int64_t)j * plan.C, plan));
+        const int slot = SCORES ? 0 : (int)(gw - mma_worker_of_chunk((int64_t)j * plan.C, plan));
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             float l = lrun[nt];
@@ -965,7 +1016,8 @@ __global__ void __launch_bounds__(Cfg<KB, VB, QJL, NT, WIDE>::kThreads, Cfg<KB, 
                 return C::kH8 ? o[0][m][2 * r + nt] : o[no][m][2 * r] + o[no][m][2 * r + 1];
             };
             if (head < a.G) {
-                float *pr = a.ws + (((int64_t)b * a.Hq + kvh * a.G + head) * plan.Smax + slot) * kPartialFloats;
+                float *pr = a.ws + (SCORES ? ((int64_t)gw + j) * a.G + head
+                                           : ((int64_t)b * a.Hq + kvh * a.G + head) * plan.Smax + slot) * kPartialFloats;
                 if constexpr (C::kRegV) {
                     // dims 16g .. 16g + 15: float4 q holds dims 16g + 4q .. + 3 = m-tiles 2q, 2q + 1, rows g, g + 8
 #pragma unroll

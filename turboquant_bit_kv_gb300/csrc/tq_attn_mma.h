@@ -52,6 +52,28 @@ __host__ __device__ inline int64_t mma_worker_of_chunk(int64_t x, const MmaPlan 
     return ((x + 1) * p.W - 1) / p.Ctot;
 }
 
+// Partition of the kernels that keep the scores: the chunks that hold tokens
+// only, so that every worker does the same work whatever the sequences'
+// lengths.  Sequence b has live_chunks(a, b) of them for each KV head; chunk x
+// of all `total` belongs to worker live_worker(x, total, W), worker w < W =
+// min(plan's workers, total) has chunks [w total / W, (w + 1) total / W), never
+// none, and its partial of segment j lies in slot w + j: as workers and
+// segments go by in order, no two pairs share a slot, and W + B Hkv hold them
+// all.
+__host__ __device__ inline int live_worker(int64_t x, int64_t total, int workers) {
+    const int64_t W = min64(workers, total);
+    return (int)(((x + 1) * W - 1) / total);
+}
+
+__device__ __forceinline__ int live_chunks(const AttnArgs &a, int b) {
+    int L = a.T;
+    if (a.seq_lens) {
+        const int sl = a.seq_lens[b];
+        L = sl < 0 ? 0 : (sl > a.T ? a.T : sl);
+    }
+    return (L + kMmaChunk - 1) / kMmaChunk;
+}
+
 // Slot groups of 128 threads in a combine CTA: one per 32 slots of Smax, at most kCombineMaxGroups.
 inline int mma_combine_groups(const MmaPlan &p) {
     const int g = (p.Smax + 31) / 32;

@@ -14,6 +14,10 @@
 // Three launches as in tq_attn_decode (query prep, attention, merge), chained
 // as programmatic dependents.
 //
+// The work is split over the chunks that hold tokens, not over the longest
+// context, so a batch of different lengths takes as long as its tokens (16
+// sequences of 0 to 8192 tokens, 55% of them: 49 us before).
+//
 // Every weight is written by one thread, its heads added in order, so results
 // do not depend on timing.  Scores, statistics and weights are float32.
 #include <cmath>
@@ -41,6 +45,7 @@ struct WeightsArgs {
     const float *ws;
     const float *scores;
     const int32_t *seq_lens;
+    const int2 *live;
     float *weights;
     void *out;
     int64_t w_stride;
@@ -50,6 +55,48 @@ struct WeightsArgs {
     uint32_t signs[4];
 };
 
+// Weights of tokens t0 .. end - 1 of a segment from its scores and its heads'
+// (maximum, 1 / sum): a warp takes two chunks of 32 tokens at a time, G rows of
+// 32 scores each, one coalesced load a row.
+template <int G>
+__device__ __forceinline__ void add_weights(const float *scores, const float (*ml)[2], float *w, int t0, int end,
+                                            float decay) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+    float mx[G], inv[G];
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+        mx[g] = ml[g][0];
+        inv[g] = ml[g][1];
+    }
+    for (int c = t0 / kMmaChunk + 2 * warp; c * kMmaChunk < end; c += 2 * nw) {
+        float s[2][G], old[2] = {0.f, 0.f};
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int t = (c + u) * kMmaChunk + lane;
+            const float *row = scores + (int64_t)(c + u) * (kMmaChunk * G) + lane;
+            if (t < end) {
+#pragma unroll
+                for (int g = 0; g < G; ++g) s[u][g] = __ldcs(row + g * kMmaChunk);
+                if (decay != 0.f) old[u] = __ldcs(w + t) * decay;
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int t = (c + u) * kMmaChunk + lane;
+            if (t < end) {
+                float p = 0.f;
+#pragma unroll
+                for (int g = 0; g < G; ++g) {
+                    float e;   // (weights below 2^-126 count as 0)
+                    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(s[u][g] - mx[g]));
+                    p = fmaf(e, inv[g], p);
+                }
+                w[t] = old[u] + p;
+            }
+        }
+    }
+}
+
 // CTAs [0, B Hq): the merge of one (sequence, query head).  The rest: the
 // weights of a.per tokens of one segment (sequence, KV head): the
 // final maximum and sum of its heads, one warp per head over the segment's
@@ -58,35 +105,40 @@ __global__ void __launch_bounds__(kAttnThreads * kCombineMaxGroups, 2) attn_weig
     const __grid_constant__ WeightsArgs a, const __grid_constant__ MmaPlan plan) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int heads = a.B * a.Hq;
-    if ((int)blockIdx.x < heads) {
-        const int64_t at = (int64_t)blockIdx.x * kD;
-        combine_mma<kMergeBatch>(a.ws, plan, blockIdx.x, a.Hq, a.Hkv, 1, a.out_scale, a.signs[0], a.signs[1], a.signs[2],
-                    a.signs[3], [&](int d, float v) {
-                        if (a.out_dtype == TQ_F32) static_cast<float *>(a.out)[at + d] = v;
-                        else if (a.out_dtype == TQ_BF16) static_cast<__nv_bfloat16 *>(a.out)[at + d] = __float2bfloat16_rn(v);
-                        else static_cast<__half *>(a.out)[at + d] = __float2half_rn(v);
-                    });
-        return;
-    }
-    __shared__ float ml[8][2];   // final maximum, 1 / sum
+    const bool merge = (int)blockIdx.x < heads;
     const int64_t unit = blockIdx.x - heads;
-    const int64_t j = unit / a.parts;
-    const int t0 = (int)(unit % a.parts) * a.per;
+    const int64_t j = merge ? (blockIdx.x / a.Hq) * a.Hkv + blockIdx.x % a.Hq / a.G : unit / a.parts;
     const int b = (int)(j / a.Hkv);
     int L = a.T;
     if (a.seq_lens) {
         const int sl = a.seq_lens[b];
         L = sl < 0 ? 0 : (sl > a.T ? a.T : sl);
     }
+    // the segment's slots: the workers whose ranges meet its chunks
+    const int2 met = __ldcg(a.live + j);
+    const int nslots = met.y;
+    const float *slots = a.ws + (met.x + j) * a.G * kPartialFloats;   // [nslots][G]
+    if (merge) {
+        const int64_t at = (int64_t)blockIdx.x * kD;
+        combine_mma<kMergeBatch>(
+            slots + blockIdx.x % a.G * kPartialFloats, a.G * kPartialFloats, nslots, 1, a.out_scale, a.signs[0],
+            a.signs[1], a.signs[2], a.signs[3], [&](int d, float v) {
+                if (a.out_dtype == TQ_F32) static_cast<float *>(a.out)[at + d] = v;
+                else if (a.out_dtype == TQ_BF16) static_cast<__nv_bfloat16 *>(a.out)[at + d] = __float2bfloat16_rn(v);
+                else static_cast<__half *>(a.out)[at + d] = __float2half_rn(v);
+            });
+        return;
+    }
+    __shared__ float ml[8][2];   // final maximum, 1 / sum
+    const int t0 = (int)(unit % a.parts) * a.per;
     if (t0 >= L) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
-    const int64_t first = mma_worker_of_chunk(j * plan.C, plan);
-    const int nslots = (int)(mma_worker_of_chunk((j + 1) * plan.C - 1, plan) - first + 1);
     for (int g = warp; g < a.G; g += nw) {
-        const float *base = a.ws + (j * a.G + g) * plan.Smax * kPartialFloats;
+        const float *base = slots + g * kPartialFloats;
         float M = -INFINITY, l = 0.f;
         for (int s = lane; s < nslots; s += 32) {
-            const float ms = __ldcg(base + (int64_t)s * kPartialFloats), ls = __ldcg(base + (int64_t)s * kPartialFloats + 1);
+            const float *ps = base + (int64_t)s * a.G * kPartialFloats;
+            const float ms = __ldcg(ps), ls = __ldcg(ps + 1);
             const float mn = fmaxf(M, ms);
             l = mn == -INFINITY ? l + ls : l * exp2f(M - mn) + ls * exp2f(ms - mn);
             M = mn;
@@ -106,29 +158,18 @@ __global__ void __launch_bounds__(kAttnThreads * kCombineMaxGroups, 2) attn_weig
         }
     }
     __syncthreads();
-    // a warp takes two chunks of 32 tokens at a time: G rows of 32 scores each, one coalesced load a row
     const int end = min(t0 + a.per, L);
     float *w = a.weights + j * a.w_stride;
-    const float *sc = a.scores + j * plan.C * (kMmaChunk * a.G) + lane;
-    for (int c = t0 / kMmaChunk + 2 * warp; c * kMmaChunk < end; c += 2 * nw) {
-        float s[2][8], old[2] = {0.f, 0.f};
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const int t = (c + u) * kMmaChunk + lane;
-            const float *row = sc + (int64_t)(c + u) * (kMmaChunk * a.G);
-#pragma unroll
-            for (int g = 0; g < 8; ++g) s[u][g] = g < a.G && t < end ? __ldcs(row + g * kMmaChunk) : 0.f;
-            if (t < end && a.decay != 0.f) old[u] = __ldcs(w + t) * a.decay;
-        }
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const int t = (c + u) * kMmaChunk + lane;
-            float p = 0.f;
-#pragma unroll
-            for (int g = 0; g < 8; ++g)
-                if (g < a.G) p = fmaf(exp2f(s[u][g] - ml[g][0]), ml[g][1], p);
-            if (t < end) w[t] = old[u] + p;
-        }
+    const float *sc = a.scores + j * plan.C * (kMmaChunk * a.G);
+    switch (a.G) {
+        case 1: add_weights<1>(sc, ml, w, t0, end, a.decay); break;
+        case 2: add_weights<2>(sc, ml, w, t0, end, a.decay); break;
+        case 3: add_weights<3>(sc, ml, w, t0, end, a.decay); break;
+        case 4: add_weights<4>(sc, ml, w, t0, end, a.decay); break;
+        case 5: add_weights<5>(sc, ml, w, t0, end, a.decay); break;
+        case 6: add_weights<6>(sc, ml, w, t0, end, a.decay); break;
+        case 7: add_weights<7>(sc, ml, w, t0, end, a.decay); break;
+        default: add_weights<8>(sc, ml, w, t0, end, a.decay); break;
     }
 }
 
@@ -171,8 +212,21 @@ int64_t scores_floats(int B, int Hq, int Hkv, int T) {
     return (int64_t)B * Hkv * ((T + kMmaChunk - 1) / kMmaChunk) * kMmaChunk * (Hq / Hkv);
 }
 
-int64_t partials_floats(int B, int Hq, int Hkv, int T, int sms) {
-    return (mma_workspace_floats(B, Hq, Hkv, T, sms) + 3) & ~(int64_t)3;
+// Workspace: partials [W + B Hkv][G][132] | query fragments [B Hkv] | segments' workers [B Hkv][2] | scores, in
+// floats; W workers, at most kMmaMaxWarpsPerSm per SM and a chunk each.
+struct Layout {
+    int64_t frag, live, scores, floats;
+    Layout(int B, int Hq, int Hkv, int T, int64_t W) {
+        const int64_t segs = (int64_t)B * Hkv;
+        frag = (W + segs) * (Hq / Hkv) * kPartialFloats;
+        live = frag + segs * kFragWords;
+        scores = live + ((segs * 2 + 3) & ~(int64_t)3);
+        floats = scores + scores_floats(B, Hq, Hkv, T);
+    }
+};
+
+int64_t most_workers(int B, int Hkv, int T) {
+    return min64((int64_t)B * Hkv * ((T + kMmaChunk - 1) / kMmaChunk), (int64_t)kMmaMaxWarpsPerSm * sm_count());
 }
 
 }  // namespace
@@ -182,7 +236,7 @@ using namespace tq;
 
 extern "C" size_t tq_attn_weights_workspace_bytes(int B, int Hq, int Hkv, int T) {
     if (B <= 0 || Hq <= 0 || Hkv <= 0 || T <= 0 || Hq % Hkv || Hq / Hkv > 8) return 0;
-    return (size_t)(partials_floats(B, Hq, Hkv, T, 0) + scores_floats(B, Hq, Hkv, T)) * sizeof(float);
+    return (size_t)Layout(B, Hq, Hkv, T, most_workers(B, Hkv, T)).floats * sizeof(float);
 }
 
 extern "C" int tq_attn_decode_weights(const void *q, int q_dtype, const uint8_t *k_blocks, const tq_codebook *kcb,
@@ -216,7 +270,7 @@ extern "C" int tq_attn_decode_weights(const void *q, int q_dtype, const uint8_t 
     const int per = ((T + parts - 1) / parts + kMmaChunk - 1) / kMmaChunk * kMmaChunk;
     parts = (T + per - 1) / per;
     const int64_t grid = (int64_t)B * Hq + (int64_t)B * Hkv * parts;
-    if (grid > 0x7FFFFFFF) return TQ_ERR_UNSUPPORTED;
+    if (grid > 0x7FFFFFFF || segs * ((T + kMmaChunk - 1) / kMmaChunk) > 0x7FFFFFFF) return TQ_ERR_UNSUPPORTED;
 
     AttnArgs a;
     std::memset(&a, 0, sizeof(a));
@@ -243,11 +297,15 @@ extern "C" int tq_attn_decode_weights(const void *q, int q_dtype, const uint8_t 
     a.table = block_table;
     a.max_pages = max_pages;
     a.page = page_tokens;
-    a.scores = a.ws + partials_floats(B, Hq, Hkv, T, 0);
 
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const int kb = kcb->bits, vb = vcb->bits, nt = G <= 4 ? 1 : 2;
     MmaPlan plan = mma_plan(B, Hq, Hkv, T, kb, vb, false, G);
+    const Layout at(B, Hq, Hkv, T, plan.W);
+    plan.frag_off = at.frag;
+    a.live = reinterpret_cast<int2 *>(a.ws + at.live);
+    a.workers = plan.W;
+    a.scores = a.ws + at.scores;
     int r = launch_attn_prep_mma(a, plan, 0, st);
     if (r != TQ_OK) return r;
     r = kb == 2 ? launch_attn_mma_scores_k2(a, plan, vb, nt, paged, st)
@@ -258,6 +316,7 @@ extern "C" int tq_attn_decode_weights(const void *q, int q_dtype, const uint8_t 
     w.ws = a.ws;
     w.scores = a.scores;
     w.seq_lens = seq_lens;
+    w.live = a.live;
     w.weights = weights;
     w.out = out;
     w.w_stride = weights_row_stride;

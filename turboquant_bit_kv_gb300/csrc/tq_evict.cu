@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
     if (tid == 0) s.listed = 0;
     __syncthreads();
     // pass 1: keys, and the histogram of their top 11 bits
-#pragma unroll 4
+#pragma unroll 8
     for (int i0 = p0; i0 < p1; i0 += 32) {
         const int i = i0 + lane;
         const bool in = i < p1;
@@ -477,7 +477,9 @@ extern "C" int tq_evict_select(const float *weights, int64_t row_stride, const i
     if (seq_lens == new_lens) return TQ_ERR_ARG;   // other rows still read the old lengths
     if (!aligned(weights, 4) || !aligned(kept, 4) || !aligned(new_lens, 4) || !aligned(seq_lens, 4)) return TQ_ERR_ALIGN;
     const int64_t rows = (int64_t)B * Hkv;
-    // CTAs per row: a chunk of at most kSelChunk keys each; while SMs would stay idle, of 8192
+    // CTAs per row: a chunk of at most kSelChunk keys each; while SMs would stay idle, of 8192.  (More
+    // CTAs read more of one another's histograms: 256 rows of 32769 take 30 us with two CTAs a row, 32
+    // with one, 47 with four, 126 with eight.)
     int C = 1;
     while (C < kMaxCluster &&
            ((T + C - 1) / C > kSelChunk || (rows * C * 2 <= sm_count() && (T + C - 1) / C > 8192)))

@@ -105,6 +105,28 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
     if (n >= a.n_tok) return;
     const int pairs = rope.rot_dim / 2;
     const bool turned = 8 * c < pairs;   // chunks past the rotated elements are copied
+    const int e0 = HALF && turned ? 8 * c : 16 * c;
+    const int e1 = HALF && turned ? pairs + 8 * c : 16 * c + 8;
+    const uint8_t *x = a.x + n * a.x_tok;
+    uint8_t *o = a.out + n * a.o_tok;
+    // heads go by in batches of kBatch; a batch is loaded before the sines (and the batch before it) are needed
+    constexpr int kBatch = DT == TQ_F32 ? 2 : 4;
+    uint4 va[kBatch][NV], vb[kBatch][NV];
+    auto load = [&](int h0) {
+#pragma unroll
+        for (int q = 0; q < kBatch; ++q) {
+            const int h = h0 + q * a.slots;
+            if (h < a.heads) {
+                const uint8_t *xr = x + h * a.x_head;
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+                    va[q][i] = __ldcs(reinterpret_cast<const uint4 *>(xr + e0 * ES) + i);
+                    vb[q][i] = __ldcs(reinterpret_cast<const uint4 *>(xr + e1 * ES) + i);
+                }
+            }
+        }
+    };
+    load(slot);
     float sn[8], cs[8];
     if (turned) {
         int64_t p[3];
@@ -117,44 +139,48 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
             rope_sincos(rope_turns(turn[8 * c + k], t), sn[k], cs[k]);
         }
     }
-    const int e0 = HALF && turned ? 8 * c : 16 * c;
-    const int e1 = HALF && turned ? pairs + 8 * c : 16 * c + 8;
-    const uint8_t *x = a.x + n * a.x_tok;
-    uint8_t *o = a.out + n * a.o_tok;
-#pragma unroll 4
-    for (int h = slot; h < a.heads; h += a.slots) {
-        const uint8_t *xr = x + h * a.x_head;
-        uint4 va[NV], vb[NV];
+    for (int h0 = slot; h0 < a.heads; h0 += kBatch * a.slots) {
+        uint4 ra[kBatch][NV], rb[kBatch][NV];
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            va[i] = __ldcs(reinterpret_cast<const uint4 *>(xr + e0 * ES) + i);
-            vb[i] = __ldcs(reinterpret_cast<const uint4 *>(xr + e1 * ES) + i);
+        for (int q = 0; q < kBatch; ++q) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                ra[q][i] = va[q][i];
+                rb[q][i] = vb[q][i];
+            }
+            if (turned && h0 + q * a.slots < a.heads) {
+                float fa[8], fb[8], ga[8], gb[8];
+                unpack8<DT>(ra[q], fa);
+                unpack8<DT>(rb[q], fb);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    if constexpr (HALF) {
+                        ga[k] = fmaf(fa[k], cs[k], -(fb[k] * sn[k]));
+                        gb[k] = fmaf(fb[k], cs[k], fa[k] * sn[k]);
+                    } else {
+                        // pair k of the chunk: elements 2k, 2k + 1 of its 16
+                        float *src = k < 4 ? fa : fb, *dst = k < 4 ? ga : gb;
+                        const int m = 2 * (k & 3);
+                        dst[m] = fmaf(src[m], cs[k], -(src[m + 1] * sn[k]));
+                        dst[m + 1] = fmaf(src[m + 1], cs[k], src[m] * sn[k]);
+                    }
+                }
+                pack8<DT>(ga, ra[q]);
+                pack8<DT>(gb, rb[q]);
+            }
         }
-        if (turned) {
-            float fa[8], fb[8], ra[8], rb[8];
-            unpack8<DT>(va, fa);
-            unpack8<DT>(vb, fb);
+        load(h0 + kBatch * a.slots);   // (rows in place: other heads than the ones written now)
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                if constexpr (HALF) {
-                    ra[k] = fmaf(fa[k], cs[k], -(fb[k] * sn[k]));
-                    rb[k] = fmaf(fb[k], cs[k], fa[k] * sn[k]);
-                } else {
-                    // pair k of the chunk: elements 2k, 2k + 1 of its 16
-                    float *src = k < 4 ? fa : fb, *dst = k < 4 ? ra : rb;
-                    const int m = 2 * (k & 3);
-                    dst[m] = fmaf(src[m], cs[k], -(src[m + 1] * sn[k]));
-                    dst[m + 1] = fmaf(src[m + 1], cs[k], src[m] * sn[k]);
+        for (int q = 0; q < kBatch; ++q) {
+            const int h = h0 + q * a.slots;
+            if (h < a.heads) {
+                uint8_t *orow = o + h * a.o_head;
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+                    __stcs(reinterpret_cast<uint4 *>(orow + e0 * ES) + i, ra[q][i]);
+                    __stcs(reinterpret_cast<uint4 *>(orow + e1 * ES) + i, rb[q][i]);
                 }
             }
-            pack8<DT>(ra, va);
-            pack8<DT>(rb, vb);
-        }
-        uint8_t *orow = o + h * a.o_head;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            reinterpret_cast<uint4 *>(orow + e0 * ES)[i] = va[i];
-            reinterpret_cast<uint4 *>(orow + e1 * ES)[i] = vb[i];
         }
     }
 }

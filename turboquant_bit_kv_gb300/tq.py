@@ -120,7 +120,7 @@ def _check(status, what):
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 # the current stream's handle without building a Stream object (3 us a call on the host)
@@ -439,10 +439,6 @@ def _on(what, *tensors):
     return _On(dev)
 
 
-def _at(t):
-    return None if t is None else t.data_ptr()
-
-
 def _need(ok, what):
     if not ok:
         raise ValueError(what)
@@ -531,9 +527,9 @@ def tq_insert_kv(k, v, pos, rope, kcb, vcb, signs, k_blocks, v_blocks, dst, dst_
     turn = rope is not None and k is not None
     pa = _axis_stride(pos, rope, n, what) if turn else 0
     with _on(what, k, v, pos if turn else None, k_blocks, v_blocks, dst):
-        _check(lib().tq_insert_kv(_at(k), strides[0], strides[1], _at(v), strides[2], strides[3], _dtype(x), n, heads,
+        _check(lib().tq_insert_kv(_ptr(k), strides[0], strides[1], _ptr(v), strides[2], strides[3], _dtype(x), n, heads,
                                   pos.data_ptr() if turn else None, pa, rope if turn else None, kcb, vcb, signs,
-                                  _at(k_blocks), _at(v_blocks), blocks, dst.data_ptr(), dst_head_stride,
+                                  _ptr(k_blocks), _ptr(v_blocks), blocks, dst.data_ptr(), dst_head_stride,
                                   _stream(stream)), what)
 
 
@@ -599,7 +595,7 @@ def tq_attn_decode_weights(q, k_blocks, kcb, v_blocks, vcb, weights, out, worksp
     pages = _pages(block_table, B, what)
     with _on(what, q, k_blocks, v_blocks, weights, out, workspace, seq_lens, block_table):
         _check(lib().tq_attn_decode_weights(q.data_ptr(), _dtype(q), k_blocks.data_ptr(), kcb, v_blocks.data_ptr(), vcb,
-                                            _at(block_table), pages, unit, _at(seq_lens), B, Hq, Hkv, unit, T, scale,
+                                            _ptr(block_table), pages, unit, _ptr(seq_lens), B, Hq, Hkv, unit, T, scale,
                                             signs, weights.data_ptr(), stride, decay, out.data_ptr(), _dtype(out),
                                             workspace.data_ptr(), workspace.numel() * workspace.element_size(),
                                             _stream(stream)), what)
@@ -625,7 +621,7 @@ def tq_evict_select(weights, kept, new_lens, T, first, last, seq_lens=None, stre
         _lens(seq_lens, B, what)
     stride = _row_of(weights, B, Hkv, T, what)
     with _on(what, weights, kept, new_lens, seq_lens):
-        _check(lib().tq_evict_select(weights.data_ptr(), stride, _at(seq_lens), B, Hkv, T, keep, first, last,
+        _check(lib().tq_evict_select(weights.data_ptr(), stride, _ptr(seq_lens), B, Hkv, T, keep, first, last,
                                      kept.data_ptr(), new_lens.data_ptr(), _stream(stream)), what)
     return kept
 
@@ -649,6 +645,6 @@ def tq_evict_compact(k_blocks, v_blocks, kept, new_lens, T, weights=None, block_
     unit = ks[2]
     stride = 0 if weights is None else _row_of(weights, B, Hkv, T, what)
     with _on(what, k_blocks, v_blocks, kept, new_lens, weights, block_table):
-        _check(lib().tq_evict_compact(k_blocks.data_ptr(), ks[3], _at(v_blocks), vbytes, _at(weights), stride,
-                                      kept.data_ptr(), keep, new_lens.data_ptr(), _at(block_table), pages, unit, ks[0],
+        _check(lib().tq_evict_compact(k_blocks.data_ptr(), ks[3], _ptr(v_blocks), vbytes, _ptr(weights), stride,
+                                      kept.data_ptr(), keep, new_lens.data_ptr(), _ptr(block_table), pages, unit, ks[0],
                                       B, Hkv, unit, T, _stream(stream)), what)
