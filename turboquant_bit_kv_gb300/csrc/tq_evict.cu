@@ -22,14 +22,14 @@ constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kSelCached = 40 * 1024;      // keys of a CTA's chunk held in shared memory (160 KB)
 constexpr int kSelChunk = 20 * 1024;       // keys a CTA gets before a row takes more CTAs
+constexpr int kSelLeast = 8192;           // (while SMs would stay idle)
 constexpr int kMaxCluster = 8;             // portable cluster size
 
 // ---- selection
 //
 // Of the tokens that are not kept anyway (the first, the last), the m largest
 // weights.  On order-preserving keys, a histogram of the top 11 bits finds the
-// bin that the m-th largest key lies in (every CTA of the row adds up all the
-// row's histograms by itself); a second pass over the keys counts what lies in
+// bin that the m-th largest key lies in; a second pass over the keys counts what lies in
 // higher bins and lists the keys of that bin, and two more rounds of 11 and 10
 // bits over the list find the m-th largest key K itself.  Everything above K
 // stays and, of the tokens equal to K, the ones of lowest index: each warp has a
@@ -70,19 +70,31 @@ struct SelShared {
 
 __device__ __forceinline__ uint32_t warp_sum(uint32_t v) { return __reduce_add_sync(0xffffffffu, v); }
 
-// The digit (of WIDTH bits) that the m-th largest key has, from the row's
-// histograms hist of all its CTAs, and how many keys have larger ones.
+// The digit (of WIDTH bits) that the m-th largest key has and how many keys
+// have larger ones, from the row's histograms hist of all its CTAs: each adds
+// its bins that are not empty to the first CTA's, and all read those.
 template <int WIDTH>
 __device__ __forceinline__ void find_digit(cg::cluster_group &cl, SelShared &s, uint32_t *hist, uint32_t &m,
                                            uint32_t &prefix) {
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, C = (int)cl.num_blocks();
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     constexpr int kNum = 1 << WIDTH, kPer = kNum / kSelThreads;
     // thread t holds the bins of digits kNum - 1 - kPer t downwards
+    uint32_t *all = cl.map_shared_rank(hist, 0);
+    if (cl.num_blocks() > 1) {
+        __syncthreads();
+        if (cl.block_rank() > 0) {
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) {
+                const int at = kNum - 1 - (tid * kPer + e);
+                if (hist[at]) atomicAdd(all + at, hist[at]);
+            }
+        }
+    }
+    cl.sync();
     uint32_t cnt[kPer], sum = 0;
 #pragma unroll
     for (int e = 0; e < kPer; ++e) {
-        cnt[e] = 0;
-        for (int p = 0; p < C; ++p) cnt[e] += cl.map_shared_rank(hist, p)[kNum - 1 - (tid * kPer + e)];
+        cnt[e] = all[kNum - 1 - (tid * kPer + e)];
         sum += cnt[e];
     }
     uint32_t inc = sum;
@@ -144,7 +156,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
 
     for (int i = tid; i < 3 * kBins; i += kSelThreads) (&s.hist[0][0])[i] = 0;
     if (tid == 0) s.listed = 0;
-    __syncthreads();
+    cl.sync();   // (the first CTA's bins are empty before the others add to them)
     // pass 1: keys, and the histogram of their top 11 bits
 #pragma unroll 8
     for (int i0 = p0; i0 < p1; i0 += 32) {
@@ -158,7 +170,6 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
         if (lane == 0) atomicAdd(&s.hist[0][d], (uint32_t)__popc(same));
         else if (in && d != lead) atomicAdd(&s.hist[0][d], 1u);
     }
-    cl.sync();
     uint32_t prefix = 0;
     find_digit<11>(cl, s, s.hist[0], m, prefix);
     // pass 2: keys of higher bins counted, those of the bin listed and their next digit counted
@@ -183,7 +194,6 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
         s.above[warp] = above;
         s.equal[warp] = 0;
     }
-    cl.sync();
     find_digit<11>(cl, s, s.hist[1], m, prefix);
     // the last digit, over the list, or over the keys again where they did not fit
     const uint32_t listed = s.listed;
@@ -196,7 +206,6 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
         for (int i = p0 + lane; i < p1; i += 32)
             if ((key(i) >> 10) == prefix) atomicAdd(&s.hist[2][key(i) & 1023u], 1u);
     }
-    cl.sync();
     find_digit<10>(cl, s, s.hist[2], m, prefix);
     // prefix: the threshold key; m: how many of the tokens equal to it stay.  The bin's keys by piece:
     if (fits) {
@@ -271,8 +280,8 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
 // eight blocks that starts and ends on a 16-byte boundary, its 16-byte pieces
 // put together from the aligned words around them in shared memory.  Otherwise
 // (and for blocks below 16 bytes) half words are read and written one by one.
-constexpr int kMovThreads = 256;
-constexpr int kMovSmem = 56 * 1024;        // four CTAs per SM: enough reads in flight
+constexpr int kMovThreads = 1024;          // of a CTA that has an SM to itself; 256 where four share one
+constexpr int kMovSmem = 56 * 1024;        // shared memory of a CTA of 256 threads
 constexpr int kMovMaxBytes = 512;          // of a block
 
 struct MovArgs {
@@ -302,15 +311,15 @@ __device__ __forceinline__ void lds16_a2(const uint8_t *p, uint32_t (&v)[4]) {
 }
 
 template <bool WIDE>
-__global__ void __launch_bounds__(kMovThreads, 4) compact_kernel(const __grid_constant__ MovArgs a) {
+__global__ void __launch_bounds__(kMovThreads, 1) compact_kernel(const __grid_constant__ MovArgs a) {
     extern __shared__ __align__(16) uint8_t mov_smem[];
     int64_t *src = reinterpret_cast<int64_t *>(mov_smem);      // [tile] source slot
     int64_t *dst = src + a.tile;                               // [tile] own slot, -1: not in the pool
     uint8_t *stage0 = reinterpret_cast<uint8_t *>(dst + a.tile);
     float *sw = reinterpret_cast<float *>(stage0 + (size_t)a.tile * (a.pitch[0] + a.pitch[1]));
-    uint16_t *place = reinterpret_cast<uint16_t *>(sw + a.tile);   // [2][tile] where a token's block starts in the stage
+    uint32_t *place = reinterpret_cast<uint32_t *>(sw + a.tile);   // [2][tile] where a token's block starts in the stage
     cg::cluster_group cl = cg::this_cluster();
-    const int tid = threadIdx.x, C = (int)cl.num_blocks(), rank = (int)cl.block_rank();
+    const int tid = threadIdx.x, threads = blockDim.x, C = (int)cl.num_blocks(), rank = (int)cl.block_rank();
     const int64_t row = blockIdx.x / C;
     const int b = (int)(row / a.Hkv), h = (int)(row % a.Hkv);
     const int32_t *kept = a.kept + row * a.keep;
@@ -333,7 +342,7 @@ __global__ void __launch_bounds__(kMovThreads, 4) compact_kernel(const __grid_co
         const int cnt = max(0, min(a.tile, n - base));
         const bool moves = cnt > 0 && kept[base + cnt - 1] != base + cnt - 1;
         if (moves) {
-            for (int i = tid; i < cnt; i += kMovThreads) {
+            for (int i = tid; i < cnt; i += threads) {
                 const int j = base + i;
                 int from = kept[j];
                 if (from < j || from >= a.T) from = j;   // not a place to take from: it stays
@@ -348,7 +357,7 @@ __global__ void __launch_bounds__(kMovThreads, 4) compact_kernel(const __grid_co
 #pragma unroll
                 for (int side = 0; side < 2; ++side)
                     place[side * a.tile + i] =
-                        (uint16_t)(i * a.pitch[side] + (WIDE ? (int)((uint32_t)s * (uint32_t)a.bytes[side] & 15u) : 0));
+                        (uint32_t)(i * a.pitch[side] + (WIDE ? (int)((uint32_t)s * (uint32_t)a.bytes[side] & 15u) : 0));
                 if (w) sw[i] = w[own < 0 ? j : from];
             }
             __syncthreads();
@@ -360,12 +369,12 @@ __global__ void __launch_bounds__(kMovThreads, 4) compact_kernel(const __grid_co
                 const uint8_t *cache = a.blocks[side];
                 if (WIDE) {
                     const int np = a.pieces[side], total = cnt * np;
-                    for (int p0 = tid; p0 < total; p0 += 4 * kMovThreads) {
+                    for (int p0 = tid; p0 < total; p0 += 4 * threads) {
                         uint4 v[4];
                         int at[4];
 #pragma unroll
                         for (int u = 0; u < 4; ++u) {
-                            const int p = p0 + u * kMovThreads;
+                            const int p = p0 + u * threads;
                             at[u] = -1;
                             if (p < total) {
                                 const int i = div_by(p, a.inv_piece[side]), q = p - i * np;
@@ -384,7 +393,7 @@ __global__ void __launch_bounds__(kMovThreads, 4) compact_kernel(const __grid_co
                 } else {
                     const int hw = bytes / 2, total = cnt * hw;
 #pragma unroll 8
-                    for (int p = tid; p < total; p += kMovThreads) {
+                    for (int p = tid; p < total; p += threads) {
                         const int i = div_by(p, a.inv_half[side]), k = p - i * hw;
                         if (src[i] >= 0)
                             *reinterpret_cast<uint16_t *>(stage + i * a.pitch[side] + 2 * k) =
@@ -402,9 +411,9 @@ __global__ void __launch_bounds__(kMovThreads, 4) compact_kernel(const __grid_co
                 const int bytes = a.bytes[side], hw = bytes / 2;
                 if (bytes == 0) continue;
                 uint8_t *cache = a.blocks[side];
-                const uint16_t *at = place + side * a.tile;
+                const uint32_t *at = place + side * a.tile;
                 const int words = WIDE ? cnt * bytes / 16 : 0;   // whole 16-byte pieces of the tile
-                for (int x = tid; x < words; x += kMovThreads) {
+                for (int x = tid; x < words; x += threads) {
                     // piece x: half words 8 x .. 8 x + 7 of the tile, of block i from its k-th on, the last
                     // 8 - r of them perhaps of the next block (blocks have 8 at least)
                     const int i = div_by(8 * x, a.inv_half[side]), k = 8 * x - i * hw, r = hw - k, o = i & ~7;
@@ -422,7 +431,7 @@ __global__ void __launch_bounds__(kMovThreads, 4) compact_kernel(const __grid_co
                             make_uint4(v[0], v[1], v[2], v[3]);
                 }
                 const int total = cnt * hw;
-                for (int p = words * 8 + tid; p < total; p += kMovThreads) {
+                for (int p = words * 8 + tid; p < total; p += threads) {
                     const int i = div_by(p, a.inv_half[side]), k = p - i * hw;
                     if (dst[i] >= 0)
                         reinterpret_cast<uint16_t *>(cache)[dst[i] * hw + k] =
@@ -431,13 +440,13 @@ __global__ void __launch_bounds__(kMovThreads, 4) compact_kernel(const __grid_co
                 stage += a.tile * a.pitch[side];
             }
             if (w)
-                for (int i = tid; i < cnt; i += kMovThreads) w[base + i] = sw[i];
+                for (int i = tid; i < cnt; i += threads) w[base + i] = sw[i];
             __syncthreads();   // the next step's blocks take this one's place
         }
     }
     // vacated slots start from zero again (all reads lie before the last meeting)
     if (w)
-        for (int t = n + rank * kMovThreads + tid; t < a.T; t += C * kMovThreads) w[t] = 0.f;
+        for (int t = n + rank * threads + tid; t < a.T; t += C * threads) w[t] = 0.f;
 }
 
 template <class K, class A>
@@ -477,12 +486,12 @@ extern "C" int tq_evict_select(const float *weights, int64_t row_stride, const i
     if (seq_lens == new_lens) return TQ_ERR_ARG;   // other rows still read the old lengths
     if (!aligned(weights, 4) || !aligned(kept, 4) || !aligned(new_lens, 4) || !aligned(seq_lens, 4)) return TQ_ERR_ALIGN;
     const int64_t rows = (int64_t)B * Hkv;
-    // CTAs per row: a chunk of at most kSelChunk keys each; while SMs would stay idle, of 8192.  (More
-    // CTAs read more of one another's histograms: 256 rows of 32769 take 30 us with two CTAs a row, 32
-    // with one, 47 with four, 126 with eight.)
+    // CTAs per row: a chunk of at most kSelChunk keys each; while SMs would stay idle, of kSelLeast.  (A
+    // cluster's meetings cost more than its CTAs save: 256 rows of 32769 take 30 us with two CTAs a row,
+    // 42 with four, 87 with eight.)
     int C = 1;
     while (C < kMaxCluster &&
-           ((T + C - 1) / C > kSelChunk || (rows * C * 2 <= sm_count() && (T + C - 1) / C > 8192)))
+           ((T + C - 1) / C > kSelChunk || (rows * C * 2 <= sm_count() && (T + C - 1) / C > kSelLeast)))
         C *= 2;
     const int chunk = (T + C - 1) / C;
     SelArgs a;
@@ -535,7 +544,7 @@ extern "C" int tq_evict_compact(uint8_t *k_blocks, int k_block_bytes, uint8_t *v
                       k_block_bytes >= 16 && (vbytes == 0 || vbytes >= 16);
     const int bytes[2] = {k_block_bytes, vbytes};
     auto inverse = [](int n) { return n < 2 ? 0u : (uint32_t)(((1ull << 32) + n - 1) / n); };
-    int token = 2 * 8 + 4 + 2 * 2;   // shared memory of a token
+    int token = 2 * 8 + 4 + 2 * 4;   // shared memory of a token
     for (int i = 0; i < 2; ++i) {
         a.bytes[i] = bytes[i];
         a.pieces[i] = bytes[i] ? (bytes[i] + 14 + 15) / 16 : 0;
@@ -553,20 +562,24 @@ extern "C" int tq_evict_compact(uint8_t *k_blocks, int k_block_bytes, uint8_t *v
     a.num_pages = num_pages;
     const int64_t rows = (int64_t)B * Hkv;
     const int m = keep < T ? keep : T;
-    // CTAs per row: while the GPU holds more (four per SM) and each still gets 64 tokens
+    // CTAs per row: while the GPU holds more (four per SM) and each still gets 64 tokens.  Few CTAs take an
+    // SM's shared memory and threads each, so that a row goes by in few steps (2 rows of 29281 to 22908: 66 us in eight steps, 29 in two)
     int C = 1;
     while (C < kMaxCluster && rows * C < 4 * (int64_t)sm_count() && m > C * 64) C *= 2;
+    int share = 4;   // CTAs per SM
+    while (share > 1 && rows * C * 2 <= (int64_t)sm_count() * share) share /= 2;
     // tokens of a CTA and step: the shared memory's worth at most, the steps of equal size, groups of eight
-    const int most = (kMovSmem / token) & ~7;
+    const int most = (kMovSmem * (4 / share) / token) & ~7;
     const int steps = (m + C * most - 1) / (C * most);
     a.tile = ((m + C * steps - 1) / (C * steps) + 7) & ~7;
     const size_t smem = (size_t)a.tile * token;
+    const int threads = kMovThreads / share;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     static int done[2][64] = {{0}};
     if (wide) {
-        if (set_smem_limit((const void *)compact_kernel<true>, kMovSmem, done[0]) != TQ_OK) return TQ_ERR_CUDA;
-        return launch_cluster(compact_kernel<true>, rows, C, kMovThreads, smem, st, a);
+        if (set_smem_limit((const void *)compact_kernel<true>, 4 * kMovSmem, done[0]) != TQ_OK) return TQ_ERR_CUDA;
+        return launch_cluster(compact_kernel<true>, rows, C, threads, smem, st, a);
     }
-    if (set_smem_limit((const void *)compact_kernel<false>, kMovSmem, done[1]) != TQ_OK) return TQ_ERR_CUDA;
-    return launch_cluster(compact_kernel<false>, rows, C, kMovThreads, smem, st, a);
+    if (set_smem_limit((const void *)compact_kernel<false>, 4 * kMovSmem, done[1]) != TQ_OK) return TQ_ERR_CUDA;
+    return launch_cluster(compact_kernel<false>, rows, C, threads, smem, st, a);
 }

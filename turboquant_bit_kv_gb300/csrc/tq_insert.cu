@@ -584,35 +584,6 @@ __global__ void __launch_bounds__(kThreads, 4) insert_kernel(const __grid_consta
         }
     }
 
-    static_assert(kThreads == 128, "a thread per cell");
-    {
-        uint32_t below = 0;
-        float edge = 3.0e38f;   // a cell without a boundary: v - edge < 0 for every v
-        for (int j = 0; j < levels - 1; ++j) {
-            const float v = sd.b[j] * kGrid;
-            const int at = (int)floorf(v + 64.5f);
-            if (at < tid) ++below;
-            if (at == tid) edge = v;
-        }
-        const uint2 e = make_uint2(__float_as_uint(edge), below + 1);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) sm.cells[tid * 16 + ((i + tid) & 15)] = e;
-    }
-    if (tid < 64) {   // word k of chunk c, thread t: elements 32 c + 8 t + 2 k, + 1
-        const int e = 2 * tid, c = e >> 5, th = (e >> 3) & 3, k = (e >> 1) & 3;
-        const uint32_t s2 = a.signs[e >> 5] >> (e & 31);
-        reinterpret_cast<uint32_t *>(&sm.flip[c][th])[k] = (s2 & 1u) << 15 | (s2 & 2u) << 30;
-    }
-    if (tid < 2) sm.listed[tid] = 0;
-    if (tid < kRopePairs && style != kRopeNone) {
-        const int pairs = rope.rot_dim / 2;
-        const int ea = style == kRopeAdjacent ? 2 * tid : tid, eb = style == kRopeAdjacent ? ea + 1 : tid + pairs;
-        const uint32_t differ = tid < pairs ? ((a.signs[ea >> 5] >> (ea & 31)) ^ (a.signs[eb >> 5] >> (eb & 31))) & 1u : 0u;
-        // (past the rotated elements: no angle)
-        sm.turn[tid] = tid < pairs ? rope.turn[tid] : 0;
-        sm.axis[tid] = (uint8_t)((tid < pairs ? rope.axis[tid] : 0) | differ << 2);
-    }
-
     // the 16 x 16 Hadamard matrix as B fragments: k = (thread t, j) in, n = (thread g / 2, j = 2 nt + g % 2)
     // out; j = 0, 1 in b[nt][0], 2, 3 in b[nt][1]; 1.0 of the products' type
     constexpr bool kBf = DT == TQ_BF16;
@@ -638,19 +609,54 @@ __global__ void __launch_bounds__(kThreads, 4) insert_kernel(const __grid_consta
         const int64_t tok0 = tile_of(unit);
         const int64_t my = tok0 + (lane & 15);
         const int64_t dst = my < a.n_tok ? a.dst[my] : -1;   // of token lane % 16
+        // positions of this thread's token (tid / 4 % 16) of tile v of the unit, on their way while the tables are
+        // built and the other warps finish
+        const int64_t first = tile_of(unit) - tile * kTok;
+        int64_t pos[3] = {0, 0, 0};
+        auto positions = [&](int v) {
+            const int64_t at = min64(first + v * kTok + ((tid >> 2) & 15), a.n_tok - 1);
+#pragma unroll
+            for (int i = 0; i < 3; ++i) pos[i] = a.pos[(i < rope.axes ? i : 0) * a.pos_axis + at];
+        };
+        if (style != kRopeNone) positions(0);
+        if (unit == cta) {
+            static_assert(kThreads == 128, "a thread per cell");
+            {
+                uint32_t below = 0;
+                float edge = 3.0e38f;   // a cell without a boundary: v - edge < 0 for every v
+                for (int j = 0; j < levels - 1; ++j) {
+                    const float v = sd.b[j] * kGrid;
+                    const int at = (int)floorf(v + 64.5f);
+                    if (at < tid) ++below;
+                    if (at == tid) edge = v;
+                }
+                const uint2 e = make_uint2(__float_as_uint(edge), below + 1);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) sm.cells[tid * 16 + ((i + tid) & 15)] = e;
+            }
+            if (tid < 64) {   // word k of chunk c, thread t: elements 32 c + 8 t + 2 k, + 1
+                const int e = 2 * tid, c = e >> 5, th = (e >> 3) & 3, k = (e >> 1) & 3;
+                const uint32_t s2 = a.signs[e >> 5] >> (e & 31);
+                reinterpret_cast<uint32_t *>(&sm.flip[c][th])[k] = (s2 & 1u) << 15 | (s2 & 2u) << 30;
+            }
+            if (tid < 2) sm.listed[tid] = 0;
+            if (tid < kRopePairs && style != kRopeNone) {
+                const int pairs = rope.rot_dim / 2;
+                const int ea = style == kRopeAdjacent ? 2 * tid : tid, eb = style == kRopeAdjacent ? ea + 1 : tid + pairs;
+                const uint32_t differ = tid < pairs ? ((a.signs[ea >> 5] >> (ea & 31)) ^ (a.signs[eb >> 5] >> (eb & 31))) & 1u : 0u;
+                // (past the rotated elements: no angle)
+                sm.turn[tid] = tid < pairs ? rope.turn[tid] : 0;
+                sm.axis[tid] = (uint8_t)((tid < pairs ? rope.axis[tid] : 0) | differ << 2);
+            }
+        }
         if (style != kRopeNone) {
             const bool adj = style == kRopeAdjacent;
-            const int64_t first = tile_of(unit) - tile * kTok;
             const int th = tid & 3;
             __syncthreads();   // the rope's copy is there, and the last unit's table no longer read
             for (int v = 0; v < a.tiles; ++v) {
-                // this thread's token of the tile, and its units tid / 64, + 2, ...
-                const int64_t at = min64(first + v * kTok + ((tid >> 2) & 15), a.n_tok - 1);
-                int64_t pos[3];
+                if (v > 0) positions(v);
 #pragma unroll
-                for (int i = 0; i < 3; ++i) pos[i] = a.pos[(i < rope.axes ? i : 0) * a.pos_axis + at];
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
+                for (int u = 0; u < 4; ++u) {   // its units tid / 64, + 2, ...
                     const int unit8 = 2 * u + (tid >> 6);
                     const int p0 = adj ? 16 * (unit8 >> 1) + 4 * th + 2 * (unit8 & 1) : 32 * (unit8 >> 2) + 8 * th + 2 * (unit8 & 3);
                     float s[2], c[2];
