@@ -100,11 +100,11 @@ KERNEL_SOURCES = {
     "ext_encode": ["tq_ext.cu", "tq_headdim_tc.cu", "tq_tc.cuh", "tq_device.cuh"],
     "append": ["tq_encode.cu", "tq_tc.cuh", "tq_device.cuh"],
     "prefill": ["tq_attn_prefill.cu", "tq_tc.cuh", "tq_device.cuh"],
-    "pair_attention": ["tq_attn.cu", "tq_attn.cuh", "tq_attn_mma.cu", "tq_attn_mma.h", "tq_attn_mma.cuh",
+    "pair_attention": ["tq_attn.cu", "tq_attn.cuh", "tq_attn_combine.cuh", "tq_attn_mma.cu", "tq_attn_mma.h", "tq_attn_mma.cuh",
                        "tq_attn_mma_k4.cu", "tq_attn_mma_k8.cu", "tq_device.cuh"],
-    "paged_attention": ["tq_attn.cu", "tq_attn.cuh", "tq_attn_mma.cu", "tq_attn_mma.h", "tq_attn_mma.cuh",
+    "paged_attention": ["tq_attn.cu", "tq_attn.cuh", "tq_attn_combine.cuh", "tq_attn_mma.cu", "tq_attn_mma.h", "tq_attn_mma.cuh",
                         "tq_attn_mma_k2.cu", "tq_attn_mma_k3.cu", "tq_attn_mma_k4.cu", "tq_device.cuh"],
-    "attention": ["tq_attn.cu", "tq_attn.cuh", "tq_attn_mma.cu", "tq_attn_mma.h", "tq_attn_mma.cuh",
+    "attention": ["tq_attn.cu", "tq_attn.cuh", "tq_attn_combine.cuh", "tq_attn_mma.cu", "tq_attn_mma.h", "tq_attn_mma.cuh",
                   "tq_attn_mma_k2.cu", "tq_attn_mma_k3.cu", "tq_attn_mma_k4.cu", "tq_attn_g1.cu",
                   "tq_attn_g2.cu", "tq_attn_g4.cu", "tq_attn_g8.cu", "tq_device.cuh"],
     "qjl": ["tq_qjl.cu", "tq_tc.cuh", "tq_codec.cu", "tq_device.cuh"],

@@ -524,7 +524,8 @@ int tq_rope_apply(const void *x, int dtype, int64_t n_tok, int heads, int64_t x_
  * then keys and values are encoded as by tq_encode_kv.  Codes and norms are
  * those of the definition evaluated in double precision (y rounded once to
  * float32 and compared with the float32 boundaries; the norm rounded once to
- * fp16), also next to a boundary.
+ * fp16): a coordinate less than about 1e-10 from a boundary may fall either
+ * way.
  *   k, v      device rows of dtype, head h of token n at n * tok_stride + h *
  *             head_stride elements (alignment as tq_rope_apply).  k with
  *             k_blocks, or v with v_blocks, may be NULL (then not written).
@@ -577,8 +578,9 @@ size_t tq_attn_weights_workspace_bytes(int B, int Hq, int Hkv, int T);
  *   workspace    >= tq_attn_weights_workspace_bytes(B, Hq, Hkv, T) bytes,
  *                16-byte aligned, clobbered; calls that overlap on the GPU
  *                must use different workspaces.
- * A query with non-finite scores gives NaN outputs and NaN weights.  Results
- * do not depend on timing.  Errors: TQ_ERR_ARG, TQ_ERR_UNSUPPORTED (turboq8,
+ * A query with a NaN or +inf score gives NaN outputs and NaN weights (of its
+ * KV head); a key of score -inf gets weight 0.  Results do not depend on
+ * timing.  Errors: TQ_ERR_ARG, TQ_ERR_UNSUPPORTED (turboq8,
  * Hq / Hkv > 8, page_tokens not a multiple of 32), TQ_ERR_ALIGN,
  * TQ_ERR_WORKSPACE, TQ_ERR_CUDA. */
 int tq_attn_decode_weights(const void *q, int q_dtype, const uint8_t *k_blocks, const tq_codebook *kcb,
@@ -612,7 +614,7 @@ int tq_evict_select(const float *weights, int64_t row_stride, const int32_t *seq
  *             [page_tokens] (any page_tokens).  No page may belong to two
  *             sequences.  v_blocks may be NULL.
  *   weights   as for tq_attn_decode_weights, or NULL.
- *   kept, new_lens   of tq_evict_select: ascending, kept[j] >= j.  An index
+ *   kept, new_lens   of tq_evict_select: strictly ascending.  An index
  *             outside j .. T - 1, or a table entry outside the pool, leaves
  *             its token where it is.
  * Errors: TQ_ERR_ARG, TQ_ERR_UNSUPPORTED, TQ_ERR_ALIGN, TQ_ERR_CUDA. */

@@ -238,6 +238,35 @@ def test_blocks_behind_the_sequence_do_not_matter(tq, kb, vb, G):
         assert all(torch.equal(a, b) for a, b in zip(*got))
 
 
+def test_attend_reports_a_wait_that_runs_out(tq):
+    """Copies that never land (the test hook): the call returns, the status says so, outputs and weights are marked,
+    and the next call is right again."""
+    rng = np.random.default_rng(2)
+    caches = [torch.from_numpy(cache_of((1, 2, 640), n, rng)[0]).cuda() for n in (4, 2)]
+    q = torch.from_numpy(rng.standard_normal((1, 8, 128))).float().cuda()
+    books, signs = [tq.tq_codebook_load(128, n) for n in (4, 2)], tq.tq_signs_from_seed(workloads.SIGN_SEED)
+    ws = torch.empty(tq.tq_attn_weights_workspace_bytes(1, 8, 2, 640), dtype=torch.uint8, device="cuda")
+
+    def call():
+        w, out = torch.zeros(1, 2, 640, device="cuda"), torch.zeros(1, 8, 128, device="cuda")
+        tq.tq_attn_decode_weights(q, caches[0], books[0], caches[1], books[1], w, out, ws, 640, SCALE, signs)
+        return w, out
+
+    tq.tq_device_status(clear=True)
+    w0, out0 = call()
+    assert tq.tq_device_status() == tq.TQ_OK
+    tq.tq_debug_drop_copies(True)
+    try:
+        w1, out1 = call()
+    finally:
+        tq.tq_debug_drop_copies(False)
+    assert tq.tq_device_status(clear=True) == tq.TQ_ERR_TIMEOUT
+    assert not torch.isfinite(out1).all() and not torch.isfinite(w1).all()
+    w2, out2 = call()
+    assert tq.tq_device_status() == tq.TQ_OK
+    assert torch.equal(w0, w2) and torch.equal(out0, out2)
+
+
 # ---------------------------------------------------------------- selection
 
 def select_reference(w, lens, keep, first, last):
@@ -359,6 +388,49 @@ def test_compact_leaves_what_it_cannot_place(tq):
     assert torch.equal(pool, want)
     tq.tq_evict_compact(pool, None, k2, torch.tensor([-3], dtype=torch.int32, device="cuda"), 16, block_table=table)
     assert torch.equal(pool, want)
+
+
+def test_compact_of_a_repeated_index(tq):
+    """The same index twice (not what the selection gives): both tokens take its block."""
+    cache = torch.randint(0, 256, (1, 1, 2000, 66), dtype=torch.uint8, device="cuda")
+    before = cache.clone()
+    kept = torch.sort(torch.randint(700, 2000, (1, 1, 600), device="cuda")).values.int()
+    kept[0, 0, 100:103] = kept[0, 0, 100]
+    tq.tq_evict_compact(cache, None, kept, torch.tensor([600], dtype=torch.int32, device="cuda"), 2000)
+    assert torch.equal(cache[0, 0, :600], before[0, 0][kept[0, 0].long()])
+    assert torch.equal(cache[0, 0, 600:], before[0, 0, 600:])
+
+
+def test_calls_on_two_streams_at_once(tq):
+    """Two streams, each with its own workspace and cache, give what one stream gives."""
+    rng = np.random.default_rng(8)
+    T, keep = 3001, 1500
+    blocks = [[torch.from_numpy(cache_of((2, 4, T + 7), n, rng)[0]).cuda() for n in (4, 2)] for _ in range(2)]
+    qs = [torch.from_numpy(rng.standard_normal((2, 16, 128))).float().cuda() for _ in range(2)]
+    books, signs = [tq.tq_codebook_load(128, n) for n in (4, 2)], tq.tq_signs_from_seed(workloads.SIGN_SEED)
+
+    def chain(i, stream):
+        with torch.cuda.stream(stream):
+            k, v = (c.clone() for c in blocks[i])
+            w, out = torch.zeros(2, 4, T, device="cuda"), torch.empty(2, 16, 128, device="cuda")
+            ws = torch.empty(tq.tq_attn_weights_workspace_bytes(2, 16, 4, T), dtype=torch.uint8, device="cuda")
+            kept = torch.empty(2, 4, keep, dtype=torch.int32, device="cuda")
+            new = torch.empty(2, dtype=torch.int32, device="cuda")
+            for _ in range(3):
+                tq.tq_attn_decode_weights(qs[i], k, books[0], v, books[1], w, out, ws, T, SCALE, signs)
+                tq.tq_evict_select(w, kept, new, T, 4, 100)
+                tq.tq_evict_compact(k, v, kept, new, T, weights=w)
+        return k, v, w, out, kept
+
+    alone = [chain(i, torch.cuda.current_stream()) for i in range(2)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    both = [chain(i, streams[i]) for i in range(2)]
+    torch.cuda.synchronize()
+    for a, b in zip(alone, both):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
 
 
 # ---------------------------------------------------------------- together

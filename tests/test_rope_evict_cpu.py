@@ -231,6 +231,8 @@ def test_binding_refusals(tq):
                             (x, x, blocks, blocks, dst[:2])):
         with pytest.raises(ValueError):
             tq.tq_insert_kv(k, v, pos, rope, cb, cb, signs, kb, vb, d, 4)
+    with pytest.raises(ValueError):
+        tq.tq_insert_kv(x, None, pos, rope, None, None, signs, blocks, None, dst, 4)
     q = torch.zeros(2, 8, 128)
     cache = torch.zeros(2, 2, 16, 66, dtype=torch.uint8)
     w = torch.zeros(2, 2, 16)

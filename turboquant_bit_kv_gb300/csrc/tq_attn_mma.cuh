@@ -754,6 +754,15 @@ __global__ void __launch_bounds__(Cfg<KB, VB, QJL, NT, WIDE>::kThreads, Cfg<KB, 
                 phase ^= 1u << cst;
             } else {
                 cp_async_wait<0>();
+                if constexpr (!C::kRawV) {
+                    // the last 16-byte piece of a partial chunk brings in up to 15 bytes of the block behind the
+                    // sequence: its norm may be anything, NaN too, and must not meet that token's P of 0
+                    const int n = L - ci * kMmaChunk;
+                    __syncwarp();
+                    if (lane == 0 && n < kMmaChunk)
+                        *reinterpret_cast<unsigned short *>(smem + C::kSmemStages + (warp * kS + cst) * C::kWarpStage +
+                                                            C::kKStage + n * C::kVBytes) = 0;
+                }
             }
             __syncwarp();
             const int nvalid = min(kMmaChunk, L - ci * kMmaChunk);
@@ -909,10 +918,8 @@ __global__ void __launch_bounds__(Cfg<KB, VB, QJL, NT, WIDE>::kThreads, Cfg<KB, 
                 float nva = 1.f, nvb = 1.f;
                 if constexpr (!C::kRawV) {
                     constexpr float vf = VB == 8 ? 1.f / 255.f : 1.f;
-                    // (the last 16-byte piece of a partial chunk brings in up to 15 bytes of the block behind the
-                    // sequence: its norm may be anything, NaN too, and must not meet that token's P of 0)
-                    nva = ta < nvalid ? __half2float(__ushort_as_half((unsigned short)lds_u16(vs_s + ta * C::kVBytes))) * vf : 0.f;
-                    nvb = tb < nvalid ? __half2float(__ushort_as_half((unsigned short)lds_u16(vs_s + tb * C::kVBytes))) * vf : 0.f;
+                    nva = __half2float(__ushort_as_half((unsigned short)lds_u16(vs_s + ta * C::kVBytes))) * vf;
+                    nvb = __half2float(__ushort_as_half((unsigned short)lds_u16(vs_s + tb * C::kVBytes))) * vf;
                 }
                 // B fragments of P (8 x 8 blocks of token rows g / g + 8, transposed): per n-tile, or
                 // (kH8) index 0: the hi parts of the 8 heads, 1: the lo parts

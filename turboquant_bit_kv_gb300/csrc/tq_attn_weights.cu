@@ -262,9 +262,9 @@ extern "C" int tq_attn_decode_weights(const void *q, int q_dtype, const uint8_t 
         !aligned(workspace, 16) || !aligned(weights, 4) || !aligned(seq_lens, 4) || !aligned(block_table, 4))
         return TQ_ERR_ALIGN;
     if (workspace_bytes < tq_attn_weights_workspace_bytes(B, Hq, Hkv, T)) return TQ_ERR_WORKSPACE;
-    // weights CTAs per segment: about eight per SM, each of kWeightsTokens tokens at least (every one of
+    // weights CTAs per segment: about 32 per SM, each of kWeightsTokens tokens at least (every one of
     // them works out its heads' maximum and sum)
-    const int64_t segs = (int64_t)B * Hkv, wanted = ((int64_t)sm_count() * 8 + segs - 1) / segs;
+    const int64_t segs = (int64_t)B * Hkv, wanted = ((int64_t)sm_count() * 32 + segs - 1) / segs;
     const int most = (T + kWeightsTokens - 1) / kWeightsTokens;
     int parts = (int)(wanted < most ? wanted : most);
     const int per = ((T + parts - 1) / parts + kMmaChunk - 1) / kMmaChunk * kMmaChunk;

@@ -509,7 +509,8 @@ def tq_insert_kv(k, v, pos, rope, kcb, vcb, signs, k_blocks, v_blocks, dst, dst_
         raise ValueError("tq_insert_kv: dst int64 [tokens] expected")
     strides, blocks = [], None
     for rows, cache, cb in ((k, k_blocks, kcb), (v, v_blocks, vcb)):
-        _need((rows is None) == (cache is None), "tq_insert_kv: rows and their blocks come together")
+        if (rows is None) != (cache is None) or (rows is not None and cb is None):
+            raise ValueError("tq_insert_kv: rows, their blocks and their codebook come together")
         if rows is None:
             strides += [0, 0]
             continue
