@@ -323,10 +323,13 @@ __global__ void __launch_bounds__(kMovThreads, 1) compact_kernel(const __grid_co
     const int64_t row = blockIdx.x / C;
     const int b = (int)(row / a.Hkv), h = (int)(row % a.Hkv);
     const int32_t *kept = a.kept + row * a.keep;
+    const int per = C * a.tile;
+    // this thread's first index of a step, requested one step ahead (the first along with the length)
+    auto index_at = [&](int j) { return j < a.keep ? kept[j] : 0; };
+    int ahead = index_at(rank * a.tile + tid);
     const int nl = a.new_lens[b];
     const int n = nl < 0 ? 0 : (nl > a.keep ? a.keep : (nl > a.T ? a.T : nl));
     float *w = a.weights ? a.weights + row * a.w_stride : nullptr;
-    const int per = C * a.tile;
     // ascending indices that end where they would without a gap: nothing moves
     const int steps = n == 0 || kept[n - 1] == n - 1 ? 0 : (n + per - 1) / per;
 
@@ -340,11 +343,11 @@ __global__ void __launch_bounds__(kMovThreads, 1) compact_kernel(const __grid_co
     for (int t = 0; t < steps; ++t) {
         const int base = t * per + rank * a.tile;
         const int cnt = max(0, min(a.tile, n - base));
-        const bool moves = cnt > 0 && kept[base + cnt - 1] != base + cnt - 1;
+        const bool moves = cnt > 0 && kept[base + cnt - 1] != base + cnt - 1;   // (a step in which nothing moves)
         if (moves) {
             for (int i = tid; i < cnt; i += threads) {
                 const int j = base + i;
-                int from = kept[j];
+                int from = i == tid ? ahead : kept[j];
                 if (from < j || from >= a.T) from = j;   // not a place to take from: it stays
                 const int64_t own = slot(j);
                 int64_t s = from == j ? own : slot(from);
@@ -358,8 +361,9 @@ __global__ void __launch_bounds__(kMovThreads, 1) compact_kernel(const __grid_co
                 for (int side = 0; side < 2; ++side)
                     place[side * a.tile + i] =
                         (uint32_t)(i * a.pitch[side] + (WIDE ? (int)((uint32_t)s * (uint32_t)a.bytes[side] & 15u) : 0));
-                if (w) sw[i] = w[own < 0 ? j : from];
+                reinterpret_cast<int *>(sw)[i] = own < 0 ? j : from;   // (its weight: once the blocks are requested)
             }
+            ahead = index_at(base + per + tid);
             __syncthreads();
             uint8_t *stage = stage0;
 #pragma unroll
@@ -402,6 +406,10 @@ __global__ void __launch_bounds__(kMovThreads, 1) compact_kernel(const __grid_co
                 }
                 stage += a.tile * a.pitch[side];
             }
+            if (w)
+                for (int i = tid; i < cnt; i += threads) sw[i] = w[reinterpret_cast<const int *>(sw)[i]];
+        } else {
+            ahead = index_at(base + per + tid);
         }
         cl.sync();   // every CTA has read its blocks of this step
         if (moves) {
