@@ -568,7 +568,7 @@ size_t tq_attn_weights_workspace_bytes(int B, int Hq, int Hkv, int T);
  *   q, k_blocks, v_blocks, seq_lens, scale, T   as tq_attn_decode.
  *   block_table  NULL: caches [B][Hkv][T_cap] (T_cap a multiple of 8); else
  *                device int32 [B][max_pages] and pools [pages][Hkv]
- *                [page_tokens], page_tokens a multiple of 32, as for
+ *                [page_tokens], page_tokens a multiple of 8, as for
  *                tq_attn_decode_paged (T_cap unused).
  *   weights      device float32, row (b, h) at (b * Hkv + h) *
  *                weights_row_stride, weights_row_stride >= T.
@@ -578,10 +578,12 @@ size_t tq_attn_weights_workspace_bytes(int B, int Hq, int Hkv, int T);
  *   workspace    >= tq_attn_weights_workspace_bytes(B, Hq, Hkv, T) bytes,
  *                16-byte aligned, clobbered; calls that overlap on the GPU
  *                must use different workspaces.
+ * Weights of a prompt: a call per query token whose weights are to count (the
+ * last ones, usually), seq_lens that token's position + 1.
  * A query with a NaN or +inf score gives NaN outputs and NaN weights (of its
  * KV head); a key of score -inf gets weight 0.  Results do not depend on
  * timing.  Errors: TQ_ERR_ARG, TQ_ERR_UNSUPPORTED (turboq8,
- * Hq / Hkv > 8, page_tokens not a multiple of 32), TQ_ERR_ALIGN,
+ * Hq / Hkv > 8, page_tokens not a multiple of 8), TQ_ERR_ALIGN,
  * TQ_ERR_WORKSPACE, TQ_ERR_CUDA. */
 int tq_attn_decode_weights(const void *q, int q_dtype, const uint8_t *k_blocks, const tq_codebook *kcb,
                            const uint8_t *v_blocks, const tq_codebook *vcb, const int32_t *block_table, int max_pages,

@@ -151,6 +151,14 @@ def test_attend_lengths(tq, T, B, Hkv, page):
     run_attend(tq, B, 4 * Hkv, Hkv, T, 3, 3, page, [T + 100] + [T // 2] * (B - 1), 0.0, "bf16", "f32", T + 1)
 
 
+@pytest.mark.parametrize("page", [8, 16, 24, 40, 48, 72, 96])
+@pytest.mark.parametrize("kb,vb,G", [(4, 2, 4), (3, 3, 7), (2, 4, 1)])
+def test_attend_page_sizes(tq, page, kb, vb, G):
+    """Pages that end inside a chunk of 32 tokens; lengths at, before and after the ends of pages and chunks."""
+    lens = [page, 8 * page, page - 1, page + 1, 333, 32, 31, 0]
+    run_attend(tq, 8, 2 * G, 2, 8 * page + 5, kb, vb, page, lens, 0.5, "bf16", "f32", page + kb)
+
+
 @pytest.mark.parametrize("B,Hkv,page", [(33, 2, 0), (70, 1, 32), (128, 1, 0)])
 def test_attend_many_sequences(tq, B, Hkv, page):
     """Batches over 32 sequences, most of them short or empty, one long: the work is split over live chunks."""

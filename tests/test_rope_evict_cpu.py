@@ -157,7 +157,7 @@ def test_attend_refusals(tq):
         assert _attend(tq, **kw) == ARG, kw
     for kw in (dict(qd=9), dict(od=9), dict(Hq=18, bytes=1 << 30), dict(kcb=tq.tq_codebook_load(128, 8)),
                dict(vcb=tq.tq_codebook_load(128, 8)), dict(vcb=tq.tq_codebook_load(96, 2)),
-               dict(table=A, mp=8, page=16), dict(table=A, mp=4, page=40)):
+               dict(table=A, mp=8, page=12), dict(table=A, mp=4, page=42)):
         assert _attend(tq, **kw) == UNSUPPORTED, kw
     for kw in (dict(k=ODD), dict(v=ODD), dict(out=ODD), dict(work=ODD), dict(w=ODD), dict(lens=ODD),
                dict(table=ODD, mp=2, page=32), dict(q=P((1 << 20) + 1))):

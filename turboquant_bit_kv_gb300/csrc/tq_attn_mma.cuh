@@ -582,10 +582,55 @@ __global__ void __launch_bounds__(Cfg<KB, VB, QJL, NT, WIDE>::kThreads, Cfg<KB, 
     uint32_t bulk_mask = 0;    // bit s: stage s was filled by bulk copies
     bool copies_ok = true;
 
+    // a chunk that pages of 8 k tokens cut into up to four pieces: each a multiple of 8 tokens, so of 16 bytes
+    auto issue_pieces = [&](int buf, int j, int t0, int n) {
+        const uint32_t dk = stage_s + buf * C::kWarpStage, dv = dk + C::kKStage;
+        auto slot = [&](int t) {   // of token t in the pools
+            const int pg = t / a.page;
+            return ((int64_t)a.table[(int64_t)(j / a.Hkv) * a.max_pages + pg] * a.Hkv + j % a.Hkv) * a.page + (t - pg * a.page);
+        };
+        if (n == kMmaChunk) {
+            const uint32_t bar = bar_s + 8 * buf;
+            if (lane == 0) mbar_expect_tx(bar, C::kChunkBytes);
+            __syncwarp();
+            const int first = a.page - t0 % a.page;   // tokens to the end of the chunk's first page
+            const int s = lane == 0 ? t0 : t0 + first + (lane - 1) * a.page;
+            if (s < t0 + kMmaChunk) {
+                const int len = min(lane == 0 ? first : a.page, t0 + kMmaChunk - s);
+                const int64_t at = slot(s);
+                bulk_g2s(dk + (s - t0) * C::kKBytes, a.k + at * C::kKBytes, len * C::kKBytes, bar);
+                bulk_g2s(dv + (s - t0) * C::kVBytes, a.v + at * C::kVBytes, len * C::kVBytes, bar);
+            }
+            bulk_mask |= 1u << buf;
+            return;
+        }
+        bulk_mask &= ~(1u << buf);
+        auto part = [&](uint32_t dst, const uint8_t *pool, int bytes, int stage) {
+            const int live = (n * bytes + 15) >> 4;
+            for (int q = lane; q < stage / 16; q += 32) {
+                const uint8_t *src = pool;
+                if (q < live) {
+                    const int t = t0 + 16 * q / bytes, ps = max(t0, t / a.page * a.page);   // token, its piece's first
+                    src = pool + slot(ps) * bytes + (16 * q - (ps - t0) * bytes);
+                }
+                cp16_zfill(dst + 16 * q, src, q < live);
+            }
+        };
+        part(dk, a.k, C::kKBytes, C::kKStage);
+        part(dv, a.v, C::kVBytes, C::kVStage);
+        cp_async_commit();
+    };
+
     // stage of chunk ci of segment j: K blocks | V blocks (raw: 272-byte rows) | sign rows | residual norms
     auto issue = [&](int buf, int j, int ci, int L) {
         const int t0 = ci * kMmaChunk;
         const int n = min(kMmaChunk, L - t0);
+        if constexpr (PAGED && SCORES) {
+            if (a.page & 31) {
+                issue_pieces(buf, j, t0, n);
+                return;
+            }
+        }
         const int64_t row0 = PAGED ? paged_row0(a, j, t0) : (int64_t)j * a.T_cap;
         const uint8_t *kbase = a.k + row0 * C::kKBytes;
         const uint8_t *vbase = a.v + row0 * C::kVBytes;

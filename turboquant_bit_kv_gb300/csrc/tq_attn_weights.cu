@@ -251,7 +251,7 @@ extern "C" int tq_attn_decode_weights(const void *q, int q_dtype, const uint8_t 
     const bool paged = block_table != nullptr;
     if (paged) {
         if (max_pages <= 0 || page_tokens <= 0 || (int64_t)max_pages * page_tokens < T) return TQ_ERR_ARG;
-        if (page_tokens & 31) return TQ_ERR_UNSUPPORTED;
+        if (page_tokens & 7) return TQ_ERR_UNSUPPORTED;
     } else if (T > T_cap || (T_cap & 7)) {
         return TQ_ERR_ARG;
     }

@@ -62,7 +62,7 @@
 namespace tq {
 namespace {
 
-constexpr int kTok = 16;             // tokens of a CTA
+constexpr int kTok = 16;             // tokens of a tile
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr float kGrid = 63.f;        // cells per unit of y
