@@ -239,3 +239,64 @@ def test_insert_consecutive_slots_at_every_offset(tq):
             dst = torch.arange(64, device="cuda") + off
             tq.tq_insert_kv(x, None, None, None, cb, None, signs, cache, None, dst, 80)
             check_side(tq, cache, x.double().cpu().numpy(), bits, dst.cpu().numpy(), 80, before)
+
+
+def inserted(tq, k, v, pos, rope, bits, dst, heads, T_cap, cuts):
+    """Caches (filled with 171) after inserting the tokens in calls cut at cuts."""
+    caches = [torch.full((heads * T_cap, 2 + 16 * b), 171, dtype=torch.uint8, device="cuda") for b in bits]
+    books = [tq.tq_codebook_load(128, b) for b in bits]
+    signs = tq.tq_signs_from_seed(workloads.SIGN_SEED)
+    for i, j in zip(cuts, cuts[1:]):
+        p = None if rope is None else pos[:, i:j].contiguous()
+        tq.tq_insert_kv(None if k is None else k[i:j], None if v is None else v[i:j], p, rope, books[0], books[1], signs,
+                        None if k is None else caches[0], None if v is None else caches[1], dst[i:j], T_cap)
+    return caches
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("case", range(1 + len(ROPES)))
+def test_insert_of_many_tokens_equals_inserts_of_few(tq, dtype, case):
+    """A call's blocks do not depend on its size (large and small calls take
+    different kernels), whatever the rows hold."""
+    n, heads, T_cap = 8209, 5, 8300
+    bits = [(4, 2), (3, 3), (2, 4)][case % 3]
+    rope = None if case == 0 else tq.tq_rope_load(**ROPES[case - 1])
+    g = torch.Generator(device="cuda").manual_seed(case)
+    loud = torch.exp(torch.randn(2 * heads, 128, generator=g, device="cuda"))
+    kv = (torch.randn(n, 2 * heads, 128, generator=g, device="cuda") * loud).to(DT[dtype])
+    kv[7::500] = 0
+    kv[8::500, 0, 3] = float("inf")
+    kv[9::500, 6, 100] = float("nan")
+    kv[10::500] *= 2.0**-14 if dtype == "f16" else 2.0**-60
+    kv[11::500, :, 1:] = 0
+    kv[14::500] = torch.randint(-3, 4, kv[14::500].shape, generator=g, device="cuda").to(DT[dtype])
+    if dtype != "f16":
+        kv[12::500] *= 2.0**-70
+        kv[13::500] *= 2.0**90
+    pos = torch.randint(-10**6, 10**6, (3, n), generator=g, device="cuda")[:1 if rope is None else rope.axes].contiguous()
+    dst = torch.randperm(T_cap, generator=g, device="cuda")[:n]
+    dst[::9] = -1
+    dst[5] = 10**9
+    k, v = kv[:, :heads], kv[:, heads:]
+    cuts = [0, 1, 3, 19, 36, 500, 1000, 2001, 4000, 6000, 8000, n]
+    one = inserted(tq, k, v, pos, rope, bits, dst, heads, T_cap, [0, n])
+    for a, b in zip(one, inserted(tq, k, v, pos, rope, bits, dst, heads, T_cap, cuts)):
+        assert torch.equal(a, b)
+    assert torch.equal(one[0], inserted(tq, k, None, pos, rope, bits, dst, heads, T_cap, [0, n])[0])
+    assert torch.equal(one[1], inserted(tq, None, v, pos, rope, bits, dst, heads, T_cap, cuts)[1])
+
+
+@pytest.mark.parametrize("n", [40, 6000])
+@pytest.mark.parametrize("dtype,bits,ones", [("bf16", 4, 128), ("f16", 3, 6), ("f32", 2, 2), ("bf16", 2, 32)])
+def test_insert_of_coordinates_on_a_boundary(tq, n, dtype, bits, ones):
+    """Rows of a few small integers: many coordinates are exactly 0, a
+    boundary of every codebook (64-bit sums of integers are exact)."""
+    heads = 5
+    g = torch.Generator(device="cuda").manual_seed(ones)
+    x = torch.zeros(n, heads, 128, device="cuda")
+    x[..., :ones] = torch.randint(-2, 3, (n, heads, ones), generator=g, device="cuda").float()
+    x = x.gather(2, torch.argsort(torch.rand(n, heads, 128, generator=g, device="cuda"), -1))
+    dst = torch.arange(n, device="cuda")
+    cache = inserted(tq, x.to(DT[dtype]), None, None, None, (bits, bits), dst, heads, n, [0, n])[0]
+    before = torch.full_like(cache, 171)
+    check_side(tq, cache, x.double().cpu().numpy(), bits, dst.cpu().numpy(), n, before)

@@ -79,6 +79,12 @@ constexpr float kEps = 1.25e-6f * kGrid * 0.08838834764831845f;
 // roundings in the same rows 1.1e-7 of the norm, two units at most).
 constexpr uint32_t kTieUlps = 5;
 
+// Rows per SM, keys and values together, up to which a warp takes a row
+// (insert_few_kernel): bfloat16 keys with rotary positions in 4 bits and values
+// in 2, 8 heads, by tokens, us against insert_kernel's: 16 3.4 / 7.6, 256 6.9 /
+// 15.0, 1024 11.8 / 16.1, 2048 (216 rows per SM) 18.6 / 16.3, 8192 61.5 / 28.7.
+constexpr int kFewRows = 160;
+
 enum { kRopeNone = 0, kRopeHalf1, kRopeHalf2, kRopeHalf3, kRopeHalf4, kRopeAdjacent };
 
 struct Side {
@@ -903,6 +909,293 @@ __global__ void __launch_bounds__(kThreads, 4) insert_kernel(const __grid_consta
                    stage);
 }
 
+// Few rows: latency is what counts.  A warp per row, four elements per lane,
+// the rotary partner and five of the transform's seven stages by shuffles; all
+// loads are under way while the CTA fills the quantiser's cells (one copy: a
+// warp's few lookups can bear the conflicts).  The whole call is then launch,
+// one memory latency and about 400 instructions, 3.4 us for 16 tokens where
+// insert_kernel's tile takes 7.6.  Six CTAs per SM in all (1024 tokens: 11.8 us;
+// four the same, eight 12.7, one CTA for every four rows 18.0).  A row that
+// float32 does not decide adds 1.2 us, 1.7 with rotary positions (near_row:
+// 4.8).
+struct SmallShared {
+    uint2 cells[128];                         // as Shared's, one copy
+    alignas(16) ff again[kWarps][kD];         // values of a row taken again
+};
+
+// The few coordinates of a row that float32 does not decide, in double-float:
+// coordinate j is the sum of +-x, so it costs one reduction and no transform.
+// near: bits i of the lane's elements 4 lane + i to decide, cell[i] the number
+// of boundaries below their cells.  Returns the lane's codes; the norm is
+// rounded again as well.
+template <int DT>
+__device__ __noinline__ uint32_t decide_few(float x0, float x1, float x2, float x3, uint32_t near, uint32_t cell,
+                                            uint32_t code, uint64_t angle0, uint64_t angle1, int partner, uint32_t flip,
+                                            const Side &sd, uint8_t *block) {
+    const int lane = threadIdx.x & 31;
+    const float x[4] = {x0, x1, x2, x3};
+    ff r[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = ff_of(x[i]);
+    if (sd.style != kRopeNone) {
+        ff s[2], c[2];
+#pragma unroll 1
+        for (int z = 0; z < 2; ++z) {
+            ff sz, cz;
+            rope_sincos_ff(z ? angle1 : angle0, sz, cz);
+            if (z) s[1] = sz, c[1] = cz;
+            else s[0] = sz, c[0] = cz;
+        }
+        const bool adj = sd.style == kRopeAdjacent, upper = partner < lane;
+        if (adj) {
+            if (partner >= 0)
+#pragma unroll
+                for (int z = 0; z < 2; ++z) {
+                    r[2 * z] = ff_add(ff_scale(c[z], x[2 * z]), ff_scale(s[z], -x[2 * z + 1]));
+                    r[2 * z + 1] = ff_add(ff_scale(c[z], x[2 * z + 1]), ff_scale(s[z], x[2 * z]));
+                }
+        } else {
+            const int from = partner < 0 ? lane : partner;
+            ff so[2], co[2];
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+                so[z] = {__shfl_sync(0xffffffffu, s[z].h, from), __shfl_sync(0xffffffffu, s[z].l, from)};
+                co[z] = {__shfl_sync(0xffffffffu, c[z].h, from), __shfl_sync(0xffffffffu, c[z].l, from)};
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float o = __shfl_sync(0xffffffffu, x[i], from);
+                const bool mine = (i >= 2) == upper;
+                if (partner >= 0)
+                    r[i] = ff_add(ff_scale(mine ? c[i & 1] : co[i & 1], x[i]), ff_scale(mine ? s[i & 1] : so[i & 1], upper ? o : -o));
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if ((flip >> i) & 1u) r[i] = ff_neg(r[i]);
+    ff squares = ff_mul(r[0], r[0]);
+#pragma unroll
+    for (int i = 1; i < 4; ++i) squares = ff_add(squares, ff_mul(r[i], r[i]));
+    uint32_t who = __ballot_sync(0xffffffffu, near != 0);
+    bool first = true;
+    do {
+        const int src = who ? __ffs(who) - 1 : 0;
+        const uint32_t bits = __shfl_sync(0xffffffffu, near, src);
+        const int e = bits ? __ffs(bits) - 1 : 0, j = 4 * src + e;
+        ff v = ff_of(0.f), ss = squares;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v = ff_add(v, __popc((4 * lane + i) & j) & 1 ? ff_neg(r[i]) : r[i]);
+#pragma unroll 1
+        for (int m = 1; m < 32; m <<= 1) {
+            v = ff_add(v, shfl_(v, m));
+            ss = ff_add(ss, shfl_(ss, m));
+        }
+        const ff nrm = ff_sqrt(ss);
+        if (first && lane == 0) *reinterpret_cast<uint16_t *>(block) = ff_half(nrm);
+        first = false;
+        if (lane == src && near) {   // y >= b as in near_row
+            const int below = (int)((cell >> (8 * e)) & 0xFFu);
+            const float b = sd.b[below];
+            const uint32_t w = __float_as_uint(b);
+            const float under = b == 0.f ? 0.f : __uint_as_float(b > 0.f ? w - 1 : w + 1);
+            const ff k = ff_mul(nrm, ff_of(11.313708498984761f, (float)(11.313708498984761 - (double)11.313708498984761f)));
+            const ff edge = ff_mul(k, ff_of(b, b == 0.f ? 0.f : 0.5f * (under - b)));
+            const uint32_t c = (uint32_t)below + (v.h > edge.h || (v.h == edge.h && v.l >= edge.l) ? 1u : 0u);
+            code = (code & ~(0xFFu << (8 * e))) | c << (8 * e);
+            near &= near - 1;
+        }
+        who = __ballot_sync(0xffffffffu, near != 0);
+    } while (who);
+    return code;
+}
+
+template <int DT>
+__global__ void __launch_bounds__(kThreads) insert_few_kernel(const __grid_constant__ tq_rope rope,
+                                                              const __grid_constant__ InsertArgs a) {
+    __shared__ SmallShared sm;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const Side &sd = a.side[a.side[0].x ? blockIdx.y : 1];
+    const int bits = sd.bits, style = sd.style;
+    const uint32_t rows = (uint32_t)a.n_tok * (uint32_t)a.heads;
+    uint32_t id = blockIdx.x * kWarps + warp;
+    // what a row needs from memory, on its way while the cells are filled
+    const uint8_t *row = nullptr;
+    int64_t tok = 0, dst = -1, pos[3] = {0, 0, 0};
+    int head = 0;
+    uint4 raw = make_uint4(0, 0, 0, 0);
+    auto load = [&]() {
+        const uint32_t n = id / (uint32_t)a.heads;
+        tok = n;
+        head = (int)(id - n * (uint32_t)a.heads);
+        row = sd.x + tok * sd.tok + head * sd.head;
+        if constexpr (DT == TQ_F32) {
+            raw = __ldcs(reinterpret_cast<const uint4 *>(row) + lane);
+        } else {
+            const uint2 v = __ldcs(reinterpret_cast<const uint2 *>(row) + lane);
+            raw.x = v.x;
+            raw.y = v.y;
+        }
+        dst = a.dst[tok];
+        if (style != kRopeNone)
+#pragma unroll
+            for (int i = 0; i < 3; ++i) pos[i] = a.pos[(i < rope.axes ? i : 0) * a.pos_axis + tok];
+    };
+    if (id < rows) load();
+
+    // the two pairs of this lane's sines: adjacent elements, or halves, where the lane of the upper half (its
+    // partner's elements + rot_dim / 2) takes the second two of the four that both need
+    const int span = style == kRopeNone ? 0 : rope.rot_dim / 8;   // lanes of half the rotated elements
+    const bool turned = lane < 2 * span, upper = lane >= span, adj = style == kRopeAdjacent;
+    const int partner = !turned || adj ? lane : upper ? lane - span : lane + span;
+    uint64_t turn[2] = {0, 0};
+    int axis[2] = {0, 0};
+    if (turned) {
+        const int p0 = adj ? 2 * lane : upper ? 4 * (lane - span) + 2 : 4 * lane;
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+            turn[z] = rope.turn[p0 + z];
+            axis[z] = rope.axis[p0 + z];
+        }
+    }
+    const uint32_t flip = a.signs[lane >> 3] >> (4 * (lane & 7));
+    {
+        uint32_t below = 0;
+        float edge = 3.0e38f;   // as in insert_kernel
+        for (int j = 0; j < (1 << bits) - 1; ++j) {
+            const float v = sd.b[j] * kGrid;
+            const int at = (int)floorf(v + 64.5f);
+            if (at < tid) ++below;
+            if (at == tid) edge = v;
+        }
+        sm.cells[tid] = make_uint2(__float_as_uint(edge), below + 1);
+    }
+    __syncthreads();
+
+    for (; id < rows; id += gridDim.x * kWarps) {
+        if (row == nullptr) load();
+        const int64_t slot = dst < 0 ? -1 : dst + head * a.dst_head;
+        if (slot >= 0 && slot < sd.n_blocks) {
+            float x[4];
+            if constexpr (DT == TQ_F32) {
+                x[0] = __uint_as_float(raw.x);
+                x[1] = __uint_as_float(raw.y);
+                x[2] = __uint_as_float(raw.z);
+                x[3] = __uint_as_float(raw.w);
+            } else if constexpr (DT == TQ_BF16) {
+                x[0] = bf16_bits_lo(raw.x);
+                x[1] = bf16_bits_hi(raw.x);
+                x[2] = bf16_bits_lo(raw.y);
+                x[3] = bf16_bits_hi(raw.y);
+            } else {
+                const float2 p = __half22float2(*reinterpret_cast<const __half2 *>(&raw.x));
+                const float2 q = __half22float2(*reinterpret_cast<const __half2 *>(&raw.y));
+                x[0] = p.x;
+                x[1] = p.y;
+                x[2] = q.x;
+                x[3] = q.y;
+            }
+            const float4 in = make_float4(x[0], x[1], x[2], x[3]);
+            uint64_t angle[2] = {0, 0};
+            if (style != kRopeNone) {
+                float s[2], c[2];
+#pragma unroll
+                for (int z = 0; z < 2; ++z) {
+                    angle[z] = rope_turns(turn[z], axis[z] == 0 ? pos[0] : axis[z] == 1 ? pos[1] : pos[2]);
+                    rope_sincos(angle[z], s[z], c[z]);
+                }
+                if (adj) {
+                    if (turned)
+#pragma unroll
+                        for (int z = 0; z < 2; ++z) {
+                            const float xa = x[2 * z], xb = x[2 * z + 1];
+                            x[2 * z] = fmaf(xa, c[z], -(xb * s[z]));
+                            x[2 * z + 1] = fmaf(xb, c[z], xa * s[z]);
+                        }
+                } else {
+                    float so[2], co[2], o[4];
+#pragma unroll
+                    for (int z = 0; z < 2; ++z) {
+                        so[z] = __shfl_sync(0xffffffffu, s[z], partner);
+                        co[z] = __shfl_sync(0xffffffffu, c[z], partner);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) o[i] = __shfl_sync(0xffffffffu, x[i], partner);
+                    if (turned)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const bool mine = (i >= 2) == upper;
+                            const float si = mine ? s[i & 1] : so[i & 1], ci = mine ? c[i & 1] : co[i & 1];
+                            x[i] = fmaf(x[i], ci, o[i] * (upper ? si : -si));
+                        }
+                }
+            }
+            float ss = fmaf(x[0], x[0], x[1] * x[1]) + fmaf(x[2], x[2], x[3] * x[3]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] = __uint_as_float(__float_as_uint(x[i]) ^ ((flip >> i) << 31));
+            {
+                const float p = x[0] + x[1], q = x[0] - x[1], r = x[2] + x[3], d = x[2] - x[3];
+                x[0] = p + r;
+                x[1] = q + d;
+                x[2] = p - r;
+                x[3] = q - d;
+            }
+#pragma unroll
+            for (int m = 1; m < 32; m <<= 1) {
+                ss += __shfl_xor_sync(0xffffffffu, ss, m);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float o = __shfl_xor_sync(0xffffffffu, x[i], m);
+                    x[i] = o + (lane & m ? -x[i] : x[i]);
+                }
+            }
+            // norm, ranges and codes as in insert_kernel
+            float inv;
+            asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(ss));
+            inv = fmaf(inv * fmaf(-ss * inv, inv, 1.f), 0.5f, inv);
+            const float nrm = ss * inv, scale = kGrid * 0.08838834764831845f * inv;
+            const bool wild = !(ss >= 7.888609052210118e-31f && ss <= 1.2676506002282294e30f);
+            const bool tie = ((__float_as_uint(nrm) & 0x1FFFu) - (0x1000u - kTieUlps)) <= 2 * kTieUlps ||
+                             !(nrm >= 6.103515625e-05f && nrm < 65504.f);
+            uint32_t near = 0, code = 0, cell = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float v = fmaf(x[i], scale, 98304.f + 64.5f);
+                const uint2 e = *reinterpret_cast<const uint2 *>(reinterpret_cast<const uint8_t *>(sm.cells) +
+                                                                 ((__float_as_uint(v) & 0x3F80u) >> 4));
+                const float d = fmaf(x[i], scale, -__uint_as_float(e.x));
+                near |= fabsf(d) < kEps ? 1u << i : 0u;
+                cell |= (e.y - 1) << (8 * i);
+                code |= ((e.y + (uint32_t)(__float_as_int(d) >> 31)) & 15u) << (8 * i);
+            }
+            uint8_t *block = sd.blocks + slot * (2 + 16 * bits);
+            if (wild) {
+                range_row<DT>(row, block, sd, rope, a, tok, reinterpret_cast<double *>(sm.again[warp]));
+            } else {
+                const uint32_t who = __ballot_sync(0xffffffffu, near != 0);
+                if (who == 0 && !tie) {
+                    if (lane == 0) *reinterpret_cast<__half *>(block) = __float2half_rn(nrm);
+                } else if (__popc(who) <= 4) {
+                    code = decide_few<DT>(in.x, in.y, in.z, in.w, near, cell, code, angle[0], angle[1], turned ? partner : -1,
+                                          flip, sd, block);
+                }
+                if (__popc(who) <= 4) write_codes(block, bits, code, lane);
+                else near_row<DT>(row, block, sd, rope, a, tok, sm.again[warp]);
+            }
+            __syncwarp();
+        }
+        row = nullptr;
+    }
+}
+
+template <int DT>
+int launch_few(const tq_rope &rope, const InsertArgs &a, int sides, cudaStream_t st) {
+    const int64_t ctas = (a.n_tok * a.heads + kWarps - 1) / kWarps;
+    const dim3 grid((unsigned)min64(ctas, (int64_t)sm_count() * 6 / sides), (unsigned)sides);
+    insert_few_kernel<DT><<<grid, kThreads, 0, st>>>(rope, a);
+    return launch_status();
+}
+
 template <int DT>
 int launch(const tq_rope &rope, const InsertArgs &a, cudaStream_t st) {
     const int smem = (int)(sizeof(Shared) + (size_t)a.tiles * sizeof(float4) * 8 * kTok * 4);
@@ -984,7 +1277,7 @@ extern "C" int tq_insert_kv(const void *k, int64_t k_tok_stride, int64_t k_head_
     a.tiles = heads == 1 ? 4 : heads == 2 ? 2 : 1;
     const int64_t tiles = (n_tok + (int64_t)kTok * a.tiles - 1) / (kTok * a.tiles);
     const int sides = (k != nullptr) + (v != nullptr);
-    const int64_t slots = (int64_t)sm_count() * 4;
+    const int64_t slots = (int64_t)sm_count() * 4, few = (int64_t)sm_count() * kFewRows;
     // with few tiles, four heads a CTA fill more SMs
     a.heads_per_cta = heads <= kWarps || tiles * sides >= slots ? heads : kWarps;
     a.groups = (heads + a.heads_per_cta - 1) / a.heads_per_cta;
@@ -998,9 +1291,10 @@ extern "C" int tq_insert_kv(const void *k, int64_t k_tok_stride, int64_t k_head_
     if (!rope) std::memset(&none, 0, sizeof(none));
     const tq_rope &r = rope ? *rope : none;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const bool small = n_tok <= few / ((int64_t)heads * sides);
     switch (dtype) {
-        case TQ_BF16: return launch<TQ_BF16>(r, a, st);
-        case TQ_F16: return launch<TQ_F16>(r, a, st);
-        default: return launch<TQ_F32>(r, a, st);
+        case TQ_BF16: return small ? launch_few<TQ_BF16>(r, a, sides, st) : launch<TQ_BF16>(r, a, st);
+        case TQ_F16: return small ? launch_few<TQ_F16>(r, a, sides, st) : launch<TQ_F16>(r, a, st);
+        default: return small ? launch_few<TQ_F32>(r, a, sides, st) : launch<TQ_F32>(r, a, st);
     }
 }
