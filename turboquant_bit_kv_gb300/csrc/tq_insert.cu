@@ -41,13 +41,17 @@
 // transformed in float32: a row with a coordinate closer to a boundary than
 // kEps or a norm closer to a rounding border of fp16 than kTieUlps (both far
 // above the float32 error; about 0.1% of rows each) is listed, and when the CTA
-// is through its tiles the listed rows are taken again in double-float
-// arithmetic, one by each of its warps (four for their norms alone).  Rows of a
-// sum of squares outside float32's safe range go through double precision.  (The
-// double-precision pipe has one sixty-fourth of the float32 rate: on it, all
-// such rows together cost 168 of the 433 us of a prompt of 131072 tokens x 8
-// heads; in double-float but one at a time between the tiles, where three warps
-// wait for the fourth, 157 of 398.)
+// is through its tiles the listed rows are taken again, one by each of its warps
+// (four for their norms alone): in float32 once more, and each coordinate near a
+// boundary as one sum in double-float.  Rows of a sum of squares outside
+// float32's safe range go through double precision.  (The double-precision pipe
+// has one sixty-fourth of the float32 rate: on it, all such rows together cost
+// 168 of the 433 us of a prompt of 131072 tokens x 8 heads; in double-float but
+// one at a time between the tiles, where three warps wait for the fourth, 157 of
+// 398.  Whole rows in double-float at the end cost 5001 tokens x 4 heads 18.5 us
+// instead of 17.0.)  A CTA whose list overflows takes all its rows again.
+//
+// Few rows go to a kernel of their own, a warp per row (insert_few_kernel).
 //
 // CTAs are persistent, four per SM, each on keys or on values; a warp's next
 // rows are on their way to shared memory (each thread copies what it will read
@@ -80,10 +84,12 @@ constexpr float kEps = 1.25e-6f * kGrid * 0.08838834764831845f;
 constexpr uint32_t kTieUlps = 5;
 
 // Rows per SM, keys and values together, up to which a warp takes a row
-// (insert_few_kernel): bfloat16 keys with rotary positions in 4 bits and values
-// in 2, 8 heads, by tokens, us against insert_kernel's: 16 3.4 / 7.6, 256 6.9 /
-// 15.0, 1024 11.8 / 16.1, 2048 (216 rows per SM) 18.6 / 16.3, 8192 61.5 / 28.7.
-constexpr int kFewRows = 160;
+// (insert_few_kernel).  us, against insert_kernel's, for bfloat16 keys with
+// rotary positions in 4 bits and values in 2, 8 heads, by tokens: 16 3.3 / 8.4,
+// 256 6.7 / 11.2, 512 8.0 / 11.3, 768 (81 rows per SM) 10.2 / 11.8, 1024 13.3 /
+// 12.2, 2048 20.2 / 12.8.  Keys alone cross at 67, without rotary positions at
+// 108 rows per SM.
+constexpr int kFewRows = 80;
 
 enum { kRopeNone = 0, kRopeHalf1, kRopeHalf2, kRopeHalf3, kRopeHalf4, kRopeAdjacent };
 
@@ -109,7 +115,6 @@ struct InsertArgs {
 };
 
 constexpr int kList = 256;               // rows to take again that a CTA can list
-constexpr uint64_t kRange = 1ull << 63;  // listed for being outside float32's safe range
 constexpr int kStage = kTok * 33 + 8;    // half words a warp stages its 16 blocks in (and the 128 values of a
                                          // row taken again)
 
@@ -120,7 +125,7 @@ struct Shared {
     uint4 flip[4][4];                         // sign bits of the 16-bit elements 32 c + 8 t .. + 7
     uint64_t turn[kRopePairs];                // the rope, and whether a pair's two signs differ (bit 2 of axis)
     uint8_t axis[kRopePairs];
-    uint64_t list[kList];                     // token * heads + head: norms from the front, rows from the back
+    int64_t list[kList];                      // token * heads + head: norms from the front, rows from the back
     int listed[2];
     // cosines and sines (negated where the pair's two signs differ) of two
     // neighbouring pairs, (c, c', s, s'); unit u of token n and thread t at
@@ -235,28 +240,21 @@ __device__ __forceinline__ N transform_row(const uint8_t *row, const Side &sd, c
     return ss;
 }
 
-// A row outside float32's safe range (or of zeros), in double precision.
+// A row outside float32's safe range (not of zeros), in double precision.
 template <int DT>
 __device__ __noinline__ void range_row(const uint8_t *row, uint8_t *block, const Side &sd, const tq_rope &rope,
                                        const InsertArgs &a, int64_t tok, double *v) {
     const int lane = threadIdx.x & 31;
-    bool any = false;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) any |= elem<DT>(row, 4 * lane + i) != 0.f;
-    uint32_t code = 0x01010101u << (sd.bits - 1), norm = 0;
-    if (__any_sync(0xffffffffu, any)) {
-        const double nrm = sqrt(transform_row<DT, double>(row, sd, rope, a, tok, v));
-        norm = __half_as_ushort(__double2half(nrm));
-        const double f = 1.0 / (nrm * 11.313708498984761);   // sqrt(128)
-        code = 0;
+    const double nrm = sqrt(transform_row<DT, double>(row, sd, rope, a, tok, v));
+    const double f = 1.0 / (nrm * 11.313708498984761);   // sqrt(128)
+    uint32_t code = 0;
 #pragma unroll 1
-        for (int i = 0; i < 4; ++i) {
-            const float y = (float)(v[4 * lane + i] * f);
+    for (int i = 0; i < 4; ++i) {
+        const float y = (float)(v[4 * lane + i] * f);
 #pragma unroll 1
-            for (int j = 0; j < (1 << sd.bits) - 1; ++j) code += sd.b[j] <= y ? 1u << (8 * i) : 0u;
-        }
+        for (int j = 0; j < (1 << sd.bits) - 1; ++j) code += sd.b[j] <= y ? 1u << (8 * i) : 0u;
     }
-    if (lane == 0) *reinterpret_cast<uint16_t *>(block) = (uint16_t)norm;
+    if (lane == 0) *reinterpret_cast<__half *>(block) = __double2half(nrm);
     write_codes(block, sd.bits, code, lane);
 }
 
@@ -289,6 +287,275 @@ __device__ __noinline__ void near_row(const uint8_t *row, uint8_t *block, const 
     write_codes(block, sd.bits, code, lane);
 }
 
+// The few coordinates of a row that float32 does not decide, in double-float:
+// coordinate j is the sum of +-x, so it costs one reduction and no transform.
+// near: bits i of the lane's elements 4 lane + i to decide, cell[i] the number
+// of boundaries below their cells.  Returns the lane's codes; the norm is
+// rounded again as well.
+template <int DT>
+__device__ __noinline__ uint32_t decide_few(float x0, float x1, float x2, float x3, uint32_t near, uint32_t cell,
+                                            uint32_t code, uint64_t angle0, uint64_t angle1, int partner, uint32_t flip,
+                                            const Side &sd, uint8_t *block) {
+    const int lane = threadIdx.x & 31;
+    const float x[4] = {x0, x1, x2, x3};
+    ff r[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = ff_of(x[i]);
+    if (sd.style != kRopeNone) {
+        ff s[2], c[2];
+#pragma unroll 1
+        for (int z = 0; z < 2; ++z) {
+            ff sz, cz;
+            rope_sincos_ff(z ? angle1 : angle0, sz, cz);
+            if (z) s[1] = sz, c[1] = cz;
+            else s[0] = sz, c[0] = cz;
+        }
+        const bool adj = sd.style == kRopeAdjacent, upper = partner < lane;
+        if (adj) {
+            if (partner >= 0)
+#pragma unroll
+                for (int z = 0; z < 2; ++z) {
+                    r[2 * z] = ff_add(ff_scale(c[z], x[2 * z]), ff_scale(s[z], -x[2 * z + 1]));
+                    r[2 * z + 1] = ff_add(ff_scale(c[z], x[2 * z + 1]), ff_scale(s[z], x[2 * z]));
+                }
+        } else {
+            const int from = partner < 0 ? lane : partner;
+            ff so[2], co[2];
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+                so[z] = {__shfl_sync(0xffffffffu, s[z].h, from), __shfl_sync(0xffffffffu, s[z].l, from)};
+                co[z] = {__shfl_sync(0xffffffffu, c[z].h, from), __shfl_sync(0xffffffffu, c[z].l, from)};
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float o = __shfl_sync(0xffffffffu, x[i], from);
+                const bool mine = (i >= 2) == upper;
+                if (partner >= 0)
+                    r[i] = ff_add(ff_scale(mine ? c[i & 1] : co[i & 1], x[i]), ff_scale(mine ? s[i & 1] : so[i & 1], upper ? o : -o));
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if ((flip >> i) & 1u) r[i] = ff_neg(r[i]);
+    ff squares = ff_mul(r[0], r[0]);
+#pragma unroll
+    for (int i = 1; i < 4; ++i) squares = ff_add(squares, ff_mul(r[i], r[i]));
+    uint32_t who = __ballot_sync(0xffffffffu, near != 0);
+    bool first = true;
+    do {
+        const int src = who ? __ffs(who) - 1 : 0;
+        const uint32_t bits = __shfl_sync(0xffffffffu, near, src);
+        const int e = bits ? __ffs(bits) - 1 : 0, j = 4 * src + e;
+        ff v = ff_of(0.f), ss = squares;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v = ff_add(v, __popc((4 * lane + i) & j) & 1 ? ff_neg(r[i]) : r[i]);
+#pragma unroll 1
+        for (int m = 1; m < 32; m <<= 1) {
+            v = ff_add(v, shfl_(v, m));
+            ss = ff_add(ss, shfl_(ss, m));
+        }
+        const ff nrm = ff_sqrt(ss);
+        if (first && lane == 0) *reinterpret_cast<uint16_t *>(block) = ff_half(nrm);
+        first = false;
+        if (lane == src && near) {   // y >= b as in near_row
+            const int below = (int)((cell >> (8 * e)) & 0xFFu);
+            const float b = sd.b[below];
+            const uint32_t w = __float_as_uint(b);
+            const float under = b == 0.f ? 0.f : __uint_as_float(b > 0.f ? w - 1 : w + 1);
+            const ff k = ff_mul(nrm, ff_of(11.313708498984761f, (float)(11.313708498984761 - (double)11.313708498984761f)));
+            const ff edge = ff_mul(k, ff_of(b, b == 0.f ? 0.f : 0.5f * (under - b)));
+            const uint32_t c = (uint32_t)below + (v.h > edge.h || (v.h == edge.h && v.l >= edge.l) ? 1u : 0u);
+            code = (code & ~(0xFFu << (8 * e))) | c << (8 * e);
+            near &= near - 1;
+        }
+        who = __ballot_sync(0xffffffffu, near != 0);
+    } while (who);
+    return code;
+}
+
+// What a lane needs of the rope and the signs: the turns of two pairs (adjacent
+// elements, or halves, where the lane of the upper half, its partner's elements
+// + rot_dim / 2, takes the second two of the four that both need).
+struct FewLane {
+    uint64_t turn[2];
+    int axis[2];
+    int partner;
+    bool turned, upper, adj;
+    uint32_t flip;
+};
+
+__device__ __forceinline__ FewLane few_lane(const Side &sd, const tq_rope &rope, const InsertArgs &a) {
+    const int lane = threadIdx.x & 31;
+    const int span = sd.style == kRopeNone ? 0 : rope.rot_dim / 8;   // lanes of half the rotated elements
+    FewLane w;
+    w.turned = lane < 2 * span;
+    w.upper = lane >= span;
+    w.adj = sd.style == kRopeAdjacent;
+    w.partner = !w.turned || w.adj ? lane : w.upper ? lane - span : lane + span;
+#pragma unroll
+    for (int z = 0; z < 2; ++z) {
+        const int p = (w.adj ? 2 * lane : w.upper ? 4 * (lane - span) + 2 : 4 * lane) + z;
+        w.turn[z] = w.turned ? rope.turn[p] : 0;
+        w.axis[z] = w.turned ? rope.axis[p] : 0;
+    }
+    w.flip = a.signs[lane >> 3] >> (4 * (lane & 7));
+    return w;
+}
+
+// A lane's elements of a row and the row's positions, as loaded.
+struct FewIn {
+    uint4 raw;
+    int64_t pos[3];
+};
+
+template <int DT>
+__device__ __forceinline__ FewIn few_load(const uint8_t *row, int64_t tok, const Side &sd, const tq_rope &rope,
+                                          const InsertArgs &a) {
+    const int lane = threadIdx.x & 31;
+    FewIn n;
+    n.raw = make_uint4(0, 0, 0, 0);
+    if constexpr (DT == TQ_F32) {
+        n.raw = __ldcs(reinterpret_cast<const uint4 *>(row) + lane);
+    } else {
+        const uint2 v = __ldcs(reinterpret_cast<const uint2 *>(row) + lane);
+        n.raw.x = v.x;
+        n.raw.y = v.y;
+    }
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+        n.pos[i] = sd.style == kRopeNone ? 0 : a.pos[(i < rope.axes ? i : 0) * a.pos_axis + tok];
+    return n;
+}
+
+// One row by a warp into its block.  cells: the quantiser's, entry c at (128 c)
+// >> shift; again: space for 128 values in double.
+template <int DT>
+__device__ __forceinline__ void few_row(const FewIn &n, const FewLane &w, const uint8_t *cells, int shift,
+                                        const uint8_t *row, uint8_t *block, const Side &sd, const tq_rope &rope,
+                                        const InsertArgs &a, int64_t tok, void *again) {
+    const int lane = threadIdx.x & 31, bits = sd.bits;
+    const uint4 raw = n.raw;
+    const int64_t (&pos)[3] = n.pos;
+    // a row of zeros (sign bits aside: of both elements of a word of 16-bit types)
+    if (!__any_sync(0xffffffffu, (raw.x | raw.y | raw.z | raw.w) & (DT == TQ_F32 ? 0x7FFFFFFFu : 0x7FFF7FFFu))) {
+        if (lane == 0) *reinterpret_cast<uint16_t *>(block) = 0;
+        write_codes(block, bits, 0x01010101u << (bits - 1), lane);
+        return;
+    }
+    float x[4];
+    if constexpr (DT == TQ_F32) {
+        x[0] = __uint_as_float(raw.x);
+        x[1] = __uint_as_float(raw.y);
+        x[2] = __uint_as_float(raw.z);
+        x[3] = __uint_as_float(raw.w);
+    } else if constexpr (DT == TQ_BF16) {
+        x[0] = bf16_bits_lo(raw.x);
+        x[1] = bf16_bits_hi(raw.x);
+        x[2] = bf16_bits_lo(raw.y);
+        x[3] = bf16_bits_hi(raw.y);
+    } else {
+        const float2 p = __half22float2(*reinterpret_cast<const __half2 *>(&raw.x));
+        const float2 q = __half22float2(*reinterpret_cast<const __half2 *>(&raw.y));
+        x[0] = p.x;
+        x[1] = p.y;
+        x[2] = q.x;
+        x[3] = q.y;
+    }
+    const float4 in = make_float4(x[0], x[1], x[2], x[3]);
+    uint64_t angle[2] = {0, 0};
+    if (sd.style != kRopeNone) {
+        float s[2], c[2];
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+            angle[z] = rope_turns(w.turn[z], w.axis[z] == 0 ? pos[0] : w.axis[z] == 1 ? pos[1] : pos[2]);
+            rope_sincos(angle[z], s[z], c[z]);
+        }
+        if (w.adj) {
+            if (w.turned)
+#pragma unroll
+                for (int z = 0; z < 2; ++z) {
+                    const float xa = x[2 * z], xb = x[2 * z + 1];
+                    x[2 * z] = fmaf(xa, c[z], -(xb * s[z]));
+                    x[2 * z + 1] = fmaf(xb, c[z], xa * s[z]);
+                }
+        } else {
+            float so[2], co[2], o[4];
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+                so[z] = __shfl_sync(0xffffffffu, s[z], w.partner);
+                co[z] = __shfl_sync(0xffffffffu, c[z], w.partner);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[i] = __shfl_sync(0xffffffffu, x[i], w.partner);
+            if (w.turned)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const bool mine = (i >= 2) == w.upper;
+                    const float si = mine ? s[i & 1] : so[i & 1], ci = mine ? c[i & 1] : co[i & 1];
+                    x[i] = fmaf(x[i], ci, o[i] * (w.upper ? si : -si));
+                }
+        }
+    }
+    float ss = fmaf(x[0], x[0], x[1] * x[1]) + fmaf(x[2], x[2], x[3] * x[3]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = __uint_as_float(__float_as_uint(x[i]) ^ ((w.flip >> i) << 31));
+    {
+        const float p = x[0] + x[1], q = x[0] - x[1], r = x[2] + x[3], d = x[2] - x[3];
+        x[0] = p + r;
+        x[1] = q + d;
+        x[2] = p - r;
+        x[3] = q - d;
+    }
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+        ss += __shfl_xor_sync(0xffffffffu, ss, m);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float o = __shfl_xor_sync(0xffffffffu, x[i], m);
+            x[i] = o + (lane & m ? -x[i] : x[i]);
+        }
+    }
+    // norm, ranges and codes as in insert_kernel
+    float inv;
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(ss));
+    inv = fmaf(inv * fmaf(-ss * inv, inv, 1.f), 0.5f, inv);
+    const float nrm = ss * inv, scale = kGrid * 0.08838834764831845f * inv;
+    const bool wild = !(ss >= 7.888609052210118e-31f && ss <= 1.2676506002282294e30f);
+    const bool tie = ((__float_as_uint(nrm) & 0x1FFFu) - (0x1000u - kTieUlps)) <= 2 * kTieUlps ||
+                     !(nrm >= 6.103515625e-05f && nrm < 65504.f);
+    uint32_t near = 0, code = 0, cell = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float v = fmaf(x[i], scale, 98304.f + 64.5f);
+        const uint2 e = *reinterpret_cast<const uint2 *>(cells + ((__float_as_uint(v) & 0x3F80u) >> shift));
+        const float d = fmaf(x[i], scale, -__uint_as_float(e.x));
+        near |= fabsf(d) < kEps ? 1u << i : 0u;
+        cell |= (e.y - 1) << (8 * i);
+        code |= ((e.y + (uint32_t)(__float_as_int(d) >> 31)) & 15u) << (8 * i);
+    }
+    if (wild) {
+        range_row<DT>(row, block, sd, rope, a, tok, static_cast<double *>(again));
+    } else {
+        const uint32_t who = __ballot_sync(0xffffffffu, near != 0);
+        if (who == 0 && !tie) {
+            if (lane == 0) *reinterpret_cast<__half *>(block) = __float2half_rn(nrm);
+        } else if (__popc(who) <= 4) {
+            code = decide_few<DT>(in.x, in.y, in.z, in.w, near, cell, code, angle[0], angle[1], w.turned ? w.partner : -1,
+                                  w.flip, sd, block);
+        }
+        if (__popc(who) <= 4) write_codes(block, bits, code, lane);
+        else near_row<DT>(row, block, sd, rope, a, tok, static_cast<ff *>(again));
+    }
+}
+
+// The same for a row of insert_kernel's list.
+template <int DT>
+__device__ __noinline__ void again_row(const uint8_t *row, uint8_t *block, const Side &sd, const tq_rope &rope,
+                                       const InsertArgs &a, int64_t tok, const uint8_t *cells, void *again) {
+    few_row<DT>(few_load<DT>(row, tok, sd, rope, a), few_lane(sd, rope, a), cells, 0, row, block, sd, rope, a, tok, again);
+}
+
 // Norms of four rows (rope keeps them), one per eight lanes.
 template <int DT>
 __device__ __noinline__ void norm_rows(const uint8_t *row, uint8_t *block, bool write) {
@@ -304,32 +571,46 @@ __device__ __noinline__ void norm_rows(const uint8_t *row, uint8_t *block, bool 
     if (write && l == 0) *reinterpret_cast<uint16_t *>(block) = ff_half(ff_sqrt(ss));
 }
 
-// The listed rows by a warp, its share of them: of the norms list[0 .. ties)
-// four at a time from i0 * 4 on, of the others, counted from the list's end,
-// one at a time from i0 on.
+// The listed rows of the CTA, a warp each (four for their norms alone).  If a
+// list overflowed (inputs of many zeros, say), all its rows.
 template <int DT>
-__device__ __noinline__ void take_again(const uint64_t *list, int size, int ties, int rows, int i0, int step,
-                                        const Side &sd, const tq_rope &rope, const InsertArgs &a, uint16_t *stage) {
-    auto place = [&](uint64_t entry, const uint8_t *&row, uint8_t *&block) {
-        const int64_t id = (int64_t)(entry & ~kRange), tok = id / a.heads;
+__device__ __noinline__ void finish(int which, const tq_rope &rope, const InsertArgs &a) {
+    extern __shared__ __align__(16) uint8_t dsmem[];
+    Shared &sm = *reinterpret_cast<Shared *>(dsmem);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const Side &sd = a.side[which];
+    const uint8_t *cells = reinterpret_cast<const uint8_t *>(sm.cells);
+    uint16_t *stage = sm.stage[warp];
+    const int ties = sm.listed[0], whole = sm.listed[1];
+    const int64_t bytes = 2 + 16 * sd.bits;
+    auto block_of = [&](int64_t tok, int head) { return sd.blocks + (a.dst[tok] + head * a.dst_head) * bytes; };
+    auto row_of = [&](int64_t tok, int head) { return sd.x + tok * sd.tok + head * sd.head; };
+    if (max(ties, whole) > kList / 2) {
+        const int cta = blockIdx.x - (which ? a.ctas[0] : 0);
+        for (int unit = cta; unit < a.units; unit += a.ctas[which]) {
+            const int64_t tok0 = (int64_t)(unit / a.groups) * a.tiles * kTok, tok1 = min64(tok0 + a.tiles * kTok, a.n_tok);
+            const int head0 = unit % a.groups * a.heads_per_cta, head1 = min(head0 + a.heads_per_cta, a.heads);
+            for (int64_t tok = tok0 + warp; tok < tok1; tok += kWarps)
+                for (int head = head0; head < head1; ++head) {
+                    const int64_t dst = a.dst[tok], slot = dst < 0 ? -1 : dst + head * a.dst_head;
+                    if (slot < 0 || slot >= sd.n_blocks) continue;
+                    again_row<DT>(row_of(tok, head), block_of(tok, head), sd, rope, a, tok, cells, stage);
+                    __syncwarp();
+                }
+        }
+        return;
+    }
+    for (int i = warp; i < whole; i += kWarps) {
+        const int64_t id = sm.list[kList - 1 - i], tok = id / a.heads;
         const int head = (int)(id - tok * a.heads);
-        row = sd.x + tok * sd.tok + head * sd.head;
-        block = sd.blocks + (a.dst[tok] + head * a.dst_head) * (2 + 16 * sd.bits);
-        return tok;
-    };
-    const uint8_t *row;
-    uint8_t *block;
-    for (int i = i0; i < rows; i += step) {
-        const uint64_t entry = list[size - 1 - i];
-        const int64_t tok = place(entry, row, block);
-        if (entry & kRange) range_row<DT>(row, block, sd, rope, a, tok, reinterpret_cast<double *>(stage));
-        else near_row<DT>(row, block, sd, rope, a, tok, reinterpret_cast<ff *>(stage));
+        again_row<DT>(row_of(tok, head), block_of(tok, head), sd, rope, a, tok, cells, stage);
         __syncwarp();
     }
-    for (int i = 4 * i0; i < ties; i += 4 * step) {
-        const int q = i + ((threadIdx.x >> 3) & 3);
-        place(list[q < ties ? q : i], row, block);
-        norm_rows<DT>(row, block, q < ties);
+    for (int i = 4 * warp; i < ties; i += 4 * kWarps) {
+        const int q = i + (lane >> 3);
+        const int64_t id = sm.list[q < ties ? q : i], tok = id / a.heads;
+        const int head = (int)(id - tok * a.heads);
+        norm_rows<DT>(row_of(tok, head), block_of(tok, head), q < ties);
     }
 }
 
@@ -869,10 +1150,9 @@ __global__ void __launch_bounds__(kThreads, 4) insert_kernel(const __grid_consta
 
             // rows to take again: bits 4 g .. of a mask for rows g and g + 8 (any thread of the quad speaks for its
             // row)
-            uint32_t todo[2], ties[2], wild[2];
+            uint32_t todo[2], ties[2];
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                wild[r] = __ballot_sync(0xffffffffu, redo[r]);
                 uint32_t m = __ballot_sync(0xffffffffu, redo[r] || near[r] < kEps);
                 m |= m >> 1;
                 todo[r] = (m | m >> 2) & 0x11111111u;
@@ -882,183 +1162,59 @@ __global__ void __launch_bounds__(kThreads, 4) insert_kernel(const __grid_consta
                 // lane n < 16 lists row n: for its norm, or whole
                 const int bit = 4 * (lane & 7), odd = lane & 8;
                 const bool whole = ((odd ? todo[1] : todo[0]) >> bit) & 1u, tied = ((odd ? ties[1] : ties[0]) >> bit) & 1u;
-                const uint64_t entry = (uint64_t)(my * a.heads + head) |
-                                       ((((odd ? wild[1] : wild[0]) >> bit) & 1u) ? kRange : 0);
-                bool full = false;
+                const int64_t entry = my * a.heads + head;
                 if (lane < kTok && ok && (whole || tied)) {
                     const int at = atomicAdd(&sm.listed[whole ? 1 : 0], 1);
-                    full = at >= kList / 2;
-                    if (!full) sm.list[whole ? kList - 1 - at : at] = entry;
-                }
-                // that half of the list is full (inputs of many zeros, say): at once
-                uint32_t m = __ballot_sync(0xffffffffu, full);
-                while (m) {
-                    const int q = __ffs(m) - 1;
-                    m &= m - 1;
-                    const uint64_t one = __shfl_sync(0xffffffffu, entry, q);
-                    const bool row = __shfl_sync(0xffffffffu, whole, q);
-                    __syncwarp();   // its block is written, and the staged blocks are read
-                    take_again<DT>(&one, 1, row ? 0 : 1, row ? 1 : 0, 0, 1, sd, rope, a, stage);
+                    if (at < kList / 2) sm.list[whole ? kList - 1 - at : at] = entry;
                 }
             }
             __syncwarp();
         }
     }
     __syncthreads();
-    take_again<DT>(sm.list, kList, min(sm.listed[0], kList / 2), min(sm.listed[1], kList / 2), warp, kWarps, sd, rope, a,
-                   stage);
+    finish<DT>(which, rope, a);
 }
 
 // Few rows: latency is what counts.  A warp per row, four elements per lane,
 // the rotary partner and five of the transform's seven stages by shuffles; all
 // loads are under way while the CTA fills the quantiser's cells (one copy: a
 // warp's few lookups can bear the conflicts).  The whole call is then launch,
-// one memory latency and about 400 instructions, 3.4 us for 16 tokens where
-// insert_kernel's tile takes 7.6.  Six CTAs per SM in all (1024 tokens: 11.8 us;
-// four the same, eight 12.7, one CTA for every four rows 18.0).  A row that
-// float32 does not decide adds 1.2 us, 1.7 with rotary positions (near_row:
-// 4.8).
+// one memory latency and about 400 instructions, 3.3 us for 16 tokens x 8 heads
+// where insert_kernel's tile takes 8.4.  Six CTAs per SM in all (1024 tokens:
+// 11.8 us; four the same, eight 12.7, one CTA for every four rows 18.0).  A row
+// that float32 does not decide adds 1.2 us, 1.7 with rotary positions (near_row:
+// 4.8).  Its float32 path errs less than insert_kernel's: over 1.2e9 coordinates
+// of the same kinds the furthest wrong decision lay 2.8e-7 of a standard
+// deviation from its boundary, of the norms' roundings 1.2e-7 of the norm.
 struct SmallShared {
     uint2 cells[128];                         // as Shared's, one copy
     alignas(16) ff again[kWarps][kD];         // values of a row taken again
 };
 
-// The few coordinates of a row that float32 does not decide, in double-float:
-// coordinate j is the sum of +-x, so it costs one reduction and no transform.
-// near: bits i of the lane's elements 4 lane + i to decide, cell[i] the number
-// of boundaries below their cells.  Returns the lane's codes; the norm is
-// rounded again as well.
-template <int DT>
-__device__ __noinline__ uint32_t decide_few(float x0, float x1, float x2, float x3, uint32_t near, uint32_t cell,
-                                            uint32_t code, uint64_t angle0, uint64_t angle1, int partner, uint32_t flip,
-                                            const Side &sd, uint8_t *block) {
-    const int lane = threadIdx.x & 31;
-    const float x[4] = {x0, x1, x2, x3};
-    ff r[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) r[i] = ff_of(x[i]);
-    if (sd.style != kRopeNone) {
-        ff s[2], c[2];
-#pragma unroll 1
-        for (int z = 0; z < 2; ++z) {
-            ff sz, cz;
-            rope_sincos_ff(z ? angle1 : angle0, sz, cz);
-            if (z) s[1] = sz, c[1] = cz;
-            else s[0] = sz, c[0] = cz;
-        }
-        const bool adj = sd.style == kRopeAdjacent, upper = partner < lane;
-        if (adj) {
-            if (partner >= 0)
-#pragma unroll
-                for (int z = 0; z < 2; ++z) {
-                    r[2 * z] = ff_add(ff_scale(c[z], x[2 * z]), ff_scale(s[z], -x[2 * z + 1]));
-                    r[2 * z + 1] = ff_add(ff_scale(c[z], x[2 * z + 1]), ff_scale(s[z], x[2 * z]));
-                }
-        } else {
-            const int from = partner < 0 ? lane : partner;
-            ff so[2], co[2];
-#pragma unroll
-            for (int z = 0; z < 2; ++z) {
-                so[z] = {__shfl_sync(0xffffffffu, s[z].h, from), __shfl_sync(0xffffffffu, s[z].l, from)};
-                co[z] = {__shfl_sync(0xffffffffu, c[z].h, from), __shfl_sync(0xffffffffu, c[z].l, from)};
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float o = __shfl_sync(0xffffffffu, x[i], from);
-                const bool mine = (i >= 2) == upper;
-                if (partner >= 0)
-                    r[i] = ff_add(ff_scale(mine ? c[i & 1] : co[i & 1], x[i]), ff_scale(mine ? s[i & 1] : so[i & 1], upper ? o : -o));
-            }
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if ((flip >> i) & 1u) r[i] = ff_neg(r[i]);
-    ff squares = ff_mul(r[0], r[0]);
-#pragma unroll
-    for (int i = 1; i < 4; ++i) squares = ff_add(squares, ff_mul(r[i], r[i]));
-    uint32_t who = __ballot_sync(0xffffffffu, near != 0);
-    bool first = true;
-    do {
-        const int src = who ? __ffs(who) - 1 : 0;
-        const uint32_t bits = __shfl_sync(0xffffffffu, near, src);
-        const int e = bits ? __ffs(bits) - 1 : 0, j = 4 * src + e;
-        ff v = ff_of(0.f), ss = squares;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v = ff_add(v, __popc((4 * lane + i) & j) & 1 ? ff_neg(r[i]) : r[i]);
-#pragma unroll 1
-        for (int m = 1; m < 32; m <<= 1) {
-            v = ff_add(v, shfl_(v, m));
-            ss = ff_add(ss, shfl_(ss, m));
-        }
-        const ff nrm = ff_sqrt(ss);
-        if (first && lane == 0) *reinterpret_cast<uint16_t *>(block) = ff_half(nrm);
-        first = false;
-        if (lane == src && near) {   // y >= b as in near_row
-            const int below = (int)((cell >> (8 * e)) & 0xFFu);
-            const float b = sd.b[below];
-            const uint32_t w = __float_as_uint(b);
-            const float under = b == 0.f ? 0.f : __uint_as_float(b > 0.f ? w - 1 : w + 1);
-            const ff k = ff_mul(nrm, ff_of(11.313708498984761f, (float)(11.313708498984761 - (double)11.313708498984761f)));
-            const ff edge = ff_mul(k, ff_of(b, b == 0.f ? 0.f : 0.5f * (under - b)));
-            const uint32_t c = (uint32_t)below + (v.h > edge.h || (v.h == edge.h && v.l >= edge.l) ? 1u : 0u);
-            code = (code & ~(0xFFu << (8 * e))) | c << (8 * e);
-            near &= near - 1;
-        }
-        who = __ballot_sync(0xffffffffu, near != 0);
-    } while (who);
-    return code;
-}
-
 template <int DT>
 __global__ void __launch_bounds__(kThreads) insert_few_kernel(const __grid_constant__ tq_rope rope,
                                                               const __grid_constant__ InsertArgs a) {
     __shared__ SmallShared sm;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = tid >> 5;
     const Side &sd = a.side[a.side[0].x ? blockIdx.y : 1];
-    const int bits = sd.bits, style = sd.style;
+    const int bits = sd.bits;
     const uint32_t rows = (uint32_t)a.n_tok * (uint32_t)a.heads;
     uint32_t id = blockIdx.x * kWarps + warp;
     // what a row needs from memory, on its way while the cells are filled
     const uint8_t *row = nullptr;
-    int64_t tok = 0, dst = -1, pos[3] = {0, 0, 0};
+    int64_t tok = 0, dst = -1;
     int head = 0;
-    uint4 raw = make_uint4(0, 0, 0, 0);
+    FewIn in;
     auto load = [&]() {
         const uint32_t n = id / (uint32_t)a.heads;
         tok = n;
         head = (int)(id - n * (uint32_t)a.heads);
         row = sd.x + tok * sd.tok + head * sd.head;
-        if constexpr (DT == TQ_F32) {
-            raw = __ldcs(reinterpret_cast<const uint4 *>(row) + lane);
-        } else {
-            const uint2 v = __ldcs(reinterpret_cast<const uint2 *>(row) + lane);
-            raw.x = v.x;
-            raw.y = v.y;
-        }
+        in = few_load<DT>(row, tok, sd, rope, a);
         dst = a.dst[tok];
-        if (style != kRopeNone)
-#pragma unroll
-            for (int i = 0; i < 3; ++i) pos[i] = a.pos[(i < rope.axes ? i : 0) * a.pos_axis + tok];
     };
     if (id < rows) load();
-
-    // the two pairs of this lane's sines: adjacent elements, or halves, where the lane of the upper half (its
-    // partner's elements + rot_dim / 2) takes the second two of the four that both need
-    const int span = style == kRopeNone ? 0 : rope.rot_dim / 8;   // lanes of half the rotated elements
-    const bool turned = lane < 2 * span, upper = lane >= span, adj = style == kRopeAdjacent;
-    const int partner = !turned || adj ? lane : upper ? lane - span : lane + span;
-    uint64_t turn[2] = {0, 0};
-    int axis[2] = {0, 0};
-    if (turned) {
-        const int p0 = adj ? 2 * lane : upper ? 4 * (lane - span) + 2 : 4 * lane;
-#pragma unroll
-        for (int z = 0; z < 2; ++z) {
-            turn[z] = rope.turn[p0 + z];
-            axis[z] = rope.axis[p0 + z];
-        }
-    }
-    const uint32_t flip = a.signs[lane >> 3] >> (4 * (lane & 7));
+    const FewLane w = few_lane(sd, rope, a);
     {
         uint32_t below = 0;
         float edge = 3.0e38f;   // as in insert_kernel
@@ -1072,116 +1228,12 @@ __global__ void __launch_bounds__(kThreads) insert_few_kernel(const __grid_const
     }
     __syncthreads();
 
+    const uint8_t *cells = reinterpret_cast<const uint8_t *>(sm.cells);
     for (; id < rows; id += gridDim.x * kWarps) {
         if (row == nullptr) load();
         const int64_t slot = dst < 0 ? -1 : dst + head * a.dst_head;
         if (slot >= 0 && slot < sd.n_blocks) {
-            float x[4];
-            if constexpr (DT == TQ_F32) {
-                x[0] = __uint_as_float(raw.x);
-                x[1] = __uint_as_float(raw.y);
-                x[2] = __uint_as_float(raw.z);
-                x[3] = __uint_as_float(raw.w);
-            } else if constexpr (DT == TQ_BF16) {
-                x[0] = bf16_bits_lo(raw.x);
-                x[1] = bf16_bits_hi(raw.x);
-                x[2] = bf16_bits_lo(raw.y);
-                x[3] = bf16_bits_hi(raw.y);
-            } else {
-                const float2 p = __half22float2(*reinterpret_cast<const __half2 *>(&raw.x));
-                const float2 q = __half22float2(*reinterpret_cast<const __half2 *>(&raw.y));
-                x[0] = p.x;
-                x[1] = p.y;
-                x[2] = q.x;
-                x[3] = q.y;
-            }
-            const float4 in = make_float4(x[0], x[1], x[2], x[3]);
-            uint64_t angle[2] = {0, 0};
-            if (style != kRopeNone) {
-                float s[2], c[2];
-#pragma unroll
-                for (int z = 0; z < 2; ++z) {
-                    angle[z] = rope_turns(turn[z], axis[z] == 0 ? pos[0] : axis[z] == 1 ? pos[1] : pos[2]);
-                    rope_sincos(angle[z], s[z], c[z]);
-                }
-                if (adj) {
-                    if (turned)
-#pragma unroll
-                        for (int z = 0; z < 2; ++z) {
-                            const float xa = x[2 * z], xb = x[2 * z + 1];
-                            x[2 * z] = fmaf(xa, c[z], -(xb * s[z]));
-                            x[2 * z + 1] = fmaf(xb, c[z], xa * s[z]);
-                        }
-                } else {
-                    float so[2], co[2], o[4];
-#pragma unroll
-                    for (int z = 0; z < 2; ++z) {
-                        so[z] = __shfl_sync(0xffffffffu, s[z], partner);
-                        co[z] = __shfl_sync(0xffffffffu, c[z], partner);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) o[i] = __shfl_sync(0xffffffffu, x[i], partner);
-                    if (turned)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const bool mine = (i >= 2) == upper;
-                            const float si = mine ? s[i & 1] : so[i & 1], ci = mine ? c[i & 1] : co[i & 1];
-                            x[i] = fmaf(x[i], ci, o[i] * (upper ? si : -si));
-                        }
-                }
-            }
-            float ss = fmaf(x[0], x[0], x[1] * x[1]) + fmaf(x[2], x[2], x[3] * x[3]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) x[i] = __uint_as_float(__float_as_uint(x[i]) ^ ((flip >> i) << 31));
-            {
-                const float p = x[0] + x[1], q = x[0] - x[1], r = x[2] + x[3], d = x[2] - x[3];
-                x[0] = p + r;
-                x[1] = q + d;
-                x[2] = p - r;
-                x[3] = q - d;
-            }
-#pragma unroll
-            for (int m = 1; m < 32; m <<= 1) {
-                ss += __shfl_xor_sync(0xffffffffu, ss, m);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float o = __shfl_xor_sync(0xffffffffu, x[i], m);
-                    x[i] = o + (lane & m ? -x[i] : x[i]);
-                }
-            }
-            // norm, ranges and codes as in insert_kernel
-            float inv;
-            asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(ss));
-            inv = fmaf(inv * fmaf(-ss * inv, inv, 1.f), 0.5f, inv);
-            const float nrm = ss * inv, scale = kGrid * 0.08838834764831845f * inv;
-            const bool wild = !(ss >= 7.888609052210118e-31f && ss <= 1.2676506002282294e30f);
-            const bool tie = ((__float_as_uint(nrm) & 0x1FFFu) - (0x1000u - kTieUlps)) <= 2 * kTieUlps ||
-                             !(nrm >= 6.103515625e-05f && nrm < 65504.f);
-            uint32_t near = 0, code = 0, cell = 0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float v = fmaf(x[i], scale, 98304.f + 64.5f);
-                const uint2 e = *reinterpret_cast<const uint2 *>(reinterpret_cast<const uint8_t *>(sm.cells) +
-                                                                 ((__float_as_uint(v) & 0x3F80u) >> 4));
-                const float d = fmaf(x[i], scale, -__uint_as_float(e.x));
-                near |= fabsf(d) < kEps ? 1u << i : 0u;
-                cell |= (e.y - 1) << (8 * i);
-                code |= ((e.y + (uint32_t)(__float_as_int(d) >> 31)) & 15u) << (8 * i);
-            }
-            uint8_t *block = sd.blocks + slot * (2 + 16 * bits);
-            if (wild) {
-                range_row<DT>(row, block, sd, rope, a, tok, reinterpret_cast<double *>(sm.again[warp]));
-            } else {
-                const uint32_t who = __ballot_sync(0xffffffffu, near != 0);
-                if (who == 0 && !tie) {
-                    if (lane == 0) *reinterpret_cast<__half *>(block) = __float2half_rn(nrm);
-                } else if (__popc(who) <= 4) {
-                    code = decide_few<DT>(in.x, in.y, in.z, in.w, near, cell, code, angle[0], angle[1], turned ? partner : -1,
-                                          flip, sd, block);
-                }
-                if (__popc(who) <= 4) write_codes(block, bits, code, lane);
-                else near_row<DT>(row, block, sd, rope, a, tok, sm.again[warp]);
-            }
+            few_row<DT>(in, w, cells, 4, row, sd.blocks + slot * (2 + 16 * bits), sd, rope, a, tok, sm.again[warp]);
             __syncwarp();
         }
         row = nullptr;
