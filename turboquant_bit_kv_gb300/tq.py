@@ -175,6 +175,10 @@ def _nvec_rows(x):
     flatten to one uniformly strided axis)."""
     if x.dim() == 1:
         return 1, 128
+    n = x.numel()
+    if n and x.is_contiguous():   # (a contiguous tensor's strides of size-1 dims can be anything)
+        d = x.shape[-1]
+        return n // d, d
     lead = x.shape[:-1]
     n = 1
     for s in lead:
@@ -504,27 +508,28 @@ def tq_insert_kv(k, v, pos, rope, kcb, vcb, signs, k_blocks, v_blocks, dst, dst_
     what = "tq_insert_kv"
     x = k if k is not None else v
     _need(x is not None, "tq_insert_kv: no rows")
-    n, heads, _, _ = _heads(x, what)
-    if dst.dtype != torch.int64 or tuple(dst.shape) != (n,) or not dst.is_contiguous():
+    n, heads, st, sh = _heads(x, what)
+    if dst.dtype != torch.int64 or dst.shape != (n,) or not dst.is_contiguous():
         raise ValueError("tq_insert_kv: dst int64 [tokens] expected")
     strides, blocks = [], None
     for rows, cache, cb in ((k, k_blocks, kcb), (v, v_blocks, vcb)):
-        if (rows is None) != (cache is None) or (rows is not None and cb is None):
-            raise ValueError("tq_insert_kv: rows, their blocks and their codebook come together")
-        if rows is None:
-            strides += [0, 0]
+        if rows is None or cache is None or cb is None:
+            if rows is not None or cache is not None:
+                raise ValueError("tq_insert_kv: rows, their blocks and their codebook come together")
+            strides += (0, 0)
             continue
-        m, hh, st, sh = _heads(rows, what)
-        if m != n or hh != heads or rows.dtype != x.dtype:
-            raise ValueError("tq_insert_kv: k and v of one shape and dtype expected")
-        size, shape = 2 + 16 * cb.bits, cache.shape
-        if cache.dtype != torch.uint8 or not cache.is_contiguous() or len(shape) == 0 or shape[-1] != size:
+        if rows is not x:
+            m, hh, st, sh = _heads(rows, what)
+            if m != n or hh != heads or rows.dtype != x.dtype:
+                raise ValueError("tq_insert_kv: k and v of one shape and dtype expected")
+        size = 2 + 16 * cb.bits
+        if cache.dtype != torch.uint8 or not cache.is_contiguous() or cache.dim() == 0 or cache.shape[-1] != size:
             raise ValueError("tq_insert_kv: contiguous uint8 blocks of %d bytes expected" % size)
         count = cache.numel() // size
         if blocks is not None and count != blocks:
             raise ValueError("tq_insert_kv: caches of different sizes")
         blocks = count
-        strides += [st, sh]
+        strides += (st, sh)
     turn = rope is not None and k is not None
     pa = _axis_stride(pos, rope, n, what) if turn else 0
     with _on(what, k, v, pos if turn else None, k_blocks, v_blocks, dst):
