@@ -555,3 +555,20 @@ def test_decode_loop(tq):
         for h in range(Hkv):
             got = state[2][b, h].double().cpu().numpy()
             assert np.abs(got[:budget] - w[b][h]).max() <= 2.0**-14 and not got[budget:].any()
+
+
+def test_one_row_of_any_strides(tq):
+    """Strides of size-1 dimensions mean nothing: one row of weights, and one token of a cache."""
+    T, keep = 100, 40
+    w = torch.rand(T, 1, 1, device="cuda").permute(1, 2, 0)    # strides (1, 1, 1)
+    assert w.stride()[2] == 1
+    kept = [torch.empty(1, 1, keep, dtype=torch.int32, device="cuda") for _ in range(2)]
+    for k, x in zip(kept, (w, w.clone(memory_format=torch.contiguous_format).view(1, 1, T))):
+        tq.tq_evict_select(x, k, torch.empty(1, dtype=torch.int32, device="cuda"), T, 3, 5)
+    assert torch.equal(kept[0], kept[1])
+    cb, signs = tq.tq_codebook_load(128, 4), tq.tq_signs_from_seed(1)
+    x = torch.randn(1, 5, 128, device="cuda").transpose(0, 1)  # [5, 1, 128], strides (128, 640, 1)
+    blocks = [torch.empty(5, 66, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    tq.tq_encode_kv(x, cb, signs, blocks[0])
+    tq.tq_encode_kv(x.reshape(5, 128).clone(), cb, signs, blocks[1])
+    assert torch.equal(blocks[0], blocks[1])

@@ -555,25 +555,28 @@ def _pages(block_table, B, what):
 
 def _row_of(w, B, Hkv, T, what):
     """Row stride of accumulators [B, Hkv, >= T]."""
-    shape, stride = w.shape, w.stride()
-    if (w.dtype != torch.float32 or len(shape) != 3 or shape[0] != B or shape[1] != Hkv or shape[2] < T or
-            stride[2] != 1 or (B > 1 and Hkv > 1 and stride[0] != Hkv * stride[1])):
-        raise ValueError("%s: weights float32 [B, Hkv, >= T] expected" % what)
-    return stride[1] if Hkv > 1 or B == 1 else stride[0]
+    if w.dtype == torch.float32 and w.dim() == 3:
+        (b, h, n), (sb, sh, st) = w.shape, w.stride()
+        if b == B and h == Hkv and n >= T and st == 1:
+            if h == 1:   # (strides of size-1 dims can be anything)
+                return sb if b > 1 else n
+            if b == 1 or sb == h * sh:
+                return sh
+    raise ValueError("%s: weights float32 [B, Hkv, >= T] expected" % what)
 
 
 def _lens(t, B, what):
-    if t.dtype != torch.int32 or tuple(t.shape) != (B,) or not t.is_contiguous():
+    if t.dtype != torch.int32 or t.shape != (B,) or not t.is_contiguous():
         raise ValueError("%s: lengths int32 [B] expected" % what)
 
 
 def _cache(t, size, first, what):
     """Shape of caches [B or pages, Hkv, tokens, bytes]; size and first checked unless None."""
-    shape = t.shape
-    if (t.dtype != torch.uint8 or len(shape) != 4 or not t.is_contiguous() or
-            (first is not None and shape[0] != first) or (size is not None and shape[3] != size)):
-        raise ValueError("%s: contiguous packed blocks expected" % what)
-    return shape
+    if t.dtype == torch.uint8 and t.dim() == 4 and t.is_contiguous():
+        shape = tuple(t.shape)
+        if (first is None or shape[0] == first) and (size is None or shape[3] == size):
+            return shape
+    raise ValueError("%s: contiguous packed blocks expected" % what)
 
 
 def tq_attn_decode_weights(q, k_blocks, kcb, v_blocks, vcb, weights, out, workspace, T, scale, signs, seq_lens=None,
