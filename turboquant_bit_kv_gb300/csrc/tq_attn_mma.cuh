@@ -593,10 +593,9 @@ __global__ void __launch_bounds__(Cfg<KB, VB, QJL, NT, WIDE>::kThreads, Cfg<KB, 
             const uint32_t bar = bar_s + 8 * buf;
             if (lane == 0) mbar_expect_tx(bar, C::kChunkBytes);
             __syncwarp();
-            const int first = a.page - t0 % a.page;   // tokens to the end of the chunk's first page
-            const int s = lane == 0 ? t0 : t0 + first + (lane - 1) * a.page;
-            if (s < t0 + kMmaChunk) {
-                const int len = min(lane == 0 ? first : a.page, t0 + kMmaChunk - s);
+            int s, len = 0;
+            if (lane < kMmaPieces) chunk_piece(t0, a.page, lane, s, len);
+            if (len > 0) {
                 const int64_t at = slot(s);
                 bulk_g2s(dk + (s - t0) * C::kKBytes, a.k + at * C::kKBytes, len * C::kKBytes, bar);
                 bulk_g2s(dv + (s - t0) * C::kVBytes, a.v + at * C::kVBytes, len * C::kVBytes, bar);

@@ -74,6 +74,17 @@ __device__ __forceinline__ int live_chunks(const AttnArgs &a, int b) {
     return (L + kMmaChunk - 1) / kMmaChunk;
 }
 
+// Pieces of a full chunk of tokens t0 .. t0 + kMmaChunk - 1 (t0 a multiple of
+// kMmaChunk) that pages of any multiple of 8 tokens cut it into, four at most:
+// piece i is tokens t .. t + len - 1, len 0 where there is none.
+constexpr int kMmaPieces = kMmaChunk / 8;
+__host__ __device__ inline void chunk_piece(int t0, int page, int i, int &t, int &len) {
+    const int64_t end = (int64_t)t0 + kMmaChunk, head = page - t0 % page;   // head: tokens to the end of the first page
+    const int64_t at = i == 0 ? t0 : t0 + head + (int64_t)(i - 1) * page;
+    t = at < end ? (int)at : t0;
+    len = at < end ? (int)min64(i == 0 ? head : page, end - at) : 0;
+}
+
 // Slot groups of 128 threads in a combine CTA: one per 32 slots of Smax, at most kCombineMaxGroups.
 inline int mma_combine_groups(const MmaPlan &p) {
     const int g = (p.Smax + 31) / 32;
