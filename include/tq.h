@@ -601,7 +601,7 @@ int tq_attn_decode_weights(const void *q, int q_dtype, const uint8_t *k_blocks, 
  *   kept      device int32 [B][Hkv][keep]: the indices in ascending order,
  *             -1 past the last one.
  *   new_lens  device int32 [B]: min(L_b, keep); not the seq_lens array.
- * first + last <= keep; T <= 2^30.  No workspace.  Errors: TQ_ERR_ARG,
+ * first + last <= keep; T and keep <= 2^30.  No workspace.  Errors: TQ_ERR_ARG,
  * TQ_ERR_UNSUPPORTED, TQ_ERR_ALIGN, TQ_ERR_CUDA. */
 int tq_evict_select(const float *weights, int64_t row_stride, const int32_t *seq_lens, int B, int Hkv, int T,
                     int keep, int first, int last, int32_t *kept, int32_t *new_lens, void *stream);

@@ -490,7 +490,7 @@ extern "C" int tq_evict_select(const float *weights, int64_t row_stride, const i
     if (B <= 0 || Hkv <= 0 || T < 1 || keep < 1 || first < 0 || last < 0 || (int64_t)first + last > keep ||
         row_stride < T)
         return TQ_ERR_ARG;
-    if (T > (1 << 30)) return TQ_ERR_UNSUPPORTED;
+    if (T > (1 << 30) || keep > (1 << 30)) return TQ_ERR_UNSUPPORTED;   // (indices plus a cluster's threads fit int)
     if (seq_lens == new_lens) return TQ_ERR_ARG;   // other rows still read the old lengths
     if (!aligned(weights, 4) || !aligned(kept, 4) || !aligned(new_lens, 4) || !aligned(seq_lens, 4)) return TQ_ERR_ALIGN;
     const int64_t rows = (int64_t)B * Hkv;
