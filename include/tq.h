@@ -583,7 +583,7 @@ size_t tq_attn_weights_workspace_bytes(int B, int Hq, int Hkv, int T);
  * A query with a NaN or +inf score gives NaN outputs and NaN weights (of its
  * KV head); a key of score -inf gets weight 0.  Results do not depend on
  * timing.  Errors: TQ_ERR_ARG, TQ_ERR_UNSUPPORTED (turboq8,
- * Hq / Hkv > 8, page_tokens not a multiple of 8), TQ_ERR_ALIGN,
+ * Hq / Hkv > 8, page_tokens not a multiple of 8, T > 2^31 - 8192), TQ_ERR_ALIGN,
  * TQ_ERR_WORKSPACE, TQ_ERR_CUDA. */
 int tq_attn_decode_weights(const void *q, int q_dtype, const uint8_t *k_blocks, const tq_codebook *kcb,
                            const uint8_t *v_blocks, const tq_codebook *vcb, const int32_t *block_table, int max_pages,

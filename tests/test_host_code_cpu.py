@@ -61,3 +61,29 @@ int main(int argc, char **argv) {
             t += n
         assert pieces == want, (t0, page)
         assert all(n >= 0 for n in v[1::2])
+
+
+def test_weights_ctas_cover_every_context(tmp_path):
+    """CTAs of equal shares cover the context once, none without a token, for contexts up to the longest."""
+    prog = program(tmp_path, r"""
+#include <cstdio>
+#include <cstdlib>
+#include "tq_attn_mma.h"
+int main(int argc, char **argv) {
+    std::printf("%d\n", tq::kMmaMaxTokens);
+    for (int i = 1; i + 2 < argc; i += 3) {
+        int64_t per;
+        const int parts = tq::weights_parts(atoi(argv[i]), atoll(argv[i + 1]), atoi(argv[i + 2]), per);
+        std::printf("%d %lld\n", parts, (long long)per);
+    }
+}
+""")
+    longest = 2**31 - 8192
+    calls = [(sms, segs, T) for sms in (1, 152) for segs in (1, 3, 32, 256, 5000, 10**6)
+             for T in (1, 31, 33, 1024, 1025, 32769, 10**6 + 1, 2**30, 2**30 + 5, 2**31 - 450000, longest)]
+    out = run(prog, *[x for c in calls for x in c]).splitlines()
+    assert int(out[0]) == longest
+    for (sms, segs, T), line in zip(calls, out[1:]):
+        parts, per = map(int, line.split())
+        assert parts >= 1 and per % 32 == 0 and parts * per >= T > (parts - 1) * per, (sms, segs, T)
+        assert parts <= max(1, -(-sms * 32 // segs)) and (per >= 512 or parts == 1)   # (1025 tokens: 2 x 544)

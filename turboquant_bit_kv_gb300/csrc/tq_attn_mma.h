@@ -85,6 +85,22 @@ __host__ __device__ inline void chunk_piece(int t0, int page, int i, int &t, int
     len = at < end ? (int)min64(i == 0 ? head : page, end - at) : 0;
 }
 
+// Most tokens of a context whose scores are kept: positions up to a round of
+// the kernels' loops (64 chunks) past the last one fit 32 bits.
+constexpr int kMmaMaxTokens = 0x7FFFFFFF - 8191;
+
+// The weights' part of the merge: CTAs per segment, each of `per` tokens (a
+// multiple of kMmaChunk): about 32 CTAs per SM, but no more than one for every
+// kWeightsTokens tokens (each works out its heads' maximum and sum).
+constexpr int kWeightsTokens = 1024;
+inline int weights_parts(int sms, int64_t segs, int T, int64_t &per) {
+    const int64_t wanted = ((int64_t)sms * 32 + segs - 1) / segs;
+    const int64_t most = ((int64_t)T + kWeightsTokens - 1) / kWeightsTokens;
+    const int64_t parts = min64(wanted, most);
+    per = ((T + parts - 1) / parts + kMmaChunk - 1) / kMmaChunk * kMmaChunk;
+    return (int)((T + per - 1) / per);
+}
+
 // Slot groups of 128 threads in a combine CTA: one per 32 slots of Smax, at most kCombineMaxGroups.
 inline int mma_combine_groups(const MmaPlan &p) {
     const int g = (p.Smax + 31) / 32;

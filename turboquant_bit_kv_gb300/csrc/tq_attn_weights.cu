@@ -39,7 +39,6 @@ int launch_attn_prep_mma(const AttnArgs &a, const MmaPlan &plan, int qjl, cudaSt
 namespace {
 
 constexpr int kMergeBatch = 16;      // slots a merging thread loads at once (one round covers 16 x groups)
-constexpr int kWeightsTokens = 1024; // tokens of a weights CTA at least
 
 struct WeightsArgs {
     const float *ws;
@@ -49,7 +48,8 @@ struct WeightsArgs {
     float *weights;
     void *out;
     int64_t w_stride;
-    int Hq, Hkv, G, T, B, parts, per;   // parts: weights CTAs per segment, of per tokens each (a multiple of 32)
+    int64_t per;
+    int Hq, Hkv, G, T, B, parts;   // parts: weights CTAs per segment, of per tokens each (a multiple of 32)
     int out_dtype;
     float decay, out_scale;
     uint32_t signs[4];
@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(kAttnThreads * kCombineMaxGroups, 2) attn_weig
         const int sl = a.seq_lens[b];
         L = sl < 0 ? 0 : (sl > a.T ? a.T : sl);
     }
-    const int t0 = merge ? 0 : (int)(unit % a.parts) * a.per;
+    const int64_t t0 = merge ? 0 : unit % a.parts * a.per;
     if (t0 >= L && !merge) return;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     // the segment's slots: the workers whose ranges meet its chunks
@@ -170,18 +170,18 @@ __global__ void __launch_bounds__(kAttnThreads * kCombineMaxGroups, 2) attn_weig
         }
         __syncthreads();
     };
-    const int end = min(t0 + a.per, L);
+    const int end = (int)min64(t0 + a.per, L);
     float *w = a.weights + j * a.w_stride;
     const float *sc = a.scores + j * plan.C * (kMmaChunk * a.G);
     switch (a.G) {
-        case 1: add_weights<1>(sc, ml, w, t0, end, a.decay, stats); break;
-        case 2: add_weights<2>(sc, ml, w, t0, end, a.decay, stats); break;
-        case 3: add_weights<3>(sc, ml, w, t0, end, a.decay, stats); break;
-        case 4: add_weights<4>(sc, ml, w, t0, end, a.decay, stats); break;
-        case 5: add_weights<5>(sc, ml, w, t0, end, a.decay, stats); break;
-        case 6: add_weights<6>(sc, ml, w, t0, end, a.decay, stats); break;
-        case 7: add_weights<7>(sc, ml, w, t0, end, a.decay, stats); break;
-        default: add_weights<8>(sc, ml, w, t0, end, a.decay, stats); break;
+        case 1: add_weights<1>(sc, ml, w, (int)t0, end, a.decay, stats); break;
+        case 2: add_weights<2>(sc, ml, w, (int)t0, end, a.decay, stats); break;
+        case 3: add_weights<3>(sc, ml, w, (int)t0, end, a.decay, stats); break;
+        case 4: add_weights<4>(sc, ml, w, (int)t0, end, a.decay, stats); break;
+        case 5: add_weights<5>(sc, ml, w, (int)t0, end, a.decay, stats); break;
+        case 6: add_weights<6>(sc, ml, w, (int)t0, end, a.decay, stats); break;
+        case 7: add_weights<7>(sc, ml, w, (int)t0, end, a.decay, stats); break;
+        default: add_weights<8>(sc, ml, w, (int)t0, end, a.decay, stats); break;
     }
 }
 
@@ -247,7 +247,7 @@ int64_t most_workers(int B, int Hkv, int T) {
 using namespace tq;
 
 extern "C" size_t tq_attn_weights_workspace_bytes(int B, int Hq, int Hkv, int T) {
-    if (B <= 0 || Hq <= 0 || Hkv <= 0 || T <= 0 || Hq % Hkv || Hq / Hkv > 8) return 0;
+    if (B <= 0 || Hq <= 0 || Hkv <= 0 || T <= 0 || T > kMmaMaxTokens || Hq % Hkv || Hq / Hkv > 8) return 0;
     return (size_t)Layout(B, Hq, Hkv, T, most_workers(B, Hkv, T)).floats * sizeof(float);
 }
 
@@ -268,19 +268,16 @@ extern "C" int tq_attn_decode_weights(const void *q, int q_dtype, const uint8_t 
         return TQ_ERR_ARG;
     }
     const int G = Hq / Hkv;
-    if (G > 8 || dtype_bytes(q_dtype) == 0 || dtype_bytes(out_dtype) == 0) return TQ_ERR_UNSUPPORTED;
+    if (G > 8 || T > kMmaMaxTokens) return TQ_ERR_UNSUPPORTED;
+    if (dtype_bytes(q_dtype) == 0 || dtype_bytes(out_dtype) == 0) return TQ_ERR_UNSUPPORTED;
     if (!codebook_ok(kcb) || !codebook_ok(vcb)) return TQ_ERR_UNSUPPORTED;
     if (!aligned(q, dtype_bytes(q_dtype)) || !aligned(k_blocks, 16) || !aligned(v_blocks, 16) || !aligned(out, 16) ||
         !aligned(workspace, 16) || !aligned(weights, 4) || !aligned(seq_lens, 4) || !aligned(block_table, 4))
         return TQ_ERR_ALIGN;
     if (workspace_bytes < tq_attn_weights_workspace_bytes(B, Hq, Hkv, T)) return TQ_ERR_WORKSPACE;
-    // weights CTAs per segment: about 32 per SM, each of kWeightsTokens tokens at least (every one of
-    // them works out its heads' maximum and sum)
-    const int64_t segs = (int64_t)B * Hkv, wanted = ((int64_t)sm_count() * 32 + segs - 1) / segs;
-    const int most = (T + kWeightsTokens - 1) / kWeightsTokens;
-    int parts = (int)(wanted < most ? wanted : most);
-    const int per = ((T + parts - 1) / parts + kMmaChunk - 1) / kMmaChunk * kMmaChunk;
-    parts = (T + per - 1) / per;
+    const int64_t segs = (int64_t)B * Hkv;
+    int64_t per;
+    const int parts = weights_parts(sm_count(), segs, T, per);
     const int64_t grid = (int64_t)B * Hq + (int64_t)B * Hkv * parts;
     if (grid > 0x7FFFFFFF || segs * ((T + kMmaChunk - 1) / kMmaChunk) > 0x7FFFFFFF) return TQ_ERR_UNSUPPORTED;
 
