@@ -524,8 +524,7 @@ int tq_rope_apply(const void *x, int dtype, int64_t n_tok, int heads, int64_t x_
  * then keys and values are encoded as by tq_encode_kv.  Codes and norms are
  * those of the definition evaluated in double precision (y rounded once to
  * float32 and compared with the float32 boundaries; the norm rounded once to
- * fp16): a coordinate less than about 1e-10 from a boundary may fall either
- * way.
+ * fp16): a coordinate less than 1e-11 from a boundary may fall either way.
  *   k, v      device rows of dtype, head h of token n at n * tok_stride + h *
  *             head_stride elements (alignment as tq_rope_apply).  k with
  *             k_blocks, or v with v_blocks, may be NULL (then not written).

@@ -5,6 +5,10 @@ import numpy as np
 import pytest
 import torch
 
+import oracle
+from oracle import codec
+from parity_util import oracle_books
+from test_gpu_rope_insert import rotated
 from turboquant_bit_kv_gb300 import workloads
 
 pytestmark = pytest.mark.gpu
@@ -46,3 +50,102 @@ def test_attend_in_one_large_page(tq, page):
         got.append((w, out))
     assert torch.isfinite(got[0][1]).all()
     assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+
+
+# ---------------------------------------------------------------- decisions next to a boundary
+
+def encoded_rows(x, bits, signs, zone=0.0):
+    """Codes and norms of float64 rows by 64-bit arithmetic, the codes' coordinates shifted by zone; signs [128] of
+    +-1."""
+    norm = np.sqrt((x * x).sum(-1))
+    y = (x * signs) @ oracle.hadamard(128).T / (np.sqrt(128) * norm[:, None]) + zone
+    return np.searchsorted(oracle_books()[bits][2], y.astype(np.float32), side="right"), codec.fp16_rne(norm)
+
+
+def check_rows(tq, x, pos, rope, bits, signs, rows, diagonal, keys=True):
+    """Rows x [n, heads, 128] as keys (or as values), in one call and in calls of at most 24 tokens (large and small
+    calls take different kernels), against rows [n * heads, 128] (float64, rotated).
+
+    A coordinate nearer than 1e-11 to a boundary may fall either way: near a boundary the kernels decide in
+    double-float, whose sines and cosines are off by less than 2^-38 together, sqrt(2) of it in a pair's sum, the
+    norms of 64 pairs 8 of the row's at most: 8 sqrt(2) 2^-38 / sqrt(128) = 3.6e-12 of y.  Sums of 128 terms in
+    double-float, the norm and its root add less than 40 * 2^-44."""
+    n, heads = x.shape[:2]
+    cb = tq.tq_codebook_load(128, bits)
+    low, norm = encoded_rows(rows, bits, diagonal, -1e-11)
+    high, _ = encoded_rows(rows, bits, diagonal, 1e-11)
+    dst = torch.arange(n, device="cuda") * heads
+    for step in (n, 24):
+        cache = torch.zeros(n * heads, 2 + 16 * bits, dtype=torch.uint8, device="cuda")
+        for i in range(0, n, step):
+            p = None if rope is None else pos[:, i:i + step].contiguous()
+            part, d = x[i:i + step], dst[i:i + step]
+            if keys:
+                tq.tq_insert_kv(part, None, p, rope, cb, None, signs, cache, None, d, 1)
+            else:
+                tq.tq_insert_kv(None, part, None, None, None, cb, signs, None, cache, d, 1)
+        code, half = codec.unpack_block(cache.cpu().numpy(), bits)
+        assert np.array_equal(half, norm)
+        wrong = np.nonzero(((code < low) | (code > high)).any(-1))[0]
+        assert wrong.size == 0, "%d of %d rows differ (calls of %d tokens), the first %s" % (
+            wrong.size, n * heads, step, wrong[:5])
+
+
+# angle (2^-32 turns) at which the float32 sine and cosine are off the furthest along the circle, 2.1 * 2^-24
+WORST_ANGLE = 531149040
+
+
+@pytest.mark.parametrize("style", [0, 1])
+@pytest.mark.parametrize("rot", [128, 96])
+@pytest.mark.parametrize("bits", [2, 4])
+def test_insert_of_rows_whose_errors_add_up(tq, style, rot, bits):
+    """Keys whose pairs are all alike and turn by one angle: the errors of its sine and cosine add up over the row,
+    in a coordinate that is within 2.5e-6 of a standard deviation of the boundary at 0."""
+    n, heads, pairs = 3000, 5, rot // 2
+    rope = tq.tq_rope_load(rot, style=style)
+    tq.tq_rope_set_freqs(rope, [WORST_ANGLE * 2 * np.pi / 2**32] * pairs)
+    rng = np.random.default_rng(rot + bits + style)
+    pos = np.where(rng.random((1, n)) < 0.5, 1, -1)
+    theta = pos[0, :, None, None] * (WORST_ANGLE * 2 * np.pi / 2**32)
+    # rotated pairs (1, -1), each a little off; the rest of the row small
+    ra, rb = (s + 1e-3 * rng.standard_normal((n, heads, pairs)) for s in (1.0, -1.0))
+    rest = 1e-2 * rng.standard_normal((n, heads, 128 - rot))
+    norm = np.sqrt((ra**2).sum(-1) + (rb**2).sum(-1) + (rest**2).sum(-1))
+    target = rng.uniform(-2.5e-6, 2.5e-6, (n, heads)) * norm
+    shift = (target - ra.sum(-1) - rb.sum(-1) - rest.sum(-1)) / rot
+    ra, rb = ra + shift[..., None], rb + shift[..., None]
+    a, b = ra * np.cos(theta) + rb * np.sin(theta), rb * np.cos(theta) - ra * np.sin(theta)
+    x = np.zeros((n, heads, 128))
+    i = np.arange(pairs)
+    fi, se = (i, i + pairs) if style == 0 else (2 * i, 2 * i + 1)
+    x[..., fi], x[..., se], x[..., rot:] = a, b, rest
+    x = torch.from_numpy(x).float().cuda()
+    turned = rotated(x.double().cpu().numpy(), pos, rope)[0].reshape(-1, 128)
+    check_rows(tq, x, torch.from_numpy(pos).cuda(), rope, bits, tq.tq_signs(), turned, np.ones(128))
+
+
+@pytest.mark.parametrize("keys", [True, False])
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_insert_of_rows_near_a_hadamard_row(tq, dtype, keys):
+    """Rows of two magnitudes that cancel in one coordinate and agree in another: partial sums as large as sums of
+    128 elements of the norm can be, and roundings that all go the same way."""
+    n, heads, bits = 3000, 5, 4
+    rng = np.random.default_rng(5)
+    h, m = oracle.hadamard(128), n * heads
+    j, k = rng.integers(1, 128, m), rng.integers(1, 128, m)
+    same = h[j] == h[k]                                            # (half of the elements, or all)
+    ulp = {"f32": 2.0**-23, "bf16": 2.0**-7, "f16": 2.0**-10}[dtype]
+    hi = 1 + rng.integers(0, 64, (m, 1)) * ulp
+    if dtype == "f32":
+        hi = 1 + rng.integers(4, 2**22, (m, 1)) * ulp
+    lo = hi + rng.integers(-3, 4, (m, 1)) * ulp
+    diagonal = oracle.sign_diagonal(workloads.SIGN_SEED)
+    x = diagonal * h[j] * np.where(same, hi, lo) * 2.0**rng.integers(-3, 4, (m, 1))
+    few = rng.random((m, 128)) < 0.02
+    x = np.where(few & (rng.random((m, 1)) < 0.5), x * 2.0**rng.integers(-22, 1, (m, 128)), x)
+    x = torch.from_numpy(x.reshape(n, heads, 128)).to({"f32": torch.float32, "bf16": torch.bfloat16,
+                                                       "f16": torch.float16}[dtype]).cuda()
+    signs = tq.tq_signs_from_seed(workloads.SIGN_SEED)
+    rows = x.double().cpu().numpy().reshape(-1, 128)
+    # sums of 128 values of 24 bits, 2^25 apart at most, are exact in 64 bits whatever their order
+    check_rows(tq, x, None, None, bits, signs, rows, diagonal, keys)

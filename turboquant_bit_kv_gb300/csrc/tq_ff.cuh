@@ -28,6 +28,17 @@ __device__ __forceinline__ ff ff_add(ff a, ff b) {
     return ff_quick(s, e + (a.l + b.l));
 }
 
+// a + b and a^2 of float32, exact.
+__device__ __forceinline__ ff ff_sum(float a, float b) {
+    ff r;
+    two_sum(a, b, r.h, r.l);
+    return r;
+}
+__device__ __forceinline__ ff ff_square(float a) {
+    const float p = __fmul_rn(a, a);
+    return {p, fmaf(a, a, -p)};
+}
+
 __device__ __forceinline__ ff ff_neg(ff a) { return {-a.h, -a.l}; }
 __device__ __forceinline__ ff ff_sub(ff a, ff b) { return ff_add(a, ff_neg(b)); }
 

@@ -38,18 +38,20 @@
 //
 // Borders.  Decisions are those of 64-bit arithmetic (y rounded once to
 // float32 and compared with the float32 boundaries), although the row is
-// transformed in float32: a row with a coordinate closer to a boundary than
-// kEps or a norm closer to a rounding border of fp16 than kTieUlps (both far
-// above the float32 error; about 0.1% of rows each) is listed, and when the CTA
-// is through its tiles the listed rows are taken again, one by each of its warps
-// (four for their norms alone): in float32 once more, and each coordinate near a
-// boundary as one sum in double-float.  Rows of a sum of squares outside
-// float32's safe range go through double precision.  (The double-precision pipe
-// has one sixty-fourth of the float32 rate: on it, all such rows together cost
-// 168 of the 433 us of a prompt of 131072 tokens x 8 heads; in double-float but
-// one at a time between the tiles, where three warps wait for the fourth, 157 of
-// 398.  Whole rows in double-float at the end cost 5001 tokens x 4 heads 18.5 us
-// instead of 17.0.)  A CTA whose list overflows takes all its rows again.
+// transformed in float32: a row with a coordinate closer to a boundary, or a
+// norm closer to a rounding border of fp16, than float32 arithmetic can be off
+// whatever the row holds (the bounds below; up to 0.8% of rows for the codes,
+// 0.2 to 0.4% for the norms) is listed, and when the CTA is through its tiles the
+// listed rows are taken again, one by each of its warps (four for their norms
+// alone): in float32 once more, and each coordinate near a boundary as one sum
+// in double-float.  Rows of a sum of squares outside float32's safe range go
+// through double precision.  (The double-precision pipe has one sixty-fourth of
+// the float32 rate.  Of the 289 us of a prompt of 131072 tokens x 8 heads the
+// listed rows are about 34: 23 more than with borders at the furthest wrong
+// decision seen on random rows, which rows made for it get past.  Between the
+// tiles, whenever 8, 16 or 32 rows are listed, they cost 77, 51 and 8 us more
+// than at the end: their code is then fetched again.)  A CTA whose list
+// overflows takes all its rows again.
 //
 // Few rows go to a kernel of their own, a warp per row (insert_few_kernel).
 //
@@ -70,25 +72,51 @@ constexpr int kTok = 16;             // tokens of a tile
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr float kGrid = 63.f;        // cells per unit of y
-// Distance to a boundary, in v = 63 y, below which a row's codes are decided
-// again: 1.25e-6 of a coordinate's standard deviation (1 / sqrt(128)).  The
-// float32 path (rope, the fp16 split, the products' accumulation, three
-// butterfly stages and the scale, each an ulp or less of partial sums of the
-// row's size) is off by 1.1e-7 of it (rms); over 1.2e9 coordinates of keys and
-// values of all types, loud channels among them, the furthest decision it got
-// wrong lay 4.3e-7 from its boundary.
-constexpr float kEps = 1.25e-6f * kGrid * 0.08838834764831845f;
-// Distance of the norm to a rounding border of fp16, in units of its last
-// float32 place: it is off by about one of them (the furthest of the wrong
-// roundings in the same rows 1.1e-7 of the norm, two units at most).
-constexpr uint32_t kTieUlps = 5;
+constexpr float kUnit = 5.568465901844061f;   // 63 / sqrt(128): a standard deviation in v = 63 y
+// How far a coordinate can be off in float32, from the operations it goes
+// through, all errors at their largest and in the same direction.  In units of
+// u = 2^-24 of a coordinate's standard deviation (the row's norm / sqrt(128));
+// the sizes of a row's elements add up to sqrt(128) = 11.3 of its norm at most,
+// the norms of its 64 pairs to 8:
+//   rope      24.3  sine and cosine, as a vector off by 2.15 u (all 2^32 angles
+//                   evaluated), add up to sqrt(2) times that in a pair's sum
+//             22.6  products and sums, 2 sqrt(2) u a pair
+//   split     22.6  two fp16 parts: 2 u of each element
+//   products  22.6  sums of 16 terms by the tensor cores, cut to 24 bits; they
+//              1.4  also cut each term at 2^-25 of the largest one's power of two
+//                   (as measured, sum by sum), which the lower parts' sum can
+//                   lose by; terms within 2^14 of the largest lose nothing, and a
+//                   smaller one takes more from the sizes' sum than its cut adds
+//   stages    11.3  each butterfly stage but the last: three after the products,
+//                   seven in insert_few_kernel
+// and, times the coordinate (the outermost boundary b at most): the norm 4.5 (10
+// more from the products where it is taken from their results; few rows 4), its
+// inverse 1.5, the constant and its product 1.6, the boundary in v 1, the
+// rounding of y to float32 1, the last stage 1.  Each sum is raised by a
+// hundredth and more for products of these errors.  (Rows whose errors do add up
+// are easily made: pairs all alike at one angle are decided wrongly up to 2e-6
+// of a standard deviation away.  Rows of random elements: 4.3e-7 in 1.2e9
+// coordinates.)
+struct Bound {
+    float row, level;   // and times b
+};
+constexpr Bound kBoundRope = {118.f, 11.5f};     // rotated rows: 116.2 + 10.6 b
+constexpr Bound kBoundSplit = {71.f, 11.5f};     // float32 rows without rope: 69.2 + 10.6 b
+constexpr Bound kBoundDirect = {46.f, 22.f};     // 16-bit rows without rope: 45.2 + 20.6 b
+constexpr Bound kBoundFewRope = {117.f, 11.5f};  // insert_few_kernel: 114.8 + 10.1 b
+constexpr Bound kBoundFew = {69.f, 11.5f};       // 67.9 + 10.1 b
+
+// How far a norm can be off, in units of its last float32 place (u of it at
+// least): 4.5 (few rows 4) from the sum of squares, 1.5 from its inverse root, 1
+// from their product, 10 more where the squares are of the products' results.
+constexpr uint32_t kTieUlps = 8, kTieUlpsDirect = 18;
 
 // Rows per SM, keys and values together, up to which a warp takes a row
 // (insert_few_kernel).  us, against insert_kernel's, for bfloat16 keys with
-// rotary positions in 4 bits and values in 2, 8 heads, by tokens: 16 3.3 / 8.4,
-// 256 6.7 / 11.2, 512 8.0 / 11.3, 768 (81 rows per SM) 10.2 / 11.8, 1024 13.3 /
-// 12.2, 2048 20.2 / 12.8.  Keys alone cross at 67, without rotary positions at
-// 108 rows per SM.
+// rotary positions in 4 bits and values in 2, 8 heads, by tokens: 16 4.2 / 11.5,
+// 256 7.4 / 12.3, 512 9.0 / 12.8, 768 (81 rows per SM) 10.7 / 13.1, 1024 12.6 /
+// 13.4, 1280 14.6 / 13.6, 2048 20.1 / 14.3.  Keys alone cross at 75, without
+// rotary positions at 130 rows per SM.
 constexpr int kFewRows = 80;
 
 enum { kRopeNone = 0, kRopeHalf1, kRopeHalf2, kRopeHalf3, kRopeHalf4, kRopeAdjacent };
@@ -99,6 +127,9 @@ struct Side {
     int64_t tok, head;      // row strides in bytes
     int64_t n_blocks;
     float b[15];            // boundaries
+    float eps, eps_few;     // distance to a boundary, in v = 63 y, below which a coordinate is decided again; the
+                            // same for insert_few_kernel's arithmetic
+    uint32_t ulps;          // distance of the norm to a rounding border of fp16 below which it is rounded again
     int bits;
     int style;              // kRope*
 };
@@ -110,13 +141,18 @@ struct InsertArgs {
     int units;              // of a side: (tile group, head group) pairs
     int heads, heads_per_cta, groups;   // groups of heads per tile group
     int tiles;              // token tiles of a CTA at once: 4, 2 or 1 for 1, 2 or more heads
+    int list;               // rows of either kind that a CTA can list
     int ctas[2];            // of each side
     uint32_t signs[4];
 };
 
-constexpr int kList = 256;               // rows to take again that a CTA can list
 constexpr int kStage = kTok * 33 + 8;    // half words a warp stages its 16 blocks in (and the 128 values of a
                                          // row taken again)
+
+struct Listed {     // a row to take again
+    int unit;
+    uint32_t row;   // head * 64 + token of the unit
+};
 
 struct Shared {
     uint2 cells[128 * 16];                    // (boundary, boundaries below + 1) x 16 copies
@@ -125,14 +161,15 @@ struct Shared {
     uint4 flip[4][4];                         // sign bits of the 16-bit elements 32 c + 8 t .. + 7
     uint64_t turn[kRopePairs];                // the rope, and whether a pair's two signs differ (bit 2 of axis)
     uint8_t axis[kRopePairs];
-    int64_t list[kList];                      // token * heads + head: norms from the front, rows from the back
-    int listed[2];
+    int listed[2];                            // rows to list: for their norms, and whole
     // cosines and sines (negated where the pair's two signs differ) of two
     // neighbouring pairs, (c, c', s, s'); unit u of token n and thread t at
     // [(u * 16 + n) * 4 + t].  Halves: unit 4 c + k holds pairs 32 c + 8 t + 2 k and the next.
-    // Adjacent: unit 2 c + k holds pairs 16 c + 4 t + 2 k and the next.  A table per token tile.
+    // Adjacent: unit 2 c + k holds pairs 16 c + 4 t + 2 k and the next.  A table per token tile, then the lists
+    // of rows for their norms and of whole rows.
     alignas(16) float4 cs[][8 * kTok * 4];
 };
+__device__ __forceinline__ Listed *list_of(Shared &sm, int tiles) { return reinterpret_cast<Listed *>(sm.cs + tiles); }
 
 template <int DT>
 struct Row {
@@ -288,59 +325,36 @@ __device__ __noinline__ void near_row(const uint8_t *row, uint8_t *block, const 
 }
 
 // The few coordinates of a row that float32 does not decide, in double-float:
-// coordinate j is the sum of +-x, so it costs one reduction and no transform.
+// coordinate j is a sum over the row's pairs, so it costs one reduction and no
+// transform.
 // near: bits i of the lane's elements 4 lane + i to decide, cell[i] the number
 // of boundaries below their cells.  Returns the lane's codes; the norm is
 // rounded again as well.
-template <int DT>
 __device__ __noinline__ uint32_t decide_few(float x0, float x1, float x2, float x3, uint32_t near, uint32_t cell,
                                             uint32_t code, uint64_t angle0, uint64_t angle1, int partner, uint32_t flip,
-                                            const Side &sd, uint8_t *block) {
+                                            int pairs, const Side &sd, uint8_t *block) {
     const int lane = threadIdx.x & 31;
-    const float x[4] = {x0, x1, x2, x3};
-    ff r[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) r[i] = ff_of(x[i]);
-    if (sd.style != kRopeNone) {
-        ff s[2], c[2];
+    // two pairs (A, B) of the row, of elements ia and ia + apart: adjacent ones, or of the halves (the lane of the
+    // upper half has the second two of the four pairs that both hold elements of)
+    const bool half = partner >= 0 && sd.style != kRopeAdjacent, upper = half && partner < lane;
+    const int from = half ? partner : lane;
+    const float o0 = __shfl_sync(0xffffffffu, upper ? x0 : x2, from);
+    const float o1 = __shfl_sync(0xffffffffu, upper ? x1 : x3, from);
+    const uint32_t other = __shfl_sync(0xffffffffu, flip, from);
+    const float A[2] = {!half ? x0 : upper ? o0 : x0, !half ? x2 : upper ? o1 : x1};
+    const float B[2] = {!half ? x1 : upper ? x2 : o0, !half ? x3 : upper ? x3 : o1};
+    const uint32_t fa = !half ? (flip & 1u) | (flip >> 1 & 2u) : upper ? other >> 2 : flip;   // (bit z)
+    const uint32_t fb = !half ? (flip >> 1 & 1u) | (flip >> 2 & 2u) : upper ? flip >> 2 : other;
+    const int ia = upper ? 4 * from + 2 : 4 * lane, next = half ? 1 : 2, apart = half ? pairs : 1;
+    ff s[2], c[2];
 #pragma unroll 1
-        for (int z = 0; z < 2; ++z) {
-            ff sz, cz;
-            rope_sincos_ff(z ? angle1 : angle0, sz, cz);
-            if (z) s[1] = sz, c[1] = cz;
-            else s[0] = sz, c[0] = cz;
-        }
-        const bool adj = sd.style == kRopeAdjacent, upper = partner < lane;
-        if (adj) {
-            if (partner >= 0)
-#pragma unroll
-                for (int z = 0; z < 2; ++z) {
-                    r[2 * z] = ff_add(ff_scale(c[z], x[2 * z]), ff_scale(s[z], -x[2 * z + 1]));
-                    r[2 * z + 1] = ff_add(ff_scale(c[z], x[2 * z + 1]), ff_scale(s[z], x[2 * z]));
-                }
-        } else {
-            const int from = partner < 0 ? lane : partner;
-            ff so[2], co[2];
-#pragma unroll
-            for (int z = 0; z < 2; ++z) {
-                so[z] = {__shfl_sync(0xffffffffu, s[z].h, from), __shfl_sync(0xffffffffu, s[z].l, from)};
-                co[z] = {__shfl_sync(0xffffffffu, c[z].h, from), __shfl_sync(0xffffffffu, c[z].l, from)};
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float o = __shfl_sync(0xffffffffu, x[i], from);
-                const bool mine = (i >= 2) == upper;
-                if (partner >= 0)
-                    r[i] = ff_add(ff_scale(mine ? c[i & 1] : co[i & 1], x[i]), ff_scale(mine ? s[i & 1] : so[i & 1], upper ? o : -o));
-            }
-        }
+    for (int z = 0; z < 2; ++z) {
+        ff sz = {0.f, 0.f}, cz = {1.f, 0.f};
+        if (partner >= 0) rope_sincos_ff(z ? angle1 : angle0, sz, cz);
+        if (z) s[1] = sz, c[1] = cz;
+        else s[0] = sz, c[0] = cz;
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if ((flip >> i) & 1u) r[i] = ff_neg(r[i]);
-    ff squares = ff_mul(r[0], r[0]);
-#pragma unroll
-    for (int i = 1; i < 4; ++i) squares = ff_add(squares, ff_mul(r[i], r[i]));
+    ff squares = ff_add(ff_add(ff_square(x0), ff_square(x1)), ff_add(ff_square(x2), ff_square(x3)));
     uint32_t who = __ballot_sync(0xffffffffu, near != 0);
     bool first = true;
     do {
@@ -349,7 +363,13 @@ __device__ __noinline__ uint32_t decide_few(float x0, float x1, float x2, float 
         const int e = bits ? __ffs(bits) - 1 : 0, j = 4 * src + e;
         ff v = ff_of(0.f), ss = squares;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v = ff_add(v, __popc((4 * lane + i) & j) & 1 ? ff_neg(r[i]) : r[i]);
+        for (int z = 0; z < 2; ++z) {
+            // +-(A c - B s) +- (B c + A s) = c (+-A +- B) + s (+-A -+ B)
+            const int at = ia + z * next;
+            const bool na = (__popc(at & j) ^ (fa >> z)) & 1, nb = (__popc((at + apart) & j) ^ (fb >> z)) & 1;
+            const ff p = ff_sum(na ? -A[z] : A[z], nb ? -B[z] : B[z]), q = ff_sum(nb ? -A[z] : A[z], na ? B[z] : -B[z]);
+            v = ff_add(v, ff_add(ff_mul(c[z], p), ff_mul(s[z], q)));
+        }
 #pragma unroll 1
         for (int m = 1; m < 32; m <<= 1) {
             v = ff_add(v, shfl_(v, m));
@@ -463,6 +483,7 @@ __device__ __forceinline__ void few_row(const FewIn &n, const FewLane &w, const 
         x[3] = q.y;
     }
     const float4 in = make_float4(x[0], x[1], x[2], x[3]);
+    float ss = fmaf(x[0], x[0], x[1] * x[1]) + fmaf(x[2], x[2], x[3] * x[3]);   // (rope keeps the norm)
     uint64_t angle[2] = {0, 0};
     if (sd.style != kRopeNone) {
         float s[2], c[2];
@@ -497,7 +518,6 @@ __device__ __forceinline__ void few_row(const FewIn &n, const FewLane &w, const 
                 }
         }
     }
-    float ss = fmaf(x[0], x[0], x[1] * x[1]) + fmaf(x[2], x[2], x[3] * x[3]);
 #pragma unroll
     for (int i = 0; i < 4; ++i) x[i] = __uint_as_float(__float_as_uint(x[i]) ^ ((w.flip >> i) << 31));
     {
@@ -520,7 +540,7 @@ __device__ __forceinline__ void few_row(const FewIn &n, const FewLane &w, const 
     float inv;
     asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(ss));
     inv = fmaf(inv * fmaf(-ss * inv, inv, 1.f), 0.5f, inv);
-    const float nrm = ss * inv, scale = kGrid * 0.08838834764831845f * inv;
+    const float nrm = ss * inv, scale = kUnit * inv;
     const bool wild = !(ss >= 7.888609052210118e-31f && ss <= 1.2676506002282294e30f);
     const bool tie = ((__float_as_uint(nrm) & 0x1FFFu) - (0x1000u - kTieUlps)) <= 2 * kTieUlps ||
                      !(nrm >= 6.103515625e-05f && nrm < 65504.f);
@@ -530,7 +550,7 @@ __device__ __forceinline__ void few_row(const FewIn &n, const FewLane &w, const 
         const float v = fmaf(x[i], scale, 98304.f + 64.5f);
         const uint2 e = *reinterpret_cast<const uint2 *>(cells + ((__float_as_uint(v) & 0x3F80u) >> shift));
         const float d = fmaf(x[i], scale, -__uint_as_float(e.x));
-        near |= fabsf(d) < kEps ? 1u << i : 0u;
+        near |= fabsf(d) < sd.eps_few ? 1u << i : 0u;
         cell |= (e.y - 1) << (8 * i);
         code |= ((e.y + (uint32_t)(__float_as_int(d) >> 31)) & 15u) << (8 * i);
     }
@@ -541,19 +561,12 @@ __device__ __forceinline__ void few_row(const FewIn &n, const FewLane &w, const 
         if (who == 0 && !tie) {
             if (lane == 0) *reinterpret_cast<__half *>(block) = __float2half_rn(nrm);
         } else if (__popc(who) <= 4) {
-            code = decide_few<DT>(in.x, in.y, in.z, in.w, near, cell, code, angle[0], angle[1], w.turned ? w.partner : -1,
-                                  w.flip, sd, block);
+            code = decide_few(in.x, in.y, in.z, in.w, near, cell, code, angle[0], angle[1], w.turned ? w.partner : -1,
+                              w.flip, rope.rot_dim / 2, sd, block);
         }
         if (__popc(who) <= 4) write_codes(block, bits, code, lane);
         else near_row<DT>(row, block, sd, rope, a, tok, static_cast<ff *>(again));
     }
-}
-
-// The same for a row of insert_kernel's list.
-template <int DT>
-__device__ __noinline__ void again_row(const uint8_t *row, uint8_t *block, const Side &sd, const tq_rope &rope,
-                                       const InsertArgs &a, int64_t tok, const uint8_t *cells, void *again) {
-    few_row<DT>(few_load<DT>(row, tok, sd, rope, a), few_lane(sd, rope, a), cells, 0, row, block, sd, rope, a, tok, again);
 }
 
 // Norms of four rows (rope keeps them), one per eight lanes.
@@ -571,7 +584,7 @@ __device__ __noinline__ void norm_rows(const uint8_t *row, uint8_t *block, bool 
     if (write && l == 0) *reinterpret_cast<uint16_t *>(block) = ff_half(ff_sqrt(ss));
 }
 
-// The listed rows of the CTA, a warp each (four for their norms alone).  If a
+// The listed rows of the CTA, a warp each (four for their norms alone).  If the
 // list overflowed (inputs of many zeros, say), all its rows.
 template <int DT>
 __device__ __noinline__ void finish(int which, const tq_rope &rope, const InsertArgs &a) {
@@ -583,33 +596,63 @@ __device__ __noinline__ void finish(int which, const tq_rope &rope, const Insert
     uint16_t *stage = sm.stage[warp];
     const int ties = sm.listed[0], whole = sm.listed[1];
     const int64_t bytes = 2 + 16 * sd.bits;
+    const int cta = blockIdx.x - (which ? a.ctas[0] : 0), step = a.ctas[which], span = kTok * a.tiles;
     auto block_of = [&](int64_t tok, int head) { return sd.blocks + (a.dst[tok] + head * a.dst_head) * bytes; };
     auto row_of = [&](int64_t tok, int head) { return sd.x + tok * sd.tok + head * sd.head; };
-    if (max(ties, whole) > kList / 2) {
-        const int cta = blockIdx.x - (which ? a.ctas[0] : 0);
-        for (int unit = cta; unit < a.units; unit += a.ctas[which]) {
-            const int64_t tok0 = (int64_t)(unit / a.groups) * a.tiles * kTok, tok1 = min64(tok0 + a.tiles * kTok, a.n_tok);
-            const int head0 = unit % a.groups * a.heads_per_cta, head1 = min(head0 + a.heads_per_cta, a.heads);
-            for (int64_t tok = tok0 + warp; tok < tok1; tok += kWarps)
-                for (int head = head0; head < head1; ++head) {
-                    const int64_t dst = a.dst[tok], slot = dst < 0 ? -1 : dst + head * a.dst_head;
-                    if (slot < 0 || slot >= sd.n_blocks) continue;
-                    again_row<DT>(row_of(tok, head), block_of(tok, head), sd, rope, a, tok, cells, stage);
-                    __syncwarp();
-                }
+    auto token_of = [&](int unit, int t) { return (int64_t)(unit / a.groups) * span + t; };
+    const Listed *list = list_of(sm, a.tiles);
+    auto find = [&](const Listed &e, int64_t &tok, int &head) {
+        tok = token_of(e.unit, (int)(e.row & 63u));
+        head = (int)(e.row >> 6);
+    };
+    // this warp's next row: of the list, or of all the CTA's
+    const bool all = max(ties, whole) > a.list;
+    int unit = cta, in_unit = warp, in_group = 0;
+    int at = warp;
+    auto next = [&](int64_t &tok, int &head) {
+        if (!all) {
+            if (at >= whole) return false;
+            find(list[a.list + at], tok, head);
+            at += kWarps;
+            return true;
         }
-        return;
-    }
-    for (int i = warp; i < whole; i += kWarps) {
-        const int64_t id = sm.list[kList - 1 - i], tok = id / a.heads;
-        const int head = (int)(id - tok * a.heads);
-        again_row<DT>(row_of(tok, head), block_of(tok, head), sd, rope, a, tok, cells, stage);
+        while (unit < a.units) {
+            const int head0 = unit % a.groups * a.heads_per_cta, heads = min(a.heads_per_cta, a.heads - head0);
+            tok = token_of(unit, in_unit);
+            if (in_unit >= span || tok >= a.n_tok) {
+                unit += step;
+                in_unit = warp;
+                in_group = 0;
+            } else if (in_group == heads) {
+                in_unit += kWarps;
+                in_group = 0;
+            } else {
+                head = head0 + in_group++;
+                const int64_t dst = a.dst[tok], slot = dst < 0 ? -1 : dst + head * a.dst_head;
+                if (slot >= 0 && slot < sd.n_blocks) return true;
+            }
+        }
+        return false;
+    };
+    const FewLane lane_part = few_lane(sd, rope, a);
+    int64_t tok = 0;
+    int head = 0;
+    FewIn in;
+    bool more = next(tok, head);
+    if (more) in = few_load<DT>(row_of(tok, head), tok, sd, rope, a);
+    while (more) {   // (the next row on its way while this one is taken)
+        const FewIn now = in;
+        const int64_t t = tok;
+        const int h = head;
+        more = next(tok, head);
+        if (more) in = few_load<DT>(row_of(tok, head), tok, sd, rope, a);
+        few_row<DT>(now, lane_part, cells, 0, row_of(t, h), block_of(t, h), sd, rope, a, t, stage);
         __syncwarp();
     }
+    if (all) return;
     for (int i = 4 * warp; i < ties; i += 4 * kWarps) {
         const int q = i + (lane >> 3);
-        const int64_t id = sm.list[q < ties ? q : i], tok = id / a.heads;
-        const int head = (int)(id - tok * a.heads);
+        find(list[q < ties ? q : i], tok, head);
         norm_rows<DT>(row_of(tok, head), block_of(tok, head), q < ties);
     }
 }
@@ -1060,8 +1103,7 @@ __global__ void __launch_bounds__(kThreads, 4) insert_kernel(const __grid_consta
                     }
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    rope_row(x[r], style, sm.cs[tile] + (g + 8 * r) * 4 + t, t);
-                    float2 q[4];
+                    float2 q[4];   // (the norm is that of the row before its rotation)
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
 #pragma unroll
@@ -1075,6 +1117,7 @@ __global__ void __launch_bounds__(kThreads, 4) insert_kernel(const __grid_consta
                     const int e = (int)(__float_as_uint(ss[r]) >> 23) - 127;
                     const float pre = __uint_as_float((uint32_t)(127 + 9 - (e >> 1)) << 23);
                     post[r] = __uint_as_float((uint32_t)(127 - 9 + (e >> 1)) << 23);
+                    rope_row(x[r], style, sm.cs[tile] + (g + 8 * r) * 4 + t, t);
                     const float2 p2 = make_float2(pre, pre);
 #pragma unroll
                     for (int i = 0; i < 16; ++i) x[r][i >> 2][i & 3] = mul2(x[r][i >> 2][i & 3], p2);
@@ -1090,8 +1133,9 @@ __global__ void __launch_bounds__(kThreads, 4) insert_kernel(const __grid_consta
                             for (int q = 0; q < 2; ++q) split2(x[r][c][2 * s + q], hi[r][q], lo[r][q]);
 #pragma unroll
                         for (int nt = 0; nt < 2; ++nt) {
-                            mma16_first<false>(u[c][s][nt], hi[0][0], hi[1][0], hi[0][1], hi[1][1], bf[nt][0], bf[nt][1]);
-                            mma16<false>(u[c][s][nt], lo[0][0], lo[1][0], lo[0][1], lo[1][1], bf[nt][0], bf[nt][1]);
+                            // (the lower parts first: a sum loses places of its largest term's size)
+                            mma16_first<false>(u[c][s][nt], lo[0][0], lo[1][0], lo[0][1], lo[1][1], bf[nt][0], bf[nt][1]);
+                            mma16<false>(u[c][s][nt], hi[0][0], hi[1][0], hi[0][1], hi[1][1], bf[nt][0], bf[nt][1]);
                         }
                     }
             }
@@ -1105,10 +1149,10 @@ __global__ void __launch_bounds__(kThreads, 4) insert_kernel(const __grid_consta
                 asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(ss[r]));
                 inv = fmaf(inv * fmaf(-ss[r] * inv, inv, 1.f), 0.5f, inv);
                 nrm[r] = ss[r] * inv;
-                sc[r] = kGrid * 0.08838834764831845f * inv * post[r];
+                sc[r] = kUnit * inv * post[r];
                 // 2^-100 .. 2^100: squares neither underflow nor overflow (false for a NaN as well)
                 redo[r] = !(ss[r] >= 7.888609052210118e-31f && ss[r] <= 1.2676506002282294e30f);
-                tie[r] = ((__float_as_uint(nrm[r]) & 0x1FFFu) - (0x1000u - kTieUlps)) <= 2 * kTieUlps ||
+                tie[r] = ((__float_as_uint(nrm[r]) & 0x1FFFu) - (0x1000u - sd.ulps)) <= 2 * sd.ulps ||
                          !(nrm[r] >= 6.103515625e-05f && nrm[r] < 65504.f);   // (or outside fp16's normal range)
             }
             uint16_t *blkA = stage + g * (bytes / 2), *blkB = stage + (g + 8) * (bytes / 2);
@@ -1153,7 +1197,7 @@ __global__ void __launch_bounds__(kThreads, 4) insert_kernel(const __grid_consta
             uint32_t todo[2], ties[2];
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                uint32_t m = __ballot_sync(0xffffffffu, redo[r] || near[r] < kEps);
+                uint32_t m = __ballot_sync(0xffffffffu, redo[r] || near[r] < sd.eps);
                 m |= m >> 1;
                 todo[r] = (m | m >> 2) & 0x11111111u;
                 ties[r] = __ballot_sync(0xffffffffu, tie[r]) & 0x11111111u;
@@ -1162,10 +1206,10 @@ __global__ void __launch_bounds__(kThreads, 4) insert_kernel(const __grid_consta
                 // lane n < 16 lists row n: for its norm, or whole
                 const int bit = 4 * (lane & 7), odd = lane & 8;
                 const bool whole = ((odd ? todo[1] : todo[0]) >> bit) & 1u, tied = ((odd ? ties[1] : ties[0]) >> bit) & 1u;
-                const int64_t entry = my * a.heads + head;
                 if (lane < kTok && ok && (whole || tied)) {
                     const int at = atomicAdd(&sm.listed[whole ? 1 : 0], 1);
-                    if (at < kList / 2) sm.list[whole ? kList - 1 - at : at] = entry;
+                    if (at < a.list)
+                        list_of(sm, a.tiles)[whole ? a.list + at : at] = {unit, (uint32_t)head << 6 | (tile * kTok + lane)};
                 }
             }
             __syncwarp();
@@ -1180,12 +1224,10 @@ __global__ void __launch_bounds__(kThreads, 4) insert_kernel(const __grid_consta
 // loads are under way while the CTA fills the quantiser's cells (one copy: a
 // warp's few lookups can bear the conflicts).  The whole call is then launch,
 // one memory latency and about 400 instructions, 3.3 us for 16 tokens x 8 heads
-// where insert_kernel's tile takes 8.4.  Six CTAs per SM in all (1024 tokens:
-// 11.8 us; four the same, eight 12.7, one CTA for every four rows 18.0).  A row
-// that float32 does not decide adds 1.2 us, 1.7 with rotary positions (near_row:
-// 4.8).  Its float32 path errs less than insert_kernel's: over 1.2e9 coordinates
-// of the same kinds the furthest wrong decision lay 2.8e-7 of a standard
-// deviation from its boundary, of the norms' roundings 1.2e-7 of the norm.
+// without a row that float32 does not decide, 4.2 with some (most calls of 256
+// rows have one), where insert_kernel's tile takes 11.5.  Six CTAs per SM in all
+// (four took 1024 tokens the same, eight 8% longer, one CTA for every four rows
+// half as long again).
 struct SmallShared {
     uint2 cells[128];                         // as Shared's, one copy
     alignas(16) ff again[kWarps][kD];         // values of a row taken again
@@ -1250,11 +1292,18 @@ int launch_few(const tq_rope &rope, const InsertArgs &a, int sides, cudaStream_t
 
 template <int DT>
 int launch(const tq_rope &rope, const InsertArgs &a, cudaStream_t st) {
-    const int smem = (int)(sizeof(Shared) + (size_t)a.tiles * sizeof(float4) * 8 * kTok * 4);
+    const int smem = (int)(sizeof(Shared) + (size_t)a.tiles * sizeof(float4) * 8 * kTok * 4 + 2 * a.list * sizeof(Listed));
     static int done[64] = {0};
     if (set_smem_limit((const void *)insert_kernel<DT>, smem, done) != TQ_OK) return TQ_ERR_CUDA;
     insert_kernel<DT><<<a.ctas[0] + a.ctas[1], kThreads, smem, st>>>(rope, a);
     return launch_status();
+}
+
+// A bound for a codebook, in v.
+float border(const Bound &e, const tq_codebook *cb) {
+    float b = 0.f;
+    for (int i = 0; i < cb->levels - 1; ++i) b = std::fmax(b, std::fabs(cb->boundaries[i]) * 11.3137085f);
+    return (e.row + e.level * b) * 5.9604645e-8f * kUnit;
 }
 
 // The quantiser's cells hold at most one boundary each, and no boundary lies
@@ -1285,6 +1334,7 @@ extern "C" int tq_insert_kv(const void *k, int64_t k_tok_stride, int64_t k_head_
                             const tq_codebook *vcb, tq_signs signs, uint8_t *k_blocks, uint8_t *v_blocks,
                             int64_t n_blocks, const int64_t *dst, int64_t dst_head_stride, void *stream) {
     if (n_tok < 0 || heads <= 0 || n_blocks < 0 || dst_head_stride < 0) return TQ_ERR_ARG;
+    if (heads >= 1 << 26) return TQ_ERR_UNSUPPORTED;   // (Listed)
     if ((k != nullptr) != (k_blocks != nullptr) || (v != nullptr) != (v_blocks != nullptr)) return TQ_ERR_ARG;
     if ((k && !kcb) || (v && !vcb) || (rope && !pos)) return TQ_ERR_ARG;
     const int es = dtype_bytes(dtype);
@@ -1313,6 +1363,10 @@ extern "C" int tq_insert_kv(const void *k, int64_t k_tok_stride, int64_t k_head_
         s.style = kRopeNone;
         if (i == 0 && rope)
             s.style = rope->style == TQ_ROPE_ADJACENT ? (int)kRopeAdjacent : kRopeHalf1 + rope->rot_dim / 32 - 1;
+        const bool direct = s.style == kRopeNone && dtype != TQ_F32;
+        s.ulps = direct ? kTieUlpsDirect : kTieUlps;
+        s.eps = border(s.style != kRopeNone ? kBoundRope : direct ? kBoundDirect : kBoundSplit, cbs[i]);
+        s.eps_few = border(s.style != kRopeNone ? kBoundFewRope : kBoundFew, cbs[i]);
     }
     if (n_tok == 0 || (!k && !v)) return TQ_OK;
     if (!dst) return TQ_ERR_ARG;
@@ -1327,6 +1381,9 @@ extern "C" int tq_insert_kv(const void *k, int64_t k_tok_stride, int64_t k_head_
     for (int i = 0; i < 4; ++i) a.signs[i] = signs.w[i];
     // token tiles of a CTA: its four warps share a tile's sines, or take a tile each where heads are few
     a.tiles = heads == 1 ? 4 : heads == 2 ? 2 : 1;
+    // the lists: what four CTAs leave of 196 KB of shared memory (with more of it, and less L1, float32 rows take 15%
+    // longer).  Of random rows one is full after 25,000 rows of a CTA, in calls of 1.1 million tokens x 8 heads.
+    a.list = a.tiles > 1 ? 128 : 190;
     const int64_t tiles = (n_tok + (int64_t)kTok * a.tiles - 1) / (kTok * a.tiles);
     const int sides = (k != nullptr) + (v != nullptr);
     const int64_t slots = (int64_t)sm_count() * 4, few = (int64_t)sm_count() * kFewRows;

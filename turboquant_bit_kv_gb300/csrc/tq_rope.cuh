@@ -69,8 +69,9 @@ __device__ __forceinline__ void rope_sincos_double(uint64_t frac, double &s, dou
     if ((q + 1u) & 2u) c = -c;
 }
 
-// The same in double-float arithmetic, to about 2^-34: the angle exact, the
-// series' terms through x^5 in double-float, the rest (below 2^-11) in float32.
+// The same in double-float arithmetic: the angle exact, the series' terms
+// through x^7 in double-float, the rest (below 2^-18 and good to 2^-21 of
+// itself, series through x^13) in float32: off by less than 2^-38.
 __device__ __forceinline__ void rope_sincos_ff(uint64_t frac, ff &s, ff &c) {
     const uint32_t q = (uint32_t)((frac + (1ull << 61)) >> 62);
     const int64_t r = (int64_t)(frac - ((uint64_t)q << 62));
@@ -79,19 +80,22 @@ __device__ __forceinline__ void rope_sincos_ff(uint64_t frac, ff &s, ff &c) {
     const float f2 = (float)(int)(rest >> 16) * 1.52587890625e-05f + (float)(int)(rest & 0xFFFF) * 2.3283064365386963e-10f;
     // times 2 pi / 2^32, as two float32
     const ff x = ff_mul(ff_quick(f1, f2), ff_of(1.46291807926715967e-09f, 1.46291807926715967e-09 - (double)1.46291807926715967e-09f));
-    const ff z = ff_mul(x, x);
-    // sin x = x (1 - z / 6 + z^2 / 120 - z^3 (1 / 7! - z / 9! + z^2 / 11!))
-    const float ts = z.h * z.h * z.h * fmaf(z.h, fmaf(z.h, 2.50521083854417188e-08f, -2.75573192239858907e-06f), 1.98412698412698413e-04f);
-    const ff z2 = ff_mul(z, z);
-    const ff k6 = {1.66666666666666667e-01f, (float)(1.66666666666666667e-01 - (double)1.66666666666666667e-01f)};
-    const ff k120 = {8.33333333333333333e-03f, (float)(8.33333333333333333e-03 - (double)8.33333333333333333e-03f)};
-    const ff k24 = {4.16666666666666667e-02f, (float)(4.16666666666666667e-02 - (double)4.16666666666666667e-02f)};
+    const ff z = ff_mul(x, x), z2 = ff_mul(z, z), z3 = ff_mul(z2, z);
+    const float z4 = z2.h * z2.h;
     const ff one = {1.f, 0.f};
-    const ff ps = ff_mul(x, ff_add(ff_sub(one, ff_mul(z, k6)), ff_sub(ff_mul(z2, k120), ff_of(ts))));
-    // cos x = 1 - z / 2 + z^2 / 24 - z^3 (1 / 6! - z / 8! + z^2 / 10! - z^3 / 12!)
-    const float tc = z.h * z.h * z.h * fmaf(z.h, fmaf(z.h, fmaf(z.h, -2.08767569878680990e-09f, 2.75573192239858907e-07f),
-                                                      -2.48015873015873016e-05f), 1.38888888888888889e-03f);
-    const ff pc = ff_add(ff_sub(one, ff_scale(z, 0.5f)), ff_sub(ff_mul(z2, k24), ff_of(tc)));
+    const ff k6 = {1.66666666666666667e-01f, (float)(1.66666666666666667e-01 - (double)1.66666666666666667e-01f)};
+    const ff k24 = {4.16666666666666667e-02f, (float)(4.16666666666666667e-02 - (double)4.16666666666666667e-02f)};
+    const ff k120 = {8.33333333333333333e-03f, (float)(8.33333333333333333e-03 - (double)8.33333333333333333e-03f)};
+    const ff k720 = {1.38888888888888889e-03f, (float)(1.38888888888888889e-03 - (double)1.38888888888888889e-03f)};
+    const ff k5040 = {1.98412698412698413e-04f, (float)(1.98412698412698413e-04 - (double)1.98412698412698413e-04f)};
+    // sin x = x (1 - z / 6 + z^2 / 120 - z^3 / 7! + z^4 (1 / 9! - z / 11! + z^2 / 13!))
+    const float ts = z4 * fmaf(z.h, fmaf(z.h, 1.60590438368216146e-10f, -2.50521083854417188e-08f), 2.75573192239858907e-06f);
+    const ff ps = ff_mul(x, ff_add(ff_sub(one, ff_mul(z, k6)),
+                                   ff_add(ff_sub(ff_mul(z2, k120), ff_mul(z3, k5040)), ff_of(ts))));
+    // cos x = 1 - z / 2 + z^2 / 24 - z^3 / 6! + z^4 (1 / 8! - z / 10! + z^2 / 12!)
+    const float tc = z4 * fmaf(z.h, fmaf(z.h, 2.08767569878680990e-09f, -2.75573192239858907e-07f), 2.48015873015873016e-05f);
+    const ff pc = ff_add(ff_sub(one, ff_scale(z, 0.5f)),
+                         ff_add(ff_sub(ff_mul(z2, k24), ff_mul(z3, k720)), ff_of(tc)));
     s = (q & 1u) ? pc : ps;
     c = (q & 1u) ? ps : pc;
     if (q & 2u) s = ff_neg(s);
