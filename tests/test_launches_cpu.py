@@ -1,0 +1,71 @@
+"""The library's host code against a stand-in for the CUDA runtime
+(fake_cudart.cpp): launches that fail, calls of two threads at once."""
+
+import ctypes
+import os
+import shutil
+import subprocess
+import threading
+import time
+
+import pytest
+
+from test_rope_evict_cpu import A, B, C, D_
+from turboquant_bit_kv_gb300 import build_lib, tq as real
+
+HERE = os.path.dirname(os.path.abspath(__file__))
+
+
+@pytest.fixture(scope="module")
+def linked(tmp_path_factory):
+    """The library linked with the stand-in."""
+    build_lib.build()
+    out = str(tmp_path_factory.mktemp("fake") / "libtq_fake.so")
+    objs = [os.path.join(build_lib.BUILD, s + ".o") for s in build_lib.SOURCES]
+    cuda = os.path.dirname(os.path.dirname(build_lib.NVCC))
+    r = subprocess.run(["g++", "-std=c++17", "-shared", "-fPIC", "-Wl,-Bsymbolic", "-I" + os.path.join(cuda, "include"), "-o", out,
+                        os.path.join(HERE, "fake_cudart.cpp")] + objs + ["-lpthread"], capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+    return out
+
+
+@pytest.fixture
+def lib(linked, tmp_path):
+    """A copy of it (with state of its own), its functions typed as the binding's."""
+    path = str(tmp_path / "libtq_fake.so")
+    shutil.copy(linked, path)
+    fake, typed = ctypes.CDLL(path), real.lib()
+    for name in ("tq_insert_kv", "tq_attn_decode_weights", "tq_attn_weights_workspace_bytes", "tq_evict_select",
+                 "tq_evict_compact", "tq_rope_apply", "tq_attn_decode", "tq_attn_decode_paged", "tq_attn_decode_d"):
+        getattr(fake, name).argtypes = getattr(typed, name).argtypes
+        getattr(fake, name).restype = getattr(typed, name).restype
+    fake.fake_reset()
+    return fake
+
+
+def insert(lib, heads, n):
+    kcb, vcb, rope = real.tq_codebook_load(128, 4), real.tq_codebook_load(128, 2), real.tq_rope_load()
+    return lib.tq_insert_kv(A, 128 * heads, 128, B, 128 * heads, 128, real.TQ_BF16, n, heads, C, n, rope, kcb, vcb,
+                            real.tq_signs(), C, D_, n * heads, A, n, None)
+
+
+def test_stand_in_takes_calls(lib):
+    assert insert(lib, 8, 16) == 0 and insert(lib, 8, 5000) == 0 and insert(lib, 1, 50000) == 0
+    assert lib.fake_launches() == 3
+
+
+def test_first_large_inserts_of_two_threads(lib):
+    """Two threads make the first large calls at once, one of which needs more shared memory: later calls of either
+    kind still launch."""
+    lib.fake_slow_limit(60 * 1024)      # (one head: four tables of sines)
+    got = {}
+    a = threading.Thread(target=lambda: got.update(one=insert(lib, 1, 50000)))
+    a.start()
+    while not lib.fake_in_slow_limit():
+        time.sleep(0.001)
+    b = threading.Thread(target=lambda: got.update(eight=insert(lib, 8, 5000)))
+    b.start()
+    b.join()
+    a.join()
+    assert got == {"one": 0, "eight": 0}
+    assert insert(lib, 1, 50000) == 0 and insert(lib, 8, 5000) == 0

@@ -25,6 +25,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstring>
+#include <mutex>
 
 #include "tq_device.cuh"
 #include "tq_internal.h"
@@ -49,6 +50,9 @@ int sm_count() {
 int set_smem_limit(const void *kernel, int bytes, int *done_for_device) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return TQ_ERR_CUDA;
+    // one thread at a time: another, with a smaller size, would lower the limit that is noted here
+    static std::mutex mu;
+    std::lock_guard<std::mutex> lock(mu);
     if (dev < 64 && done_for_device[dev] >= bytes) return TQ_OK;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
         return TQ_ERR_CUDA;

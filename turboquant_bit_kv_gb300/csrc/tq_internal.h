@@ -25,7 +25,8 @@ bool codebook_ok(const tq_codebook *cb);
 // Streaming multiprocessors of the current device (cached per device).
 int sm_count();
 
-// Raise a kernel's dynamic shared-memory limit once per process and device.
+// Raise a kernel's dynamic shared-memory limit to at least `bytes` on the current device (never lowered; may be
+// called by several threads at once).
 int set_smem_limit(const void *kernel, int bytes, int *done_for_device);
 
 // QJL sketch of bf16 / fp16 keys on the tensor cores (tq_qjl.cu).  Returns 1
