@@ -69,3 +69,48 @@ def test_first_large_inserts_of_two_threads(lib):
     a.join()
     assert got == {"one": 0, "eight": 0}
     assert insert(lib, 1, 50000) == 0 and insert(lib, 8, 5000) == 0
+
+
+def calls(lib):
+    """Name -> a valid call of the library (its pointers are never read)."""
+    k4, v2 = real.tq_codebook_load(128, 4), real.tq_codebook_load(128, 2)
+    k4d = real.tq_codebook_load(96, 4)
+    s, big = real.tq_signs(), 1 << 40
+    return {
+        "weights": lambda: lib.tq_attn_decode_weights(A, real.TQ_BF16, B, k4, C, v2, None, 0, 0, None, 2, 8, 2, 512, 500,
+                                                      0.1, s, D_, 500, 1.0, A, real.TQ_F32, B, big, None),
+        "weights, pages": lambda: lib.tq_attn_decode_weights(A, real.TQ_BF16, B, v2, C, v2, D_, 16, 40, None, 2, 8, 2, 0, 500,
+                                                             0.1, s, D_, 500, 1.0, A, real.TQ_F32, B, big, None),
+        "decode": lambda: lib.tq_attn_decode(A, real.TQ_BF16, B, k4, C, v2, None, 2, 8, 2, 512, 500, 0.1, s, None, None, None,
+                                             A, B, big, None),
+        "decode, pages": lambda: lib.tq_attn_decode_paged(A, real.TQ_BF16, B, k4, C, v2, D_, 16, 32, None, 2, 8, 2, 500, 0.1,
+                                                          s, A, B, big, None),
+        "decode, 96": lambda: lib.tq_attn_decode_d(A, real.TQ_BF16, B, k4d, C, k4d, None, 2, 8, 2, 512, 500, 96, 0.1, D_, A,
+                                                   B, big, None),
+        "select": lambda: lib.tq_evict_select(A, 500, B, 2, 2, 500, 100, 4, 10, C, D_, None),
+        "compact": lambda: lib.tq_evict_compact(A, 66, B, 34, C, 500, D_, 100, A, None, 0, 0, 0, 2, 2, 512, 500, None),
+        "insert": lambda: insert(lib, 8, 5000),
+        "insert, few": lambda: insert(lib, 8, 16),
+        "rope": lambda: lib.tq_rope_apply(A, real.TQ_BF16, 4, 2, 256, 128, B, 4, real.tq_rope_load(), C, 256, 128, None),
+    }
+
+
+NAMES = ["weights", "weights, pages", "decode", "decode, pages", "decode, 96", "select", "compact", "insert",
+         "insert, few", "rope"]
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_a_failed_launch_does_not_fail_the_next_call(lib, name):
+    """Each launch of a call in turn fails: the call says so, and the next one, whose launches succeed, does not."""
+    call = calls(lib)[name]
+    assert sorted(calls(lib)) == sorted(NAMES)
+    assert call() == 0
+    n = lib.fake_launches()
+    assert n >= 1
+    for i in range(1, n + 1):
+        lib.fake_fail_at(i)
+        assert call() == real.TQ_ERR_CUDA, i
+        assert lib.fake_launches() == i     # (and nothing is launched after it)
+        lib.fake_fail_at(0)
+        assert calls(lib)["rope"]() == 0, i
+        assert call() == 0, i

@@ -237,10 +237,8 @@ int mma_path(AttnArgs &a, int kb, int vb, bool qjl, bool packed_v, tq_signs sign
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, attn_combine_mma_kernel, (const float *)a.ws, mp, a.Hq, a.Hkv, packed_v ? 1 : 0,
-                           signs.w[0], signs.w[1], signs.w[2], signs.w[3], out) != cudaSuccess)
-        return TQ_ERR_CUDA;
-    return launch_status();
+    return launch_status(cudaLaunchKernelEx(&cfg, attn_combine_mma_kernel, (const float *)a.ws, mp, a.Hq, a.Hkv,
+                                            packed_v ? 1 : 0, signs.w[0], signs.w[1], signs.w[2], signs.w[3], out));
 }
 
 }  // namespace

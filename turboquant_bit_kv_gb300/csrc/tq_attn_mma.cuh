@@ -1117,9 +1117,7 @@ int launch_cfg_w(const AttnArgs &a, MmaPlan &plan, cudaStream_t st) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, attn_mma_kernel<KB, VB, QJL, NT, WIDE, PAGED, SCORES>, a, plan) != cudaSuccess)
-        return TQ_ERR_CUDA;
-    return launch_status();
+    return launch_status(cudaLaunchKernelEx(&cfg, attn_mma_kernel<KB, VB, QJL, NT, WIDE, PAGED, SCORES>, a, plan));
 }
 
 // Only 2-bit values with one n-tile have a narrow (12-warp) variant.

@@ -350,6 +350,5 @@ extern "C" int tq_attn_decode_weights(const void *q, int q_dtype, const uint8_t 
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, attn_weights_kernel, w, plan) != cudaSuccess) return TQ_ERR_CUDA;
-    return launch_status();
+    return launch_status(cudaLaunchKernelEx(&cfg, attn_weights_kernel, w, plan));
 }

@@ -54,8 +54,10 @@ int set_smem_limit(const void *kernel, int bytes, int *done_for_device) {
     static std::mutex mu;
     std::lock_guard<std::mutex> lock(mu);
     if (dev < 64 && done_for_device[dev] >= bytes) return TQ_OK;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) {
+        cudaGetLastError();   // (not left for the next call)
         return TQ_ERR_CUDA;
+    }
     if (dev < 64) done_for_device[dev] = bytes;
     return TQ_OK;
 }

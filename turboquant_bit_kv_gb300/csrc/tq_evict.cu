@@ -472,11 +472,7 @@ int launch_cluster(K kernel, int64_t rows, int C, int threads, size_t smem, cuda
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, kernel, args) != cudaSuccess) {
-        cudaGetLastError();
-        return TQ_ERR_CUDA;
-    }
-    return launch_status();
+    return launch_status(cudaLaunchKernelEx(&cfg, kernel, args));
 }
 
 }  // namespace

@@ -516,8 +516,7 @@ int hd_launch_attn(HdAttnArgs &a, cudaStream_t st) {
     cfg.blockDim = dim3(kHdThreads);
     cfg.gridDim = dim3(D / kHdTile, (unsigned)((rows + kHdCRows - 1) / kHdCRows));
     cfg.dynamicSmemBytes = smem_c;
-    if (cudaLaunchKernelEx(&cfg, attn_d_combine_kernel<ND>, a) != cudaSuccess) return TQ_ERR_CUDA;
-    return launch_status();
+    return launch_status(cudaLaunchKernelEx(&cfg, attn_d_combine_kernel<ND>, a));
 }
 
 }  // namespace

@@ -44,8 +44,7 @@ int hd_attn_mma_launch(const HdAttnArgs &a, int d, cudaStream_t st) {
     cfg.gridDim = dim3(a.splits, a.Hkv, a.B);
     cfg.dynamicSmemBytes = smem;
     void *args[] = {const_cast<HdAttnArgs *>(&a)};
-    if (cudaLaunchKernelExC(&cfg, k.fn, args) != cudaSuccess) return TQ_ERR_CUDA;
-    return TQ_OK;
+    return launch_status(cudaLaunchKernelExC(&cfg, k.fn, args));
 }
 
 }  // namespace tq

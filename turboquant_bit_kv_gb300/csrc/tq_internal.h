@@ -75,8 +75,16 @@ int hd_encode_tc(const void *x, int x_dtype, int64_t n_vec, int d, const tq_code
 int ext_encode_tc(const void *x, int x_dtype, int64_t n_vec, int64_t x_stride_bytes, const tq_codebook *cb,
                   const uint32_t *signs, int nc, int dense, uint8_t *blocks, cudaStream_t st);
 
+// Status of the calls since the last one, which is cleared: a failure must not
+// be left for the next call to find.
 inline int launch_status() {
     return cudaGetLastError() == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
+}
+
+// Status of a launch that returned e.
+inline int launch_status(cudaError_t e) {
+    const int st = launch_status();
+    return e == cudaSuccess ? st : TQ_ERR_CUDA;
 }
 
 }  // namespace tq
