@@ -509,8 +509,9 @@ int tq_rope_set_freqs(tq_rope *rope, const double *freqs);
  *   x, out   device rows of 128 elements of dtype (TQ_F32 / TQ_BF16 /
  *            TQ_F16); head h of token n at n * tok_stride + h * head_stride
  *            elements (strides times the element size multiples of 16, bases
- *            16-byte aligned).  out may be x itself with the same strides
- *            (in place); otherwise they must not overlap.
+ *            16-byte aligned).  No two rows of out may overlap.  out may be x
+ *            itself with the same strides (in place); otherwise x and out must
+ *            not overlap.
  *   pos      device int64: axis a of token n at pos[a * pos_axis_stride + n].
  *            Any int64 value (positions may be negative).
  * n_tok == 0 is a no-op.  Errors: TQ_ERR_ARG, TQ_ERR_UNSUPPORTED, TQ_ERR_ALIGN,

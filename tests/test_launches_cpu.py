@@ -3,6 +3,7 @@
 
 import ctypes
 import os
+import random
 import shutil
 import subprocess
 import threading
@@ -10,7 +11,7 @@ import time
 
 import pytest
 
-from test_rope_evict_cpu import A, B, C, D_
+from test_rope_evict_cpu import ARG, A, B, C, D_
 from turboquant_bit_kv_gb300 import build_lib, tq as real
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -114,3 +115,25 @@ def test_a_failed_launch_does_not_fail_the_next_call(lib, name):
         lib.fake_fail_at(0)
         assert calls(lib)["rope"]() == 0, i
         assert call() == 0, i
+
+
+def test_rope_refuses_rows_that_overlap(lib):
+    """Layouts of the output in which two (token, head) rows share an element are refused, the others are not: against
+    all pairs of rows."""
+    rng = random.Random(1)
+    rope = real.tq_rope_load()
+    seen = [0, 0]
+    layouts = [(2, 128, 2, 128), (5, 128, 1, 64), (1, 8, 7, 128), (4, 256, 2, 128), (4, 128, 3, 512), (3, 128, 3, 376),
+               (2, 256, 2, 384), (2, 256, 3, 384), (4, 136, 4, 136), (1000, 128, 1000, 128000), (1000, 128, 1000, 127992),
+               (3000, 128, 2, 3000 * 128 - 8), (2, 1 << 40, 2, 1 << 40)]
+    layouts += [(rng.randint(1, 9), 8 * rng.randint(12, 80), rng.randint(1, 9), 8 * rng.randint(12, 80)) for _ in range(2000)]
+    for n, s, m, t in layouts:
+        if n * m <= 10000:
+            at = sorted(i * s + j * t for i in range(n) for j in range(m))
+            overlap = any(b - a < 128 for a, b in zip(at, at[1:]))
+        else:
+            overlap = not (s >= (m - 1) * t + 128 or t >= (n - 1) * s + 128)
+        got = lib.tq_rope_apply(A, real.TQ_BF16, n, m, 0, 0, B, 0, rope, C, s, t, None)
+        assert got == (ARG if overlap else 0), (n, s, m, t, overlap)
+        seen[overlap] += 1
+    assert min(seen) > 200

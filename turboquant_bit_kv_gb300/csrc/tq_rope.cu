@@ -207,6 +207,23 @@ uint64_t turn_of(double f) {
     return ((uint64_t)(int64_t)ah << 32) + (uint64_t)(int64_t)std::nearbyint(al) + (uint64_t)(int64_t)std::nearbyint(b);
 }
 
+// Whether two of the rows of kD elements at i s + j t, i < n, j < m, share an
+// element (they would be written twice, in any order).
+bool rows_overlap(int64_t n, int64_t s, int64_t m, int64_t t) {
+    if ((n > 1 && s < kD) || (m > 1 && t < kD)) return true;
+    if (n <= 1 || m <= 1) return false;
+    if ((s - kD) / t >= m - 1 || (t - kD) / s >= n - 1) return false;   // all j before the next i, or the other way round
+    if (n > m) return rows_overlap(m, t, n, s);
+    for (int64_t i = 1; i < n; ++i) {   // the j nearest to row (i, 0)
+        const __int128 at = (__int128)i * s;
+        const int64_t near = (int64_t)((at + t / 2) / t), j = near < 1 ? 1 : (near < m ? near : m - 1);
+        const __int128 d = at - (__int128)j * t;
+        if (d < kD && d > -kD) return true;
+        if (near >= m) return false;   // (further i are further away)
+    }
+    return false;
+}
+
 }  // namespace
 }  // namespace tq
 
@@ -272,11 +289,10 @@ extern "C" int tq_rope_apply(const void *x, int dtype, int64_t n_tok, int heads,
     if (!x || !pos || !out || x_tok_stride < 0 || x_head_stride < 0 || out_tok_stride < 0 || out_head_stride < 0 ||
         pos_axis_stride < 0)
         return TQ_ERR_ARG;
-    // rows of one output must not overlap
-    if ((heads > 1 && out_head_stride < kD) || (n_tok > 1 && out_tok_stride < kD)) return TQ_ERR_ARG;
     if (!aligned(x, 16) || !aligned(out, 16) || !aligned(pos, 8) || ((x_tok_stride * es) & 15) ||
         ((x_head_stride * es) & 15) || ((out_tok_stride * es) & 15) || ((out_head_stride * es) & 15))
         return TQ_ERR_ALIGN;
+    if (rows_overlap(n_tok, out_tok_stride, heads, out_head_stride)) return TQ_ERR_ARG;
     RopeArgs a;
     a.x = static_cast<const uint8_t *>(x);
     a.out = static_cast<uint8_t *>(out);
