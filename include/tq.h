@@ -478,8 +478,10 @@ typedef enum { TQ_ROPE_HALF = 0, TQ_ROPE_ADJACENT = 1 } tq_rope_style;
  * video token).  The first rot_dim elements of a head form rot_dim / 2 pairs:
  * pair i is elements (i, i + rot_dim / 2) (TQ_ROPE_HALF) or (2i, 2i + 1)
  * (TQ_ROPE_ADJACENT); it turns by position[axis[i]] times its frequency.
- * turn[i] is the frequency in 2^-64 turns per position (modulo one turn), so
- * angles of far positions are exact.  Travels by value, like tq_codebook. */
+ * turn[i] is the frequency in 2^-64 turns per position (modulo one turn),
+ * rounded to a whole number of them: the angle of position p is off by
+ * |p| 2^-64 turns at most (2^-24 radians at |p| = 2^37), besides what the
+ * frequency, a double, was rounded by.  Travels by value, like tq_codebook. */
 typedef struct {
     int head_dim;        /* 128 */
     int rot_dim;         /* 32, 64, 96 or 128 */

@@ -1,6 +1,8 @@
 """Rotary insert, weighted attention and eviction at the edges of what their
 calls allow."""
 
+from decimal import Decimal, getcontext
+
 import numpy as np
 import pytest
 import torch
@@ -149,3 +151,28 @@ def test_insert_of_rows_near_a_hadamard_row(tq, dtype, keys):
     rows = x.double().cpu().numpy().reshape(-1, 128)
     # sums of 128 values of 24 bits, 2^25 apart at most, are exact in 64 bits whatever their order
     check_rows(tq, x, None, None, bits, signs, rows, diagonal, keys)
+
+
+# ---------------------------------------------------------------- far positions
+
+PI = Decimal("3.14159265358979323846264338327950288419716939937510582097494459230781640628620899")
+
+
+@pytest.mark.parametrize("far", [2**32, 2**37, 2**40, 2**50, 2**53])
+def test_apply_far_positions_follow_the_frequencies(tq, far):
+    """Angles against position times frequency in 80 digits: a rope's turns are whole numbers of 2^-64, so an angle is
+    off by 2 pi |position| 2^-64 at most, on top of sine and cosine (2^-22 of a pair of ones, as for near
+    positions)."""
+    getcontext().prec = 80
+    freqs = [500000.0 ** (-2.0 * i / 128) for i in range(64)]
+    rope = tq.tq_rope_set_freqs(tq.tq_rope_load(128), freqs)
+    where = [far, -far, far - 1, -far + 12345, far // 3]
+    x = torch.zeros(len(where), 1, 128, device="cuda")
+    x[..., :64] = 1.0
+    out = torch.empty_like(x)
+    tq.tq_rope_apply(x, torch.tensor(where, device="cuda"), rope, out)
+    angle = np.array([[float(Decimal(p) * Decimal(f) % (2 * PI)) for f in freqs] for p in where])
+    tol = 2.0**-22 + 2 * np.pi * 2.0**-64 * abs(far) + 2.0**-50
+    got = out[:, 0].double().cpu().numpy()
+    assert np.abs(got[:, :64] - np.cos(angle)).max() <= tol
+    assert np.abs(got[:, 64:] - np.sin(angle)).max() <= tol

@@ -1,12 +1,12 @@
-// Rotary positions on the device: exact angle reduction and the sine and
+// Rotary positions on the device: reduction of the angle and the sine and
 // cosine of one (token, pair).
 //
 // The angle of pair i at position t is t * f_i radians.  A rope holds f_i as
 // a 64-bit fraction of a turn, F_i = f_i / (2 pi) * 2^64 mod 2^64, so that
-// the low 64 bits of t * F_i are the angle modulo one turn with an error of
-// at most t * 2^-65 turns: far positions lose nothing (a float32 product
-// t * f_i is off by up to 0.06 rad at t = 10^6), and negative positions work
-// by two's complement.
+// the low 64 bits of t * F_i are the angle modulo one turn, off by |t| 2^-64
+// turns at most (F_i is rounded to a whole number): positions up to 2^37 lose
+// nothing that float32 could hold (a float32 product t * f_i is off by up to
+// 0.06 rad at t = 10^6), and negative positions work by two's complement.
 #pragma once
 
 #include <stdint.h>
