@@ -294,13 +294,8 @@ extern "C" int tq_attn_decode(const void *q, int q_dtype, const uint8_t *k_block
         return TQ_ERR_ALIGN;
     if (workspace_bytes < tq_attn_workspace_bytes(B, Hq, Hkv, T_cap)) return TQ_ERR_WORKSPACE;
 
-    AttnArgs a;
+    AttnArgs a = {};
     a.drop = drop_copies();
-    a.table = nullptr;
-    a.max_pages = 0;
-    a.page = 0;
-    a.scores = nullptr;
-    a.live = nullptr;
     a.q = q;
     a.q_dtype = q_dtype;
     a.k = k_blocks;
@@ -361,7 +356,7 @@ extern "C" int tq_attn_decode_paged(const void *q, int q_dtype, const uint8_t *k
             !aligned(workspace, 16))
             return TQ_ERR_ALIGN;
         if (workspace_bytes < tq_attn_workspace_bytes(B, Hq, Hkv, T8)) return TQ_ERR_WORKSPACE;
-        AttnArgs a;
+        AttnArgs a = {};
         a.drop = drop_copies();
         a.q = q;
         a.q_dtype = q_dtype;
@@ -388,8 +383,6 @@ extern "C" int tq_attn_decode_paged(const void *q, int q_dtype, const uint8_t *k
         a.table = block_table;
         a.max_pages = max_pages;
         a.page = page_tokens;
-        a.scores = nullptr;
-    a.live = nullptr;
         return mma_path(a, kb, vb, false, true, signs, out, true, static_cast<cudaStream_t>(stream));
     }
     // otherwise the one-token case of the tensor-core causal attention (no workspace)

@@ -42,10 +42,11 @@ struct AttnArgs {
     uint32_t signs[4];
     int drop;                // test hook: issue no bulk copies (the waits for them run out)
     // paged cache (the paged kernels only): token t of sequence b is slot t % page of page
-    // table[b * max_pages + t / page] of pools [pages][Hkv][page]; page a multiple of 32
+    // table[b * max_pages + t / page] of pools [pages][Hkv][page]; page a multiple of 32 (a chunk is
+    // one copy), or of 8 for the kernels that keep the scores (a copy for each piece of a chunk)
     const int32_t *table;
     int max_pages, page;
-    // the kernels that keep the scores only:
+    // the kernels that keep the scores only (others: null; the query prep writes live where it is not):
     float *scores;           // [B * Hkv][chunks][G][32] log2-domain scores
     int2 *live;              // [B * Hkv]: a segment's first worker, and how many workers meet it
     int workers;

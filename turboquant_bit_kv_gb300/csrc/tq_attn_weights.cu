@@ -281,8 +281,7 @@ extern "C" int tq_attn_decode_weights(const void *q, int q_dtype, const uint8_t 
     const int64_t grid = (int64_t)B * Hq + (int64_t)B * Hkv * parts;
     if (grid > 0x7FFFFFFF || segs * ((T + kMmaChunk - 1) / kMmaChunk) > 0x7FFFFFFF) return TQ_ERR_UNSUPPORTED;
 
-    AttnArgs a;
-    std::memset(&a, 0, sizeof(a));
+    AttnArgs a = {};
     a.drop = drop_copies();
     a.q = q;
     a.q_dtype = q_dtype;
