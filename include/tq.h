@@ -541,9 +541,10 @@ int tq_rope_apply(const void *x, int dtype, int64_t n_tok, int heads, int64_t x_
  *             (padding) and blocks past n_blocks are not written.  Two tokens
  *             must not name the same block.
  * n_tok == 0 is a no-op.  A row with a non-finite element stores a non-finite
- * norm and codes 0.  Errors: TQ_ERR_ARG, TQ_ERR_UNSUPPORTED (also a codebook
- * whose boundaries are not those of tq_codebook_load), TQ_ERR_ALIGN,
- * TQ_ERR_CUDA. */
+ * norm and codes 0.  Errors: TQ_ERR_ARG, TQ_ERR_UNSUPPORTED (also 2^26 heads
+ * or more, and a codebook whose boundaries lie closer together than those of
+ * tq_codebook_load: two in one cell [k - 1/2, k + 1/2) / 63, or one within
+ * 1/64 of a cell of its edge), TQ_ERR_ALIGN, TQ_ERR_CUDA. */
 int tq_insert_kv(const void *k, int64_t k_tok_stride, int64_t k_head_stride, const void *v, int64_t v_tok_stride,
                  int64_t v_head_stride, int dtype, int64_t n_tok, int heads, const int64_t *pos,
                  int64_t pos_axis_stride, const tq_rope *rope, const tq_codebook *kcb, const tq_codebook *vcb,

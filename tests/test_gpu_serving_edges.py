@@ -153,6 +153,26 @@ def test_insert_of_rows_near_a_hadamard_row(tq, dtype, keys):
     check_rows(tq, x, None, None, bits, signs, rows, diagonal, keys)
 
 
+@pytest.mark.parametrize("bits", [2, 3, 4])
+@pytest.mark.parametrize("n", [20, 4000])
+def test_insert_with_a_codebook_of_ones_own(tq, bits, n):
+    """Boundaries moved off 0: a row of zeros takes the cell that 0 lies in, other rows theirs."""
+    cb = tq.tq_codebook_load(128, bits)
+    moved = np.array(cb.boundaries[:cb.levels - 1], np.float32) + np.float32(0.003)
+    for i, b in enumerate(moved):
+        cb.boundaries[i] = b
+    heads = 5
+    rng = np.random.default_rng(bits)
+    x = rng.standard_normal((n, heads, 128))
+    x[::3] = 0
+    x = torch.from_numpy(x).to(torch.bfloat16).cuda()
+    cache = torch.zeros(n * heads, 2 + 16 * bits, dtype=torch.uint8, device="cuda")
+    signs = tq.tq_signs_from_seed(workloads.SIGN_SEED)
+    tq.tq_insert_kv(x, None, None, None, cb, None, signs, cache, None, torch.arange(n, device="cuda") * heads, 1)
+    idx, norm, _ = codec.encode(x.double().cpu().numpy().reshape(-1, 128), oracle.sign_diagonal(workloads.SIGN_SEED), moved)
+    assert np.array_equal(cache.cpu().numpy(), codec.pack_block(idx, norm, bits))
+
+
 # ---------------------------------------------------------------- far positions
 
 PI = Decimal("3.14159265358979323846264338327950288419716939937510582097494459230781640628620899")

@@ -460,7 +460,8 @@ __device__ __forceinline__ void few_row(const FewIn &n, const FewLane &w, const 
     // a row of zeros (sign bits aside: of both elements of a word of 16-bit types)
     if (!__any_sync(0xffffffffu, (raw.x | raw.y | raw.z | raw.w) & (DT == TQ_F32 ? 0x7FFFFFFFu : 0x7FFF7FFFu))) {
         if (lane == 0) *reinterpret_cast<uint16_t *>(block) = 0;
-        write_codes(block, bits, 0x01010101u << (bits - 1), lane);
+        const uint2 e = *reinterpret_cast<const uint2 *>(cells + ((64 * 128) >> shift));   // the cell of 0
+        write_codes(block, bits, 0x01010101u * (e.y - (__uint_as_float(e.x) > 0.f)), lane);
         return;
     }
     float x[4];
