@@ -173,6 +173,31 @@ def test_insert_with_a_codebook_of_ones_own(tq, bits, n):
     assert np.array_equal(cache.cpu().numpy(), codec.pack_block(idx, norm, bits))
 
 
+@pytest.mark.parametrize("heads", [1, 2, 3, 9])
+@pytest.mark.parametrize("kind", ["random", "boundary"])
+def test_insert_of_many_rows_by_heads(tq, heads, kind):
+    """Large calls by number of heads (one and two heads take several tiles of tokens at once): random rows, some of
+    which are taken again, and rows that all are (more of them than a CTA can list)."""
+    n, bits = 150000 // heads, 2
+    g = torch.Generator(device="cuda").manual_seed(heads)
+    if kind == "random":
+        x = torch.randn(n, heads, 128, generator=g, device="cuda").to(torch.float16)
+    else:   # two elements of 128: most coordinates are exactly 0
+        x = torch.zeros(n, heads, 128, device="cuda", dtype=torch.float16)
+        at = torch.randint(0, 127, (n, heads, 1), generator=g, device="cuda")
+        x.scatter_(2, at, 1.0).scatter_(2, at + 1, 1.0)
+    cb, signs = tq.tq_codebook_load(128, bits), tq.tq_signs_from_seed(workloads.SIGN_SEED)
+    cache = torch.full((n * heads, 34), 171, dtype=torch.uint8, device="cuda")
+    dst = torch.arange(n, device="cuda") * heads
+    dst[::7] = -1
+    tq.tq_insert_kv(None, x, None, None, None, cb, signs, None, cache, dst, 1)
+    rows = x.double().cpu().numpy().reshape(-1, 128)
+    idx, norm, _ = codec.encode(rows, oracle.sign_diagonal(workloads.SIGN_SEED), oracle_books()[bits][2])
+    want = codec.pack_block(idx, norm, bits).reshape(n, heads, 34)
+    want[::7] = 171
+    assert np.array_equal(cache.cpu().numpy().reshape(n, heads, 34), want)
+
+
 # ---------------------------------------------------------------- far positions
 
 PI = Decimal("3.14159265358979323846264338327950288419716939937510582097494459230781640628620899")

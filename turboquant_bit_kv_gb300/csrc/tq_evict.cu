@@ -36,8 +36,11 @@ constexpr int kMaxCluster = 8;             // portable cluster size
 // contiguous piece of the row's tokens and knows how many stay before it, so a
 // last pass writes the indices in order.  Weights are read from memory once
 // (chunks beyond kSelCached keys are read again from L2) and the indices
-// written once: 4 bytes in a token, 4 out a kept one.  Issue bounds it: about
-// 50 instructions per 32 keys.
+// written once: 4 bytes in a token, 4 out a kept one.  What bounds it is what
+// every CTA does whatever its keys (three histograms cleared, searched and
+// merged, the cluster's meetings) and the latency of one key per lane and
+// iteration: 256 rows of up to 32769 tokens, 2.8 million keys in the 108 that
+// have more than 16384, take about 280 warp instructions per 32 keys.
 
 // Key of a weight: ascending with it as unsigned integers, -0 equal to +0,
 // every NaN above +inf.
@@ -566,8 +569,9 @@ extern "C" int tq_evict_compact(uint8_t *k_blocks, int k_block_bytes, uint8_t *v
     a.num_pages = num_pages;
     const int64_t rows = (int64_t)B * Hkv;
     const int m = keep < T ? keep : T;
-    // CTAs per row: while the GPU holds more (four per SM) and each still gets 64 tokens.  Few CTAs take an
-    // SM's shared memory and threads each, so that a row goes by in few steps (2 rows of 29281 to 22908: 66 us in eight steps, 29 in two)
+    // CTAs per row: doubled while there are fewer than the GPU holds (four per SM; the last doubling may pass that,
+    // 128 rows get 1024 CTAs for 608 places) and each still gets 64 tokens.  Few CTAs take an SM's shared memory and
+    // threads each, so that a row goes by in few steps (2 rows of 29281 to 22908: 66 us in eight steps, 29 in two)
     int C = 1;
     while (C < kMaxCluster && rows * C < 4 * (int64_t)sm_count() && m > C * 64) C *= 2;
     int share = 4;   // CTAs per SM

@@ -540,6 +540,8 @@ def tq_insert_kv(k, v, pos, rope, kcb, vcb, signs, k_blocks, v_blocks, dst, dst_
 
 
 def tq_attn_weights_workspace_bytes(B, Hq, Hkv, T):
+    """Workspace bytes of tq_attn_decode_weights on the current device: make the tensors' device current first where
+    devices are not alike (a workspace too small for its device is refused)."""
     return int(lib().tq_attn_weights_workspace_bytes(B, Hq, Hkv, T))
 
 
