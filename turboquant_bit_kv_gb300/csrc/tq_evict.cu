@@ -40,7 +40,7 @@ constexpr int kMaxCluster = 8;             // portable cluster size
 // every CTA does whatever its keys (three histograms cleared, searched and
 // merged, the cluster's meetings) and the latency of one key per lane and
 // iteration: 256 rows of up to 32769 tokens, 2.8 million keys in the 108 that
-// have more than 16384, take about 280 warp instructions per 32 keys.
+// have more than 16384, take 16.7 million warp instructions, 190 per 32 keys.
 
 // Key of a weight: ascending with it as unsigned integers, -0 equal to +0,
 // every NaN above +inf.
