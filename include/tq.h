@@ -523,7 +523,7 @@ int tq_rope_apply(const void *x, int dtype, int64_t n_tok, int heads, int64_t x_
                   int64_t out_tok_stride, int64_t out_head_stride, void *stream);
 
 /* Insert the keys and values of n_tok new tokens into packed caches in one
- * launch: keys are rotated by rope (as tq_rope_apply, but kept in float32),
+ * launch (one for about every half million tokens of 8 heads): keys are rotated by rope (as tq_rope_apply, but kept in float32),
  * then keys and values are encoded as by tq_encode_kv.  Codes and norms are
  * those of the definition evaluated in double precision (y rounded once to
  * float32 and compared with the float32 boundaries; the norm rounded once to

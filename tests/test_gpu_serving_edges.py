@@ -198,6 +198,24 @@ def test_insert_of_many_rows_by_heads(tq, heads, kind):
     assert np.array_equal(cache.cpu().numpy().reshape(n, heads, 34), want)
 
 
+def test_insert_of_very_many_tokens(tq):
+    """A call of several launches gives what calls of its parts give."""
+    n, bits = 13_000_000, 2
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn(n // 100, 1, 128, generator=g, device="cuda").to(torch.bfloat16).repeat(100, 1, 1)
+    pos = torch.randint(0, 10**6, (2, n), generator=g, device="cuda")
+    rope = tq.tq_rope_load(128, sections=[30, 34])
+    dst = torch.arange(n, device="cuda").flip(0).contiguous()
+    cb, signs = tq.tq_codebook_load(128, bits), tq.tq_signs_from_seed(workloads.SIGN_SEED)
+    caches = [torch.full((n, 34), 171, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    for cache, step in zip(caches, (n, 1_000_003)):
+        for i in range(0, n, step):
+            tq.tq_insert_kv(x[i:i + step], None, pos[:, i:i + step].contiguous(), rope, cb, None, signs, cache, None,
+                            dst[i:i + step], 1)
+    assert torch.equal(caches[0], caches[1])
+    assert not (caches[0][:, 2:] == 171).all(1).any()
+
+
 # ---------------------------------------------------------------- far positions
 
 PI = Decimal("3.14159265358979323846264338327950288419716939937510582097494459230781640628620899")

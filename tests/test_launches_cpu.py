@@ -23,7 +23,7 @@ def linked(tmp_path_factory):
     build_lib.build()
     out = str(tmp_path_factory.mktemp("fake") / "libtq_fake.so")
     objs = [os.path.join(build_lib.BUILD, s + ".o") for s in build_lib.SOURCES]
-    cuda = os.path.dirname(os.path.dirname(build_lib.NVCC))
+    cuda = os.path.dirname(os.path.dirname(shutil.which(build_lib.NVCC) or build_lib.NVCC))
     r = subprocess.run(["g++", "-std=c++17", "-shared", "-fPIC", "-Wl,-Bsymbolic", "-I" + os.path.join(cuda, "include"), "-o", out,
                         os.path.join(HERE, "fake_cudart.cpp")] + objs + ["-lpthread"], capture_output=True, text=True)
     assert r.returncode == 0, r.stderr
@@ -137,3 +137,12 @@ def test_rope_refuses_rows_that_overlap(lib):
         assert got == (ARG if overlap else 0), (n, s, m, t, overlap)
         seen[overlap] += 1
     assert min(seen) > 200
+
+
+def test_launches_of_an_insert(lib):
+    """One launch, of very many tokens a few: a CTA has places for the rows that it takes again among 15200 rows."""
+    for heads, n, want in ((8, 16, 1), (8, 131072, 1), (8, 460000, 1), (8, 1000000, 3), (1, 2000000, 1), (1, 10000000, 5),
+                           (40, 200000, 3), (100000, 100, 2)):
+        lib.fake_reset()
+        assert insert(lib, heads, n) == 0
+        assert lib.fake_launches() == want, (heads, n, lib.fake_launches())

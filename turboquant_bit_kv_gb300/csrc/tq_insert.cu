@@ -1300,6 +1300,15 @@ int launch(const tq_rope &rope, const InsertArgs &a, cudaStream_t st) {
     return launch_status();
 }
 
+int launch_part(int dtype, const tq_rope &rope, const InsertArgs &a, int sides, cudaStream_t st) {
+    const bool small = a.n_tok <= (int64_t)sm_count() * kFewRows / ((int64_t)a.heads * sides);
+    switch (dtype) {
+        case TQ_BF16: return small ? launch_few<TQ_BF16>(rope, a, sides, st) : launch<TQ_BF16>(rope, a, st);
+        case TQ_F16: return small ? launch_few<TQ_F16>(rope, a, sides, st) : launch<TQ_F16>(rope, a, st);
+        default: return small ? launch_few<TQ_F32>(rope, a, sides, st) : launch<TQ_F32>(rope, a, st);
+    }
+}
+
 // A bound for a codebook, in v.
 float border(const Bound &e, const tq_codebook *cb) {
     float b = 0.f;
@@ -1377,34 +1386,39 @@ extern "C" int tq_insert_kv(const void *k, int64_t k_tok_stride, int64_t k_head_
     a.pos_axis = pos_axis_stride;
     a.dst = dst;
     a.dst_head = dst_head_stride;
-    a.n_tok = n_tok;
     a.heads = heads;
     for (int i = 0; i < 4; ++i) a.signs[i] = signs.w[i];
     // token tiles of a CTA: its four warps share a tile's sines, or take a tile each where heads are few
     a.tiles = heads == 1 ? 4 : heads == 2 ? 2 : 1;
     // the lists: what four CTAs leave of 196 KB of shared memory (with more of it, and less L1, float32 rows take 15%
-    // longer).  Of random rows one is full after 25,000 rows of a CTA, in calls of 1.1 million tokens x 8 heads.
+    // longer)
     a.list = a.tiles > 1 ? 128 : 190;
-    const int64_t tiles = (n_tok + (int64_t)kTok * a.tiles - 1) / (kTok * a.tiles);
     const int sides = (k != nullptr) + (v != nullptr);
-    const int64_t slots = (int64_t)sm_count() * 4, few = (int64_t)sm_count() * kFewRows;
-    // with few tiles, four heads a CTA fill more SMs
-    a.heads_per_cta = heads <= kWarps || tiles * sides >= slots ? heads : kWarps;
-    a.groups = (heads + a.heads_per_cta - 1) / a.heads_per_cta;
-    if (tiles * a.groups > 0x3FFFFFFF) return TQ_ERR_UNSUPPORTED;
-    a.units = (int)(tiles * a.groups);
+    const int64_t slots = (int64_t)sm_count() * 4;
     // a rotated key costs about half as much again as a value
     const int64_t share = sides == 1 ? slots : a.side[0].style == kRopeNone ? slots / 2 : slots * 3 / 5;
-    a.ctas[0] = k ? (int)min64(a.units, share) : 0;
-    a.ctas[1] = v ? (int)min64(a.units, k ? slots - share : slots) : 0;
+    // A launch takes 80 rows of a CTA for every place of a list at most: of random rows up to 0.8% come on one, and a
+    // CTA whose list overflows takes all its rows again, four times as long.  Half a million tokens x 8 heads.
+    const int64_t fewest = sides == 1 ? slots : min64(share, slots - share);
+    const int64_t most = max64(64, (int64_t)a.list * 80 * fewest / heads & ~(int64_t)63);
     tq_rope none;
     if (!rope) std::memset(&none, 0, sizeof(none));
-    const tq_rope &r = rope ? *rope : none;
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const bool small = n_tok <= few / ((int64_t)heads * sides);
-    switch (dtype) {
-        case TQ_BF16: return small ? launch_few<TQ_BF16>(r, a, sides, st) : launch<TQ_BF16>(r, a, st);
-        case TQ_F16: return small ? launch_few<TQ_F16>(r, a, sides, st) : launch<TQ_F16>(r, a, st);
-        default: return small ? launch_few<TQ_F32>(r, a, sides, st) : launch<TQ_F32>(r, a, st);
+    for (int64_t done = 0; done < n_tok; done += most) {
+        a.n_tok = min64(most, n_tok - done);
+        const int64_t tiles = (a.n_tok + (int64_t)kTok * a.tiles - 1) / (kTok * a.tiles);
+        // with few tiles, four heads a CTA fill more SMs
+        a.heads_per_cta = heads <= kWarps || tiles * sides >= slots ? heads : kWarps;
+        a.groups = (heads + a.heads_per_cta - 1) / a.heads_per_cta;
+        if (tiles * a.groups > 0x3FFFFFFF) return TQ_ERR_UNSUPPORTED;
+        a.units = (int)(tiles * a.groups);
+        a.ctas[0] = k ? (int)min64(a.units, share) : 0;
+        a.ctas[1] = v ? (int)min64(a.units, k ? slots - share : slots) : 0;
+        const int status = launch_part(dtype, rope ? *rope : none, a, sides, static_cast<cudaStream_t>(stream));
+        if (status != TQ_OK) return status;
+        for (Side &s : a.side)
+            if (s.x) s.x += a.n_tok * s.tok;
+        if (rope) a.pos += a.n_tok;
+        a.dst += a.n_tok;
     }
+    return TQ_OK;
 }
