@@ -628,6 +628,124 @@ int tq_evict_compact(uint8_t *k_blocks, int k_block_bytes, uint8_t *v_blocks, in
                      const int32_t *block_table, int max_pages, int page_tokens, int num_pages, int B, int Hkv,
                      int T_cap, int T, void *stream);
 
+/* ---- A serving step over paged caches: what the calls above take, made on the
+ * GPU from the requests' lengths (tq_page_plan), queries and keys as
+ * projections leave them (tq_norm_rope_apply), and decode attention of a batch
+ * behind one prefix (tq_attn_decode_shared).  In a step they run in this order,
+ * tq_insert_kv (without a rope: the keys are turned already) before the
+ * attention. */
+
+/* Block tables, slots and positions of a step.  Request b has cached_lens[b]
+ * tokens in the cache and fresh_lens[b] new ones (negative: 0), and holds the
+ * first held[b] pages of its row of the table.  Requests are served in order:
+ * one that needs more pages than it holds for cached + fresh tokens takes them
+ * from the end of the list of free pages, the last one first, and enters them
+ * behind those that it holds; the first for which too few are left, and every
+ * later one that needs any, is refused.  Refused are also requests of more
+ * tokens than max_pages pages hold, and those whose tokens end past n_tok.  A
+ * refused request takes no page and keeps its length.
+ *   pos_start       device int64 [B]: position of a request's first new token
+ *                   (after an eviction positions run ahead of slots); NULL:
+ *                   cached_lens[b].
+ *   block_table     device int32, request b's row at b * table_row_stride,
+ *                   max_pages entries: entries from held[b] on are written as
+ *                   pages are taken, all others left as they are.  A page that
+ *                   several requests name (of a shared prefix) must be full.
+ *   held, new_held  device int32 [B]; new_held may be held.
+ *   free_pages      device int32 [n_free], of which the first free_count[0]
+ *                   (clamped to [0, n_free]) are free; new_free_count (may be
+ *                   free_count) is what is left of them.  Pages are returned by
+ *                   appending them.
+ *   seq_lens        device int32 [B]: cached + fresh, or cached of a refused
+ *                   request.
+ *   tok_start       device int32 [B + 1]: the first of a request's new tokens,
+ *                   request after request (refused ones too); held at 2^31 - 1.
+ *   dst, pos        device int64 [n_tok]: the slot of head 0 of a new token as
+ *                   tq_insert_kv takes it (pools [pages][Hkv][page_tokens], head
+ *                   stride page_tokens), and its position.  Tokens of refused
+ *                   requests have dst -1; tokens behind the last request's
+ *                   (padding) have dst -1 and position 0.
+ * Outputs must not be inputs, other than as stated.  Errors: TQ_ERR_ARG,
+ * TQ_ERR_UNSUPPORTED (n_tok above 2^31 - 1, more than 2^24 requests),
+ * TQ_ERR_ALIGN, TQ_ERR_CUDA. */
+int tq_page_plan(const int32_t *cached_lens, const int32_t *fresh_lens, const int64_t *pos_start, int B, int Hkv,
+                 int page_tokens, int32_t *block_table, int64_t table_row_stride, int max_pages, const int32_t *held,
+                 int32_t *new_held, const int32_t *free_pages, int n_free, const int32_t *free_count,
+                 int32_t *new_free_count, int32_t *seq_lens, int32_t *tok_start, int64_t *dst, int64_t *pos,
+                 int64_t n_tok, void *stream);
+
+/* Normalise the heads of queries and keys one by one and turn them, in one
+ * pass: y = x / sqrt(mean(x^2) + eps) * weight, then as tq_rope_apply, in
+ * float32, rounded once to dtype.
+ *   q, k, q_out, k_out   device rows of 128 elements of dtype; head h of token n
+ *             at n * tok_stride + h * head_stride elements (alignment as
+ *             tq_rope_apply).  q_heads or k_heads may be 0 (pointers then
+ *             unused).  No two rows of an output may overlap, nor q_out and
+ *             k_out.  q_out may be q itself, k_out k, with the same strides (in
+ *             place); otherwise outputs must not overlap inputs.
+ *   q_weight, k_weight   device [128] of weight_dtype, or NULL (ones).
+ *   eps       at least 2^-100.
+ *   pos, rope as tq_rope_apply; rope NULL: normalised only (pos then unused).
+ * A row with an infinite or NaN element gives NaN there (and zeros in place of
+ * its finite elements, NaN if it holds a NaN).  n_tok == 0 is a no-op.
+ * Errors: TQ_ERR_ARG, TQ_ERR_UNSUPPORTED (also more than 2^26 heads),
+ * TQ_ERR_ALIGN, TQ_ERR_CUDA. */
+int tq_norm_rope_apply(const void *q, int q_heads, int64_t q_tok_stride, int64_t q_head_stride, const void *k,
+                       int k_heads, int64_t k_tok_stride, int64_t k_head_stride, int dtype, int64_t n_tok,
+                       const void *q_weight, const void *k_weight, int weight_dtype, float eps, const int64_t *pos,
+                       int64_t pos_axis_stride, const tq_rope *rope, void *q_out, int64_t q_out_tok_stride,
+                       int64_t q_out_head_stride, void *k_out, int64_t k_out_tok_stride, int64_t k_out_head_stride,
+                       void *stream);
+
+/* Workspace bytes of tq_attn_decode_shared for prefixes of up to P and own
+ * contexts of up to T tokens on the current device.  Host only.  0 for an
+ * invalid shape. */
+size_t tq_attn_shared_workspace_bytes(int B, int Hq, int Hkv, int P, int T);
+
+/* Decode attention (one query token per sequence) of a batch whose sequences
+ * all start with the same prefix, which is read, and its codes looked up, once
+ * for the batch: every sequence attends to the prefix's tokens and, behind them,
+ * to its own.
+ *   q            device [B][Hq][128] of q_dtype, Hq / Hkv <= 8.  Rotated and
+ *                scaled (times scale log2 e) its elements must stay below 65504.
+ *   k_prefix, v_prefix   device blocks [Hkv][P_cap] (P_cap a multiple of 8), or,
+ *                with tables, pools [pages][Hkv][page_tokens] (page_tokens a
+ *                multiple of 8) in which token t of the prefix is slot t %
+ *                page_tokens of page prefix_table[t / page_tokens] (device
+ *                int32, P_cap the tokens that its pages hold).
+ *   P, prefix_len   the prefix's length is prefix_len[0] (device int32, clamped
+ *                to [0, P]), or P where prefix_len is NULL; 1 <= P <= P_cap.
+ *   k_blocks, v_blocks   the own tokens', as tq_attn_decode_weights: [B][Hkv]
+ *                [T_cap], or with a block_table pools (which may be the
+ *                prefix's).  Token t of sequence b is slot t % page_tokens of
+ *                page block_table[b * table_row_stride + t / page_tokens],
+ *                max_pages entries: of a table whose rows start with the
+ *                prefix's pages, the columns behind them.  block_table and
+ *                prefix_table come together.
+ *   seq_lens     device int32 [B]: own tokens (at most T; NULL: T).  0: the
+ *                prefix only; negative: the sequence is not there, its output 0.
+ *   kcb, vcb     2-, 3- or 4-bit codebooks of tq_codebook_load(128, bits), for
+ *                the prefix and the own tokens (4 bits: antisymmetric).
+ *   out          device [B][Hq][128] of out_dtype.  Keys and values of the
+ *                prefix and values of the own tokens enter the tensor cores in
+ *                16 bits: float32 outputs are good to about 1e-4 of their
+ *                largest element.
+ *   workspace    >= tq_attn_shared_workspace_bytes(B, Hq, Hkv, P, T) bytes,
+ *                16-byte aligned, clobbered; calls that overlap on the GPU must
+ *                use different workspaces.
+ * No token at all (empty prefix, no own tokens) gives output 0; NaN and +inf
+ * scores give NaN outputs.  Results do not depend on timing.  Errors:
+ * TQ_ERR_ARG, TQ_ERR_UNSUPPORTED (turboq8, Hq / Hkv > 8, page_tokens not a
+ * multiple of 8, P or T > 2^31 - 8192, B Hq > 2^24), TQ_ERR_ALIGN,
+ * TQ_ERR_WORKSPACE, TQ_ERR_CUDA. */
+int tq_attn_decode_shared(const void *q, int q_dtype, const uint8_t *k_prefix, const uint8_t *v_prefix,
+                          const int32_t *prefix_table, int P_cap, int P, const int32_t *prefix_len,
+                          const uint8_t *k_blocks, const tq_codebook *kcb, const uint8_t *v_blocks,
+                          const tq_codebook *vcb, const int32_t *block_table, int64_t table_row_stride, int max_pages,
+                          int page_tokens, const int32_t *seq_lens, int B, int Hq, int Hkv, int T_cap, int T,
+                          float scale, tq_signs signs, void *out, int out_dtype, void *workspace,
+                          size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

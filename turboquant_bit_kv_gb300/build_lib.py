@@ -17,9 +17,10 @@ SOURCES = ["tq_host.cpp", "tq_encode.cu", "tq_decode.cu", "tq_codec.cu", "tq_qjl
            "tq_attn_mma_k3.cu", "tq_attn_mma_k4.cu", "tq_attn_mma_k8.cu", "tq_status.cu",
            "tq_attn_prefill.cu", "tq_ext.cu", "tq_headdim.cu", "tq_headdim_tc.cu", "tq_headdim_mma.cu",
            "tq_headdim_mma8.cu", "tq_rope.cu", "tq_insert.cu", "tq_evict.cu",
-           "tq_attn_weights.cu", "tq_attn_mma_k2w.cu", "tq_attn_mma_k3w.cu", "tq_attn_mma_k4w.cu"]
+           "tq_attn_weights.cu", "tq_attn_mma_k2w.cu", "tq_attn_mma_k3w.cu", "tq_attn_mma_k4w.cu",
+           "tq_attn_shared.cu", "tq_norm_rope.cu", "tq_page_plan.cu"]
 HEADERS = ["tq_device.cuh", "tq_tc.cuh", "tq_attn.cuh", "tq_attn_mma.h", "tq_attn_mma.cuh", "tq_internal.h", "tq_headdim.cuh",
-           "tq_headdim_mma.cuh", "tq_rope.cuh", "tq_attn_combine.cuh", "tq_ff.cuh"]
+           "tq_headdim_mma.cuh", "tq_rope.cuh", "tq_attn_combine.cuh", "tq_ff.cuh", "tq_rows.cuh"]
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

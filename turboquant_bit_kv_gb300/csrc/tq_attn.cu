@@ -123,6 +123,19 @@ __global__ void __launch_bounds__(kAttnThreads) attn_prep_mma_kernel(const __gri
         }
         const float f = a.qscale * 0.08838834764831845f;
         reinterpret_cast<float4 *>(qs + h * kD)[lane] = make_float4(v[0] * f, v[1] * f, v[2] * f, v[3] * f);
+        if (a.q_tiles && h < a.G) {
+            // row b G + h of the KV head's operand tiles (128-byte swizzle): hi parts, then lo parts
+            const int row = b * a.G + h, r = row & 127;
+            uint8_t *tile = a.q_tiles + ((int64_t)kvh * a.q_tile_count + (row >> 7)) * 65536 + r * 128;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int p = operand_place(4 * lane + k, a.q_tile_bits);
+                uint8_t *at = tile + (p >> 6) * 16384 + ((((p & 63) >> 3) ^ (r & 7)) << 4) + (p & 7) * 2;
+                const __half hi = __float2half_rn(v[k] * f);
+                *reinterpret_cast<__half *>(at) = hi;
+                *reinterpret_cast<__half *>(at + 32768) = __float2half_rn(v[k] * f - __half2float(hi));
+            }
+        }
     }
     __syncthreads();
     if (qjl) {

@@ -50,7 +50,18 @@ struct AttnArgs {
     float *scores;           // [B * Hkv][chunks][G][32] log2-domain scores
     int2 *live;              // [B * Hkv]: a segment's first worker, and how many workers meet it
     int workers;
+    // attention behind a shared prefix only (others: null): the rotated queries also as operand tiles
+    // [Hkv][q_tile_count][hi, lo] of 128 query rows b * G + g, dims in the places of q_tile_bits-bit keys
+    uint8_t *q_tiles;
+    int q_tile_count, q_tile_bits;
 };
+
+// Place of dim d among an operand tile's columns, where codes of `bits` bits are
+// turned into levels 16 dims at a time in the order that costs least.
+__host__ __device__ inline int operand_place(int d, int bits) {
+    const int e = d & 15;
+    return (d & ~15) | (bits == 4 ? e : bits == 3 ? 8 * (e & 1) + (e >> 1) : 4 * (e & 3) + (e >> 2));
+}
 
 __host__ __device__ inline int attn_tiles(int T) { return (T + kTT - 1) / kTT; }
 

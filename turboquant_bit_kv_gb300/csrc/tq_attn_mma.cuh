@@ -514,8 +514,9 @@ __device__ __forceinline__ void live_place(const AttnArgs &a, int x, int inc, in
     }
 }
 
-// SCORES: every live token's scores (log2 domain, before the softmax) are also
-// written to a.scores, from which attn_weights_kernel takes the attention
+// SCORES: work is split over the chunks that hold tokens, and, where a.scores is
+// given, every live token's scores (log2 domain, before the softmax) are also
+// written to it, from which attn_weights_kernel takes the attention
 // weights once the softmax statistics are final.
 template <int KB, int VB, bool QJL, int NT, bool WIDE, bool PAGED = false, bool SCORES = false>
 __global__ void __launch_bounds__(Cfg<KB, VB, QJL, NT, WIDE>::kThreads, Cfg<KB, VB, QJL, NT, WIDE>::kMinBlocks)
@@ -919,7 +920,7 @@ __global__ void __launch_bounds__(Cfg<KB, VB, QJL, NT, WIDE>::kThreads, Cfg<KB, 
                     s[nt][mt][1] = tb < nvalid ? eb : -INFINITY;
                 }
             }
-            if constexpr (SCORES) {
+            if (SCORES && a.scores) {   // (attention behind a shared prefix keeps none)
                 // per chunk G rows of 32 tokens: a warp's store of one fragment row fills 32-byte pieces of
                 // 4 rows
                 float *sc = a.scores + ((int64_t)j * plan.C + ci) * (kMmaChunk * a.G);

@@ -101,6 +101,10 @@ inline int weights_parts(int sms, int64_t segs, int T, int64_t &per) {
     return (int)((T + per - 1) / per);
 }
 
+// A common factor for a codebook's centroids under which their fp16 roundings
+// are smallest (tq_attn_weights.cu).
+float attn_centroid_factor(const tq_codebook *cb);
+
 // Slot groups of 128 threads in a combine CTA: one per 32 slots of Smax, at most kCombineMaxGroups.
 inline int mma_combine_groups(const MmaPlan &p) {
     const int g = (p.Smax + 31) / 32;

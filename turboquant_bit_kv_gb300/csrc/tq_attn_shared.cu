@@ -1,0 +1,953 @@
+// tq_attn_decode_shared: one query token per sequence over a packed cache
+// whose first part, a prefix, is the same for the whole batch.
+//
+//   o_b = sum_t softmax(s_b)_t v_t over the prefix's tokens and sequence b's own,
+//   s_t = scale * n_t <R q, c[code_t]>,  values summed in the rotated domain,
+//   o = R^T (sum) / sqrt(128) at the end.
+//
+// A sequence at a time, the prefix would be read and its codes looked up once
+// per sequence; looking them up is what bounds the decode attention.  Together,
+// the B x G query rows of a KV head meet the same keys, so the prefix is two
+// dense products on the 5th-generation tensor cores and every code is turned
+// into a number once per 256 rows.  The sequences' own tokens go through the
+// decode attention's kernel (tq_attn_mma.cuh) as they are; a merge adds the two
+// parts up: each part of the context leaves the maximum, the sum and the sum of
+// values of its softmax, and those join exactly.
+//
+// Four launches, chained as programmatic dependents: query prep (rotated once,
+// as operand tiles and as fragments), prefix, own tokens, merge.
+//
+// The prefix kernel.  A CTA takes 256 query rows (two tiles of 128, one
+// stream each) or, where a KV head has an odd tile, 128 (both streams take that
+// tile, every other key tile each), and a range of the prefix in tiles of 128
+// keys:
+//   S[128 rows x 128 keys] = Q K^T   Q split hi + lo into fp16, K single fp16
+//   O[128 rows x 128 dims] += P V    P split hi + lo, in tensor memory, V single
+// accumulated in float32 in tensor memory.  Centroids are fp16 under a common
+// factor that makes their roundings small (attn_centroid_factor: at most 2^-18
+// / 2^-15 / 2^-13.5 of the level for 2 / 3 / 4 bits), so one product with K
+// does where the decode kernel's own factor of 1 needs two.  Key norms scale
+// the scores, value norms the probabilities.
+//
+// Tensor memory: S of stream x at column 128 x, O at 256 + 128 x.  P takes the
+// place of S: a thread reads 32 scores of its row and writes their
+// probabilities' hi (16 columns) and lo parts over them.  The products are
+// issued in the order P V of one stream, S of the same stream's next tile, then
+// the other stream, so one stream's softmax runs while the other's products do.
+//
+// Roles (448 threads, one CTA per SM):
+//   warps 0-3, 4-7  rows of stream 0, 1: a thread a row (its tensor-memory
+//              lane).  The reference of a row's exponents is its largest score
+//              plus the tile's largest value norm (in log2), and moves only
+//              when it is exceeded by more than 8, so O is rarely rescaled and
+//              P times the value norm stays below 2^15 whatever the norms are.
+//   warps 8-11 a thread a key: codes to fp16 in registers (byte permutes over
+//              the levels' bytes; no lookups in shared memory, which the
+//              products keep busy), into the swizzled K and V tiles.
+//   warp 12    bulk copies: the query tiles, then the packed blocks.
+//   warp 13    one thread issues the products.
+// Every wait is bounded; one that gives up is recorded (tq_device_status).
+#include <cmath>
+
+#include "tq_attn.cuh"
+#include "tq_attn_combine.cuh"
+#include "tq_attn_mma.h"
+#include "tq_internal.h"
+#include "tq_tc.cuh"
+
+namespace tq {
+
+int launch_attn_mma_scores_k2(const AttnArgs &a, MmaPlan &plan, int vb, int nt, bool paged, cudaStream_t st);
+int launch_attn_mma_scores_k3(const AttnArgs &a, MmaPlan &plan, int vb, int nt, bool paged, cudaStream_t st);
+int launch_attn_mma_scores_k4(const AttnArgs &a, MmaPlan &plan, int vb, int nt, bool paged, cudaStream_t st);
+int launch_attn_prep_mma(const AttnArgs &a, const MmaPlan &plan, int qjl, cudaStream_t st);
+
+namespace {
+
+constexpr int kShKeys = 128;                 // keys per tile
+constexpr int kShRows = 128;                 // rows per stream
+constexpr int kShRowWarps = 8, kShKeyWarps = 4;
+constexpr int kShProducer = kShRowWarps + kShKeyWarps, kShMma = kShProducer + 1;
+constexpr int kShThreads = 32 * (kShMma + 1);
+constexpr uint32_t kShCols = 512, kShColO = 256;
+constexpr int kShNormSlot = (2 * kShKeys + 4) * 4;   // key norms | value norms | four maxima of log2 value norm
+constexpr float kShUp = 128.f;               // P is held times this
+
+// mbarriers
+enum {
+    kQFull = 0,        // query tiles landed
+    kKFull = 1,        // [2] packed key blocks landed
+    kKEmpty = 3,       // [2] ... and turned into the operand tile
+    kVFull = 5,        // [2]
+    kVEmpty = 7,       // [2]
+    kKReady = 9,       // [2] operand tile of keys written (4 key warps)
+    kKFree = 11,       // [2] the products that read it completed
+    kVReady = 13,      // [2]
+    kVFree = 15,       // [2]
+    kNReady = 17,      // [4] norms of a tile written
+    kSReady = 21,      // [2] stream's scores in tensor memory
+    kPReady = 23,      // [2] stream's P in their place (4 row warps)
+    kODone = 25,       // [2] stream's last product completed
+    kDrain = 27,
+    kShBars = 28
+};
+
+// Shared memory, from a 1024-byte aligned base.  A KV head's even tiles of
+// rows: Q of the two streams, one K and one V tile; an odd one: Q, and a K and
+// a V tile for each stream.  32 KB apiece: hi and lo of Q, K, V.
+template <int KB, int VB>
+struct ShSmem {
+    static constexpr int kTile = 32768;
+    static constexpr int kKBlk = 6 * kTile;                          // packed key blocks, kNK stages
+    static constexpr int kKBytes = kShKeys * (2 + 16 * KB), kVBytes = kShKeys * (2 + 16 * VB);
+    static constexpr int kRest = 4 * kShNormSlot + kShBars * 8 + 16 + 1024;
+    // value blocks two tiles ahead (their norms are wanted before the tile's turn), key blocks too where
+    // there is room
+    static constexpr int kNV = 2;
+    static constexpr int kNK = kKBlk + 2 * kKBytes + 2 * kVBytes + kRest <= 232448 ? 2 : 1;
+    static constexpr int kVBlk = kKBlk + kNK * kKBytes;
+    static constexpr int kNorm = kVBlk + kNV * kVBytes;              // [4] slots
+    static constexpr int kBars = kNorm + 4 * kShNormSlot;
+    static constexpr int kSlot = kBars + kShBars * 8;                // tensor-memory base, failure flag
+    static constexpr int kTotal = kSlot + 16 + 1024;
+    static_assert(kTotal <= 232448, "shared memory of one CTA");
+    static_assert(kNorm % 16 == 0 && kBars % 8 == 0, "alignment");
+};
+
+// Partition of the prefix's work: per KV head `pairs` CTAs' worth of 256 rows in
+// s2 ranges of the prefix each and, with an odd tile, one of 128 in s1 ranges.
+struct SharedPlan {
+    int tiles, pairs, odd, s2, s1, per_head, ctas;
+};
+
+struct SharedArgs {
+    const uint8_t *q;         // operand tiles [Hkv][tiles][hi, lo][32 KB]
+    const uint8_t *k, *v;     // the prefix's blocks [Hkv][cap], or pools with a table
+    const int32_t *table;
+    const int32_t *len;       // tokens of the prefix (null: P)
+    float *part;              // [ctas][2][128][132]
+    int rows, Hkv, P, cap, page;
+    SharedPlan plan;
+    float k_norm;             // 1 / the key centroids' factor
+    uint32_t kt[4], vt[4];    // bytes of the levels (see levels4)
+    int drop;                 // test hook: the copies' barriers wait for an arrival that never comes
+};
+
+__device__ __forceinline__ int shared_len(const int32_t *len, int P) {
+    if (!len) return P;
+    const int n = *len;
+    return n < 0 ? 0 : (n > P ? P : n);
+}
+
+// Range w of n tiles cut into W = min(ranges, n) equal parts.
+__device__ __forceinline__ void shared_range(int n, int ranges, int w, int &lo, int &hi) {
+    const int W = n < ranges ? n : ranges;
+    lo = w < W ? (int)((int64_t)w * n / W) : 0;
+    hi = w < W ? (int)(((int64_t)w + 1) * n / W) : 0;
+}
+
+__device__ __forceinline__ uint32_t sh_prmt(uint32_t a, uint32_t b, uint32_t sel) {
+    uint32_t r;
+    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t sh_lds32(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr));
+    return v;
+}
+
+__device__ __forceinline__ uint32_t sh_lds16(uint32_t addr) {
+    unsigned short v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr));
+    return v;
+}
+
+__device__ __forceinline__ void sh_sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+__device__ __forceinline__ void sh_bulk(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+
+// Shared-memory descriptor of an operand tile in the 128-byte swizzle layout.
+__device__ __forceinline__ uint64_t sh_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) |
+           ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+
+// kind::f16, float32 accumulator, fp16 operands, M = N = 128; mn: B is MN-major.
+__host__ __device__ constexpr uint32_t sh_idesc(uint32_t mn) {
+    return (1u << 4) | (mn << 16) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
+}
+
+// D (+)= A B, A in tensor memory (rows in lanes, two fp16 a column).
+__device__ __forceinline__ void sh_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::
+            "r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ void sh_st32(uint32_t taddr, const uint32_t (&v)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
+        "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
+        "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+        : "memory");
+}
+
+// 2^x (the special-function unit's approximation, a few ulp; 2^-inf = 0).
+__device__ __forceinline__ float sh_ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// (hi, lo) fp16 parts of two floats: x = hi + lo to about 2^-22.
+__device__ __forceinline__ void sh_split(float x0, float x1, uint32_t &hi, uint32_t &lo) {
+    const __half2 h = __floats2half2_rn(x0, x1);
+    const float2 f = __half22float2(h);
+    const __half2 l = __floats2half2_rn(x0 - f.x, x1 - f.y);
+    hi = *reinterpret_cast<const uint32_t *>(&h);
+    lo = *reinterpret_cast<const uint32_t *>(&l);
+}
+
+// ---- codes to fp16 levels.  A byte permute picks four bytes by the four low
+// nibbles of its selector, each from eight: the levels' high and low bytes,
+// which two more permutes put together into two pairs.  Tables t: 2 bits: high
+// bytes, low bytes of the four levels; 3 bits: high bytes (two words), low
+// bytes (two words) of the eight; 4 bits: the same of the eight positive levels
+// (the other half mirrored, their sign set).  The order in which the dims come
+// out is the one that costs least; operand_place gives a dim's place, and Q
+// and the sums of values follow it.
+
+// Eight levels as four words of two, from a selector of eight nibbles (3, 4 bits).
+template <int BITS>
+__device__ __forceinline__ void levels8(const uint32_t (&t)[4], uint32_t sel, uint32_t raw, uint32_t (&o)[4]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const uint32_t s = h ? sel >> 16 : sel;
+        uint32_t hb = sh_prmt(t[0], t[1], s);
+        const uint32_t lb = sh_prmt(t[2], t[3], s);
+        if constexpr (BITS == 4) {
+            // bit 3 of a nibble copies the byte's top bit into all of it: 0xFF for the upper half, else
+            // 0x80; bit 6 of that, inverted, is the sign
+            const uint32_t r = sh_prmt(0x80808080u, 0x80808080u, h ? raw >> 16 : raw);
+            hb |= ~(r << 1) & 0x80808080u;
+        }
+        o[2 * h] = sh_prmt(lb, hb, 0x5140u);
+        o[2 * h + 1] = sh_prmt(lb, hb, 0x7362u);
+    }
+}
+
+// Levels of 16 dims as eight words of two, in the operand's order: w the code
+// words of those dims (4 bits: two, 3 bits: the low plane's and, in its low
+// half, the high plane's, 2 bits: one).
+template <int BITS>
+__device__ __forceinline__ void levels16(const uint32_t (&t)[4], uint32_t w0, uint32_t w1, uint32_t (&o)[8]) {
+    if constexpr (BITS == 4) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t w = i ? w1 : w0;
+            const uint32_t flip = ((~w >> 3) & 0x11111111u) * 7u;   // the lower half counts down
+            uint32_t q[4];
+            levels8<4>(t, (w ^ flip) & 0x77777777u, w, q);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) o[4 * i + k] = q[k];
+        }
+    } else if constexpr (BITS == 3) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            // even (odd) dims: the low plane's pairs of bits are nibbles as they are, the high plane's
+            // bits are spread to them
+            uint32_t x = (w1 >> s) & 0x5555u;
+            x = (x | (x << 8)) & 0x00FF00FFu;
+            x = (x | (x << 4)) & 0x05050505u;
+            x = (x | (x << 2)) & 0x11111111u;
+            uint32_t q[4];
+            levels8<3>(t, ((w0 >> (2 * s)) & 0x33333333u) | (x << 2), 0, q);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) o[4 * s + k] = q[k];
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            // the codes of dims 4 i + k in bytes; nibbles code + 4 (low byte), code (high byte) pick a level whole
+            const uint32_t d = ((w0 >> (2 * k)) & 0x03030303u) * 17u | 0x04040404u;
+            o[2 * k] = sh_prmt(t[0], t[1], d);
+            o[2 * k + 1] = sh_prmt(t[0], t[1], d >> 16);
+        }
+    }
+}
+
+// A block's codes (block at shared address blk, 2-byte aligned) into row r of an
+// operand tile at `tile`.
+template <int BITS>
+__device__ __forceinline__ void dequant_row(const uint32_t (&t)[4], uint32_t blk, uint32_t tile, int r) {
+    constexpr int NW = BITS == 4 ? 16 : 8;
+    const uint32_t at = blk + 2, base = at & ~3u, sh = (at & 3u) * 8u;
+    uint32_t hp[4] = {0, 0, 0, 0};
+    if constexpr (BITS == 3) {
+        uint32_t raw[5];
+#pragma unroll
+        for (int i = 0; i < 5; ++i) raw[i] = sh_lds32(base + 32 + 4 * i);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) hp[i] = __funnelshift_r(raw[i], raw[i + 1], sh);
+    }
+    constexpr int WPG = NW / 8;   // words per 16 dims
+    uint32_t prev = sh_lds32(base);
+#pragma unroll
+    for (int a = 0; a < 8; ++a) {
+        uint32_t w[2] = {0, 0};
+#pragma unroll
+        for (int i = 0; i < WPG; ++i) {
+            const uint32_t next = sh_lds32(base + 4 * (WPG * a + i + 1));
+            w[i] = __funnelshift_r(prev, next, sh);
+            prev = next;
+        }
+        if constexpr (BITS == 3) w[1] = (hp[a >> 1] >> (16 * (a & 1))) & 0xFFFFu;
+        uint32_t o[8];
+        levels16<BITS>(t, w[0], w[1], o);
+        const uint32_t row = tile + (a >> 2) * 16384 + r * 128;
+        const uint32_t c = 2 * (a & 3);
+        sh_sts128(row + ((c ^ (r & 7)) << 4), o[0], o[1], o[2], o[3]);
+        sh_sts128(row + (((c + 1) ^ (r & 7)) << 4), o[4], o[5], o[6], o[7]);
+    }
+}
+
+template <int KB, int VB>
+__global__ void __launch_bounds__(kShThreads, 1) attn_shared_kernel(const __grid_constant__ SharedArgs a) {
+    using S = ShSmem<KB, VB>;
+    extern __shared__ __align__(16) uint8_t sh_smem_raw[];
+    const uint32_t raw_s = (uint32_t)__cvta_generic_to_shared(sh_smem_raw);
+    const uint32_t base_s = (raw_s + 1023u) & ~1023u;
+    uint8_t *smem = sh_smem_raw + (base_s - raw_s);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    auto bar = [&](int i) { return base_s + S::kBars + 8u * (uint32_t)i; };
+    volatile int *fail_s = reinterpret_cast<volatile int *>(smem + S::kSlot + 4);
+    float *norms = reinterpret_cast<float *>(smem + S::kNorm);
+
+    // ---- the CTA's rows and key tiles
+    const SharedPlan &p = a.plan;
+    const int kvh = blockIdx.x / p.per_head, in = blockIdx.x % p.per_head;
+    const bool two = in < p.pairs * p.s2;
+    const int qt = two ? 2 * (in / p.s2) : 2 * p.pairs;   // first tile of rows
+    const int len = shared_len(a.len, a.P);
+    int tile0, tile1;
+    shared_range((len + kShKeys - 1) / kShKeys, two ? p.s2 : p.s1, two ? in % p.s2 : in - p.pairs * p.s2, tile0, tile1);
+    const int nt = tile1 - tile0;
+    // operand tiles: Q of stream x, and key / value tiles of stage st
+    auto q_at = [&](int x) { return base_s + (two ? x : 0) * 2 * S::kTile; };
+    auto k_at = [&](int st) { return base_s + (two ? 4 : 2 + 2 * st) * S::kTile; };
+    auto v_at = [&](int st) { return k_at(st) + S::kTile; };
+    // tile i of the CTA: its operand stage, and how often that has been used before
+    auto stage = [&](int i) { return two ? 0 : i & 1; };
+    auto use = [&](int i) { return two ? i : i >> 1; };
+
+    if (tid == 0) {
+        const int extra = a.drop ? 1 : 0;   // (test hook)
+        tc_mbar_init(bar(kQFull), 1 + extra);
+        for (int s = 0; s < 2; ++s) {
+            tc_mbar_init(bar(kKFull + s), 1 + extra);
+            tc_mbar_init(bar(kVFull + s), 1 + extra);
+            tc_mbar_init(bar(kKEmpty + s), kShKeyWarps);
+            tc_mbar_init(bar(kVEmpty + s), kShKeyWarps);
+            tc_mbar_init(bar(kKReady + s), kShKeyWarps);
+            tc_mbar_init(bar(kVReady + s), kShKeyWarps);
+            tc_mbar_init(bar(kKFree + s), two ? 2 : 1);
+            tc_mbar_init(bar(kVFree + s), two ? 2 : 1);
+            tc_mbar_init(bar(kSReady + s), 1);
+            tc_mbar_init(bar(kPReady + s), 4);
+            tc_mbar_init(bar(kODone + s), 1);
+        }
+        for (int s = 0; s < 4; ++s) tc_mbar_init(bar(kNReady + s), kShKeyWarps);
+        tc_mbar_init(bar(kDrain), 1);
+        *fail_s = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 0) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(base_s + S::kSlot),
+                     "r"(kShCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + S::kSlot);
+    asm volatile("griddepcontrol.launch_dependents;");
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // the query tiles come from the prep kernel
+
+    // a bounded wait; one that gives up is recorded, and the caller's role makes no further waits
+    auto wait = [&](bool &ok, int b, uint32_t parity) {
+        if (ok && !tc_mbar_wait(bar(b), parity & 1u)) {
+            ok = false;
+            *fail_s = 1;
+            note_wait_failed();
+        }
+    };
+
+    if (warp == kShProducer) {
+        // ---- copies: lane l takes piece l of a tile (one, or one for each page it meets: 17 at most)
+        bool ok = true;
+        if (nt > 0 && lane == 0) {
+            const int n = two ? 4 : 2;
+            const uint8_t *src = a.q + ((int64_t)kvh * p.tiles + qt) * (2 * S::kTile);
+            tc_mbar_expect_tx(bar(kQFull), (uint32_t)(n * S::kTile));
+            for (int i = 0; i < n; ++i) sh_bulk(base_s + i * S::kTile, src + (int64_t)i * S::kTile, S::kTile, bar(kQFull));
+        }
+        for (int i = 0; i < nt && ok; ++i) {
+            const int t0 = (tile0 + i) * kShKeys;
+            const int end = min(t0 + kShKeys, (len + 7) & ~7);
+            int64_t slot = 0;
+            int from = t0, n = 0;
+            if (!a.table) {
+                slot = (int64_t)kvh * a.cap + t0;
+                n = lane == 0 ? end - t0 : 0;
+            } else {
+                const int64_t pg = t0 / a.page + lane;
+                const int64_t lo = pg * a.page > t0 ? pg * a.page : t0, hi = min64((pg + 1) * a.page, end);
+                if (lo < hi) {
+                    from = (int)lo;
+                    n = (int)(hi - lo);
+                    slot = ((int64_t)a.table[pg] * a.Hkv + kvh) * a.page + (lo - pg * a.page);
+                }
+            }
+#pragma unroll
+            for (int kv = 0; kv < 2; ++kv) {
+                const int ns = kv ? S::kNV : S::kNK, s = i % ns, bytes = (kv ? S::kVBytes : S::kKBytes) / kShKeys;
+                if (i >= ns) wait(ok, (kv ? kVEmpty : kKEmpty) + s, (uint32_t)(i / ns - 1));
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                const uint32_t full = bar((kv ? kVFull : kKFull) + s);
+                if (lane == 0) tc_mbar_expect_tx(full, (uint32_t)((end - t0) * bytes));
+                __syncwarp();
+                const uint32_t dst = base_s + (kv ? S::kVBlk + s * S::kVBytes : S::kKBlk + s * S::kKBytes);
+                if (n > 0) sh_bulk(dst + (from - t0) * bytes, (kv ? a.v : a.k) + slot * bytes, (uint32_t)(n * bytes), full);
+            }
+        }
+    } else if (warp == kShMma) {
+        // ---- the products: item e is stream e & 1's tile e >> 1 (two) or tile e
+        if (lane == 0) {
+            bool ok = true;
+            const int items = two ? 2 * nt : nt;
+            auto tile_of = [&](int e) { return two ? e >> 1 : e; };
+            auto scores = [&](int e) {
+                const int i = tile_of(e), x = e & 1, st = stage(i);
+                if (!two || x == 0) wait(ok, kKReady + st, (uint32_t)use(i));
+                if (!ok) return;
+                tc_fence_after();
+                const uint32_t d = tmem + 128u * (uint32_t)x, kb = k_at(st), qb = q_at(x);
+#pragma unroll
+                for (int part = 0; part < 2; ++part)
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks) {
+                        const uint32_t off = (uint32_t)((ks >> 2) * 16384 + (ks & 3) * 32);
+                        tc_mma(d, sh_desc(qb + part * S::kTile + off, 16, 1024), sh_desc(kb + off, 16, 1024), sh_idesc(0),
+                               (part > 0 || ks > 0) ? 1u : 0u);
+                    }
+                tc_commit(bar(kSReady + x));
+                tc_commit(bar(kKFree + st));
+            };
+            auto values = [&](int e) {
+                const int i = tile_of(e), x = e & 1, st = stage(i);
+                if (!two || x == 0) wait(ok, kVReady + st, (uint32_t)use(i));
+                wait(ok, kPReady + x, (uint32_t)(e >> 1));
+                if (!ok) return;
+                tc_fence_after();
+                const uint32_t vb = v_at(st), pa = tmem + 128u * (uint32_t)x;
+#pragma unroll
+                for (int part = 0; part < 2; ++part)
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks)
+                        sh_mma_ts(tmem + kShColO + 128u * (uint32_t)x, pa + 32 * (ks >> 1) + 8 * (ks & 1) + 16 * part,
+                                  sh_desc(vb + ks * 2048, 16384, 1024), sh_idesc(1),
+                                  (e > 1 || part > 0 || ks > 0) ? 1u : 0u);
+                tc_commit(bar(kVFree + st));
+                if (e + 2 >= items) tc_commit(bar(kODone + x));
+            };
+            if (items > 0) wait(ok, kQFull, 0);
+            for (int e = 0; e < 2 && e < items; ++e) scores(e);
+            for (int e = 0; e < items && ok; ++e) {
+                values(e);
+                if (ok && e + 2 < items) scores(e + 2);
+            }
+            // before teardown: every product issued here has completed
+            tc_commit(bar(kDrain));
+            tc_mbar_wait(bar(kDrain), 0u);
+        }
+    } else if (warp >= kShRowWarps) {
+        // ---- key warps: thread = key of the tile
+        const int k = tid - 32 * kShRowWarps;
+        bool ok = true;
+        for (int i = 0; i < nt; ++i) {
+            const int st = stage(i), u = use(i);
+            const int sk = i % S::kNK, sv = i % S::kNV;
+            const uint32_t kblk = base_s + S::kKBlk + sk * S::kKBytes + k * (2 + 16 * KB);
+            const uint32_t vblk = base_s + S::kVBlk + sv * S::kVBytes + k * (2 + 16 * VB);
+            wait(ok, kKFull + sk, (uint32_t)(i / S::kNK));
+            wait(ok, kVFull + sv, (uint32_t)(i / S::kNV));
+            if (u >= 1) wait(ok, kKFree + st, (uint32_t)(u - 1));
+            // (and tile i - 4's norms have been read: its P came before the products of tile i - 2)
+            const bool live = (tile0 + i) * kShKeys + k < len;
+            float *nm = norms + (i & 3) * (kShNormSlot / 4);
+            const float kn = __half2float(__ushort_as_half((unsigned short)sh_lds16(kblk)));
+            const float vn = __half2float(__ushort_as_half((unsigned short)sh_lds16(vblk)));
+            nm[k] = live ? kn * a.k_norm : 0.f;
+            nm[kShKeys + k] = live ? vn * kShUp : 0.f;
+            // the largest value norm, in [2^-14, 2^16] whatever it is
+            float lv = live ? fminf(fmaxf(vn, 0x1p-14f), 0x1p16f) : 0x1p-14f;
+#pragma unroll
+            for (int m = 16; m >= 1; m >>= 1) lv = fmaxf(lv, __shfl_xor_sync(0xffffffffu, lv, m));
+            if (lane == 0) nm[2 * kShKeys + warp - kShRowWarps] = log2f(lv);
+            __syncwarp();
+            if (lane == 0) tc_mbar_arrive(bar(kNReady + (i & 3)));
+            dequant_row<KB>(a.kt, kblk, k_at(st), k);
+            // the tiles were written by ordinary stores and are read by the tensor cores
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) {
+                tc_mbar_arrive(bar(kKEmpty + sk));
+                tc_mbar_arrive(bar(kKReady + st));
+            }
+            if (u >= 1) wait(ok, kVFree + st, (uint32_t)(u - 1));
+            dequant_row<VB>(a.vt, vblk, v_at(st), k);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) {
+                tc_mbar_arrive(bar(kVEmpty + sv));
+                tc_mbar_arrive(bar(kVReady + st));
+            }
+        }
+    } else {
+        // ---- row warps: thread = row of stream x, keys of the stream's tiles
+        const int x = warp >> 2, r = tid & 127;
+        const uint32_t lane_t = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+        const uint32_t s_col = lane_t + 128u * (uint32_t)x, o_col = lane_t + kShColO + 128u * (uint32_t)x;
+        const int mine = two ? nt : (nt - x + 1) >> 1;
+        float m_ref = -INFINITY, l = 0.f;
+        bool ok = true;
+        for (int t = 0; t < mine; ++t) {
+            const int i = two ? t : 2 * t + x;
+            const float *nm = norms + (i & 3) * (kShNormSlot / 4);
+            wait(ok, kNReady + (i & 3), (uint32_t)(i >> 2));
+            wait(ok, kSReady + x, (uint32_t)t);
+            tc_fence_after();
+            const int nvalid = len - (tile0 + i) * kShKeys;   // (of 128)
+            // the row's largest score
+            float mx = -INFINITY;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                float sv[32];
+                tc_ld32(s_col + 32 * c, sv);
+                tc_wait_ld();
+                const float4 *kn = reinterpret_cast<const float4 *>(nm + 32 * c);
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    const float4 n = kn[q];
+                    float e[4] = {sv[4 * q] * n.x, sv[4 * q + 1] * n.y, sv[4 * q + 2] * n.z, sv[4 * q + 3] * n.w};
+                    if (nvalid < kShKeys) {
+#pragma unroll
+                        for (int w = 0; w < 4; ++w)
+                            if (32 * c + 4 * q + w >= nvalid) e[w] = -INFINITY;
+                    }
+                    mx = fmaxf(mx, fmaxf(fmaxf(e[0], e[1]), fmaxf(e[2], e[3])));
+                }
+            }
+            const float4 lv = *reinterpret_cast<const float4 *>(nm + 2 * kShKeys);
+            const float top = mx + fmaxf(fmaxf(lv.x, lv.y), fmaxf(lv.z, lv.w));
+            const bool move = top > m_ref + 8.f;
+            const float m_new = move ? top : m_ref;
+            const float factor = move ? (m_ref == -INFINITY ? 0.f : exp2f(m_ref - m_new)) : 1.f;
+            if (t >= 1 && __any_sync(0xffffffffu, move)) {
+                // (the stream's products before this tile's scores have completed)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    float o[32];
+                    tc_ld32(o_col + 32 * c, o);
+                    tc_wait_ld();
+                    uint32_t w[32];
+#pragma unroll
+                    for (int q = 0; q < 32; ++q) w[q] = __float_as_uint(o[q] * factor);
+                    sh_st32(o_col + 32 * c, w);
+                }
+            }
+            // no finite score so far: scores are -inf (P 0) or NaN (which stays NaN)
+            const float mref = m_new == -INFINITY ? 0.f : m_new;
+            float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                float sv[32];
+                tc_ld32(s_col + 32 * c, sv);
+                tc_wait_ld();
+                const float4 *kn = reinterpret_cast<const float4 *>(nm + 32 * c);
+                const float4 *vn = reinterpret_cast<const float4 *>(nm + kShKeys + 32 * c);
+                uint32_t w[32];   // hi parts of the 32 probabilities, then lo parts
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    const float4 n = kn[q], v = vn[q];
+                    float2 p0 = make_float2(sh_ex2(fmaf(sv[4 * q], n.x, -mref)), sh_ex2(fmaf(sv[4 * q + 1], n.y, -mref)));
+                    float2 p1 =
+                        make_float2(sh_ex2(fmaf(sv[4 * q + 2], n.z, -mref)), sh_ex2(fmaf(sv[4 * q + 3], n.w, -mref)));
+                    if (nvalid < kShKeys) {
+                        const int at = 32 * c + 4 * q;
+                        if (at >= nvalid) p0.x = 0.f;
+                        if (at + 1 >= nvalid) p0.y = 0.f;
+                        if (at + 2 >= nvalid) p1.x = 0.f;
+                        if (at + 3 >= nvalid) p1.y = 0.f;
+                    }
+                    sum = __fadd2_rn(sum, __fadd2_rn(p0, p1));
+                    p0 = __fmul2_rn(p0, make_float2(v.x, v.y));
+                    p1 = __fmul2_rn(p1, make_float2(v.z, v.w));
+                    sh_split(p0.x, p0.y, w[2 * q], w[16 + 2 * q]);
+                    sh_split(p1.x, p1.y, w[2 * q + 1], w[16 + 2 * q + 1]);
+                }
+                sh_st32(s_col + 32 * c, w);
+            }
+            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+            l = l * factor + (sum.x + sum.y);
+            m_ref = m_new;
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) tc_mbar_arrive(bar(kPReady + x));
+        }
+        // ---- this row's partial: maximum, sum, sums of values by dim
+        if (mine > 0) wait(ok, kODone + x, 0);
+        tc_fence_after();
+        const int row = (qt + (two ? x : 0)) * kShRows + r;
+        float *out = a.part + (((int64_t)blockIdx.x * 2 + x) * kShRows + r) * kPartialFloats;
+        if (row < a.rows) {
+            out[0] = m_ref;
+            out[1] = ok ? l : __int_as_float(0x7fc00000);   // NaN marks a failed wait
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            float o[32];
+            if (mine > 0) {   // (the whole warp)
+                tc_ld32(o_col + 32 * c, o);
+                tc_wait_ld();
+            } else {
+#pragma unroll
+                for (int q = 0; q < 32; ++q) o[q] = 0.f;
+            }
+            if (row < a.rows) {
+                float d[32];
+#pragma unroll
+                for (int q = 0; q < 32; ++q)   // dims of a 16: place -> dim, the inverse of operand_place
+                    d[(q & 16) + (VB == 4 ? (q & 15)
+                                          : VB == 3 ? 2 * (q & 7) + ((q >> 3) & 1) : 4 * (q & 3) + ((q >> 2) & 3))] =
+                        o[q] * (1.f / kShUp);
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                    reinterpret_cast<float4 *>(out + 4 + 32 * c)[q] =
+                        make_float4(d[4 * q], d[4 * q + 1], d[4 * q + 2], d[4 * q + 3]);
+            }
+        }
+    }
+
+    // ---- teardown: every product completed (the issuing thread waited for its last commit), every
+    // tensor-memory access completed; copies still in flight after a failed wait land first
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (*fail_s) {
+        if (tid == 0) spin_ns(100000000ull);
+        __syncthreads();
+    }
+    if (warp == 0)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kShCols) : "memory");
+}
+
+struct MergeArgs {
+    const float *part, *own;
+    const int32_t *len, *seq_lens;
+    const int2 *live;
+    void *out;
+    int P, Hq, Hkv, G, out_dtype;
+    SharedPlan plan;
+    float out_scale;
+    uint32_t signs[4];
+};
+
+constexpr int kMergeBatch = 16;   // slots a merging thread loads at once
+
+// One CTA for one (sequence, query head): the prefix's slots, then the own
+// tokens'.
+__global__ void __launch_bounds__(kAttnThreads * kCombineMaxGroups) attn_shared_merge_kernel(
+    const __grid_constant__ MergeArgs a) {
+    const int b = blockIdx.x / a.Hq, h = blockIdx.x % a.Hq, kvh = h / a.G, g = h % a.G;
+    const SharedPlan &p = a.plan;
+    const int row = b * a.G + g, tile = row / kShRows;
+    const bool two = tile < 2 * p.pairs;
+    const int n = (shared_len(a.len, a.P) + kShKeys - 1) / kShKeys, ranges = two ? p.s2 : p.s1;
+    const int used = n < ranges ? n : ranges;
+    // slots of the prefix: one per range, or (an odd tile) one per range and stream
+    int before = two ? used : 2 * used;
+    const float *part =
+        a.part + ((int64_t)(kvh * p.per_head + (two ? (tile >> 1) * p.s2 : p.pairs * p.s2)) * 2 * kShRows +
+                  (two ? (tile & 1) * kShRows : 0) + row % kShRows) * kPartialFloats;
+    const int64_t step = (int64_t)(two ? 2 : 1) * kShRows * kPartialFloats;
+    const bool empty = a.seq_lens && a.seq_lens[b] < 0;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int64_t j = (int64_t)b * a.Hkv + kvh;
+    const int2 met = __ldcg(a.live + j);
+    const float *own = a.own + ((met.x + j) * a.G + g) * kPartialFloats;
+    const int64_t own_step = (int64_t)a.G * kPartialFloats;
+    if (empty) before = 0;
+    const int64_t at = (int64_t)blockIdx.x * kD;
+    combine_slots<kMergeBatch>(
+        [&](int i) { return i < before ? part + i * step : own + (i - before) * own_step; },
+        empty ? 0 : before + met.y, 1, a.out_scale, a.signs[0], a.signs[1], a.signs[2], a.signs[3],
+        [&](int d, float v) {
+            if (a.out_dtype == TQ_F32) static_cast<float *>(a.out)[at + d] = v;
+            else if (a.out_dtype == TQ_BF16) static_cast<__nv_bfloat16 *>(a.out)[at + d] = __float2bfloat16_rn(v);
+            else static_cast<__half *>(a.out)[at + d] = __float2half_rn(v);
+        });
+}
+
+// Ranges of the prefix: of all counts that give every CTA a tile, the one whose
+// slowest SM is done first, a pair's CTA taking two units a tile, and about
+// three for its start and end.
+SharedPlan shared_plan(int sms, int B, int Hq, int Hkv, int P) {
+    SharedPlan p;
+    const int64_t rows = (int64_t)B * (Hq / Hkv);
+    p.tiles = (int)((rows + kShRows - 1) / kShRows);
+    p.pairs = p.tiles / 2;
+    p.odd = p.tiles & 1;
+    const int64_t n = ((int64_t)P + kShKeys - 1) / kShKeys;
+    int64_t best = INT64_MAX;
+    p.s2 = 1;
+    for (int64_t s = 1; s <= n && s <= 2 * (int64_t)sms; ++s) {
+        const int64_t ctas = Hkv * (p.pairs * s + (p.pairs ? (s + 1) / 2 : s) * p.odd);
+        const int64_t cost = (ctas + sms - 1) / sms * (3 + (p.pairs ? 2 : 1) * ((n + s - 1) / s));
+        if (cost < best) {
+            best = cost;
+            p.s2 = (int)s;
+        }
+        if (ctas > 4 * (int64_t)sms) break;
+    }
+    p.s1 = p.pairs ? (p.s2 + 1) / 2 : p.s2;
+    p.per_head = p.pairs * p.s2 + p.odd * p.s1;
+    p.ctas = Hkv * p.per_head;
+    return p;
+}
+
+int64_t most_workers(int B, int Hkv, int T) {
+    return min64((int64_t)B * Hkv * ((T + kMmaChunk - 1) / kMmaChunk), (int64_t)kMmaMaxWarpsPerSm * sm_count());
+}
+
+// Workspace: the prefix's partials | the own tokens' [W + B Hkv][G][132] | query fragments [B Hkv] | query tiles |
+// segments' workers [B Hkv][2], in floats.
+struct Layout {
+    int64_t own, frag, tiles, live, floats;
+    Layout(const SharedPlan &p, int B, int Hq, int Hkv, int64_t W) {
+        const int64_t segs = (int64_t)B * Hkv;
+        own = (int64_t)p.ctas * 2 * kShRows * kPartialFloats;
+        frag = own + (W + segs) * (Hq / Hkv) * kPartialFloats;
+        tiles = (frag + segs * kFragWords + 3) & ~(int64_t)3;
+        live = tiles + (int64_t)Hkv * p.tiles * (2 * 32768 / 4);
+        floats = live + ((segs * 2 + 3) & ~(int64_t)3);
+    }
+};
+
+bool shape_ok(int B, int Hq, int Hkv, int P, int T) {
+    return B > 0 && Hq > 0 && Hkv > 0 && P > 0 && T > 0 && Hq % Hkv == 0;
+}
+
+// What the kernels' 32-bit indices hold.
+bool size_ok(int B, int Hq, int Hkv, int P, int T) {
+    return Hq / Hkv <= 8 && P <= kMmaMaxTokens && T <= kMmaMaxTokens && (int64_t)B * Hq <= (1 << 24) &&
+           (int64_t)B * Hkv * ((T + kMmaChunk - 1) / kMmaChunk) <= 0x7FFFFFFF;
+}
+
+template <int KB, int VB>
+int launch_shared(const SharedArgs &a, cudaStream_t st) {
+    using S = ShSmem<KB, VB>;
+    static int done[64] = {0};
+    if (set_smem_limit((const void *)attn_shared_kernel<KB, VB>, S::kTotal, done) != TQ_OK) return TQ_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)a.plan.ctas);
+    cfg.blockDim = dim3(kShThreads);
+    cfg.dynamicSmemBytes = S::kTotal;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return launch_status(cudaLaunchKernelEx(&cfg, attn_shared_kernel<KB, VB>, a));
+}
+
+template <int KB>
+int launch_shared_v(const SharedArgs &a, int vb, cudaStream_t st) {
+    return vb == 2 ? launch_shared<KB, 2>(a, st) : vb == 3 ? launch_shared<KB, 3>(a, st) : launch_shared<KB, 4>(a, st);
+}
+
+// The bytes from which levels16 takes a codebook's levels times f.
+void level_bytes(const tq_codebook *cb, float f, uint32_t (&t)[4]) {
+    for (int i = 0; i < 4; ++i) t[i] = 0;
+    const int n = cb->bits == 4 ? 8 : cb->levels, from = cb->bits == 4 ? 8 : 0;
+    for (int i = 0; i < n; ++i) {
+        const __half h = __float2half_rn(cb->centroids[from + i] * f);
+        uint16_t w;
+        static_assert(sizeof(h) == sizeof(w), "fp16");
+        __builtin_memcpy(&w, &h, 2);
+        // 2 bits: word 0 high bytes, 1 low bytes; else words 0, 1 high bytes, 2, 3 low bytes
+        t[i / 4] |= (uint32_t)(w >> 8) << (8 * (i % 4));
+        t[(cb->bits == 2 ? 1 : 2) + i / 4] |= (uint32_t)(w & 255) << (8 * (i % 4));
+    }
+}
+
+// The mirrored half of a 4-bit codebook is taken from the other.
+bool symmetric(const tq_codebook *cb) {
+    if (cb->bits != 4) return true;
+    for (int i = 0; i < 8; ++i)
+        if (!(cb->centroids[8 + i] > 0.f) || cb->centroids[7 - i] != -cb->centroids[8 + i]) return false;
+    return true;
+}
+
+}  // namespace
+
+int wait_failed_shared(unsigned *v, bool clear) { return read_wait_failed(v, clear); }
+
+}  // namespace tq
+
+using namespace tq;
+
+extern "C" size_t tq_attn_shared_workspace_bytes(int B, int Hq, int Hkv, int P, int T) {
+    if (!shape_ok(B, Hq, Hkv, P, T) || !size_ok(B, Hq, Hkv, P, T)) return 0;
+    const SharedPlan p = shared_plan(sm_count(), B, Hq, Hkv, P);
+    return (size_t)Layout(p, B, Hq, Hkv, most_workers(B, Hkv, T)).floats * sizeof(float);
+}
+
+extern "C" int tq_attn_decode_shared(const void *q, int q_dtype, const uint8_t *k_prefix, const uint8_t *v_prefix,
+                                     const int32_t *prefix_table, int P_cap, int P, const int32_t *prefix_len,
+                                     const uint8_t *k_blocks, const tq_codebook *kcb, const uint8_t *v_blocks,
+                                     const tq_codebook *vcb, const int32_t *block_table, int64_t table_row_stride,
+                                     int max_pages, int page_tokens, const int32_t *seq_lens, int B, int Hq, int Hkv,
+                                     int T_cap, int T, float scale, tq_signs signs, void *out, int out_dtype,
+                                     void *workspace, size_t workspace_bytes, void *stream) {
+    if (!q || !k_prefix || !v_prefix || !k_blocks || !kcb || !v_blocks || !vcb || !out || !workspace) return TQ_ERR_ARG;
+    if (!shape_ok(B, Hq, Hkv, P, T) || P > P_cap || !std::isfinite(scale)) return TQ_ERR_ARG;
+    if (!prefix_table != !block_table) return TQ_ERR_ARG;
+    const bool paged = block_table != nullptr;
+    if (paged) {
+        if (max_pages <= 0 || page_tokens <= 0 || (int64_t)max_pages * page_tokens < T ||
+            table_row_stride < (B > 1 ? max_pages : 0) || table_row_stride > 0x7FFFFFFF)
+            return TQ_ERR_ARG;
+        if (page_tokens & 7) return TQ_ERR_UNSUPPORTED;
+    } else if (T > T_cap || (T_cap & 7) || (P_cap & 7)) {
+        return TQ_ERR_ARG;
+    }
+    if (!size_ok(B, Hq, Hkv, P, T)) return TQ_ERR_UNSUPPORTED;
+    if (dtype_bytes(q_dtype) == 0 || dtype_bytes(out_dtype) == 0) return TQ_ERR_UNSUPPORTED;
+    if (!codebook_ok(kcb) || !codebook_ok(vcb) || !symmetric(kcb) || !symmetric(vcb)) return TQ_ERR_UNSUPPORTED;
+    if (!aligned(q, dtype_bytes(q_dtype)) || !aligned(k_prefix, 16) || !aligned(v_prefix, 16) ||
+        !aligned(k_blocks, 16) || !aligned(v_blocks, 16) || !aligned(out, 16) || !aligned(workspace, 16) ||
+        !aligned(prefix_table, 4) || !aligned(prefix_len, 4) || !aligned(block_table, 4) || !aligned(seq_lens, 4))
+        return TQ_ERR_ALIGN;
+    if (workspace_bytes < tq_attn_shared_workspace_bytes(B, Hq, Hkv, P, T)) return TQ_ERR_WORKSPACE;
+
+    const int kb = kcb->bits, vb = vcb->bits, G = Hq / Hkv;
+    const SharedPlan sp = shared_plan(sm_count(), B, Hq, Hkv, P);
+    MmaPlan plan = mma_plan(B, Hq, Hkv, T, kb, vb, false, G);
+    const Layout at(sp, B, Hq, Hkv, most_workers(B, Hkv, T));
+    float *ws = static_cast<float *>(workspace);
+    plan.frag_off = at.frag - at.own;
+    const float kf = attn_centroid_factor(kcb), vf = attn_centroid_factor(vcb);
+
+    AttnArgs a = {};   // the own tokens
+    a.drop = drop_copies();
+    a.q = q;
+    a.q_dtype = q_dtype;
+    a.k = k_blocks;
+    a.v = v_blocks;
+    a.seq_lens = seq_lens;
+    a.ws = ws + at.own;
+    a.B = B;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.G = G;
+    a.T_cap = paged ? (T + 7) & ~7 : T_cap;
+    a.T = T;
+    a.qscale = scale * 1.4426950408889634f;
+    for (int i = 0; i < 16; ++i) {
+        a.kc[i] = kcb->centroids[i];
+        a.vc[i] = vcb->centroids[i] * vf;
+    }
+    for (int i = 0; i < 4; ++i) a.signs[i] = signs.w[i];
+    a.table = block_table;
+    a.max_pages = (int)table_row_stride;
+    a.page = page_tokens;
+    a.live = reinterpret_cast<int2 *>(ws + at.live);
+    a.workers = plan.W;
+    a.q_tiles = reinterpret_cast<uint8_t *>(ws + at.tiles);
+    a.q_tile_count = sp.tiles;
+    a.q_tile_bits = kb;
+
+    SharedArgs s = {};
+    s.q = a.q_tiles;
+    s.k = k_prefix;
+    s.v = v_prefix;
+    s.table = prefix_table;
+    s.len = prefix_len;
+    s.part = ws;
+    s.rows = B * G;
+    s.Hkv = Hkv;
+    s.P = P;
+    s.cap = P_cap;
+    s.page = page_tokens;
+    s.plan = sp;
+    s.k_norm = 1.f / kf;
+    level_bytes(kcb, kf, s.kt);
+    level_bytes(vcb, vf, s.vt);
+    s.drop = a.drop;
+
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    int r = launch_attn_prep_mma(a, plan, 0, st);
+    if (r != TQ_OK) return r;
+    r = kb == 2 ? launch_shared_v<2>(s, vb, st) : kb == 3 ? launch_shared_v<3>(s, vb, st) : launch_shared_v<4>(s, vb, st);
+    if (r != TQ_OK) return r;
+    const int nt = G <= 4 ? 1 : 2;
+    r = kb == 2 ? launch_attn_mma_scores_k2(a, plan, vb, nt, paged, st)
+                : kb == 3 ? launch_attn_mma_scores_k3(a, plan, vb, nt, paged, st)
+                          : launch_attn_mma_scores_k4(a, plan, vb, nt, paged, st);
+    if (r != TQ_OK) return r;
+
+    MergeArgs m = {};
+    m.part = s.part;
+    m.own = a.ws;
+    m.len = prefix_len;
+    m.seq_lens = seq_lens;
+    m.live = a.live;
+    m.out = out;
+    m.P = P;
+    m.Hq = Hq;
+    m.Hkv = Hkv;
+    m.G = G;
+    m.out_dtype = out_dtype;
+    m.plan = sp;
+    m.out_scale = 0.08838834764831845f / vf;
+    for (int i = 0; i < 4; ++i) m.signs[i] = signs.w[i];
+    const int slots = (sp.pairs ? sp.s2 : 0) > 2 * sp.s1 ? sp.s2 : 2 * sp.s1;
+    const int groups = (slots + plan.Smax + kMergeBatch - 1) / kMergeBatch;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(B * Hq));
+    cfg.blockDim = dim3(kAttnThreads * (groups > kCombineMaxGroups ? kCombineMaxGroups : groups));
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return launch_status(cudaLaunchKernelEx(&cfg, attn_shared_merge_kernel, m));
+}

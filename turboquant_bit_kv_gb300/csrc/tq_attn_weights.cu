@@ -36,6 +36,41 @@ int launch_attn_mma_scores_k3(const AttnArgs &a, MmaPlan &plan, int vb, int nt, 
 int launch_attn_mma_scores_k4(const AttnArgs &a, MmaPlan &plan, int vb, int nt, bool paged, cudaStream_t st);
 int launch_attn_prep_mma(const AttnArgs &a, const MmaPlan &plan, int qjl, cudaStream_t st);
 
+// A common factor for a codebook's centroids under which their fp16 roundings
+// are smallest (the values, and the keys of a shared prefix, enter the tensor cores
+// as fp16; the factor is taken out again later): the best of 2^14 factors in [1, 2).
+// The codebook is antisymmetric, so L / 2 magnitudes have to fall close to
+// fp16 numbers at once: the worst rounding drops from 2^-12 to about 2^-18
+// (2 bits), 2^-15 (3 bits), 2^-13.5 (4 bits).
+float attn_centroid_factor(const tq_codebook *cb) {
+    static std::mutex mu;
+    static tq_codebook known[5];
+    static float factor[5];
+    std::lock_guard<std::mutex> lock(mu);
+    const int n = cb->bits;
+    if (factor[n] != 0.f && std::memcmp(known[n].centroids, cb->centroids, sizeof(float) * cb->levels) == 0)
+        return factor[n];
+    float best = 1.f, err = INFINITY;
+    for (int i = 0; i < (1 << 14); ++i) {
+        const float f = 1.f + i / 16384.f;
+        float e = 0.f;
+        for (int q = 0; q < cb->levels; ++q) {
+            const float c = std::fabs(cb->centroids[q]) * f;
+            if (!(c > 0.f)) continue;
+            int ex;
+            const float m = std::frexp(c, &ex) * 2048.f;   // 11 significant bits
+            e = std::fmax(e, std::fabs(m - std::nearbyint(m)) / m);
+        }
+        if (e < err) {
+            err = e;
+            best = f;
+        }
+    }
+    known[n] = *cb;
+    factor[n] = best;
+    return best;
+}
+
 namespace {
 
 constexpr int kMergeBatch = 16;      // slots a merging thread loads at once (one round covers 16 x groups)
@@ -185,41 +220,6 @@ __global__ void __launch_bounds__(kAttnThreads * kCombineMaxGroups, 2) attn_weig
     }
 }
 
-// A common factor for a codebook's centroids under which their fp16 roundings
-// are smallest (the values enter the tensor cores as fp16; the factor is taken
-// out again when the output is written): the best of 2^14 factors in [1, 2).
-// The codebook is antisymmetric, so L / 2 magnitudes have to fall close to
-// fp16 numbers at once: the worst rounding drops from 2^-12 to about 2^-18
-// (2 bits), 2^-15 (3 bits), 2^-13.5 (4 bits).
-float value_factor(const tq_codebook *cb) {
-    static std::mutex mu;
-    static tq_codebook known[5];
-    static float factor[5];
-    std::lock_guard<std::mutex> lock(mu);
-    const int n = cb->bits;
-    if (factor[n] != 0.f && std::memcmp(known[n].centroids, cb->centroids, sizeof(float) * cb->levels) == 0)
-        return factor[n];
-    float best = 1.f, err = INFINITY;
-    for (int i = 0; i < (1 << 14); ++i) {
-        const float f = 1.f + i / 16384.f;
-        float e = 0.f;
-        for (int q = 0; q < cb->levels; ++q) {
-            const float c = std::fabs(cb->centroids[q]) * f;
-            if (!(c > 0.f)) continue;
-            int ex;
-            const float m = std::frexp(c, &ex) * 2048.f;   // 11 significant bits
-            e = std::fmax(e, std::fabs(m - std::nearbyint(m)) / m);
-        }
-        if (e < err) {
-            err = e;
-            best = f;
-        }
-    }
-    known[n] = *cb;
-    factor[n] = best;
-    return best;
-}
-
 int64_t scores_floats(int B, int Hq, int Hkv, int T) {
     return (int64_t)B * Hkv * ((T + kMmaChunk - 1) / kMmaChunk) * kMmaChunk * (Hq / Hkv);
 }
@@ -296,7 +296,7 @@ extern "C" int tq_attn_decode_weights(const void *q, int q_dtype, const uint8_t 
     a.T_cap = paged ? (T + 7) & ~7 : T_cap;
     a.T = T;
     a.qscale = scale * 1.4426950408889634f;
-    const float vf = value_factor(vcb);
+    const float vf = attn_centroid_factor(vcb);
     for (int i = 0; i < 16; ++i) {
         a.kc[i] = kcb->centroids[i];
         a.vc[i] = vcb->centroids[i] * vf;

@@ -59,6 +59,7 @@ int wait_failed_attn_k3w(unsigned *v, bool clear);
 int wait_failed_attn_k4w(unsigned *v, bool clear);
 int wait_failed_prefill(unsigned *v, bool clear);
 int wait_failed_headdim(unsigned *v, bool clear);
+int wait_failed_shared(unsigned *v, bool clear);
 
 // Encode at head dims 64 / 96 / 128 / 160 with the caller's rotation R on
 // the tensor cores (tq_headdim_tc.cu): bf16 / fp16 rows, at least

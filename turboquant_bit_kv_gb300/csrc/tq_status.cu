@@ -28,7 +28,7 @@ extern "C" int tq_device_status(int clear, void *stream) {
     int (*const readers[])(unsigned *, bool) = {wait_failed_encode, wait_failed_qjl, wait_failed_attn_k2,
                                                wait_failed_attn_k3, wait_failed_attn_k4, wait_failed_attn_k8,
                                                wait_failed_prefill, wait_failed_headdim, wait_failed_attn_k2w,
-                                               wait_failed_attn_k3w, wait_failed_attn_k4w};
+                                               wait_failed_attn_k3w, wait_failed_attn_k4w, wait_failed_shared};
     unsigned any = 0;
     for (auto rd : readers) {
         unsigned v = 0;

@@ -110,6 +110,15 @@ def lib():
         L.tq_evict_select.argtypes = [vp, i64, vp, c_int, c_int, c_int, c_int, c_int, c_int, vp, vp, vp]
         L.tq_evict_compact.argtypes = [vp, c_int, vp, c_int, vp, i64, vp, c_int, vp, vp, c_int, c_int, c_int, c_int,
                                        c_int, c_int, c_int, vp]
+        L.tq_page_plan.argtypes = [vp, vp, vp, c_int, c_int, c_int, vp, i64, c_int, vp, vp, vp, c_int, vp, vp, vp, vp,
+                                   vp, vp, i64, vp]
+        L.tq_norm_rope_apply.argtypes = [vp, c_int, i64, i64, vp, c_int, i64, i64, c_int, i64, vp, vp, c_int,
+                                         ctypes.c_float, vp, i64, rp, vp, i64, i64, vp, i64, i64, vp]
+        L.tq_attn_shared_workspace_bytes.argtypes = [c_int] * 5
+        L.tq_attn_shared_workspace_bytes.restype = sz
+        L.tq_attn_decode_shared.argtypes = [vp, c_int, vp, vp, vp, c_int, c_int, vp, vp, cbp, vp, cbp, vp, i64, c_int,
+                                            c_int, vp, c_int, c_int, c_int, c_int, c_int, ctypes.c_float, tq_signs,
+                                            vp, c_int, vp, sz, vp]
         _lib = L
     return _lib
 
@@ -659,3 +668,140 @@ def tq_evict_compact(k_blocks, v_blocks, kept, new_lens, T, weights=None, block_
         _check(lib().tq_evict_compact(k_blocks.data_ptr(), ks[3], _ptr(v_blocks), vbytes, _ptr(weights), stride,
                                       kept.data_ptr(), keep, new_lens.data_ptr(), _ptr(block_table), pages, unit, ks[0],
                                       B, Hkv, unit, T, _stream(stream)), what)
+
+
+# ---- a serving step over paged caches: page plan, norms with rotary positions, shared-prefix attention
+
+def _ints(t, shape, dtype, what, name):
+    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError("%s: %s %s %s expected" % (what, name, str(dtype)[6:], list(shape)))
+
+
+def tq_page_plan(cached_lens, fresh_lens, held, block_table, free_pages, free_count, page_tokens, Hkv, new_held,
+                 new_free_count, seq_lens, tok_start, dst, pos, pos_start=None, stream=None):
+    """Pages, slots and positions of a step's new tokens.  int32 [B]: cached_lens,
+    fresh_lens, held, new_held, seq_lens; block_table int32 [B, max_pages] (rows
+    may be strided); free_pages int32 [n], free_count and new_free_count int32
+    [1]; tok_start int32 [B + 1]; dst, pos int64 [tokens]; pos_start int64 [B].
+    new_held may be held, new_free_count free_count."""
+    what = "tq_page_plan"
+    shape, i32 = block_table.shape, torch.int32
+    if block_table.dtype != i32 or len(shape) != 2 or (shape[1] > 1 and block_table.stride(1) != 1):
+        raise ValueError("%s: block_table int32 [B, max_pages] expected" % what)
+    B = shape[0]
+    for name, t in (("cached_lens", cached_lens), ("fresh_lens", fresh_lens), ("held", held), ("new_held", new_held),
+                    ("seq_lens", seq_lens)):
+        _ints(t, (B,), i32, what, name)
+    for name, t, n in (("free_count", free_count, 1), ("new_free_count", new_free_count, 1),
+                       ("tok_start", tok_start, B + 1), ("free_pages", free_pages, free_pages.numel())):
+        _ints(t, (n,), i32, what, name)
+    n_tok = dst.numel()
+    _ints(dst, (n_tok,), torch.int64, what, "dst")
+    _ints(pos, (n_tok,), torch.int64, what, "pos")
+    if pos_start is not None:
+        _ints(pos_start, (B,), torch.int64, what, "pos_start")
+    with _on(what, cached_lens, fresh_lens, held, block_table, free_pages, free_count, new_held, new_free_count,
+             seq_lens, tok_start, dst, pos, pos_start):
+        _check(lib().tq_page_plan(cached_lens.data_ptr(), fresh_lens.data_ptr(), _ptr(pos_start), B, Hkv, page_tokens,
+                                  block_table.data_ptr(), block_table.stride(0) if B > 1 else shape[1], shape[1],
+                                  held.data_ptr(), new_held.data_ptr(), free_pages.data_ptr(), free_pages.numel(),
+                                  free_count.data_ptr(), new_free_count.data_ptr(), seq_lens.data_ptr(),
+                                  tok_start.data_ptr(), dst.data_ptr(), pos.data_ptr(), n_tok, _stream(stream)), what)
+    return seq_lens
+
+
+def tq_norm_rope_apply(q, k, q_weight, k_weight, eps, pos, rope, q_out, k_out, stream=None):
+    """RMS-normalise queries q [n, Hq, 128] and keys k [n, Hkv, 128] head by head
+    (weights [128] or None) and rotate them into q_out and k_out (same shapes and
+    dtype; they may be q and k).  k with k_out, or q with q_out, may be None; rope
+    None: normalised only (pos then unused)."""
+    what = "tq_norm_rope_apply"
+    x = q if q is not None else k
+    _need(x is not None, "tq_norm_rope_apply: no rows")
+    n, args = x.shape[0], []
+    for rows, out in ((q, q_out), (k, k_out)):
+        if rows is None or out is None:
+            if rows is not None or out is not None:
+                raise ValueError("tq_norm_rope_apply: rows and their output come together")
+            args.append((None, 0, 0, 0, None, 0, 0))
+            continue
+        m, heads, st, sh = _heads(rows, what)
+        mo, oheads, ot, oh = _heads(out, what)
+        if m != n or mo != n or oheads != heads or rows.dtype != x.dtype or out.dtype != x.dtype:
+            raise ValueError("tq_norm_rope_apply: rows of one length and dtype, outputs of their shapes expected")
+        args.append((rows.data_ptr(), heads, st, sh, out.data_ptr(), ot, oh))
+    wd = None
+    for w in (q_weight, k_weight):
+        if w is not None:
+            if w.shape != (128,) or not w.is_contiguous() or (wd is not None and w.dtype != wd):
+                raise ValueError("tq_norm_rope_apply: weights [128] of one dtype expected")
+            wd = w.dtype
+    w = q_weight if q_weight is not None else k_weight
+    turn = rope is not None
+    pa = _axis_stride(pos, rope, n, what) if turn else 0
+    (qp, qh, qt, qs, qo, qot, qoh), (kp, kh, kt, ks, ko, kot, koh) = args
+    with _on(what, q, k, q_out, k_out, q_weight, k_weight, pos if turn else None):
+        _check(lib().tq_norm_rope_apply(qp, qh, qt, qs, kp, kh, kt, ks, _dtype(x), n, _ptr(q_weight), _ptr(k_weight),
+                                        TQ_F32 if w is None else _dtype(w), eps, pos.data_ptr() if turn else None, pa,
+                                        rope if turn else None, qo, qot, qoh, ko, kot, koh, _stream(stream)), what)
+
+
+def tq_attn_shared_workspace_bytes(B, Hq, Hkv, P, T):
+    """Workspace bytes of tq_attn_decode_shared on the current device (as tq_attn_weights_workspace_bytes)."""
+    return int(lib().tq_attn_shared_workspace_bytes(B, Hq, Hkv, P, T))
+
+
+def tq_attn_decode_shared(q, k_prefix, v_prefix, k_blocks, kcb, v_blocks, vcb, out, workspace, P, T, scale, signs,
+                          prefix_len=None, prefix_table=None, seq_lens=None, block_table=None, stream=None):
+    """Decode attention behind a prefix that the whole batch shares.  q [B, Hq,
+    128]; prefix uint8 [Hkv, P_cap, bytes] and own tokens [B, Hkv, T_cap, bytes],
+    or with prefix_table int32 [pages of the prefix] and block_table int32 [B,
+    max_pages] (rows may be strided) pools [pages, Hkv, page, bytes]; seq_lens
+    int32 [B] own tokens (negative: no sequence); prefix_len int32 [1]; out
+    [B, Hq, 128] float32, bfloat16 or float16."""
+    what = "tq_attn_decode_shared"
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != 128 or not q.is_contiguous():
+        raise ValueError("%s: contiguous q [B, Hq, 128] expected" % what)
+    B, Hq = shape[0], shape[1]
+    paged = block_table is not None
+    if paged != (prefix_table is not None):
+        raise ValueError("%s: block_table and prefix_table come together" % what)
+    kb, vb = 2 + 16 * kcb.bits, 2 + 16 * vcb.bits
+    ks, vs = _cache(k_blocks, kb, None if paged else B, what), _cache(v_blocks, vb, None if paged else B, what)
+    Hkv, unit = ks[1], ks[2]
+    if paged:
+        kp, vp = _cache(k_prefix, kb, None, what), _cache(v_prefix, vb, None, what)
+        if kp[1:3] != ks[1:3]:
+            raise ValueError("%s: pools of one page expected" % what)
+        tshape = block_table.shape
+        if block_table.dtype != torch.int32 or len(tshape) != 2 or tshape[0] != B or (
+                tshape[1] > 1 and block_table.stride(1) != 1):
+            raise ValueError("%s: block_table int32 [B, max_pages] expected" % what)
+        if prefix_table.dtype != torch.int32 or prefix_table.dim() != 1 or not prefix_table.is_contiguous():
+            raise ValueError("%s: prefix_table int32 [pages] expected" % what)
+        P_cap, pages = min(prefix_table.numel() * unit, 0x7FFFFFFF), tshape[1]
+        row = block_table.stride(0) if B > 1 else pages
+    else:
+        kp, vp = tuple(k_prefix.shape), tuple(v_prefix.shape)
+        for t, size in ((k_prefix, kb), (v_prefix, vb)):
+            if t.dtype != torch.uint8 or t.dim() != 3 or not t.is_contiguous() or t.shape[0] != Hkv or t.shape[2] != size:
+                raise ValueError("%s: prefix blocks [Hkv, P_cap, bytes] expected" % what)
+        P_cap, pages, row = kp[1], 0, 0
+    if ks[:3] != vs[:3] or kp[:-1] != vp[:-1]:
+        raise ValueError("%s: caches of one shape expected" % what)
+    if out.shape != shape or not out.is_contiguous():
+        raise ValueError("%s: contiguous out of q's shape expected" % what)
+    if seq_lens is not None:
+        _lens(seq_lens, B, what)
+    if prefix_len is not None:
+        _lens(prefix_len, 1, what)
+    with _on(what, q, k_prefix, v_prefix, k_blocks, v_blocks, out, workspace, prefix_len, prefix_table, seq_lens,
+             block_table):
+        _check(lib().tq_attn_decode_shared(q.data_ptr(), _dtype(q), k_prefix.data_ptr(), v_prefix.data_ptr(),
+                                           _ptr(prefix_table), P_cap, P, _ptr(prefix_len), k_blocks.data_ptr(), kcb,
+                                           v_blocks.data_ptr(), vcb, _ptr(block_table), row, pages, unit,
+                                           _ptr(seq_lens), B, Hq, Hkv, unit, T, scale, signs, out.data_ptr(),
+                                           _dtype(out), workspace.data_ptr(),
+                                           workspace.numel() * workspace.element_size(), _stream(stream)), what)
+    return out
