@@ -8,7 +8,7 @@
 namespace tq {
 
 // Merge for the tensor-core kernel's partition, by one CTA for one (sequence,
-// query head): the partials at slot(i), i < nslots.  128 x ng
+// query head): the partials at base + i * stride, i < nslots.  128 x ng
 // threads: thread d of slot group g reduces output dim d over batches g, g +
 // ng, ... of kBatch slots.  Reading what other SMs just wrote costs a full L2
 // round trip, so each thread issues every load of a batch at once (m and l of
@@ -16,9 +16,10 @@ namespace tq {
 // only then reduces, with the running max rescaled between batches; the groups
 // run their rounds side by side and meet in shared memory.  rotate_back applies
 // D H with the factor out_scale; store(d, value) takes the output.
-template <int kBatch, class Slot, class Store>
-__device__ __forceinline__ void combine_slots(Slot slot, int nslots, int rotate_back, float out_scale, uint32_t s0,
-                                              uint32_t s1, uint32_t s2, uint32_t s3, Store store) {
+template <int kBatch, class Store>
+__device__ __forceinline__ void combine_mma(const float *base, int stride, int nslots, int rotate_back,
+                                            float out_scale, uint32_t s0, uint32_t s1, uint32_t s2, uint32_t s3,
+                                            Store store) {
     __shared__ float buf[kD];
     __shared__ float gacc[kCombineMaxGroups][kD];
     __shared__ float gml[kCombineMaxGroups][2];
@@ -29,7 +30,7 @@ __device__ __forceinline__ void combine_slots(Slot slot, int nslots, int rotate_
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
             const bool ok = sb + i < nslots;
-            const float *ps = slot(sb + i);
+            const float *ps = base + (int64_t)(sb + i) * stride;
             mv[i] = ok ? __ldcg(ps) : -INFINITY;
             lv[i] = ok ? __ldcg(ps + 1) : 0.f;
             xv[i] = ok ? __ldcg(ps + 4 + d) : 0.f;
@@ -105,15 +106,6 @@ __device__ __forceinline__ void combine_slots(Slot slot, int nslots, int rotate_
         const float v = buf[d] * out_scale;
         store(d, ((sw[d >> 5] >> (d & 31)) & 1u) ? -v : v);
     }
-}
-
-// The same of partials at base + i * stride.
-template <int kBatch, class Store>
-__device__ __forceinline__ void combine_mma(const float *base, int stride, int nslots, int rotate_back,
-                                            float out_scale, uint32_t s0, uint32_t s1, uint32_t s2, uint32_t s3,
-                                            Store store) {
-    combine_slots<kBatch>([&](int i) { return base + (int64_t)i * stride; }, nslots, rotate_back, out_scale, s0, s1,
-                          s2, s3, store);
 }
 
 }  // namespace tq

@@ -50,7 +50,6 @@
 #include <cmath>
 
 #include "tq_attn.cuh"
-#include "tq_attn_combine.cuh"
 #include "tq_attn_mma.h"
 #include "tq_internal.h"
 #include "tq_tc.cuh"
@@ -269,7 +268,7 @@ __device__ __forceinline__ void levels16(const uint32_t (&t)[4], uint32_t w0, ui
         for (int s = 0; s < 2; ++s) {
             // even (odd) dims: the low plane's pairs of bits are nibbles as they are, the high plane's
             // bits are spread to them
-            uint32_t x = (w1 >> s) & 0x5555u;
+            uint32_t x = (w1 >> s) & 0x5555u;   // (of the 16 low bits)
             x = (x | (x << 8)) & 0x00FF00FFu;
             x = (x | (x << 4)) & 0x05050505u;
             x = (x | (x << 2)) & 0x11111111u;
@@ -290,38 +289,99 @@ __device__ __forceinline__ void levels16(const uint32_t (&t)[4], uint32_t w0, ui
 }
 
 // A block's codes (block at shared address blk, 2-byte aligned) into row r of an
-// operand tile at `tile`.
+// operand tile at `tile`, 32 dims at a time (rolled: straight-line code for a
+// whole row would be fetched anew for every tile).
 template <int BITS>
 __device__ __forceinline__ void dequant_row(const uint32_t (&t)[4], uint32_t blk, uint32_t tile, int r) {
-    constexpr int NW = BITS == 4 ? 16 : 8;
+    constexpr int NW = BITS == 4 ? 4 : 2;   // words per 32 dims (3 bits: of the low plane)
     const uint32_t at = blk + 2, base = at & ~3u, sh = (at & 3u) * 8u;
-    uint32_t hp[4] = {0, 0, 0, 0};
-    if constexpr (BITS == 3) {
-        uint32_t raw[5];
+    const uint32_t row = tile + r * 128;
+#pragma unroll 1
+    for (int g = 0; g < 4; ++g) {
+        uint32_t raw[NW + 1], w[NW], hp = 0;
 #pragma unroll
-        for (int i = 0; i < 5; ++i) raw[i] = sh_lds32(base + 32 + 4 * i);
+        for (int i = 0; i <= NW; ++i) raw[i] = sh_lds32(base + 4 * NW * g + 4 * i);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) hp[i] = __funnelshift_r(raw[i], raw[i + 1], sh);
-    }
-    constexpr int WPG = NW / 8;   // words per 16 dims
-    uint32_t prev = sh_lds32(base);
+        for (int i = 0; i < NW; ++i) w[i] = __funnelshift_r(raw[i], raw[i + 1], sh);
+        if constexpr (BITS == 3)
+            hp = __funnelshift_r(sh_lds32(base + 32 + 4 * g), sh_lds32(base + 36 + 4 * g), sh);
+        const uint32_t half = row + (g >> 1) * 16384;
 #pragma unroll
-    for (int a = 0; a < 8; ++a) {
-        uint32_t w[2] = {0, 0};
-#pragma unroll
-        for (int i = 0; i < WPG; ++i) {
-            const uint32_t next = sh_lds32(base + 4 * (WPG * a + i + 1));
-            w[i] = __funnelshift_r(prev, next, sh);
-            prev = next;
+        for (int a = 0; a < 2; ++a) {
+            uint32_t o[8];
+            levels16<BITS>(t, BITS == 4 ? w[(2 * a) % NW] : w[a % NW], BITS == 4 ? w[(2 * a + 1) % NW] : hp >> (16 * a), o);
+            const uint32_t c = 4 * (g & 1) + 2 * a;
+            sh_sts128(half + ((c ^ (r & 7)) << 4), o[0], o[1], o[2], o[3]);
+            sh_sts128(half + (((c + 1) ^ (r & 7)) << 4), o[4], o[5], o[6], o[7]);
         }
-        if constexpr (BITS == 3) w[1] = (hp[a >> 1] >> (16 * (a & 1))) & 0xFFFFu;
-        uint32_t o[8];
-        levels16<BITS>(t, w[0], w[1], o);
-        const uint32_t row = tile + (a >> 2) * 16384 + r * 128;
-        const uint32_t c = 2 * (a & 3);
-        sh_sts128(row + ((c ^ (r & 7)) << 4), o[0], o[1], o[2], o[3]);
-        sh_sts128(row + (((c + 1) ^ (r & 7)) << 4), o[4], o[5], o[6], o[7]);
     }
+}
+
+// The largest of a row's 128 scores (NaN aside; keys from `valid` on do not count).
+template <bool TAIL>
+__device__ __forceinline__ float row_max(uint32_t s_col, const float *kn, int valid) {
+    float mx = -INFINITY, my = -INFINITY;
+#pragma unroll 1
+    for (int c = 0; c < 128; c += 32) {
+        float s[32];
+        tc_ld32(s_col + c, s);
+        tc_wait_ld();
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            const float4 n = reinterpret_cast<const float4 *>(kn + c)[q];
+            float2 a = __fmul2_rn(make_float2(s[4 * q], s[4 * q + 1]), make_float2(n.x, n.y));
+            float2 b = __fmul2_rn(make_float2(s[4 * q + 2], s[4 * q + 3]), make_float2(n.z, n.w));
+            if constexpr (TAIL) {
+                const int at = valid - c - 4 * q;
+                if (at <= 0) a.x = -INFINITY;
+                if (at <= 1) a.y = -INFINITY;
+                if (at <= 2) b.x = -INFINITY;
+                if (at <= 3) b.y = -INFINITY;
+            }
+            mx = fmaxf(mx, fmaxf(a.x, a.y));
+            my = fmaxf(my, fmaxf(b.x, b.y));
+        }
+    }
+    return fmaxf(mx, my);
+}
+
+// Probabilities 2^(s - mref) of a row's 128 scores, times the value norms as
+// fp16 hi and lo parts over the scores; returns the sum.  (A key from `valid`
+// on has the value norm 0.)
+template <bool TAIL>
+__device__ __forceinline__ float row_weights(uint32_t s_col, const float *kn, const float *vn, int valid, float mref) {
+    float2 sum = make_float2(0.f, 0.f);
+    const float2 m2 = make_float2(-mref, -mref);
+#pragma unroll 1
+    for (int c = 0; c < 128; c += 32) {
+        float s[32];
+        tc_ld32(s_col + c, s);
+        tc_wait_ld();
+        uint32_t w[32];   // hi parts of the 32 probabilities, then lo parts
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            const float4 n = reinterpret_cast<const float4 *>(kn + c)[q];
+            const float4 v = reinterpret_cast<const float4 *>(vn + c)[q];
+            float2 x = __ffma2_rn(make_float2(s[4 * q], s[4 * q + 1]), make_float2(n.x, n.y), m2);
+            float2 y = __ffma2_rn(make_float2(s[4 * q + 2], s[4 * q + 3]), make_float2(n.z, n.w), m2);
+            if constexpr (TAIL) {
+                const int at = valid - c - 4 * q;
+                if (at <= 0) x.x = -INFINITY;
+                if (at <= 1) x.y = -INFINITY;
+                if (at <= 2) y.x = -INFINITY;
+                if (at <= 3) y.y = -INFINITY;
+            }
+            float2 p = make_float2(sh_ex2(x.x), sh_ex2(x.y)), r = make_float2(sh_ex2(y.x), sh_ex2(y.y));
+            sum = __fadd2_rn(sum, __fadd2_rn(p, r));
+            p = __fmul2_rn(p, make_float2(v.x, v.y));
+            r = __fmul2_rn(r, make_float2(v.z, v.w));
+            sh_split(p.x, p.y, w[2 * q], w[16 + 2 * q]);
+            sh_split(r.x, r.y, w[2 * q + 1], w[16 + 2 * q + 1]);
+        }
+        sh_st32(s_col + c, w);
+    }
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+    return sum.x + sum.y;
 }
 
 template <int KB, int VB>
@@ -447,14 +507,14 @@ __global__ void __launch_bounds__(kShThreads, 1) attn_shared_kernel(const __grid
                 if (!ok) return;
                 tc_fence_after();
                 const uint32_t d = tmem + 128u * (uint32_t)x, kb = k_at(st), qb = q_at(x);
+                // (rolled: 32 pairs of descriptors would not fit the registers)
+#pragma unroll 1
+                for (int i = 0; i < 16; i += 4) {
+                    const uint32_t off = (uint32_t)((i >> 2) & 1) * 16384u;
+                    const uint64_t qd = sh_desc(qb + (i >> 3) * S::kTile + off, 16, 1024), kd = sh_desc(kb + off, 16, 1024);
 #pragma unroll
-                for (int part = 0; part < 2; ++part)
-#pragma unroll
-                    for (int ks = 0; ks < 8; ++ks) {
-                        const uint32_t off = (uint32_t)((ks >> 2) * 16384 + (ks & 3) * 32);
-                        tc_mma(d, sh_desc(qb + part * S::kTile + off, 16, 1024), sh_desc(kb + off, 16, 1024), sh_idesc(0),
-                               (part > 0 || ks > 0) ? 1u : 0u);
-                    }
+                    for (int ks = 0; ks < 4; ++ks) tc_mma(d, qd + 2 * ks, kd + 2 * ks, sh_idesc(0), i + ks > 0 ? 1u : 0u);
+                }
                 tc_commit(bar(kSReady + x));
                 tc_commit(bar(kKFree + st));
             };
@@ -465,13 +525,15 @@ __global__ void __launch_bounds__(kShThreads, 1) attn_shared_kernel(const __grid
                 if (!ok) return;
                 tc_fence_after();
                 const uint32_t vb = v_at(st), pa = tmem + 128u * (uint32_t)x;
+                const uint64_t vd = sh_desc(vb, 16384, 1024);
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {   // 32 keys: two steps of the hi parts, two of the lo parts
 #pragma unroll
-                for (int part = 0; part < 2; ++part)
-#pragma unroll
-                    for (int ks = 0; ks < 8; ++ks)
-                        sh_mma_ts(tmem + kShColO + 128u * (uint32_t)x, pa + 32 * (ks >> 1) + 8 * (ks & 1) + 16 * part,
-                                  sh_desc(vb + ks * 2048, 16384, 1024), sh_idesc(1),
-                                  (e > 1 || part > 0 || ks > 0) ? 1u : 0u);
+                    for (int i = 0; i < 4; ++i)
+                        sh_mma_ts(tmem + kShColO + 128u * (uint32_t)x, pa + 32u * c + 8u * i,
+                                  vd + (uint64_t)(4096 / 16) * c + (2048 / 16) * (i & 1), sh_idesc(1),
+                                  (e > 1 || c > 0 || i > 0) ? 1u : 0u);
+                }
                 tc_commit(bar(kVFree + st));
                 if (e + 2 >= items) tc_commit(bar(kODone + x));
             };
@@ -543,26 +605,8 @@ __global__ void __launch_bounds__(kShThreads, 1) attn_shared_kernel(const __grid
             wait(ok, kSReady + x, (uint32_t)t);
             tc_fence_after();
             const int nvalid = len - (tile0 + i) * kShKeys;   // (of 128)
-            // the row's largest score
-            float mx = -INFINITY;
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                float sv[32];
-                tc_ld32(s_col + 32 * c, sv);
-                tc_wait_ld();
-                const float4 *kn = reinterpret_cast<const float4 *>(nm + 32 * c);
-#pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                    const float4 n = kn[q];
-                    float e[4] = {sv[4 * q] * n.x, sv[4 * q + 1] * n.y, sv[4 * q + 2] * n.z, sv[4 * q + 3] * n.w};
-                    if (nvalid < kShKeys) {
-#pragma unroll
-                        for (int w = 0; w < 4; ++w)
-                            if (32 * c + 4 * q + w >= nvalid) e[w] = -INFINITY;
-                    }
-                    mx = fmaxf(mx, fmaxf(fmaxf(e[0], e[1]), fmaxf(e[2], e[3])));
-                }
-            }
+            const bool tail = nvalid < kShKeys;
+            const float mx = tail ? row_max<true>(s_col, nm, nvalid) : row_max<false>(s_col, nm, kShKeys);
             const float4 lv = *reinterpret_cast<const float4 *>(nm + 2 * kShKeys);
             const float top = mx + fmaxf(fmaxf(lv.x, lv.y), fmaxf(lv.z, lv.w));
             const bool move = top > m_ref + 8.f;
@@ -570,7 +614,7 @@ __global__ void __launch_bounds__(kShThreads, 1) attn_shared_kernel(const __grid
             const float factor = move ? (m_ref == -INFINITY ? 0.f : exp2f(m_ref - m_new)) : 1.f;
             if (t >= 1 && __any_sync(0xffffffffu, move)) {
                 // (the stream's products before this tile's scores have completed)
-#pragma unroll
+#pragma unroll 1
                 for (int c = 0; c < 4; ++c) {
                     float o[32];
                     tc_ld32(o_col + 32 * c, o);
@@ -583,38 +627,9 @@ __global__ void __launch_bounds__(kShThreads, 1) attn_shared_kernel(const __grid
             }
             // no finite score so far: scores are -inf (P 0) or NaN (which stays NaN)
             const float mref = m_new == -INFINITY ? 0.f : m_new;
-            float2 sum = make_float2(0.f, 0.f);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                float sv[32];
-                tc_ld32(s_col + 32 * c, sv);
-                tc_wait_ld();
-                const float4 *kn = reinterpret_cast<const float4 *>(nm + 32 * c);
-                const float4 *vn = reinterpret_cast<const float4 *>(nm + kShKeys + 32 * c);
-                uint32_t w[32];   // hi parts of the 32 probabilities, then lo parts
-#pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                    const float4 n = kn[q], v = vn[q];
-                    float2 p0 = make_float2(sh_ex2(fmaf(sv[4 * q], n.x, -mref)), sh_ex2(fmaf(sv[4 * q + 1], n.y, -mref)));
-                    float2 p1 =
-                        make_float2(sh_ex2(fmaf(sv[4 * q + 2], n.z, -mref)), sh_ex2(fmaf(sv[4 * q + 3], n.w, -mref)));
-                    if (nvalid < kShKeys) {
-                        const int at = 32 * c + 4 * q;
-                        if (at >= nvalid) p0.x = 0.f;
-                        if (at + 1 >= nvalid) p0.y = 0.f;
-                        if (at + 2 >= nvalid) p1.x = 0.f;
-                        if (at + 3 >= nvalid) p1.y = 0.f;
-                    }
-                    sum = __fadd2_rn(sum, __fadd2_rn(p0, p1));
-                    p0 = __fmul2_rn(p0, make_float2(v.x, v.y));
-                    p1 = __fmul2_rn(p1, make_float2(v.z, v.w));
-                    sh_split(p0.x, p0.y, w[2 * q], w[16 + 2 * q]);
-                    sh_split(p1.x, p1.y, w[2 * q + 1], w[16 + 2 * q + 1]);
-                }
-                sh_st32(s_col + 32 * c, w);
-            }
-            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-            l = l * factor + (sum.x + sum.y);
+            const float sum = tail ? row_weights<true>(s_col, nm, nm + kShKeys, nvalid, mref)
+                                   : row_weights<false>(s_col, nm, nm + kShKeys, kShKeys, mref);
+            l = l * factor + sum;
             m_ref = m_new;
             tc_fence_before();
             __syncwarp();
@@ -624,32 +639,63 @@ __global__ void __launch_bounds__(kShThreads, 1) attn_shared_kernel(const __grid
         if (mine > 0) wait(ok, kODone + x, 0);
         tc_fence_after();
         const int row = (qt + (two ? x : 0)) * kShRows + r;
-        float *out = a.part + (((int64_t)blockIdx.x * 2 + x) * kShRows + r) * kPartialFloats;
-        if (row < a.rows) {
-            out[0] = m_ref;
-            out[1] = ok ? l : __int_as_float(0x7fc00000);   // NaN marks a failed wait
-        }
+        const bool store = row < a.rows;
+        // 32 columns of sums to dims: place -> dim of each 16, the inverse of operand_place
+        auto put = [&](float *out, const float (&o)[32]) {
+            float d[32];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            float o[32];
-            if (mine > 0) {   // (the whole warp)
-                tc_ld32(o_col + 32 * c, o);
-                tc_wait_ld();
-            } else {
+            for (int q = 0; q < 32; ++q)
+                d[(q & 16) + (VB == 4 ? (q & 15) : VB == 3 ? 2 * (q & 7) + ((q >> 3) & 1) : 4 * (q & 3) + ((q >> 2) & 3))] = o[q];
 #pragma unroll
-                for (int q = 0; q < 32; ++q) o[q] = 0.f;
+            for (int q = 0; q < 8; ++q)
+                reinterpret_cast<float4 *>(out)[q] = make_float4(d[4 * q], d[4 * q + 1], d[4 * q + 2], d[4 * q + 3]);
+        };
+        if (!ok) l = __int_as_float(0x7fc00000);   // NaN marks a failed wait
+        if (two) {
+            float *out = a.part + ((int64_t)(2 * blockIdx.x + x) * kShRows + r) * kPartialFloats;
+            if (store) {
+                out[0] = m_ref;
+                out[1] = l;
             }
-            if (row < a.rows) {
-                float d[32];
+#pragma unroll 1
+            for (int c = 0; c < 128; c += 32) {
+                float o[32];
+                if (mine > 0) {   // (the whole warp)
+                    tc_ld32(o_col + c, o);
+                    tc_wait_ld();
+                }
 #pragma unroll
-                for (int q = 0; q < 32; ++q)   // dims of a 16: place -> dim, the inverse of operand_place
-                    d[(q & 16) + (VB == 4 ? (q & 15)
-                                          : VB == 3 ? 2 * (q & 7) + ((q >> 3) & 1) : 4 * (q & 3) + ((q >> 2) & 3))] =
-                        o[q] * (1.f / kShUp);
+                for (int q = 0; q < 32; ++q) o[q] = mine > 0 ? o[q] * (1.f / kShUp) : 0.f;
+                if (store) put(out + 4 + c, o);
+            }
+        } else {
+            // both streams' sums of a row lie in its lane: join them, each thread half of the dims (every
+            // product has completed, so the statistics take the query tile's place)
+            auto rows_sync = [&]() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kShRowWarps) : "memory"); };
+            float2 *stat = reinterpret_cast<float2 *>(smem);
+            rows_sync();
+            stat[x * kShRows + r] = make_float2(m_ref, l);
+            rows_sync();
+            const float2 s0 = stat[r], s1 = stat[kShRows + r];
+            const float M = fmaxf(s0.x, s1.x);
+            const float f0 = s0.x == -INFINITY ? 0.f : exp2f(s0.x - M), f1 = s1.x == -INFINITY ? 0.f : exp2f(s1.x - M);
+            float *out = a.part + ((int64_t)2 * blockIdx.x * kShRows + r) * kPartialFloats;
+            if (store && x == 0) {
+                // (a sum that is not finite, of scores that are not, shows whatever its maximum)
+                out[0] = M;
+                out[1] = (s0.x == -INFINITY ? s0.y : f0 * s0.y) + (s1.x == -INFINITY ? s1.y : f1 * s1.y);
+            }
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 64 * x; c < 64 * x + 64; c += 32) {
+                float o[32], o1[32];
+                if (nt > 0) tc_ld32(lane_t + kShColO + c, o);
+                if (nt > 1) tc_ld32(lane_t + kShColO + 128 + c, o1);
+                tc_wait_ld();
 #pragma unroll
-                for (int q = 0; q < 8; ++q)
-                    reinterpret_cast<float4 *>(out + 4 + 32 * c)[q] =
-                        make_float4(d[4 * q], d[4 * q + 1], d[4 * q + 2], d[4 * q + 3]);
+                for (int q = 0; q < 32; ++q)
+                    o[q] = ((nt > 0 ? o[q] * f0 : 0.f) + (nt > 1 ? o1[q] * f1 : 0.f)) * (1.f / kShUp);
+                if (store) put(out + 4 + c, o);
             }
         }
     }
@@ -678,40 +724,152 @@ struct MergeArgs {
     uint32_t signs[4];
 };
 
-constexpr int kMergeBatch = 16;   // slots a merging thread loads at once
+constexpr int kMergeMaxWarps = 16;
+constexpr int kMergeDepth = 8;   // slots a warp has on their way at once
 
-// One CTA for one (sequence, query head): the prefix's slots, then the own
-// tokens'.
-__global__ void __launch_bounds__(kAttnThreads * kCombineMaxGroups) attn_shared_merge_kernel(
-    const __grid_constant__ MergeArgs a) {
+// One CTA for one (sequence, query head).  A warp takes every slot of its own
+// turn, a lane four dims of it: the prefix's slots, then the own tokens', each
+// batch's loads issued before the one ahead of it is added up (reading what
+// other SMs have just written costs a round trip through L2).  The warps'
+// states meet in shared memory, and the first turns the output back.
+__global__ void __launch_bounds__(32 * kMergeMaxWarps) attn_shared_merge_kernel(const __grid_constant__ MergeArgs a) {
+    __shared__ __align__(16) float accs[kMergeMaxWarps][kD];
+    __shared__ float ms[kMergeMaxWarps], ls[kMergeMaxWarps];
     const int b = blockIdx.x / a.Hq, h = blockIdx.x % a.Hq, kvh = h / a.G, g = h % a.G;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
     const SharedPlan &p = a.plan;
     const int row = b * a.G + g, tile = row / kShRows;
     const bool two = tile < 2 * p.pairs;
     const int n = (shared_len(a.len, a.P) + kShKeys - 1) / kShKeys, ranges = two ? p.s2 : p.s1;
-    const int used = n < ranges ? n : ranges;
-    // slots of the prefix: one per range, or (an odd tile) one per range and stream
-    int before = two ? used : 2 * used;
-    const float *part =
-        a.part + ((int64_t)(kvh * p.per_head + (two ? (tile >> 1) * p.s2 : p.pairs * p.s2)) * 2 * kShRows +
-                  (two ? (tile & 1) * kShRows : 0) + row % kShRows) * kPartialFloats;
-    const int64_t step = (int64_t)(two ? 2 : 1) * kShRows * kPartialFloats;
+    const float *part = a.part + ((int64_t)(kvh * p.per_head + (two ? (tile >> 1) * p.s2 : p.pairs * p.s2)) * 2 * kShRows +
+                                  (two ? (tile & 1) * kShRows : 0) + row % kShRows) * kPartialFloats;
     const bool empty = a.seq_lens && a.seq_lens[b] < 0;
+    const int before = empty ? 0 : (n < ranges ? n : ranges);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int64_t j = (int64_t)b * a.Hkv + kvh;
     const int2 met = __ldcg(a.live + j);
+
+    struct Batch {
+        float4 x[kMergeDepth];
+        float m, l;   // (of slot `lane` of the batch)
+    };
+    float M = -INFINITY, l = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto load = [&](Batch &t, const float *base, int64_t step, int from, int slots) {
+        t.m = -INFINITY;
+        t.l = 0.f;
+        const int mine = from + warp + nw * lane;
+        if (lane < kMergeDepth && mine < slots) {
+            t.m = __ldcg(base + mine * step);
+            t.l = __ldcg(base + mine * step + 1);
+        }
+#pragma unroll
+        for (int i = 0; i < kMergeDepth; ++i) {
+            const int s = from + warp + nw * i;
+            t.x[i] = s < slots ? __ldcg(reinterpret_cast<const float4 *>(base + s * step + 4) + lane)
+                               : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+    };
+    auto add = [&](const Batch &t) {
+        float mb = t.m;
+#pragma unroll
+        for (int o = 1; o < kMergeDepth; o <<= 1) mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, o));
+        const float Mn = fmaxf(M, __shfl_sync(0xffffffffu, mb, 0));
+        // (a slot without a finite score has the sum 0, or NaN, which shows)
+        const float w = t.m == -INFINITY ? 0.f : exp2f(t.m - Mn);
+        const float f = M == -INFINITY ? 0.f : exp2f(M - Mn);
+        float lb = t.m == -INFINITY ? t.l : w * t.l;
+#pragma unroll
+        for (int o = 1; o < kMergeDepth; o <<= 1) lb += __shfl_xor_sync(0xffffffffu, lb, o);
+        l = (M == -INFINITY ? l : l * f) + __shfl_sync(0xffffffffu, lb, 0);
+        acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+        M = Mn;
+#pragma unroll
+        for (int i = 0; i < kMergeDepth; ++i) {
+            const float wi = __shfl_sync(0xffffffffu, w, i);
+            acc = make_float4(fmaf(wi, t.x[i].x, acc.x), fmaf(wi, t.x[i].y, acc.y), fmaf(wi, t.x[i].z, acc.z),
+                              fmaf(wi, t.x[i].w, acc.w));
+        }
+    };
+    const int64_t step = (int64_t)2 * kShRows * kPartialFloats, own_step = (int64_t)a.G * kPartialFloats;
     const float *own = a.own + ((met.x + j) * a.G + g) * kPartialFloats;
-    const int64_t own_step = (int64_t)a.G * kPartialFloats;
-    if (empty) before = 0;
-    const int64_t at = (int64_t)blockIdx.x * kD;
-    combine_slots<kMergeBatch>(
-        [&](int i) { return i < before ? part + i * step : own + (i - before) * own_step; },
-        empty ? 0 : before + met.y, 1, a.out_scale, a.signs[0], a.signs[1], a.signs[2], a.signs[3],
-        [&](int d, float v) {
-            if (a.out_dtype == TQ_F32) static_cast<float *>(a.out)[at + d] = v;
-            else if (a.out_dtype == TQ_BF16) static_cast<__nv_bfloat16 *>(a.out)[at + d] = __float2bfloat16_rn(v);
-            else static_cast<__half *>(a.out)[at + d] = __float2half_rn(v);
-        });
+    const int after = empty ? 0 : met.y, round = nw * kMergeDepth;
+    Batch t, u;
+    load(t, part, step, 0, before);
+    load(u, own, own_step, 0, after);
+    for (int s = round; s < before; s += round) {
+        add(t);
+        load(t, part, step, s, before);
+    }
+    add(t);
+    for (int s = round; s < after; s += round) {
+        add(u);
+        load(u, own, own_step, s, after);
+    }
+    add(u);
+    reinterpret_cast<float4 *>(accs[warp])[lane] = acc;
+    if (lane == 0) {
+        ms[warp] = M;
+        ls[warp] = l;
+    }
+    __syncthreads();
+    if (warp) return;
+    M = lane < nw ? ms[lane] : -INFINITY;
+    l = lane < nw ? ls[lane] : 0.f;
+    float Mt = M;
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) Mt = fmaxf(Mt, __shfl_xor_sync(0xffffffffu, Mt, o));
+    const float w = M == -INFINITY ? 0.f : exp2f(M - Mt);
+    float lt = M == -INFINITY ? l : w * l;
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) lt += __shfl_xor_sync(0xffffffffu, lt, o);
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int i = 0; i < nw; ++i) {
+        const float wi = __shfl_sync(0xffffffffu, w, i);
+        const float4 x = reinterpret_cast<const float4 *>(accs[i])[lane];
+        v[0] = fmaf(wi, x.x, v[0]);
+        v[1] = fmaf(wi, x.y, v[1]);
+        v[2] = fmaf(wi, x.z, v[2]);
+        v[3] = fmaf(wi, x.w, v[3]);
+    }
+    // o = D H (sums / l) / sqrt(128), 0 where nothing was seen (a NaN l, of a failed copy too, shows)
+    const bool seen = lt > 0.f || lt != lt;
+    const float inv = a.out_scale / lt;
+    const float x0 = v[0] + v[1], x1 = v[0] - v[1], x2 = v[2] + v[3], x3 = v[2] - v[3];
+    v[0] = x0 + x2;
+    v[2] = x0 - x2;
+    v[1] = x1 + x3;
+    v[3] = x1 - x3;
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float o = __shfl_xor_sync(0xffffffffu, v[k], m);
+            v[k] = (lane & m) ? (o - v[k]) : (v[k] + o);
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int d = 4 * lane + k;
+        v[k] = seen ? v[k] * inv : 0.f;
+        if ((a.signs[d >> 5] >> (d & 31)) & 1u) v[k] = -v[k];
+    }
+    const int64_t at = (int64_t)blockIdx.x * kD + 4 * lane;
+    if (a.out_dtype == TQ_F32) {
+        *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at) = make_float4(v[0], v[1], v[2], v[3]);
+    } else {
+        uint32_t o[2];
+        if (a.out_dtype == TQ_BF16) {
+            const __nv_bfloat162 e = __floats2bfloat162_rn(v[0], v[1]), f = __floats2bfloat162_rn(v[2], v[3]);
+            o[0] = *reinterpret_cast<const uint32_t *>(&e);
+            o[1] = *reinterpret_cast<const uint32_t *>(&f);
+        } else {
+            const __half2 e = __floats2half2_rn(v[0], v[1]), f = __floats2half2_rn(v[2], v[3]);
+            o[0] = *reinterpret_cast<const uint32_t *>(&e);
+            o[1] = *reinterpret_cast<const uint32_t *>(&f);
+        }
+        *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(a.out) + 2 * at) = make_uint2(o[0], o[1]);
+    }
 }
 
 // Ranges of the prefix: of all counts that give every CTA a tile, the one whose
@@ -938,11 +1096,13 @@ extern "C" int tq_attn_decode_shared(const void *q, int q_dtype, const uint8_t *
     m.plan = sp;
     m.out_scale = 0.08838834764831845f / vf;
     for (int i = 0; i < 4; ++i) m.signs[i] = signs.w[i];
-    const int slots = (sp.pairs ? sp.s2 : 0) > 2 * sp.s1 ? sp.s2 : 2 * sp.s1;
-    const int groups = (slots + plan.Smax + kMergeBatch - 1) / kMergeBatch;
+    // warps of a merging CTA: enough that the longer part is one batch, 4 to 16
+    const int slots = (int)max64(sp.pairs ? sp.s2 : sp.s1, plan.Smax);
+    int warps = (slots + kMergeDepth - 1) / kMergeDepth;
+    warps = warps < 4 ? 4 : (warps > kMergeMaxWarps ? kMergeMaxWarps : warps);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(B * Hq));
-    cfg.blockDim = dim3(kAttnThreads * (groups > kCombineMaxGroups ? kCombineMaxGroups : groups));
+    cfg.blockDim = dim3(32 * warps);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
