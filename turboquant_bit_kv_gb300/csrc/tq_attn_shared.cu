@@ -35,17 +35,17 @@
 // issued in the order P V of one stream, S of the same stream's next tile, then
 // the other stream, so one stream's softmax runs while the other's products do.
 //
-// Roles (448 threads, one CTA per SM):
+// Roles (576 threads, one CTA per SM):
 //   warps 0-3, 4-7  rows of stream 0, 1: a thread a row (its tensor-memory
 //              lane).  The reference of a row's exponents is its largest score
 //              plus the tile's largest value norm (in log2), and moves only
 //              when it is exceeded by more than 8, so O is rarely rescaled and
 //              P times the value norm stays below 2^15 whatever the norms are.
-//   warps 8-11 a thread a key: codes to fp16 in registers (byte permutes over
+//   warps 8-11, 12-15  a thread a key, a thread a value: codes to fp16 in registers (byte permutes over
 //              the levels' bytes; no lookups in shared memory, which the
 //              products keep busy), into the swizzled K and V tiles.
-//   warp 12    bulk copies: the query tiles, then the packed blocks.
-//   warp 13    one thread issues the products.
+//   warp 16    bulk copies: the query tiles, then the packed blocks.
+//   warp 17    one thread issues the products.
 // Every wait is bounded; one that gives up is recorded (tq_device_status).
 #include <cmath>
 
@@ -66,7 +66,8 @@ namespace {
 constexpr int kShKeys = 128;                 // keys per tile
 constexpr int kShRows = 128;                 // rows per stream
 constexpr int kShRowWarps = 8, kShKeyWarps = 4;
-constexpr int kShProducer = kShRowWarps + kShKeyWarps, kShMma = kShProducer + 1;
+constexpr int kShValueWarp = kShRowWarps + kShKeyWarps;   // (the first of as many)
+constexpr int kShProducer = kShValueWarp + kShKeyWarps, kShMma = kShProducer + 1;
 constexpr int kShThreads = 32 * (kShMma + 1);
 constexpr uint32_t kShCols = 512, kShColO = 256;
 constexpr int kShNormSlot = (2 * kShKeys + 4) * 4;   // key norms | value norms | four maxima of log2 value norm
@@ -420,7 +421,7 @@ __global__ void __launch_bounds__(kShThreads, 1) attn_shared_kernel(const __grid
             tc_mbar_init(bar(kKFull + s), 1 + extra);
             tc_mbar_init(bar(kVFull + s), 1 + extra);
             tc_mbar_init(bar(kKEmpty + s), kShKeyWarps);
-            tc_mbar_init(bar(kVEmpty + s), kShKeyWarps);
+            tc_mbar_init(bar(kVEmpty + s), 2 * kShKeyWarps);   // (values, and their norms)
             tc_mbar_init(bar(kKReady + s), kShKeyWarps);
             tc_mbar_init(bar(kVReady + s), kShKeyWarps);
             tc_mbar_init(bar(kKFree + s), two ? 2 : 1);
@@ -547,15 +548,32 @@ __global__ void __launch_bounds__(kShThreads, 1) attn_shared_kernel(const __grid
             tc_commit(bar(kDrain));
             tc_mbar_wait(bar(kDrain), 0u);
         }
+    } else if (warp >= kShValueWarp) {
+        // ---- value warps: thread = key of the tile
+        const int k = tid - 32 * kShValueWarp;
+        bool ok = true;
+        for (int i = 0; i < nt; ++i) {
+            const int st = stage(i), u = use(i), sv = i % S::kNV;
+            const uint32_t vblk = base_s + S::kVBlk + sv * S::kVBytes + k * (2 + 16 * VB);
+            wait(ok, kVFull + sv, (uint32_t)(i / S::kNV));
+            if (u >= 1) wait(ok, kVFree + st, (uint32_t)(u - 1));
+            dequant_row<VB>(a.vt, vblk, v_at(st), k);
+            // the tiles were written by ordinary stores and are read by the tensor cores
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) {
+                tc_mbar_arrive(bar(kVEmpty + sv));
+                tc_mbar_arrive(bar(kVReady + st));
+            }
+        }
     } else if (warp >= kShRowWarps) {
-        // ---- key warps: thread = key of the tile
+        // ---- key warps: thread = key of the tile; its value's norm too, which the rows want with the scores
         const int k = tid - 32 * kShRowWarps;
         bool ok = true;
         for (int i = 0; i < nt; ++i) {
             const int st = stage(i), u = use(i);
             const int sk = i % S::kNK, sv = i % S::kNV;
             const uint32_t kblk = base_s + S::kKBlk + sk * S::kKBytes + k * (2 + 16 * KB);
-            const uint32_t vblk = base_s + S::kVBlk + sv * S::kVBytes + k * (2 + 16 * VB);
             wait(ok, kKFull + sk, (uint32_t)(i / S::kNK));
             wait(ok, kVFull + sv, (uint32_t)(i / S::kNV));
             if (u >= 1) wait(ok, kKFree + st, (uint32_t)(u - 1));
@@ -563,31 +581,25 @@ __global__ void __launch_bounds__(kShThreads, 1) attn_shared_kernel(const __grid
             const bool live = (tile0 + i) * kShKeys + k < len;
             float *nm = norms + (i & 3) * (kShNormSlot / 4);
             const float kn = __half2float(__ushort_as_half((unsigned short)sh_lds16(kblk)));
-            const float vn = __half2float(__ushort_as_half((unsigned short)sh_lds16(vblk)));
+            const float vn = __half2float(__ushort_as_half((unsigned short)sh_lds16(
+                base_s + S::kVBlk + sv * S::kVBytes + k * (2 + 16 * VB))));
             nm[k] = live ? kn * a.k_norm : 0.f;
             nm[kShKeys + k] = live ? vn * kShUp : 0.f;
             // the largest value norm, in [2^-14, 2^16] whatever it is
             float lv = live ? fminf(fmaxf(vn, 0x1p-14f), 0x1p16f) : 0x1p-14f;
-#pragma unroll
-            for (int m = 16; m >= 1; m >>= 1) lv = fmaxf(lv, __shfl_xor_sync(0xffffffffu, lv, m));
+            lv = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(lv)));   // (positive: ordered as integers)
             if (lane == 0) nm[2 * kShKeys + warp - kShRowWarps] = log2f(lv);
             __syncwarp();
-            if (lane == 0) tc_mbar_arrive(bar(kNReady + (i & 3)));
+            if (lane == 0) {
+                tc_mbar_arrive(bar(kVEmpty + sv));
+                tc_mbar_arrive(bar(kNReady + (i & 3)));
+            }
             dequant_row<KB>(a.kt, kblk, k_at(st), k);
-            // the tiles were written by ordinary stores and are read by the tensor cores
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (lane == 0) {
                 tc_mbar_arrive(bar(kKEmpty + sk));
                 tc_mbar_arrive(bar(kKReady + st));
-            }
-            if (u >= 1) wait(ok, kVFree + st, (uint32_t)(u - 1));
-            dequant_row<VB>(a.vt, vblk, v_at(st), k);
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
-            if (lane == 0) {
-                tc_mbar_arrive(bar(kVEmpty + sv));
-                tc_mbar_arrive(bar(kVReady + st));
             }
         }
     } else {
