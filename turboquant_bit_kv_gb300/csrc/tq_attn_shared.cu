@@ -45,7 +45,7 @@
 //              the levels' bytes; no lookups in shared memory, which the
 //              products keep busy), into the swizzled K and V tiles.
 //   warp 16    bulk copies: the query tiles, then the packed blocks.
-//   warp 17    one thread issues the products.
+//   warp 17    one of its threads issues the products.
 // Every wait is bounded; one that gives up is recorded (tq_device_status).
 #include <cmath>
 
@@ -185,12 +185,52 @@ __host__ __device__ constexpr uint32_t sh_idesc(uint32_t mn) {
     return (1u << 4) | (mn << 16) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
 }
 
-// D (+)= A B, A in tensor memory (rows in lanes, two fp16 a column).
-__device__ __forceinline__ void sh_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+// Products and commits issued by one lane of a warp that runs as a whole:
+// their operands are then uniform across the warp, and cost no instructions to
+// bring into uniform registers.  `lead` is set in the lane that issues.
+__device__ __forceinline__ void sh_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate,
+                                       uint32_t lead) {
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::
-            "r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(lead)
+        : "memory");
+}
+
+// The same with A in tensor memory (rows in lanes, two fp16 a column).
+__device__ __forceinline__ void sh_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate,
+                                          uint32_t lead) {
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(lead)
+        : "memory");
+}
+
+__device__ __forceinline__ void sh_commit(uint32_t bar, uint32_t lead) {
+    asm volatile(
+        "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
+        " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(bar),
+        "r"(lead)
+        : "memory");
+}
+
+__device__ __forceinline__ void tc_st16(uint32_t taddr, const uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+}
+
+__device__ __forceinline__ void tc_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
         : "memory");
 }
 
@@ -212,11 +252,13 @@ __device__ __forceinline__ float sh_ex2(float x) {
     return y;
 }
 
-// (hi, lo) fp16 parts of two floats: x = hi + lo to about 2^-22.
-__device__ __forceinline__ void sh_split(float x0, float x1, uint32_t &hi, uint32_t &lo) {
-    const __half2 h = __floats2half2_rn(x0, x1);
-    const float2 f = __half22float2(h);
-    const __half2 l = __floats2half2_rn(x0 - f.x, x1 - f.y);
+// (hi, lo) fp16 parts of two floats of at most 2^15: hi the ten leading bits after the first, lo what is left of
+// them, x = hi + lo to about 2^-21 (2^-25 where x is below fp16's normal numbers).
+__device__ __forceinline__ void sh_split(float2 x, uint32_t &hi, uint32_t &lo) {
+    const float2 t = make_float2(__uint_as_float(__float_as_uint(x.x) & 0xFFFFE000u),
+                                 __uint_as_float(__float_as_uint(x.y) & 0xFFFFE000u));
+    const float2 r = __fadd2_rn(x, make_float2(-t.x, -t.y));
+    const __half2 h = __floats2half2_rn(t.x, t.y), l = __floats2half2_rn(r.x, r.y);
     hi = *reinterpret_cast<const uint32_t *>(&h);
     lo = *reinterpret_cast<const uint32_t *>(&l);
 }
@@ -318,71 +360,106 @@ __device__ __forceinline__ void dequant_row(const uint32_t (&t)[4], uint32_t blk
     }
 }
 
-// The largest of a row's 128 scores (NaN aside; keys from `valid` on do not count).
-template <bool TAIL>
-__device__ __forceinline__ float row_max(uint32_t s_col, const float *kn, int valid) {
-    float mx = -INFINITY, my = -INFINITY;
+// A row's softmax over a tile of 128 keys.  m: the reference of its exponents
+// (-inf before the first finite score), l: the sum of 2^(s - m).
+struct RowState {
+    float m, l;
+};
+
+// The reference moves up by `up` (a whole number; 0 for rows that stay) or is
+// set: what the row has summed up, the stream's O (of the tiles before, if any)
+// and the `done` keys of this tile whose P is written already are scaled down.
+// Rare: out of line.
+__device__ __noinline__ void move_reference(uint32_t s_col, uint32_t o_col, bool scale_o, int done, float f) {
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");   // P of the keys done
+    if (scale_o) {
 #pragma unroll 1
-    for (int c = 0; c < 128; c += 32) {
-        float s[32];
-        tc_ld32(s_col + c, s);
-        tc_wait_ld();
+        for (int c = 0; c < 128; c += 16) {
+            uint32_t w[16];
+            tc_ld16(o_col + c, w);
+            tc_wait_ld();
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-            const float4 n = reinterpret_cast<const float4 *>(kn + c)[q];
-            float2 a = __fmul2_rn(make_float2(s[4 * q], s[4 * q + 1]), make_float2(n.x, n.y));
-            float2 b = __fmul2_rn(make_float2(s[4 * q + 2], s[4 * q + 3]), make_float2(n.z, n.w));
-            if constexpr (TAIL) {
-                const int at = valid - c - 4 * q;
-                if (at <= 0) a.x = -INFINITY;
-                if (at <= 1) a.y = -INFINITY;
-                if (at <= 2) b.x = -INFINITY;
-                if (at <= 3) b.y = -INFINITY;
-            }
-            mx = fmaxf(mx, fmaxf(a.x, a.y));
-            my = fmaxf(my, fmaxf(b.x, b.y));
+            for (int q = 0; q < 16; ++q) w[q] = __float_as_uint(__uint_as_float(w[q]) * f);
+            tc_st16(o_col + c, w);
         }
     }
-    return fmaxf(mx, my);
+    const __half2 f2 = __float2half2_rn(f);   // (a power of two: exact, or below what P holds)
+#pragma unroll 1
+    for (int c = 0; c < done; c += 16) {
+        uint32_t w[16];
+        tc_ld16(s_col + c, w);
+        tc_wait_ld();
+#pragma unroll
+        for (int q = 0; q < 16; ++q) {
+            const __half2 p = __hmul2(*reinterpret_cast<const __half2 *>(&w[q]), f2);
+            w[q] = *reinterpret_cast<const uint32_t *>(&p);
+        }
+        tc_st16(s_col + c, w);
+    }
 }
 
-// Probabilities 2^(s - mref) of a row's 128 scores, times the value norms as
-// fp16 hi and lo parts over the scores; returns the sum.  (A key from `valid`
-// on has the value norm 0.)
+// The row's scores, 32 keys at a time: P = 2^(s - m) times the value norms, as
+// fp16 hi and lo parts, over the scores.  kn, vn: norms of the tile's keys and
+// values, lv: log2 of the largest value norm.  m is kept above every s + lv - 8,
+// so that P times 2^7 stays below 2^15.  TAIL: only `valid` keys are there
+// (the others have the value norm 0).
 template <bool TAIL>
-__device__ __forceinline__ float row_weights(uint32_t s_col, const float *kn, const float *vn, int valid, float mref) {
+__device__ __forceinline__ void row_tile(RowState &st, uint32_t s_col, uint32_t o_col, bool scale_o, const float *kn,
+                                         const float *vn, float lv, int valid) {
     float2 sum = make_float2(0.f, 0.f);
-    const float2 m2 = make_float2(-mref, -mref);
 #pragma unroll 1
     for (int c = 0; c < 128; c += 32) {
         float s[32];
         tc_ld32(s_col + c, s);
         tc_wait_ld();
-        uint32_t w[32];   // hi parts of the 32 probabilities, then lo parts
+        // no finite score so far: scores are -inf (P 0) or NaN (which stays NaN)
+        float mref = st.m == -INFINITY ? 0.f : st.m;
+        const float2 m2 = make_float2(-mref, -mref);
+        float mx = -INFINITY, my = -INFINITY;
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
             const float4 n = reinterpret_cast<const float4 *>(kn + c)[q];
-            const float4 v = reinterpret_cast<const float4 *>(vn + c)[q];
-            float2 x = __ffma2_rn(make_float2(s[4 * q], s[4 * q + 1]), make_float2(n.x, n.y), m2);
-            float2 y = __ffma2_rn(make_float2(s[4 * q + 2], s[4 * q + 3]), make_float2(n.z, n.w), m2);
+            const float2 x = __ffma2_rn(make_float2(s[4 * q], s[4 * q + 1]), make_float2(n.x, n.y), m2);
+            const float2 y = __ffma2_rn(make_float2(s[4 * q + 2], s[4 * q + 3]), make_float2(n.z, n.w), m2);
+            s[4 * q] = x.x;
+            s[4 * q + 1] = x.y;
+            s[4 * q + 2] = y.x;
+            s[4 * q + 3] = y.y;
             if constexpr (TAIL) {
-                const int at = valid - c - 4 * q;
-                if (at <= 0) x.x = -INFINITY;
-                if (at <= 1) x.y = -INFINITY;
-                if (at <= 2) y.x = -INFINITY;
-                if (at <= 3) y.y = -INFINITY;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (c + 4 * q + e >= valid) s[4 * q + e] = -INFINITY;
             }
-            float2 p = make_float2(sh_ex2(x.x), sh_ex2(x.y)), r = make_float2(sh_ex2(y.x), sh_ex2(y.y));
+            mx = fmaxf(fmaxf(mx, s[4 * q]), s[4 * q + 1]);
+            my = fmaxf(fmaxf(my, s[4 * q + 2]), s[4 * q + 3]);
+        }
+        const float top = fmaxf(mx, my) + lv;   // (above m)
+        const bool set = st.m == -INFINITY && top > -INFINITY;
+        const bool move = set || top > 8.f;
+        if (__any_sync(0xffffffffu, move)) {
+            const float up = move ? ceilf(top) : 0.f;
+            const float f = set || !move ? 1.f : exp2f(-up);   // (unset: nothing has been summed up)
+            move_reference(s_col, o_col, scale_o, c, f);
+            st.l *= f;
+            sum = make_float2(sum.x * f, sum.y * f);
+            if (move) st.m = mref + up;
+#pragma unroll
+            for (int q = 0; q < 32; ++q) s[q] -= up;
+        }
+        uint32_t w[32];   // hi parts of 32 probabilities, then lo parts
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            const float4 v = reinterpret_cast<const float4 *>(vn + c)[q];
+            const float2 p = make_float2(sh_ex2(s[4 * q]), sh_ex2(s[4 * q + 1]));
+            const float2 r = make_float2(sh_ex2(s[4 * q + 2]), sh_ex2(s[4 * q + 3]));
             sum = __fadd2_rn(sum, __fadd2_rn(p, r));
-            p = __fmul2_rn(p, make_float2(v.x, v.y));
-            r = __fmul2_rn(r, make_float2(v.z, v.w));
-            sh_split(p.x, p.y, w[2 * q], w[16 + 2 * q]);
-            sh_split(r.x, r.y, w[2 * q + 1], w[16 + 2 * q + 1]);
+            sh_split(__fmul2_rn(p, make_float2(v.x, v.y)), w[2 * q], w[16 + 2 * q]);
+            sh_split(__fmul2_rn(r, make_float2(v.z, v.w)), w[2 * q + 1], w[16 + 2 * q + 1]);
         }
         sh_st32(s_col + c, w);
     }
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-    return sum.x + sum.y;
+    st.l += sum.x + sum.y;
 }
 
 template <int KB, int VB>
@@ -446,7 +523,6 @@ __global__ void __launch_bounds__(kShThreads, 1) attn_shared_kernel(const __grid
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + S::kSlot);
     asm volatile("griddepcontrol.launch_dependents;");
-    asm volatile("griddepcontrol.wait;" ::: "memory");   // the query tiles come from the prep kernel
 
     // a bounded wait; one that gives up is recorded, and the caller's role makes no further waits
     auto wait = [&](bool &ok, int b, uint32_t parity) {
@@ -460,12 +536,18 @@ __global__ void __launch_bounds__(kShThreads, 1) attn_shared_kernel(const __grid
     if (warp == kShProducer) {
         // ---- copies: lane l takes piece l of a tile (one, or one for each page it meets: 17 at most)
         bool ok = true;
-        if (nt > 0 && lane == 0) {
-            const int n = two ? 4 : 2;
-            const uint8_t *src = a.q + ((int64_t)kvh * p.tiles + qt) * (2 * S::kTile);
-            tc_mbar_expect_tx(bar(kQFull), (uint32_t)(n * S::kTile));
-            for (int i = 0; i < n; ++i) sh_bulk(base_s + i * S::kTile, src + (int64_t)i * S::kTile, S::kTile, bar(kQFull));
-        }
+        // the query tiles come from the prep kernel; the blocks do not, and the first go ahead
+        auto queries = [&]() {
+            asm volatile("griddepcontrol.wait;" ::: "memory");
+            if (nt > 0 && lane == 0) {
+                const int n = two ? 4 : 2;
+                const uint8_t *src = a.q + ((int64_t)kvh * p.tiles + qt) * (2 * S::kTile);
+                tc_mbar_expect_tx(bar(kQFull), (uint32_t)(n * S::kTile));
+                for (int i = 0; i < n; ++i)
+                    sh_bulk(base_s + i * S::kTile, src + (int64_t)i * S::kTile, S::kTile, bar(kQFull));
+            }
+        };
+        if (nt == 0) queries();   // (waits, as every CTA does: who waits for this grid counts on the prep kernel's end)
         for (int i = 0; i < nt && ok; ++i) {
             const int t0 = (tile0 + i) * kShKeys;
             const int end = min(t0 + kShKeys, (len + 7) & ~7);
@@ -495,59 +577,58 @@ __global__ void __launch_bounds__(kShThreads, 1) attn_shared_kernel(const __grid
                 const uint32_t dst = base_s + (kv ? S::kVBlk + s * S::kVBytes : S::kKBlk + s * S::kKBytes);
                 if (n > 0) sh_bulk(dst + (from - t0) * bytes, (kv ? a.v : a.k) + slot * bytes, (uint32_t)(n * bytes), full);
             }
+            if (i == 0) queries();
         }
     } else if (warp == kShMma) {
         // ---- the products: item e is stream e & 1's tile e >> 1 (two) or tile e
-        if (lane == 0) {
-            bool ok = true;
-            const int items = two ? 2 * nt : nt;
-            auto tile_of = [&](int e) { return two ? e >> 1 : e; };
-            auto scores = [&](int e) {
-                const int i = tile_of(e), x = e & 1, st = stage(i);
-                if (!two || x == 0) wait(ok, kKReady + st, (uint32_t)use(i));
-                if (!ok) return;
-                tc_fence_after();
-                const uint32_t d = tmem + 128u * (uint32_t)x, kb = k_at(st), qb = q_at(x);
-                // (rolled: 32 pairs of descriptors would not fit the registers)
-#pragma unroll 1
-                for (int i = 0; i < 16; i += 4) {
-                    const uint32_t off = (uint32_t)((i >> 2) & 1) * 16384u;
-                    const uint64_t qd = sh_desc(qb + (i >> 3) * S::kTile + off, 16, 1024), kd = sh_desc(kb + off, 16, 1024);
+        const uint32_t lead = lane == 0;
+        bool ok = true;
+        const int items = two ? 2 * nt : nt;
+        auto tile_of = [&](int e) { return two ? e >> 1 : e; };
+        auto warp_wait = [&](int b, uint32_t parity) {
+            wait(ok, b, parity);
+            ok = __all_sync(0xffffffffu, ok);
+        };
+        auto scores = [&](int e) {
+            const int i = tile_of(e), x = e & 1, st = stage(i);
+            if (!two || x == 0) warp_wait(kKReady + st, (uint32_t)use(i));
+            if (!ok) return;
+            tc_fence_after();
+            const uint32_t d = tmem + 128u * (uint32_t)x;
+            const uint64_t kd = sh_desc(k_at(st), 16, 1024), qd = sh_desc(q_at(x), 16, 1024);
 #pragma unroll
-                    for (int ks = 0; ks < 4; ++ks) tc_mma(d, qd + 2 * ks, kd + 2 * ks, sh_idesc(0), i + ks > 0 ? 1u : 0u);
-                }
-                tc_commit(bar(kSReady + x));
-                tc_commit(bar(kKFree + st));
-            };
-            auto values = [&](int e) {
-                const int i = tile_of(e), x = e & 1, st = stage(i);
-                if (!two || x == 0) wait(ok, kVReady + st, (uint32_t)use(i));
-                wait(ok, kPReady + x, (uint32_t)(e >> 1));
-                if (!ok) return;
-                tc_fence_after();
-                const uint32_t vb = v_at(st), pa = tmem + 128u * (uint32_t)x;
-                const uint64_t vd = sh_desc(vb, 16384, 1024);
-#pragma unroll 1
-                for (int c = 0; c < 4; ++c) {   // 32 keys: two steps of the hi parts, two of the lo parts
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        sh_mma_ts(tmem + kShColO + 128u * (uint32_t)x, pa + 32u * c + 8u * i,
-                                  vd + (uint64_t)(4096 / 16) * c + (2048 / 16) * (i & 1), sh_idesc(1),
-                                  (e > 1 || c > 0 || i > 0) ? 1u : 0u);
-                }
-                tc_commit(bar(kVFree + st));
-                if (e + 2 >= items) tc_commit(bar(kODone + x));
-            };
-            if (items > 0) wait(ok, kQFull, 0);
-            for (int e = 0; e < 2 && e < items; ++e) scores(e);
-            for (int e = 0; e < items && ok; ++e) {
-                values(e);
-                if (ok && e + 2 < items) scores(e + 2);
+            for (int n = 0; n < 16; ++n) {   // 16 dims at a time: with the hi parts of Q, then the lo parts
+                const uint32_t off = ((n & 7) >> 2) * (16384 / 16) + (n & 3) * (32 / 16);
+                sh_mma(d, qd + off + (n >> 3) * (S::kTile / 16), kd + off, sh_idesc(0), n > 0, lead);
             }
-            // before teardown: every product issued here has completed
-            tc_commit(bar(kDrain));
-            tc_mbar_wait(bar(kDrain), 0u);
+            sh_commit(bar(kSReady + x), lead);
+            sh_commit(bar(kKFree + st), lead);
+        };
+        auto values = [&](int e) {
+            const int i = tile_of(e), x = e & 1, st = stage(i);
+            if (!two || x == 0) warp_wait(kVReady + st, (uint32_t)use(i));
+            warp_wait(kPReady + x, (uint32_t)(e >> 1));
+            if (!ok) return;
+            tc_fence_after();
+            const uint32_t pa = tmem + 128u * (uint32_t)x, d = tmem + kShColO + 128u * (uint32_t)x;
+            const uint64_t vd = sh_desc(v_at(st), 16384, 1024);
+#pragma unroll
+            for (int n = 0; n < 16; ++n)   // 16 keys at a time: of 32, the hi parts, then the lo parts
+                sh_mma_ts(d, pa + 8u * n, vd + (4096 / 16) * (n >> 2) + (2048 / 16) * (n & 1), sh_idesc(1),
+                          e > 1 || n > 0, lead);
+            sh_commit(bar(kVFree + st), lead);
+            if (e + 2 >= items) sh_commit(bar(kODone + x), lead);
+        };
+        if (items > 0) warp_wait(kQFull, 0);
+        for (int e = 0; e < 2 && e < items; ++e) scores(e);
+        for (int e = 0; e < items && ok; ++e) {
+            values(e);
+            if (ok && e + 2 < items) scores(e + 2);
         }
+        // before teardown: every product issued here has completed
+        sh_commit(bar(kDrain), lead);
+        __syncwarp();
+        tc_mbar_wait(bar(kDrain), 0u);
     } else if (warp >= kShValueWarp) {
         // ---- value warps: thread = key of the tile
         const int k = tid - 32 * kShValueWarp;
@@ -608,7 +689,7 @@ __global__ void __launch_bounds__(kShThreads, 1) attn_shared_kernel(const __grid
         const uint32_t lane_t = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
         const uint32_t s_col = lane_t + 128u * (uint32_t)x, o_col = lane_t + kShColO + 128u * (uint32_t)x;
         const int mine = two ? nt : (nt - x + 1) >> 1;
-        float m_ref = -INFINITY, l = 0.f;
+        RowState state = {-INFINITY, 0.f};
         bool ok = true;
         for (int t = 0; t < mine; ++t) {
             const int i = two ? t : 2 * t + x;
@@ -617,37 +698,17 @@ __global__ void __launch_bounds__(kShThreads, 1) attn_shared_kernel(const __grid
             wait(ok, kSReady + x, (uint32_t)t);
             tc_fence_after();
             const int nvalid = len - (tile0 + i) * kShKeys;   // (of 128)
-            const bool tail = nvalid < kShKeys;
-            const float mx = tail ? row_max<true>(s_col, nm, nvalid) : row_max<false>(s_col, nm, kShKeys);
-            const float4 lv = *reinterpret_cast<const float4 *>(nm + 2 * kShKeys);
-            const float top = mx + fmaxf(fmaxf(lv.x, lv.y), fmaxf(lv.z, lv.w));
-            const bool move = top > m_ref + 8.f;
-            const float m_new = move ? top : m_ref;
-            const float factor = move ? (m_ref == -INFINITY ? 0.f : exp2f(m_ref - m_new)) : 1.f;
-            if (t >= 1 && __any_sync(0xffffffffu, move)) {
-                // (the stream's products before this tile's scores have completed)
-#pragma unroll 1
-                for (int c = 0; c < 4; ++c) {
-                    float o[32];
-                    tc_ld32(o_col + 32 * c, o);
-                    tc_wait_ld();
-                    uint32_t w[32];
-#pragma unroll
-                    for (int q = 0; q < 32; ++q) w[q] = __float_as_uint(o[q] * factor);
-                    sh_st32(o_col + 32 * c, w);
-                }
-            }
-            // no finite score so far: scores are -inf (P 0) or NaN (which stays NaN)
-            const float mref = m_new == -INFINITY ? 0.f : m_new;
-            const float sum = tail ? row_weights<true>(s_col, nm, nm + kShKeys, nvalid, mref)
-                                   : row_weights<false>(s_col, nm, nm + kShKeys, kShKeys, mref);
-            l = l * factor + sum;
-            m_ref = m_new;
+            const float4 lv4 = *reinterpret_cast<const float4 *>(nm + 2 * kShKeys);
+            const float lv = fmaxf(fmaxf(lv4.x, lv4.y), fmaxf(lv4.z, lv4.w));
+            // (the stream's products before this tile's scores have completed: O may be scaled)
+            if (nvalid < kShKeys) row_tile<true>(state, s_col, o_col, t > 0, nm, nm + kShKeys, lv, nvalid);
+            else row_tile<false>(state, s_col, o_col, t > 0, nm, nm + kShKeys, lv, kShKeys);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) tc_mbar_arrive(bar(kPReady + x));
         }
-        // ---- this row's partial: maximum, sum, sums of values by dim
+        // ---- this row's partial: reference, sum, sums of values by dim
+        float m_ref = state.m, l = state.l;
         if (mine > 0) wait(ok, kODone + x, 0);
         tc_fence_after();
         const int row = (qt + (two ? x : 0)) * kShRows + r;
