@@ -185,34 +185,22 @@ __host__ __device__ constexpr uint32_t sh_idesc(uint32_t mn) {
     return (1u << 4) | (mn << 16) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
 }
 
-// Products and commits issued by one lane of a warp that runs as a whole:
-// their operands are then uniform across the warp, and cost no instructions to
-// bring into uniform registers.  `lead` is set in the lane that issues.
-__device__ __forceinline__ void sh_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate,
-                                       uint32_t lead) {
+// D (+)= A B, A in tensor memory (rows in lanes, two fp16 a column).
+__device__ __forceinline__ void sh_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
-        "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
-        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(lead)
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::
+            "r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
         : "memory");
 }
 
-// The same with A in tensor memory (rows in lanes, two fp16 a column).
-__device__ __forceinline__ void sh_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate,
-                                          uint32_t lead) {
-    asm volatile(
-        "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
-        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(lead)
-        : "memory");
-}
-
-__device__ __forceinline__ void sh_commit(uint32_t bar, uint32_t lead) {
-    asm volatile(
-        "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
-        " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(bar),
-        "r"(lead)
-        : "memory");
+// One lane of a converged warp.  Products are issued under it, group by group,
+// by a warp that otherwise runs as a whole: their operands are then the same
+// in every lane, and cost no instructions to bring into uniform registers.
+__device__ __forceinline__ bool sh_elect() {
+    uint32_t one;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(one));
+    return one != 0;
 }
 
 __device__ __forceinline__ void tc_st16(uint32_t taddr, const uint32_t (&v)[16]) {
@@ -581,7 +569,6 @@ __global__ void __launch_bounds__(kShThreads, 1) attn_shared_kernel(const __grid
         }
     } else if (warp == kShMma) {
         // ---- the products: item e is stream e & 1's tile e >> 1 (two) or tile e
-        const uint32_t lead = lane == 0;
         bool ok = true;
         const int items = two ? 2 * nt : nt;
         auto tile_of = [&](int e) { return two ? e >> 1 : e; };
@@ -596,13 +583,16 @@ __global__ void __launch_bounds__(kShThreads, 1) attn_shared_kernel(const __grid
             tc_fence_after();
             const uint32_t d = tmem + 128u * (uint32_t)x;
             const uint64_t kd = sh_desc(k_at(st), 16, 1024), qd = sh_desc(q_at(x), 16, 1024);
+            if (sh_elect()) {
 #pragma unroll
-            for (int n = 0; n < 16; ++n) {   // 16 dims at a time: with the hi parts of Q, then the lo parts
-                const uint32_t off = ((n & 7) >> 2) * (16384 / 16) + (n & 3) * (32 / 16);
-                sh_mma(d, qd + off + (n >> 3) * (S::kTile / 16), kd + off, sh_idesc(0), n > 0, lead);
+                for (int n = 0; n < 16; ++n) {   // 16 dims at a time: with the hi parts of Q, then the lo parts
+                    const uint32_t off = ((n & 7) >> 2) * (16384 / 16) + (n & 3) * (32 / 16);
+                    tc_mma(d, qd + off + (n >> 3) * (S::kTile / 16), kd + off, sh_idesc(0), n > 0);
+                }
+                tc_commit(bar(kSReady + x));
+                tc_commit(bar(kKFree + st));
             }
-            sh_commit(bar(kSReady + x), lead);
-            sh_commit(bar(kKFree + st), lead);
+            __syncwarp();
         };
         auto values = [&](int e) {
             const int i = tile_of(e), x = e & 1, st = stage(i);
@@ -612,12 +602,15 @@ __global__ void __launch_bounds__(kShThreads, 1) attn_shared_kernel(const __grid
             tc_fence_after();
             const uint32_t pa = tmem + 128u * (uint32_t)x, d = tmem + kShColO + 128u * (uint32_t)x;
             const uint64_t vd = sh_desc(v_at(st), 16384, 1024);
+            if (sh_elect()) {
 #pragma unroll
-            for (int n = 0; n < 16; ++n)   // 16 keys at a time: of 32, the hi parts, then the lo parts
-                sh_mma_ts(d, pa + 8u * n, vd + (4096 / 16) * (n >> 2) + (2048 / 16) * (n & 1), sh_idesc(1),
-                          e > 1 || n > 0, lead);
-            sh_commit(bar(kVFree + st), lead);
-            if (e + 2 >= items) sh_commit(bar(kODone + x), lead);
+                for (int n = 0; n < 16; ++n)   // 16 keys at a time: of 32, the hi parts, then the lo parts
+                    sh_mma_ts(d, pa + 8u * n, vd + (4096 / 16) * (n >> 2) + (2048 / 16) * (n & 1), sh_idesc(1),
+                              e > 1 || n > 0);
+                tc_commit(bar(kVFree + st));
+                if (e + 2 >= items) tc_commit(bar(kODone + x));
+            }
+            __syncwarp();
         };
         if (items > 0) warp_wait(kQFull, 0);
         for (int e = 0; e < 2 && e < items; ++e) scores(e);
@@ -626,7 +619,7 @@ __global__ void __launch_bounds__(kShThreads, 1) attn_shared_kernel(const __grid
             if (ok && e + 2 < items) scores(e + 2);
         }
         // before teardown: every product issued here has completed
-        sh_commit(bar(kDrain), lead);
+        if (sh_elect()) tc_commit(bar(kDrain));
         __syncwarp();
         tc_mbar_wait(bar(kDrain), 0u);
     } else if (warp >= kShValueWarp) {
