@@ -415,6 +415,24 @@ def test_shared_loud_values_far_from_the_queries(tq):
     c.check(out)
 
 
+@pytest.mark.parametrize("B,P", [(3, 300), (40, 300), (40, 1000)])
+@pytest.mark.parametrize("down", [False, True])
+def test_shared_scores_that_grow(tq, B, P, down):
+    """Key norms that grow (or shrink) along the prefix by four orders of magnitude: the references of the rows'
+    exponents move in every tile, in its first and its second half."""
+    c = Case(B, 8, 1, P, 8, 2, 3, 0, None, seed=7, q_size=0.5)
+    norm = np.exp(np.linspace(-3, 7, P))[::-1 if down else 1]
+    h = codec.fp16_rne(norm)
+    k = c.k_prefix.cpu().numpy()
+    idx, old = codec.unpack_block(k[0, :P], 2)
+    k[0, :P] = codec.pack_block(idx, h, 2)
+    c.k_prefix = torch.from_numpy(k).cuda()
+    c.kp = (c.kp[0] / codec.norm_value(old)[:, None] * codec.norm_value(h)[:, None])[None]
+    args, kw, out = c.args(tq, "f32")
+    tq.tq_attn_decode_shared(*args, **kw)
+    c.check(out)
+
+
 def test_shared_equals_plain_decode(tq):
     """The same tokens as one cache of each sequence: within both calls' tolerances of each other."""
     c = Case(4, 8, 2, 320, 64, 4, 2, 64, [64, 0, 17, 40], seed=9)

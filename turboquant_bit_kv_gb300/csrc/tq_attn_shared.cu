@@ -70,6 +70,7 @@ constexpr int kShValueWarp = kShRowWarps + kShKeyWarps;   // (the first of as ma
 constexpr int kShProducer = kShValueWarp + kShKeyWarps, kShMma = kShProducer + 1;
 constexpr int kShThreads = 32 * (kShMma + 1);
 constexpr uint32_t kShCols = 512, kShColO = 256;
+constexpr int kShNormSlots = 8;
 constexpr int kShNormSlot = (2 * kShKeys + 4) * 4;   // key norms | value norms | four maxima of log2 value norm
 constexpr float kShUp = 128.f;               // P is held times this
 
@@ -84,12 +85,12 @@ enum {
     kKFree = 11,       // [2] the products that read it completed
     kVReady = 13,      // [2]
     kVFree = 15,       // [2]
-    kNReady = 17,      // [4] norms of a tile written
-    kSReady = 21,      // [2] stream's scores in tensor memory
-    kPReady = 23,      // [2] stream's P in their place (4 row warps)
-    kODone = 25,       // [2] stream's last product completed
-    kDrain = 27,
-    kShBars = 28
+    kNReady = 17,      // [8] norms of a tile written
+    kSReady = 25,      // [2] stream's scores in tensor memory
+    kPReady = 27,      // [2] stream's P in their place (4 row warps)
+    kODone = 29,       // [2] stream's last product completed
+    kDrain = 31,
+    kShBars = 32
 };
 
 // Shared memory, from a 1024-byte aligned base.  A KV head's even tiles of
@@ -100,14 +101,14 @@ struct ShSmem {
     static constexpr int kTile = 32768;
     static constexpr int kKBlk = 6 * kTile;                          // packed key blocks, kNK stages
     static constexpr int kKBytes = kShKeys * (2 + 16 * KB), kVBytes = kShKeys * (2 + 16 * VB);
-    static constexpr int kRest = 4 * kShNormSlot + kShBars * 8 + 16 + 1024;
+    static constexpr int kRest = kShNormSlots * kShNormSlot + kShBars * 8 + 16 + 1024;
     // value blocks two tiles ahead (their norms are wanted before the tile's turn), key blocks too where
     // there is room
     static constexpr int kNV = 2;
     static constexpr int kNK = kKBlk + 2 * kKBytes + 2 * kVBytes + kRest <= 232448 ? 2 : 1;
     static constexpr int kVBlk = kKBlk + kNK * kKBytes;
-    static constexpr int kNorm = kVBlk + kNV * kVBytes;              // [4] slots
-    static constexpr int kBars = kNorm + 4 * kShNormSlot;
+    static constexpr int kNorm = kVBlk + kNV * kVBytes;              // [kShNormSlots]
+    static constexpr int kBars = kNorm + kShNormSlots * kShNormSlot;
     static constexpr int kSlot = kBars + kShBars * 8;                // tensor-memory base, failure flag
     static constexpr int kTotal = kSlot + 16 + 1024;
     static_assert(kTotal <= 232448, "shared memory of one CTA");
@@ -245,7 +246,7 @@ __device__ __forceinline__ float sh_ex2(float x) {
 __device__ __forceinline__ void sh_split(float2 x, uint32_t &hi, uint32_t &lo) {
     const float2 t = make_float2(__uint_as_float(__float_as_uint(x.x) & 0xFFFFE000u),
                                  __uint_as_float(__float_as_uint(x.y) & 0xFFFFE000u));
-    const float2 r = __fadd2_rn(x, make_float2(-t.x, -t.y));
+    const float2 r = __ffma2_rn(t, make_float2(-1.f, -1.f), x);   // (exact)
     const __half2 h = __floats2half2_rn(t.x, t.y), l = __floats2half2_rn(r.x, r.y);
     hi = *reinterpret_cast<const uint32_t *>(&h);
     lo = *reinterpret_cast<const uint32_t *>(&l);
@@ -434,17 +435,18 @@ __device__ __forceinline__ void row_tile(RowState &st, uint32_t s_col, uint32_t 
 #pragma unroll
             for (int q = 0; q < 32; ++q) s[q] -= up;
         }
-        uint32_t w[32];   // hi parts of 32 probabilities, then lo parts
+        uint32_t wh[16], wl[16];
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
             const float4 v = reinterpret_cast<const float4 *>(vn + c)[q];
             const float2 p = make_float2(sh_ex2(s[4 * q]), sh_ex2(s[4 * q + 1]));
             const float2 r = make_float2(sh_ex2(s[4 * q + 2]), sh_ex2(s[4 * q + 3]));
             sum = __fadd2_rn(sum, __fadd2_rn(p, r));
-            sh_split(__fmul2_rn(p, make_float2(v.x, v.y)), w[2 * q], w[16 + 2 * q]);
-            sh_split(__fmul2_rn(r, make_float2(v.z, v.w)), w[2 * q + 1], w[16 + 2 * q + 1]);
+            sh_split(__fmul2_rn(p, make_float2(v.x, v.y)), wh[2 * q], wl[2 * q]);
+            sh_split(__fmul2_rn(r, make_float2(v.z, v.w)), wh[2 * q + 1], wl[2 * q + 1]);
         }
-        sh_st32(s_col + c, w);
+        tc_st16(s_col + c, wh);
+        tc_st16(s_col + c + 16, wl);
     }
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
     st.l += sum.x + sum.y;
@@ -495,7 +497,7 @@ __global__ void __launch_bounds__(kShThreads, 1) attn_shared_kernel(const __grid
             tc_mbar_init(bar(kPReady + s), 4);
             tc_mbar_init(bar(kODone + s), 1);
         }
-        for (int s = 0; s < 4; ++s) tc_mbar_init(bar(kNReady + s), kShKeyWarps);
+        for (int s = 0; s < kShNormSlots; ++s) tc_mbar_init(bar(kNReady + s), kShKeyWarps);
         tc_mbar_init(bar(kDrain), 1);
         *fail_s = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -650,10 +652,10 @@ __global__ void __launch_bounds__(kShThreads, 1) attn_shared_kernel(const __grid
             const uint32_t kblk = base_s + S::kKBlk + sk * S::kKBytes + k * (2 + 16 * KB);
             wait(ok, kKFull + sk, (uint32_t)(i / S::kNK));
             wait(ok, kVFull + sv, (uint32_t)(i / S::kNV));
-            if (u >= 1) wait(ok, kKFree + st, (uint32_t)(u - 1));
-            // (and tile i - 4's norms have been read: its P came before the products of tile i - 2)
+            // (the norms of tile i - 8 have been read: the last wait for a stage says that the products of tile
+            // i - 4, or a later one, are done, and P of tile i - 6 came before them)
             const bool live = (tile0 + i) * kShKeys + k < len;
-            float *nm = norms + (i & 3) * (kShNormSlot / 4);
+            float *nm = norms + (i % kShNormSlots) * (kShNormSlot / 4);
             const float kn = __half2float(__ushort_as_half((unsigned short)sh_lds16(kblk)));
             const float vn = __half2float(__ushort_as_half((unsigned short)sh_lds16(
                 base_s + S::kVBlk + sv * S::kVBytes + k * (2 + 16 * VB))));
@@ -666,8 +668,9 @@ __global__ void __launch_bounds__(kShThreads, 1) attn_shared_kernel(const __grid
             __syncwarp();
             if (lane == 0) {
                 tc_mbar_arrive(bar(kVEmpty + sv));
-                tc_mbar_arrive(bar(kNReady + (i & 3)));
+                tc_mbar_arrive(bar(kNReady + i % kShNormSlots));
             }
+            if (u >= 1) wait(ok, kKFree + st, (uint32_t)(u - 1));
             dequant_row<KB>(a.kt, kblk, k_at(st), k);
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
@@ -686,8 +689,8 @@ __global__ void __launch_bounds__(kShThreads, 1) attn_shared_kernel(const __grid
         bool ok = true;
         for (int t = 0; t < mine; ++t) {
             const int i = two ? t : 2 * t + x;
-            const float *nm = norms + (i & 3) * (kShNormSlot / 4);
-            wait(ok, kNReady + (i & 3), (uint32_t)(i >> 2));
+            const float *nm = norms + (i % kShNormSlots) * (kShNormSlot / 4);
+            wait(ok, kNReady + i % kShNormSlots, (uint32_t)(i / kShNormSlots));
             wait(ok, kSReady + x, (uint32_t)t);
             tc_fence_after();
             const int nvalid = len - (tile0 + i) * kShKeys;   // (of 128)
@@ -704,8 +707,10 @@ __global__ void __launch_bounds__(kShThreads, 1) attn_shared_kernel(const __grid
         float m_ref = state.m, l = state.l;
         if (mine > 0) wait(ok, kODone + x, 0);
         tc_fence_after();
-        const int row = (qt + (two ? x : 0)) * kShRows + r;
-        const bool store = row < a.rows;
+        // Rows are put together in shared memory (where the queries were: every product has completed) and
+        // leave as one copy a stream, as far as there are rows.
+        auto rows_sync = [&]() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kShRowWarps) : "memory"); };
+        float *own = reinterpret_cast<float *>(smem) + (two ? x * kShRows + r : r) * kPartialFloats;
         // 32 columns of sums to dims: place -> dim of each 16, the inverse of operand_place
         auto put = [&](float *out, const float (&o)[32]) {
             float d[32];
@@ -717,12 +722,10 @@ __global__ void __launch_bounds__(kShThreads, 1) attn_shared_kernel(const __grid
                 reinterpret_cast<float4 *>(out)[q] = make_float4(d[4 * q], d[4 * q + 1], d[4 * q + 2], d[4 * q + 3]);
         };
         if (!ok) l = __int_as_float(0x7fc00000);   // NaN marks a failed wait
+        rows_sync();
         if (two) {
-            float *out = a.part + ((int64_t)(2 * blockIdx.x + x) * kShRows + r) * kPartialFloats;
-            if (store) {
-                out[0] = m_ref;
-                out[1] = l;
-            }
+            own[0] = m_ref;
+            own[1] = l;
 #pragma unroll 1
             for (int c = 0; c < 128; c += 32) {
                 float o[32];
@@ -732,24 +735,20 @@ __global__ void __launch_bounds__(kShThreads, 1) attn_shared_kernel(const __grid
                 }
 #pragma unroll
                 for (int q = 0; q < 32; ++q) o[q] = mine > 0 ? o[q] * (1.f / kShUp) : 0.f;
-                if (store) put(out + 4 + c, o);
+                put(own + 4 + c, o);
             }
         } else {
-            // both streams' sums of a row lie in its lane: join them, each thread half of the dims (every
-            // product has completed, so the statistics take the query tile's place)
-            auto rows_sync = [&]() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kShRowWarps) : "memory"); };
-            float2 *stat = reinterpret_cast<float2 *>(smem);
-            rows_sync();
+            // both streams' sums of a row lie in its lane: join them, each thread half of the dims
+            float2 *stat = reinterpret_cast<float2 *>(smem + S::kKBlk);   // (the packed blocks' place)
             stat[x * kShRows + r] = make_float2(m_ref, l);
             rows_sync();
             const float2 s0 = stat[r], s1 = stat[kShRows + r];
             const float M = fmaxf(s0.x, s1.x);
             const float f0 = s0.x == -INFINITY ? 0.f : exp2f(s0.x - M), f1 = s1.x == -INFINITY ? 0.f : exp2f(s1.x - M);
-            float *out = a.part + ((int64_t)2 * blockIdx.x * kShRows + r) * kPartialFloats;
-            if (store && x == 0) {
+            if (x == 0) {
                 // (a sum that is not finite, of scores that are not, shows whatever its maximum)
-                out[0] = M;
-                out[1] = (s0.x == -INFINITY ? s0.y : f0 * s0.y) + (s1.x == -INFINITY ? s1.y : f1 * s1.y);
+                own[0] = M;
+                own[1] = (s0.x == -INFINITY ? s0.y : f0 * s0.y) + (s1.x == -INFINITY ? s1.y : f1 * s1.y);
             }
             tc_fence_after();
 #pragma unroll 1
@@ -761,8 +760,21 @@ __global__ void __launch_bounds__(kShThreads, 1) attn_shared_kernel(const __grid
 #pragma unroll
                 for (int q = 0; q < 32; ++q)
                     o[q] = ((nt > 0 ? o[q] * f0 : 0.f) + (nt > 1 ? o1[q] * f1 : 0.f)) * (1.f / kShUp);
-                if (store) put(out + 4 + c, o);
+                put(own + 4 + c, o);
             }
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        rows_sync();
+        const int streams = two ? 2 : 1;
+        if (r == 0 && x < streams) {
+            const int rows = min(kShRows, a.rows - (qt + x) * kShRows);
+            asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(
+                             a.part + (int64_t)(2 * blockIdx.x + x) * kShRows * kPartialFloats),
+                         "r"(base_s + (uint32_t)(x * kShRows * kPartialFloats * 4)),
+                         "r"((uint32_t)(rows * kPartialFloats * 4))
+                         : "memory");
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+            asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");   // (before the memory is given back)
         }
     }
 
@@ -790,19 +802,20 @@ struct MergeArgs {
     uint32_t signs[4];
 };
 
-constexpr int kMergeMaxWarps = 16;
-constexpr int kMergeDepth = 8;   // slots a warp has on their way at once
+constexpr int kMergeWarps = 2;
+constexpr int kMergeDepth = 16;  // slots a warp has on their way at once
 
-// One CTA for one (sequence, query head).  A warp takes every slot of its own
-// turn, a lane four dims of it: the prefix's slots, then the own tokens', each
-// batch's loads issued before the one ahead of it is added up (reading what
-// other SMs have just written costs a round trip through L2).  The warps'
-// states meet in shared memory, and the first turns the output back.
-__global__ void __launch_bounds__(32 * kMergeMaxWarps) attn_shared_merge_kernel(const __grid_constant__ MergeArgs a) {
-    __shared__ __align__(16) float accs[kMergeMaxWarps][kD];
-    __shared__ float ms[kMergeMaxWarps], ls[kMergeMaxWarps];
+// One CTA for one (sequence, query head): 32 slots at a time, the prefix's, then
+// the own tokens'.  Both warps take the maxima and sums of all of them, a lane a
+// slot, and the sums of values of half of them, a lane four dims, all requested
+// at once (reading what other SMs have just written costs a round trip through
+// L2; four warps of eight slots took 0.8 us more on 1792 rows, eight of four 4
+// us); their sums of values meet in shared memory, and the first turns the
+// output back.
+__global__ void __launch_bounds__(32 * kMergeWarps) attn_shared_merge_kernel(const __grid_constant__ MergeArgs a) {
+    __shared__ __align__(16) float accs[kMergeWarps][kD];
     const int b = blockIdx.x / a.Hq, h = blockIdx.x % a.Hq, kvh = h / a.G, g = h % a.G;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const SharedPlan &p = a.plan;
     const int row = b * a.G + g, tile = row / kShRows;
     const bool two = tile < 2 * p.pairs;
@@ -811,92 +824,62 @@ __global__ void __launch_bounds__(32 * kMergeMaxWarps) attn_shared_merge_kernel(
                                   (two ? (tile & 1) * kShRows : 0) + row % kShRows) * kPartialFloats;
     const bool empty = a.seq_lens && a.seq_lens[b] < 0;
     const int before = empty ? 0 : (n < ranges ? n : ranges);
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int64_t j = (int64_t)b * a.Hkv + kvh;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int2 met = __ldcg(a.live + j);
-
-    struct Batch {
-        float4 x[kMergeDepth];
-        float m, l;   // (of slot `lane` of the batch)
+    const int total = before + (empty ? 0 : met.y);
+    const float *own = a.own + ((met.x + j) * a.G + g) * kPartialFloats;
+    auto slot = [&](int s) {
+        return s < before ? part + s * ((int64_t)2 * kShRows * kPartialFloats)
+                          : own + (int64_t)(s - before) * a.G * kPartialFloats;
     };
     float M = -INFINITY, l = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    auto load = [&](Batch &t, const float *base, int64_t step, int from, int slots) {
-        t.m = -INFINITY;
-        t.l = 0.f;
-        const int mine = from + warp + nw * lane;
-        if (lane < kMergeDepth && mine < slots) {
-            t.m = __ldcg(base + mine * step);
-            t.l = __ldcg(base + mine * step + 1);
+    for (int s0 = 0; s0 < total; s0 += 32) {
+        float ms = -INFINITY, ls = 0.f;
+        if (s0 + lane < total) {
+            const float2 v = __ldcg(reinterpret_cast<const float2 *>(slot(s0 + lane)));
+            ms = v.x;
+            ls = v.y;
         }
+        float4 x[kMergeDepth];
 #pragma unroll
         for (int i = 0; i < kMergeDepth; ++i) {
-            const int s = from + warp + nw * i;
-            t.x[i] = s < slots ? __ldcg(reinterpret_cast<const float4 *>(base + s * step + 4) + lane)
-                               : make_float4(0.f, 0.f, 0.f, 0.f);
+            const int s = s0 + warp + kMergeWarps * i;
+            x[i] = s < total ? __ldcg(reinterpret_cast<const float4 *>(slot(s) + 4) + lane) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
-    };
-    auto add = [&](const Batch &t) {
-        float mb = t.m;
+        float Mn = ms;
 #pragma unroll
-        for (int o = 1; o < kMergeDepth; o <<= 1) mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, o));
-        const float Mn = fmaxf(M, __shfl_sync(0xffffffffu, mb, 0));
+        for (int o = 16; o >= 1; o >>= 1) Mn = fmaxf(Mn, __shfl_xor_sync(0xffffffffu, Mn, o));
+        Mn = fmaxf(M, Mn);
         // (a slot without a finite score has the sum 0, or NaN, which shows)
-        const float w = t.m == -INFINITY ? 0.f : exp2f(t.m - Mn);
+        const float w = ms == -INFINITY ? 0.f : exp2f(ms - Mn);
         const float f = M == -INFINITY ? 0.f : exp2f(M - Mn);
-        float lb = t.m == -INFINITY ? t.l : w * t.l;
+        float lb = ms == -INFINITY ? ls : w * ls;
 #pragma unroll
-        for (int o = 1; o < kMergeDepth; o <<= 1) lb += __shfl_xor_sync(0xffffffffu, lb, o);
-        l = (M == -INFINITY ? l : l * f) + __shfl_sync(0xffffffffu, lb, 0);
-        acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+        for (int o = 16; o >= 1; o >>= 1) lb += __shfl_xor_sync(0xffffffffu, lb, o);
+        l = (M == -INFINITY ? l : l * f) + lb;
         M = Mn;
+        acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
 #pragma unroll
         for (int i = 0; i < kMergeDepth; ++i) {
-            const float wi = __shfl_sync(0xffffffffu, w, i);
-            acc = make_float4(fmaf(wi, t.x[i].x, acc.x), fmaf(wi, t.x[i].y, acc.y), fmaf(wi, t.x[i].z, acc.z),
-                              fmaf(wi, t.x[i].w, acc.w));
+            const float wi = __shfl_sync(0xffffffffu, w, warp + kMergeWarps * i);
+            acc = make_float4(fmaf(wi, x[i].x, acc.x), fmaf(wi, x[i].y, acc.y), fmaf(wi, x[i].z, acc.z),
+                              fmaf(wi, x[i].w, acc.w));
         }
-    };
-    const int64_t step = (int64_t)2 * kShRows * kPartialFloats, own_step = (int64_t)a.G * kPartialFloats;
-    const float *own = a.own + ((met.x + j) * a.G + g) * kPartialFloats;
-    const int after = empty ? 0 : met.y, round = nw * kMergeDepth;
-    Batch t, u;
-    load(t, part, step, 0, before);
-    load(u, own, own_step, 0, after);
-    for (int s = round; s < before; s += round) {
-        add(t);
-        load(t, part, step, s, before);
     }
-    add(t);
-    for (int s = round; s < after; s += round) {
-        add(u);
-        load(u, own, own_step, s, after);
-    }
-    add(u);
     reinterpret_cast<float4 *>(accs[warp])[lane] = acc;
-    if (lane == 0) {
-        ms[warp] = M;
-        ls[warp] = l;
-    }
     __syncthreads();
     if (warp) return;
-    M = lane < nw ? ms[lane] : -INFINITY;
-    l = lane < nw ? ls[lane] : 0.f;
-    float Mt = M;
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) Mt = fmaxf(Mt, __shfl_xor_sync(0xffffffffu, Mt, o));
-    const float w = M == -INFINITY ? 0.f : exp2f(M - Mt);
-    float lt = M == -INFINITY ? l : w * l;
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) lt += __shfl_xor_sync(0xffffffffu, lt, o);
+    const float lt = l;
     float v[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int i = 0; i < nw; ++i) {
-        const float wi = __shfl_sync(0xffffffffu, w, i);
+#pragma unroll
+    for (int i = 0; i < kMergeWarps; ++i) {
         const float4 x = reinterpret_cast<const float4 *>(accs[i])[lane];
-        v[0] = fmaf(wi, x.x, v[0]);
-        v[1] = fmaf(wi, x.y, v[1]);
-        v[2] = fmaf(wi, x.z, v[2]);
-        v[3] = fmaf(wi, x.w, v[3]);
+        v[0] += x.x;
+        v[1] += x.y;
+        v[2] += x.z;
+        v[3] += x.w;
     }
     // o = D H (sums / l) / sqrt(128), 0 where nothing was seen (a NaN l, of a failed copy too, shows)
     const bool seen = lt > 0.f || lt != lt;
@@ -1162,13 +1145,9 @@ extern "C" int tq_attn_decode_shared(const void *q, int q_dtype, const uint8_t *
     m.plan = sp;
     m.out_scale = 0.08838834764831845f / vf;
     for (int i = 0; i < 4; ++i) m.signs[i] = signs.w[i];
-    // warps of a merging CTA: enough that the longer part is one batch, 4 to 16
-    const int slots = (int)max64(sp.pairs ? sp.s2 : sp.s1, plan.Smax);
-    int warps = (slots + kMergeDepth - 1) / kMergeDepth;
-    warps = warps < 4 ? 4 : (warps > kMergeMaxWarps ? kMergeMaxWarps : warps);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(B * Hq));
-    cfg.blockDim = dim3(32 * warps);
+    cfg.blockDim = dim3(32 * kMergeWarps);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

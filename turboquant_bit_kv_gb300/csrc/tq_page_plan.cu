@@ -10,10 +10,13 @@
 // table[(c + i) / page] * Hkv * page + (c + i) % page.
 //
 // There is next to nothing to move (16 bytes a token, 24 a request): the call
-// is launch, load latency and two scans.  One CTA does the requests, 1024 at a
-// time, with their pages entered by all its threads; it does the tokens too
-// where there are few (one launch), else a grid of its own does, launched as a
-// programmatic dependent.
+// is launch, load latency and scans.  So every CTA scans all requests, 1024 at a
+// time, and places the tokens of its own range: a page that its request has just
+// taken is known from the scan, and entered by the request's first token in it.
+// Few tokens are one CTA's and one launch.  With more, no CTA may write what
+// another still reads (new_held may be held, new_free_count free_count): a
+// second launch of one CTA, a programmatic dependent that has scanned by the
+// time the first is done, writes those two.
 #include <cstdint>
 
 #include "tq_device.cuh"
@@ -23,9 +26,9 @@ namespace tq {
 namespace {
 
 constexpr int kThreads = 1024;
-constexpr int kTokenThreads = 256;
-// Tokens that the requests' CTA does itself.
-constexpr int64_t kFewTokens = 4096;
+// Tokens of one CTA: up to this many are one launch (measured: TODO), else each
+// CTA takes so many at least.
+constexpr int64_t kFewTokens = 4096, kTokens = 1024;
 
 struct PlanArgs {
     const int32_t *cached, *fresh, *held, *free_pages, *free_count;
@@ -33,8 +36,12 @@ struct PlanArgs {
     int32_t *table, *new_held, *new_count, *seq_lens, *tok_start;
     int64_t *dst, *pos;
     int64_t row, n_tok, most;    // row: of the table; most: tokens a row's pages hold
+    int64_t per;                 // tokens of a CTA
     int B, Hkv, page, max_pages, n_free;
 };
+
+// What a launch writes: kPlace the tokens, pages, lengths and first tokens, kState new_held and new_free_count.
+enum { kPlace = 1, kState = 2 };
 
 // Inclusive sums of x over the CTA's threads, in order, and the sum of all.
 __device__ __forceinline__ int64_t block_scan(int64_t x, int64_t *warps, int64_t &all) {
@@ -58,107 +65,91 @@ __device__ __forceinline__ int64_t block_scan(int64_t x, int64_t *warps, int64_t
     return x + (warp ? before : 0);
 }
 
-// First of the n ascending values that is above x (n if none is).
-template <class T>
-__device__ __forceinline__ int first_above(const T *v, int n, T x) {
-    int lo = 0;
-    while (n > 0) {
-        const int half = n >> 1;
-        if (v[lo + half] <= x) {
-            lo += half + 1;
-            n -= half + 1;
-        } else {
-            n = half;
-        }
-    }
-    return lo;
-}
-
-// Slot and position of token n, token i of request b.
-__device__ __forceinline__ void place(const PlanArgs &a, int64_t n, int b, int64_t i, int64_t c, bool ok) {
-    const int64_t t = c + i, pg = t / a.page;
-    a.dst[n] = ok ? (int64_t)a.table[b * a.row + pg] * a.Hkv * a.page + (t - pg * a.page) : -1;
-    a.pos[n] = (a.pos_start ? a.pos_start[b] : c) + i;
-}
-
-__global__ void __launch_bounds__(kThreads) plan_requests_kernel(const __grid_constant__ PlanArgs a, int tokens_too) {
+template <int WHAT>
+__global__ void __launch_bounds__(kThreads) page_plan_kernel(const __grid_constant__ PlanArgs a) {
     __shared__ int64_t warps[32];
-    __shared__ int64_t last_tok[kThreads], last_page[kThreads];   // past the request's last token / page taken
-    __shared__ int64_t top;
-    __shared__ int32_t held_s[kThreads], ok_s[kThreads], cached_s[kThreads];
+    // of a round's requests: past their last token, cached tokens, pages held (negative: -1 - them, of a refused
+    // one), pages that those before have taken
+    __shared__ int32_t end_s[kThreads], cached_s[kThreads], held_s[kThreads], page_s[kThreads];
+    __shared__ int32_t given;
     asm volatile("griddepcontrol.launch_dependents;");
     const int count = min(max(*a.free_count, 0), a.n_free);
-    int64_t toks = 0, pages = 0, taken = 0;   // before this round's requests; pages: needed, taken: given
-    if (threadIdx.x == 0) a.tok_start[0] = 0;
+    const int64_t lo = (int64_t)blockIdx.x * a.per, hi = min64(lo + a.per, a.n_tok);   // this CTA's tokens
+    int64_t toks = 0, pages = 0;   // of the requests before this round; pages: needed
+    if (threadIdx.x == 0) given = 0;
     for (int b0 = 0; b0 < a.B; b0 += kThreads) {
         const int b = b0 + threadIdx.x;
         const bool live = b < a.B;
         const int32_t c = live ? max(a.cached[b], 0) : 0, m = live ? max(a.fresh[b], 0) : 0;
         const int32_t h = live ? min(max(a.held[b], 0), a.max_pages) : 0;
-        const int64_t total = (int64_t)c + m;
+        const int64_t total = (int64_t)c + m, first = toks;
         int64_t all;
         const int64_t end = toks + block_scan(m, warps, all);
-        const bool fits = total <= a.most && end <= a.n_tok;
-        const int64_t first = toks;
         toks += all;
+        const bool fits = total <= a.most && end <= a.n_tok;
         int64_t need = fits && m > 0 ? (total + a.page - 1) / a.page - h : 0;
         if (need < 0) need = 0;
         const int64_t upto = pages + block_scan(need, warps, all);
-        const bool ok = fits && (need == 0 || upto <= count);
         pages += all;
-        if (!ok) need = 0;
-        last_tok[threadIdx.x] = end;
-        last_page[threadIdx.x] = upto;
-        held_s[threadIdx.x] = h;
-        ok_s[threadIdx.x] = ok;
-        cached_s[threadIdx.x] = c;
-        if (threadIdx.x == 0) top = taken;
-        __syncthreads();
-        // sums only grow: those up to the list's length are the pages taken, the last of them all that are
-        if (upto <= count && (threadIdx.x == kThreads - 1 || last_page[threadIdx.x + 1] > count)) top = upto;
-        if (live) {
-            a.tok_start[b + 1] = (int32_t)min64(end, 0x7FFFFFFF);
-            a.new_held[b] = h + (int32_t)need;
-            a.seq_lens[b] = ok ? (int32_t)total : c;
+        const bool ok = fits && (need == 0 || upto <= count);
+        if (WHAT & kPlace) {
+            end_s[threadIdx.x] = (int32_t)min64(end, 0x7FFFFFFF);
+            cached_s[threadIdx.x] = c;
+            held_s[threadIdx.x] = ok ? h : -1 - h;
+            page_s[threadIdx.x] = ok && need > 0 ? (int32_t)(upto - need) : 0;   // (at most count)
+            if (live && blockIdx.x == 0) {
+                a.tok_start[b + 1] = (int32_t)min64(end, 0x7FFFFFFF);
+                a.seq_lens[b] = ok ? (int32_t)total : c;
+            }
         }
-        __syncthreads();
-        const int64_t before = taken;
-        taken = top;
-        for (int64_t p = before + threadIdx.x; p < taken; p += kThreads) {
-            const int r = first_above(last_page, kThreads, p);
-            a.table[(b0 + r) * a.row + held_s[r] + (p - (r ? last_page[r - 1] : before))] = a.free_pages[count - 1 - p];
+        if (WHAT & kState) {
+            // sums only grow: those up to the list's length are the pages taken, the last of them all that are
+            if (!(WHAT & kPlace) && b0 == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+            if (live) a.new_held[b] = h + (ok ? (int32_t)need : 0);
+            if (ok && need > 0) atomicMax(&given, (int32_t)upto);
         }
-        if (tokens_too) {
+        if (WHAT & kPlace) {
             __syncthreads();
-            const int64_t stop = min64(toks, a.n_tok);
-            for (int64_t n = first + threadIdx.x; n < stop; n += kThreads) {
-                const int r = first_above(last_tok, kThreads, n);
-                place(a, n, b0 + r, n - (r ? last_tok[r - 1] : first), cached_s[r], ok_s[r]);
+            const int64_t from = max64(lo, first), stop = min64(hi, toks);
+            for (int64_t n = from + threadIdx.x; n < stop; n += kThreads) {
+                // the first request that ends past token n
+                int r = 0;
+#pragma unroll
+                for (int half = kThreads / 2; half > 0; half >>= 1)
+                    if (end_s[r + half - 1] <= n) r += half;
+                const int64_t i = n - (r ? end_s[r - 1] : first), base = cached_s[r], t = base + i;
+                const int32_t held = held_s[r];
+                int64_t slot = -1;
+                if (held >= 0) {
+                    const int32_t pg = (int32_t)(t / a.page), off = (int32_t)(t - (int64_t)pg * a.page);
+                    int32_t *row = a.table + (b0 + r) * a.row;
+                    const int32_t *taken = a.free_pages + (count - 1 - page_s[r]) + held;   // entry e: taken[-e]
+                    int32_t id;
+                    if (pg < held) {
+                        id = row[pg];
+                    } else {
+                        id = taken[-pg];
+                        if (off == 0 || i == 0) row[pg] = id;
+                        if (i == 0)
+                            for (int32_t e = held; e < pg; ++e) row[e] = taken[-e];   // (fewer held than cached)
+                    }
+                    slot = (int64_t)id * a.Hkv * a.page + off;
+                }
+                a.dst[n] = slot;
+                a.pos[n] = (a.pos_start ? a.pos_start[b0 + r] : base) + i;
             }
         }
     }
-    if (threadIdx.x == 0) *a.new_count = count - (int32_t)taken;
-    if (tokens_too) {
-        for (int64_t n = toks + threadIdx.x; n < a.n_tok; n += kThreads) {
+    if (WHAT & kPlace) {
+        for (int64_t n = max64(lo, toks) + threadIdx.x; n < hi; n += kThreads) {
             a.dst[n] = -1;
             a.pos[n] = 0;
         }
+        if (threadIdx.x == 0 && blockIdx.x == 0) a.tok_start[0] = 0;
     }
-}
-
-__global__ void __launch_bounds__(kTokenThreads) plan_tokens_kernel(const __grid_constant__ PlanArgs a) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int64_t all = min64(a.tok_start[a.B], a.n_tok);
-    const int64_t step = (int64_t)gridDim.x * kTokenThreads;
-    for (int64_t n = (int64_t)blockIdx.x * kTokenThreads + threadIdx.x; n < a.n_tok; n += step) {
-        if (n >= all) {
-            a.dst[n] = -1;
-            a.pos[n] = 0;
-            continue;
-        }
-        const int b = first_above(a.tok_start + 1, a.B, (int32_t)n);
-        const int64_t c = max(a.cached[b], 0);
-        place(a, n, b, n - a.tok_start[b], c, a.seq_lens[b] == c + a.fresh[b]);
+    if (WHAT & kState) {
+        __syncthreads();
+        if (threadIdx.x == 0) *a.new_count = count - given;
     }
 }
 
@@ -214,18 +205,24 @@ extern "C" int tq_page_plan(const int32_t *cached_lens, const int32_t *fresh_len
     a.n_free = n_free;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const bool few = n_tok <= kFewTokens;
-    plan_requests_kernel<<<1, kThreads, 0, st>>>(a, few ? 1 : 0);
+    // a CTA an SM at most: each scans all requests
+    const int64_t even = (n_tok + sm_count() - 1) / sm_count();
+    a.per = few ? kFewTokens : (even > kTokens ? even : kTokens);
+    if (few) {
+        page_plan_kernel<kPlace | kState><<<1, kThreads, 0, st>>>(a);
+        return launch_status();
+    }
+    page_plan_kernel<kPlace><<<(unsigned)((n_tok + a.per - 1) / a.per), kThreads, 0, st>>>(a);
     const int r = launch_status();
-    if (r != TQ_OK || few) return r;
-    const int64_t blocks = (n_tok + kTokenThreads - 1) / kTokenThreads, most_blocks = (int64_t)sm_count() * 8;
+    if (r != TQ_OK) return r;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(blocks < most_blocks ? blocks : most_blocks));
-    cfg.blockDim = dim3(kTokenThreads);
+    cfg.gridDim = dim3(1);
+    cfg.blockDim = dim3(kThreads);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return launch_status(cudaLaunchKernelEx(&cfg, plan_tokens_kernel, a));
+    return launch_status(cudaLaunchKernelEx(&cfg, page_plan_kernel<kState>, a));
 }
