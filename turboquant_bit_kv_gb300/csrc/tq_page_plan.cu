@@ -26,9 +26,10 @@ namespace tq {
 namespace {
 
 constexpr int kThreads = 1024;
-// Tokens of one CTA: up to this many are one launch (measured: TODO), else each
-// CTA takes so many at least.
-constexpr int64_t kFewTokens = 4096, kTokens = 1024;
+// Up to kFewTokens are one CTA's (64 requests of 1000 tokens: one launch 4.6 us,
+// two 4.7; of 2048: 5.5 and 4.7), else a CTA takes kTokens at least (of 8192:
+// 4.4 us; with 1024 a CTA 4.8, with 2048 6.1).
+constexpr int64_t kFewTokens = 1024, kTokens = 512;
 
 struct PlanArgs {
     const int32_t *cached, *fresh, *held, *free_pages, *free_count;
