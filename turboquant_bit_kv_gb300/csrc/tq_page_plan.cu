@@ -26,7 +26,7 @@ namespace tq {
 namespace {
 
 constexpr int kThreads = 1024;
-// Up to kFewTokens are one CTA's (64 requests of 1000 tokens: one launch 4.6 us,
+// Up to kFewTokens are one CTA's (64 requests of 1000 tokens: one launch 4.3 us,
 // two 4.7; of 2048: 5.5 and 4.7), else a CTA takes kTokens at least (of 8192:
 // 4.4 us; with 1024 a CTA 4.8, with 2048 6.1).
 constexpr int64_t kFewTokens = 1024, kTokens = 512;

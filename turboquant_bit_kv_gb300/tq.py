@@ -672,9 +672,13 @@ def tq_evict_compact(k_blocks, v_blocks, kept, new_lens, T, weights=None, block_
 
 # ---- a serving step over paged caches: page plan, norms with rotary positions, shared-prefix attention
 
-def _ints(t, shape, dtype, what, name):
-    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
-        raise ValueError("%s: %s %s %s expected" % (what, name, str(dtype)[6:], list(shape)))
+def _flat(t, n, dtype, dev, what, name):
+    """Address of a tensor [n] of dtype on device dev."""
+    if t.dtype is not dtype or t.shape != (n,) or not t.is_contiguous():
+        raise ValueError("%s: %s %s [%d] expected" % (what, name, str(dtype)[6:], n))
+    if t.get_device() != dev:
+        raise ValueError("%s: CUDA tensors of one device expected" % what)
+    return t.data_ptr()
 
 
 def tq_page_plan(cached_lens, fresh_lens, held, block_table, free_pages, free_count, page_tokens, Hkv, new_held,
@@ -684,29 +688,22 @@ def tq_page_plan(cached_lens, fresh_lens, held, block_table, free_pages, free_co
     may be strided); free_pages int32 [n], free_count and new_free_count int32
     [1]; tok_start int32 [B + 1]; dst, pos int64 [tokens]; pos_start int64 [B].
     new_held may be held, new_free_count free_count."""
-    what = "tq_page_plan"
-    shape, i32 = block_table.shape, torch.int32
-    if block_table.dtype != i32 or len(shape) != 2 or (shape[1] > 1 and block_table.stride(1) != 1):
+    what, i32, i64 = "tq_page_plan", torch.int32, torch.int64
+    B, most = block_table.shape if block_table.dim() == 2 else (0, 0)
+    if block_table.dtype is not i32 or B == 0 or (most > 1 and block_table.stride(1) != 1):
         raise ValueError("%s: block_table int32 [B, max_pages] expected" % what)
-    B = shape[0]
-    for name, t in (("cached_lens", cached_lens), ("fresh_lens", fresh_lens), ("held", held), ("new_held", new_held),
-                    ("seq_lens", seq_lens)):
-        _ints(t, (B,), i32, what, name)
-    for name, t, n in (("free_count", free_count, 1), ("new_free_count", new_free_count, 1),
-                       ("tok_start", tok_start, B + 1), ("free_pages", free_pages, free_pages.numel())):
-        _ints(t, (n,), i32, what, name)
-    n_tok = dst.numel()
-    _ints(dst, (n_tok,), torch.int64, what, "dst")
-    _ints(pos, (n_tok,), torch.int64, what, "pos")
-    if pos_start is not None:
-        _ints(pos_start, (B,), torch.int64, what, "pos_start")
-    with _on(what, cached_lens, fresh_lens, held, block_table, free_pages, free_count, new_held, new_free_count,
-             seq_lens, tok_start, dst, pos, pos_start):
-        _check(lib().tq_page_plan(cached_lens.data_ptr(), fresh_lens.data_ptr(), _ptr(pos_start), B, Hkv, page_tokens,
-                                  block_table.data_ptr(), block_table.stride(0) if B > 1 else shape[1], shape[1],
-                                  held.data_ptr(), new_held.data_ptr(), free_pages.data_ptr(), free_pages.numel(),
-                                  free_count.data_ptr(), new_free_count.data_ptr(), seq_lens.data_ptr(),
-                                  tok_start.data_ptr(), dst.data_ptr(), pos.data_ptr(), n_tok, _stream(stream)), what)
+    dev, n_tok, n_free = block_table.get_device(), dst.numel(), free_pages.numel()
+    if dev < 0:
+        raise ValueError("%s: CUDA tensors expected" % what)
+    args = (_flat(cached_lens, B, i32, dev, what, "cached_lens"), _flat(fresh_lens, B, i32, dev, what, "fresh_lens"),
+            None if pos_start is None else _flat(pos_start, B, i64, dev, what, "pos_start"), B, Hkv, page_tokens,
+            block_table.data_ptr(), block_table.stride(0) if B > 1 else most, most, _flat(held, B, i32, dev, what, "held"),
+            _flat(new_held, B, i32, dev, what, "new_held"), _flat(free_pages, n_free, i32, dev, what, "free_pages"), n_free,
+            _flat(free_count, 1, i32, dev, what, "free_count"), _flat(new_free_count, 1, i32, dev, what, "new_free_count"),
+            _flat(seq_lens, B, i32, dev, what, "seq_lens"), _flat(tok_start, B + 1, i32, dev, what, "tok_start"),
+            _flat(dst, n_tok, i64, dev, what, "dst"), _flat(pos, n_tok, i64, dev, what, "pos"), n_tok)
+    with _On(dev):
+        _check(lib().tq_page_plan(*args, _stream(stream)), what)
     return seq_lens
 
 
