@@ -153,6 +153,37 @@ def test_page_plan_large(tq):
     assert got[3].tolist() == [8] and got[5].tolist() == [4, 5, 6, 7]
 
 
+@pytest.mark.parametrize("most_new", [3, 2000])
+def test_page_plan_holds_fewer_than_cached(tq, most_new):
+    """Requests that hold fewer pages than their cached tokens fill take those too; requests that hold more than their
+    row has are taken to hold its pages."""
+    rng = np.random.default_rng(most_new)
+    B, page = 30, 16
+    cached, fresh = rng.integers(0, 200, B), rng.integers(0, most_new + 1, B)
+    most = (200 + most_new) // page + 2
+    held = rng.integers(0, -(-cached // page) + 1)
+    held[3], held[4] = most + 5, -2
+    ids = rng.permutation(3 * B * most)
+    table = np.where(np.arange(most) < held[:, None], ids[:B * most].reshape(B, most), -1)
+    total = int(fresh.sum())
+    for count in (2 * B * most, 40):
+        args = (cached, fresh, held, table, ids[B * most:], count, page, 2, total + 9, None)
+        same_plan(plan_call(tq, *args), plan_reference(*args))
+        same_plan(plan_call(tq, *args, in_place=True, stride=1), plan_reference(*args))
+
+
+def test_page_plan_far_pages(tq):
+    """Page numbers whose slots pass 32 bits."""
+    top = 2**31 - 1
+    cached, fresh, page, Hkv = np.array([5, 0]), np.array([200, 3]), 128, 8
+    table = np.full((2, 3), -1)
+    table[0, 0] = top
+    free = np.array([7, top - 1, top - 2])
+    want = plan_reference(cached, fresh, np.array([1, 0]), table, free, 3, page, Hkv, 203, None)
+    assert want[5].max() > 2**40
+    same_plan(plan_call(tq, cached, fresh, [1, 0], table, free, 3, page, Hkv, 203, None), want)
+
+
 # ---------------------------------------------------------------- norms with rotary positions
 
 def norm_reference(x, w, eps, pos, rope):
@@ -200,6 +231,22 @@ def test_norm_rope(tq, dtype, wdtype, kw, n, hq, hkv):
     tq.tq_norm_rope_apply(q, k, w[0], w[1], 1e-6, pos, rope, q, k)
     assert torch.equal(q, qo[:, :hq]) and torch.equal(k, ko)
     assert torch.equal(buf[:, hq + hkv:], before[:, hq + hkv:])
+
+
+def test_norm_rope_far_rows(tq):
+    """Rows past 2^32 bytes and 2^31 elements."""
+    n, hq, hkv = 140000, 112, 16
+    x = torch.empty(n, hq + hkv, 128, dtype=torch.bfloat16, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(1)
+    rows = torch.tensor([0, 1, 65535, 131071, 139999], device="cuda")
+    x.fill_(1.0)
+    x[rows] = torch.randn(5, hq + hkv, 128, generator=g, device="cuda").bfloat16()
+    pos = torch.arange(n, device="cuda")
+    rope = tq.tq_rope_load()
+    qo, ko = torch.empty(n, hq, 128, dtype=x.dtype, device="cuda"), torch.empty(n, hkv, 128, dtype=x.dtype, device="cuda")
+    tq.tq_norm_rope_apply(x[:, :hq], x[:, hq:], None, None, 1e-6, pos, rope, qo, ko)
+    want, tol = norm_reference(x[rows].double().cpu().numpy(), 1.0, float(np.float32(1e-6)), pos[rows][None].cpu().numpy(), rope)
+    check_norm(torch.cat([qo[rows], ko[rows]], 1), want, tol, x.dtype)
 
 
 def test_norm_rope_ranges(tq):
@@ -352,6 +399,26 @@ def run_shared(tq, *a, od="f32", **kw):
 def test_shared_formats(tq, kb, vb):
     run_shared(tq, 3, 8, 2, 300, 77, kb, vb, 0, [77, 0, 12], seed=kb * 10 + vb)
     run_shared(tq, 40, 14, 2, 300, 40, kb, vb, 16, [40 - b for b in range(40)], seed=kb * 10 + vb, qd="f16", od="f16")
+
+
+def test_shared_far_pages(tq):
+    """Pools past 2^32 bytes, the pages in use at their end."""
+    c = Case(5, 8, 1, 300, 70, 4, 4, 64, [70, 0, 64, 3, 33], seed=77, qd="f32")
+    far = 1100000
+    pools = []
+    for pool in (c.k, c.v):
+        big = torch.empty(far + pool.shape[0], *pool.shape[1:], dtype=torch.uint8, device="cuda")
+        assert big.numel() > 2**32
+        big[far:] = pool
+        pools.append(big)
+    c.k = c.k_prefix = pools[0]
+    c.v = c.v_prefix = pools[1]
+    np_ = c.prefix_table.numel()
+    c.full = torch.where(c.full >= 0, c.full + far, c.full)
+    c.prefix_table, c.table = c.full[0, :np_], c.full[:, np_:]
+    args, kw, out = c.args(tq, "f32")
+    tq.tq_attn_decode_shared(*args, **kw)
+    c.check(out)
 
 
 @pytest.mark.parametrize("P", [1, 7, 8, 127, 128, 129, 255, 256, 257, 1000, 4133])
