@@ -57,10 +57,11 @@ struct AttnArgs {
 };
 
 // Place of dim d among an operand tile's columns, where codes of `bits` bits are
-// turned into levels 16 dims at a time in the order that costs least.
+// turned into levels 16 dims (3 bits: 32) at a time in the order that costs least.
 __host__ __device__ inline int operand_place(int d, int bits) {
     const int e = d & 15;
-    return (d & ~15) | (bits == 4 ? e : bits == 3 ? 8 * (e & 1) + (e >> 1) : 4 * (e & 3) + (e >> 2));
+    if (bits == 3) return (d & ~31) | 8 * (d & 3) | 2 * (e >> 2) | ((d >> 4) & 1);
+    return (d & ~15) | (bits == 4 ? e : 4 * (e & 3) + (e >> 2));
 }
 
 __host__ __device__ inline int attn_tiles(int T) { return (T + kTT - 1) / kTT; }

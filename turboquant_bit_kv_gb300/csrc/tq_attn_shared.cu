@@ -269,9 +269,27 @@ __device__ __forceinline__ void levels8(const uint32_t (&t)[4], uint32_t sel, ui
     }
 }
 
-// Levels of 16 dims as eight words of two, in the operand's order: w the code
-// words of those dims (4 bits: two, 3 bits: the low plane's and, in its low
-// half, the high plane's, 2 bits: one).
+// Levels of 32 dims of 3-bit codes, in the operand's order: l0, l1 the low
+// plane's words of dims 0 .. 15 and 16 .. 31, h the high plane's.  Selector j
+// takes dims 4 i + j into its nibbles 2 i and dims 16 + 4 i + j into 2 i + 1: the
+// low plane's bits lie in l0's and l1's bytes i, and the high plane's four
+// nibbles of 16 dims are spread to bytes once for all four selectors.
+__device__ __forceinline__ void levels32(const uint32_t (&t)[4], uint32_t l0, uint32_t l1, uint32_t h, uint32_t (&o)[16]) {
+    const uint32_t p = sh_prmt(h, 0, 0x1100u), q = sh_prmt(h, 0, 0x3322u);
+    const uint32_t u = (p & 0x000F000Fu) | ((p >> 4) & 0x0F000F00u) | ((q << 4) & 0x00F000F0u) | (q & 0xF000F000u);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint32_t b = j < 2 ? l1 << (4 - 2 * j) : l1 >> (2 * j - 4);
+        const uint32_t c = j < 2 ? u << (2 - j) : u >> (j - 2);
+        uint32_t e[4];
+        levels8<3>(t, ((l0 >> (2 * j)) & 0x03030303u) | (b & 0x30303030u) | (c & 0x44444444u), 0, e);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[4 * j + k] = e[k];
+    }
+}
+
+// Levels of 16 dims of 2- or 4-bit codes as eight words of two, in the operand's
+// order: w the code words of those dims (4 bits: two, 2 bits: one).
 template <int BITS>
 __device__ __forceinline__ void levels16(const uint32_t (&t)[4], uint32_t w0, uint32_t w1, uint32_t (&o)[8]) {
     if constexpr (BITS == 4) {
@@ -283,20 +301,6 @@ __device__ __forceinline__ void levels16(const uint32_t (&t)[4], uint32_t w0, ui
             levels8<4>(t, (w ^ flip) & 0x77777777u, w, q);
 #pragma unroll
             for (int k = 0; k < 4; ++k) o[4 * i + k] = q[k];
-        }
-    } else if constexpr (BITS == 3) {
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            // even (odd) dims: the low plane's pairs of bits are nibbles as they are, the high plane's
-            // bits are spread to them
-            uint32_t x = (w1 >> s) & 0x5555u;   // (of the 16 low bits)
-            x = (x | (x << 8)) & 0x00FF00FFu;
-            x = (x | (x << 4)) & 0x05050505u;
-            x = (x | (x << 2)) & 0x11111111u;
-            uint32_t q[4];
-            levels8<3>(t, ((w0 >> (2 * s)) & 0x33333333u) | (x << 2), 0, q);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) o[4 * s + k] = q[k];
         }
     } else {
 #pragma unroll
@@ -327,14 +331,21 @@ __device__ __forceinline__ void dequant_row(const uint32_t (&t)[4], uint32_t blk
         if constexpr (BITS == 3)
             hp = __funnelshift_r(sh_lds32(base + 32 + 4 * g), sh_lds32(base + 36 + 4 * g), sh);
         const uint32_t half = row + (g >> 1) * 16384;
+        uint32_t o[16];
+        if constexpr (BITS == 3) {
+            levels32(t, w[0], w[1], hp, o);
+        } else {
 #pragma unroll
-        for (int a = 0; a < 2; ++a) {
-            uint32_t o[8];
-            levels16<BITS>(t, BITS == 4 ? w[(2 * a) % NW] : w[a % NW], BITS == 4 ? w[(2 * a + 1) % NW] : hp >> (16 * a), o);
-            const uint32_t c = 4 * (g & 1) + 2 * a;
-            sh_sts128(half + ((c ^ (r & 7)) << 4), o[0], o[1], o[2], o[3]);
-            sh_sts128(half + (((c + 1) ^ (r & 7)) << 4), o[4], o[5], o[6], o[7]);
+            for (int a = 0; a < 2; ++a) {
+                uint32_t e[8];
+                levels16<BITS>(t, w[(a * NW / 2) % NW], w[(a * NW / 2 + 1) % NW], e);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) o[8 * a + k] = e[k];
+            }
         }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            sh_sts128(half + ((((uint32_t)(4 * (g & 1) + k)) ^ (r & 7)) << 4), o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
     }
 }
 
@@ -700,12 +711,12 @@ __global__ void __launch_bounds__(kShThreads, 1) attn_shared_kernel(const __grid
         // leave as one copy a stream, as far as there are rows.
         auto rows_sync = [&]() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kShRowWarps) : "memory"); };
         float *own = reinterpret_cast<float *>(smem) + (two ? x * kShRows + r : r) * kPartialFloats;
-        // 32 columns of sums to dims: place -> dim of each 16, the inverse of operand_place
+        // 32 columns of sums to dims: place -> dim, the inverse of operand_place
         auto put = [&](float *out, const float (&o)[32]) {
             float d[32];
 #pragma unroll
             for (int q = 0; q < 32; ++q)
-                d[(q & 16) + (VB == 4 ? (q & 15) : VB == 3 ? 2 * (q & 7) + ((q >> 3) & 1) : 4 * (q & 3) + ((q >> 2) & 3))] = o[q];
+                d[VB == 4 ? q : VB == 3 ? 16 * (q & 1) + 4 * ((q >> 1) & 3) + (q >> 3) : (q & 16) + 4 * (q & 3) + ((q >> 2) & 3)] = o[q];
 #pragma unroll
             for (int q = 0; q < 8; ++q)
                 reinterpret_cast<float4 *>(out)[q] = make_float4(d[4 * q], d[4 * q + 1], d[4 * q + 2], d[4 * q + 3]);
