@@ -643,7 +643,8 @@ int tq_evict_compact(uint8_t *k_blocks, int k_block_bytes, uint8_t *v_blocks, in
  * behind those that it holds; the first for which too few are left, and every
  * later one that needs any, is refused.  Refused are also requests of more
  * tokens than max_pages pages hold, and those whose tokens end past n_tok.  A
- * refused request takes no page and keeps its length.
+ * refused request takes no page and keeps its length; one without new tokens
+ * takes none either.
  *   pos_start       device int64 [B]: position of a request's first new token
  *                   (after an eviction positions run ahead of slots); NULL:
  *                   cached_lens[b].
@@ -736,8 +737,8 @@ size_t tq_attn_shared_workspace_bytes(int B, int Hq, int Hkv, int P, int T);
  * No token at all (empty prefix, no own tokens) gives output 0; NaN and +inf
  * scores give NaN outputs.  Results do not depend on timing.  Errors:
  * TQ_ERR_ARG, TQ_ERR_UNSUPPORTED (turboq8, Hq / Hkv > 8, page_tokens not a
- * multiple of 8, P or T > 2^31 - 8192, B Hq > 2^24), TQ_ERR_ALIGN,
- * TQ_ERR_WORKSPACE, TQ_ERR_CUDA. */
+ * multiple of 8, P or T > 2^31 - 8192, B Hq > 2^24, B Hkv ceil(T / 32) > 2^31
+ * - 1), TQ_ERR_ALIGN, TQ_ERR_WORKSPACE, TQ_ERR_CUDA. */
 int tq_attn_decode_shared(const void *q, int q_dtype, const uint8_t *k_prefix, const uint8_t *v_prefix,
                           const int32_t *prefix_table, int P_cap, int P, const int32_t *prefix_len,
                           const uint8_t *k_blocks, const tq_codebook *kcb, const uint8_t *v_blocks,

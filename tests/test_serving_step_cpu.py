@@ -34,7 +34,8 @@ PLAN_BAD = [(ARG, kw) for kw in (
     dict(cached=None), dict(fresh=None), dict(table=None), dict(held=None), dict(nheld=None), dict(free=None),
     dict(count=None), dict(ncount=None), dict(seq=None), dict(tok=None), dict(dst=None), dict(pos=None), dict(B=0),
     dict(Hkv=0), dict(page=0), dict(most=0), dict(nfree=-1), dict(n=-1), dict(row=9), dict(row=-1), dict(seq=A), dict(tok=B),
-    dict(table=D_), dict(dst=E), dict(pos=F), dict(start=J))] + [(ALIGN, kw) for kw in (
+    dict(table=D_), dict(dst=E), dict(pos=F), dict(start=J),
+    dict(nheld=A), dict(nheld=F), dict(ncount=B), dict(ncount=D_), dict(ncount=E))] + [(ALIGN, kw) for kw in (
         dict(cached=ODD), dict(fresh=ODD), dict(table=ODD), dict(held=ODD), dict(nheld=ODD), dict(free=ODD),
         dict(count=ODD), dict(ncount=ODD), dict(seq=ODD), dict(tok=ODD), dict(dst=ODD), dict(pos=ODD),
         dict(start=ODD))] + [(UNSUPPORTED, kw) for kw in (dict(n=1 << 31), dict(B=(1 << 24) + 1))]
@@ -144,6 +145,27 @@ def test_shared_refusals(lib):  # noqa: F811
         assert _shared(L) == real.TQ_ERR_CUDA and L.fake_launches() == i
         L.fake_fail_at(0)
         assert _shared(L) == 0
+
+
+@pytest.mark.parametrize("B,Hq,Hkv", [(1, 32, 8), (64, 56, 8), (200, 16, 2), (5, 8, 1), (33, 64, 8)])
+def test_shared_workspace_holds_shorter(lib, B, Hq, Hkv):  # noqa: F811
+    """A workspace for P and T tokens is one for fewer, at every number of tiles (the work is cut otherwise for each)."""
+    L = _typed(lib)
+    last = 0
+    for P in (1, 128, *range(129, 90000, 128), 10**6, 2**31 - 8192):
+        n = L.tq_attn_shared_workspace_bytes(B, Hq, Hkv, P, 100)
+        assert n >= last, P
+        last = n
+    assert _shared(L, B=B, Hq=Hq, Hkv=Hkv, P=20 * 128 + 1, P_cap=20 * 128 + 8,
+                   bytes=L.tq_attn_shared_workspace_bytes(B, Hq, Hkv, 21 * 128 + 1, 50)) == 0
+    last = 0
+    for T in (1, 31, 32, 33, 1000, 5000, 10**6, 2**31 - 8192):
+        n = L.tq_attn_shared_workspace_bytes(B, Hq, Hkv, 1000, T)
+        if B * Hkv * -(-T // 32) > 2**31 - 1:   # pieces of 32 tokens are counted in 31 bits: refused
+            assert n == 0
+            continue
+        assert n >= last, T
+        last = n
 
 
 def test_binding_refusals(tq):  # noqa: F811

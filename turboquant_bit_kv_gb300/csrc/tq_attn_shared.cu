@@ -36,17 +36,25 @@
 // the other stream, so one stream's softmax runs while the other's products do.
 //
 // Roles (576 threads, one CTA per SM):
-//   warps 0-3, 4-7  rows of stream 0, 1: a thread a row (its tensor-memory
-//              lane).  The reference of a row's exponents is its largest score
-//              plus the tile's largest value norm (in log2), and moves only
-//              when it is exceeded by more than 8, so O is rarely rescaled and
-//              P times the value norm stays below 2^15 whatever the norms are.
-//   warps 8-11, 12-15  a thread a key, a thread a value: codes to fp16 in registers (byte permutes over
-//              the levels' bytes; no lookups in shared memory, which the
-//              products keep busy), into the swizzled K and V tiles.
+//   warps 0-3, 4-7    rows of stream 0, 1: a thread a row (its tensor-memory
+//       lane), in one pass over its scores.  The reference of a row's exponents
+//       moves only when 32 keys' largest score plus the tile's largest value
+//       norm (in log2) exceeds it by more than 8, so O is rarely rescaled, and P
+//       times the value norm stays below 2^8 (as held, 2^15) whatever the norms
+//       are.
+//   warps 8-11, 12-15    a thread a key, a thread a value: codes to fp16 in
+//       registers (byte permutes over the levels' bytes; no lookups in shared
+//       memory, which the products keep busy), into the swizzled K and V tiles.
+//       The key warps also unpack both norms, which the rows want first.
 //   warp 16    bulk copies: the query tiles, then the packed blocks.
-//   warp 17    one of its threads issues the products.
+//   warp 17    issues the products.
 // Every wait is bounded; one that gives up is recorded (tq_device_status).
+//
+// What bounds it: 256 rows x 128 keys are 4096 cycles of products and take some
+// 6400, because the exponentials and splits of 32768 probabilities (two thirds
+// of the instructions) and the levels of 256 blocks fill the issue slots of four
+// schedulers, and shared memory serves the products and the levels' stores at
+// once.  MEASURED
 #include <cmath>
 
 #include "tq_attn.cuh"
@@ -119,6 +127,7 @@ struct ShSmem {
 // s2 ranges of the prefix each and, with an odd tile, one of 128 in s1 ranges.
 struct SharedPlan {
     int tiles, pairs, odd, s2, s1, per_head, ctas;
+    int most;   // CTAs of no plan for this prefix or a shorter one are more
 };
 
 struct SharedArgs {
@@ -130,7 +139,7 @@ struct SharedArgs {
     int rows, Hkv, P, cap, page;
     SharedPlan plan;
     float k_norm;             // 1 / the key centroids' factor
-    uint32_t kt[4], vt[4];    // bytes of the levels (see levels4)
+    uint32_t kt[4], vt[4];    // bytes of the levels (level_bytes)
     int drop;                 // test hook: the copies' barriers wait for an arrival that never comes
 };
 
@@ -721,7 +730,8 @@ __global__ void __launch_bounds__(kShThreads, 1) attn_shared_kernel(const __grid
             for (int q = 0; q < 8; ++q)
                 reinterpret_cast<float4 *>(out)[q] = make_float4(d[4 * q], d[4 * q + 1], d[4 * q + 2], d[4 * q + 3]);
         };
-        if (!ok) l = __int_as_float(0x7fc00000);   // NaN marks a failed wait
+        // NaN marks a failed wait, of the roles that these rows' numbers come from too
+        if (!ok || *fail_s) l = __int_as_float(0x7fc00000);
         rows_sync();
         if (two) {
             own[0] = m_ref;
@@ -923,7 +933,8 @@ __global__ void __launch_bounds__(32 * kMergeWarps) attn_shared_merge_kernel(con
 
 // Ranges of the prefix: of all counts that give every CTA a tile, the one whose
 // slowest SM is done first, a pair's CTA taking two units a tile, and about
-// three for its start and end.
+// three for its start and end.  The counts tried for a shorter prefix are the
+// first of a longer one's, so the last bounds the CTAs of both.
 SharedPlan shared_plan(int sms, int B, int Hq, int Hkv, int P) {
     SharedPlan p;
     const int64_t rows = (int64_t)B * (Hq / Hkv);
@@ -933,6 +944,7 @@ SharedPlan shared_plan(int sms, int B, int Hq, int Hkv, int P) {
     const int64_t n = ((int64_t)P + kShKeys - 1) / kShKeys;
     int64_t best = INT64_MAX;
     p.s2 = 1;
+    p.most = 0;
     for (int64_t s = 1; s <= n && s <= 2 * (int64_t)sms; ++s) {
         const int64_t ctas = Hkv * (p.pairs * s + (p.pairs ? (s + 1) / 2 : s) * p.odd);
         const int64_t cost = (ctas + sms - 1) / sms * (3 + (p.pairs ? 2 : 1) * ((n + s - 1) / s));
@@ -940,6 +952,7 @@ SharedPlan shared_plan(int sms, int B, int Hq, int Hkv, int P) {
             best = cost;
             p.s2 = (int)s;
         }
+        p.most = (int)ctas;   // (grows with s)
         if (ctas > 4 * (int64_t)sms) break;
     }
     p.s1 = p.pairs ? (p.s2 + 1) / 2 : p.s2;
@@ -953,12 +966,13 @@ int64_t most_workers(int B, int Hkv, int T) {
 }
 
 // Workspace: the prefix's partials | the own tokens' [W + B Hkv][G][132] | query fragments [B Hkv] | query tiles |
-// segments' workers [B Hkv][2], in floats.
+// segments' workers [B Hkv][2], in floats.  Room for p.most CTAs: what holds a
+// prefix holds every shorter one.
 struct Layout {
     int64_t own, frag, tiles, live, floats;
     Layout(const SharedPlan &p, int B, int Hq, int Hkv, int64_t W) {
         const int64_t segs = (int64_t)B * Hkv;
-        own = (int64_t)p.ctas * 2 * kShRows * kPartialFloats;
+        own = (int64_t)p.most * 2 * kShRows * kPartialFloats;
         frag = own + (W + segs) * (Hq / Hkv) * kPartialFloats;
         tiles = (frag + segs * kFragWords + 3) & ~(int64_t)3;
         live = tiles + (int64_t)Hkv * p.tiles * (2 * 32768 / 4);
@@ -1062,12 +1076,12 @@ extern "C" int tq_attn_decode_shared(const void *q, int q_dtype, const uint8_t *
         !aligned(k_blocks, 16) || !aligned(v_blocks, 16) || !aligned(out, 16) || !aligned(workspace, 16) ||
         !aligned(prefix_table, 4) || !aligned(prefix_len, 4) || !aligned(block_table, 4) || !aligned(seq_lens, 4))
         return TQ_ERR_ALIGN;
-    if (workspace_bytes < tq_attn_shared_workspace_bytes(B, Hq, Hkv, P, T)) return TQ_ERR_WORKSPACE;
+    const SharedPlan sp = shared_plan(sm_count(), B, Hq, Hkv, P);
+    const Layout at(sp, B, Hq, Hkv, most_workers(B, Hkv, T));
+    if (workspace_bytes < (size_t)at.floats * sizeof(float)) return TQ_ERR_WORKSPACE;
 
     const int kb = kcb->bits, vb = vcb->bits, G = Hq / Hkv;
-    const SharedPlan sp = shared_plan(sm_count(), B, Hq, Hkv, P);
     MmaPlan plan = mma_plan(B, Hq, Hkv, T, kb, vb, false, G);
-    const Layout at(sp, B, Hq, Hkv, most_workers(B, Hkv, T));
     float *ws = static_cast<float *>(workspace);
     plan.frag_off = at.frag - at.own;
     const float kf = attn_centroid_factor(kcb), vf = attn_centroid_factor(vcb);

@@ -175,6 +175,8 @@ extern "C" int tq_page_plan(const int32_t *cached_lens, const int32_t *fresh_len
     for (const void *o : out)
         for (const void *i : in)
             if (o && o == i) return TQ_ERR_ARG;
+    for (const void *i : in)
+        if (i && ((i == new_held && i != held) || (i == new_free_count && i != free_count))) return TQ_ERR_ARG;
     if (n_tok > 0x7FFFFFFF || B > (1 << 24)) return TQ_ERR_UNSUPPORTED;
     if (!aligned(cached_lens, 4) || !aligned(fresh_lens, 4) || !aligned(block_table, 4) || !aligned(held, 4) ||
         !aligned(new_held, 4) || !aligned(free_pages, 4) || !aligned(free_count, 4) || !aligned(new_free_count, 4) ||
