@@ -13,9 +13,11 @@
 // keys, so that the sines of a thread's 8 pairs are worked out once for all of
 // them.  All its heads are requested at once, each thread's elements into a place
 // of its own in shared memory: 192 KB an SM on their way, and no registers held
-// for them.  HBM bounds it: 16411 tokens x 40 heads (336 MB) in 53.8 us, 0.92 of
+// for them.  HBM bounds it: 16411 tokens x 40 heads (336 MB) in 53.3 us, 0.93 of
 // the measured copy rate (requested into registers 63.8 us at 16 warps an SM;
-// sixteen threads a row, which need fewer, 78).
+// sixteen threads a row, which need fewer, 78).  Blocks are small and take the
+// memory that their heads need, so that a few thousand tokens are one even wave:
+// 2049 tokens x 32 heads 8.8 us, with blocks of 256 threads 11.0, of 64 9.0.
 #include <cmath>
 #include <type_traits>
 
@@ -27,7 +29,7 @@
 namespace tq {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 
 struct NormRopeArgs {
     const uint8_t *x[2];                             // queries, keys
@@ -71,7 +73,7 @@ __device__ __forceinline__ float weight_at(const void *w, int dtype, int e) {
     return __half2float(static_cast<const __half *>(w)[e]);
 }
 
-// Heads of a group: as many as 64 KB hold for a block.
+// Heads of a group: as many as 32 KB hold for a block.
 template <int DT>
 __host__ __device__ constexpr int heads_walked() {
     return DT == TQ_F32 ? 4 : 8;
@@ -89,8 +91,8 @@ __device__ __forceinline__ void walk_heads(Step step) {
 // Thread (token, group of heads, chunk c of 8): the row's 16 elements of chunk c
 // are two runs of 8, at elements e0 and e1.
 template <int DT, bool HALF>
-__global__ void __launch_bounds__(kThreads, 3) norm_rope_kernel(const __grid_constant__ tq_rope rope,
-                                                             const __grid_constant__ NormRopeArgs a) {
+__global__ void __launch_bounds__(kThreads, 6) norm_rope_kernel(const __grid_constant__ tq_rope rope,
+                                                                const __grid_constant__ NormRopeArgs a) {
     constexpr int NV = Elem<DT>::kVecs, ES = DT == TQ_F32 ? 4 : 2;
     // weights of the 16 elements of each chunk, four at a time side by side
     __shared__ float4 weight[2][4][8];
@@ -219,10 +221,11 @@ __global__ void __launch_bounds__(kThreads, 3) norm_rope_kernel(const __grid_con
 
 template <int DT, bool HALF>
 int launch_style(const tq_rope &rope, const NormRopeArgs &a, unsigned grid, cudaStream_t st) {
-    constexpr int smem = heads_walked<DT>() * 2 * Elem<DT>::kVecs * 16 * kThreads;
+    constexpr int each = 2 * Elem<DT>::kVecs * 16 * kThreads;
     static int done[64] = {0};
-    if (set_smem_limit((const void *)norm_rope_kernel<DT, HALF>, smem, done) != TQ_OK) return TQ_ERR_CUDA;
-    norm_rope_kernel<DT, HALF><<<grid, kThreads, smem, st>>>(rope, a);
+    if (set_smem_limit((const void *)norm_rope_kernel<DT, HALF>, heads_walked<DT>() * each, done) != TQ_OK)
+        return TQ_ERR_CUDA;
+    norm_rope_kernel<DT, HALF><<<grid, kThreads, a.walk * each, st>>>(rope, a);
     return launch_status();
 }
 
@@ -285,7 +288,8 @@ extern "C" int tq_norm_rope_apply(const void *q, int q_heads, int64_t q_tok_stri
     a.weight_dtype = weight_dtype;
     a.eps = eps;
     // heads of a group: with few tokens every head has threads of its own; once the groups fill the
-    // GPU (128 per SM; on 2049 tokens x 32 heads 11.1 us, with 256 11.9, with 64 12.3) they walk as many heads as a block holds
+    // GPU (128 per SM; on 2049 tokens x 32 heads 8.8 us, with 256 10.6, with 64 10.5) they walk as many
+    // heads as a block holds
     int walk = 1;
     const int most = dtype == TQ_F32 ? heads_walked<TQ_F32>() : heads_walked<TQ_BF16>();
     while (walk < most && n_tok * ((int64_t)q_heads + k_heads) > (int64_t)sm_count() * 128 * walk) walk *= 2;
