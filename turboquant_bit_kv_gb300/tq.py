@@ -672,13 +672,15 @@ def tq_evict_compact(k_blocks, v_blocks, kept, new_lens, T, weights=None, block_
 
 # ---- a serving step over paged caches: page plan, norms with rotary positions, shared-prefix attention
 
-def _flat(t, n, dtype, dev, what, name):
-    """Address of a tensor [n] of dtype on device dev."""
-    if t.dtype is not dtype or t.shape != (n,) or not t.is_contiguous():
-        raise ValueError("%s: %s %s [%d] expected" % (what, name, str(dtype)[6:], n))
-    if t.get_device() != dev:
-        raise ValueError("%s: CUDA tensors of one device expected" % what)
-    return t.data_ptr()
+def _launch(what, dev, stream, args):
+    """The library's function `what` on args and the stream, with device dev current."""
+    if stream is None and _raw_stream is not None and dev == torch.cuda.current_device():
+        status = getattr(lib(), what)(*args, _raw_stream(dev))
+    else:
+        with _On(dev):
+            status = getattr(lib(), what)(*args, _stream(stream))
+    if status != TQ_OK:
+        raise TQError(status, what)
 
 
 def tq_page_plan(cached_lens, fresh_lens, held, block_table, free_pages, free_count, page_tokens, Hkv, new_held,
@@ -692,18 +694,27 @@ def tq_page_plan(cached_lens, fresh_lens, held, block_table, free_pages, free_co
     B, most = block_table.shape if block_table.dim() == 2 else (0, 0)
     if block_table.dtype is not i32 or B == 0 or (most > 1 and block_table.stride(1) != 1):
         raise ValueError("%s: block_table int32 [B, max_pages] expected" % what)
-    dev, n_tok, n_free = block_table.get_device(), dst.numel(), free_pages.numel()
+    dev, n_tok, n_free, each, one = block_table.get_device(), dst.numel(), free_pages.numel(), (B,), (1,)
     if dev < 0:
         raise ValueError("%s: CUDA tensors expected" % what)
-    args = (_flat(cached_lens, B, i32, dev, what, "cached_lens"), _flat(fresh_lens, B, i32, dev, what, "fresh_lens"),
-            None if pos_start is None else _flat(pos_start, B, i64, dev, what, "pos_start"), B, Hkv, page_tokens,
-            block_table.data_ptr(), block_table.stride(0) if B > 1 else most, most, _flat(held, B, i32, dev, what, "held"),
-            _flat(new_held, B, i32, dev, what, "new_held"), _flat(free_pages, n_free, i32, dev, what, "free_pages"), n_free,
-            _flat(free_count, 1, i32, dev, what, "free_count"), _flat(new_free_count, 1, i32, dev, what, "new_free_count"),
-            _flat(seq_lens, B, i32, dev, what, "seq_lens"), _flat(tok_start, B + 1, i32, dev, what, "tok_start"),
-            _flat(dst, n_tok, i64, dev, what, "dst"), _flat(pos, n_tok, i64, dev, what, "pos"), n_tok)
-    with _On(dev):
-        _check(lib().tq_page_plan(*args, _stream(stream)), what)
+    at = []
+    for t, shape, dtype in ((cached_lens, each, i32), (fresh_lens, each, i32), (held, each, i32), (new_held, each, i32),
+                            (free_pages, (n_free,), i32), (free_count, one, i32), (new_free_count, one, i32),
+                            (seq_lens, each, i32), (tok_start, (B + 1,), i32), (dst, (n_tok,), i64),
+                            (pos, (n_tok,), i64), (pos_start, each, i64)):
+        if t is None and len(at) == 11:   # (pos_start)
+            at.append(None)
+            break
+        if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+            name = ("cached_lens", "fresh_lens", "held", "new_held", "free_pages", "free_count", "new_free_count",
+                    "seq_lens", "tok_start", "dst", "pos", "pos_start")[len(at)]
+            raise ValueError("%s: %s %s %s expected" % (what, name, str(dtype)[6:], list(shape)))
+        if t.get_device() != dev:
+            raise ValueError("%s: CUDA tensors of one device expected" % what)
+        at.append(t.data_ptr())
+    _launch(what, dev, stream, (at[0], at[1], at[11], B, Hkv, page_tokens, block_table.data_ptr(),
+                                block_table.stride(0) if B > 1 else most, most, at[2], at[3], at[4], n_free, at[5],
+                                at[6], at[7], at[8], at[9], at[10], n_tok))
     return seq_lens
 
 
@@ -715,32 +726,43 @@ def tq_norm_rope_apply(q, k, q_weight, k_weight, eps, pos, rope, q_out, k_out, s
     what = "tq_norm_rope_apply"
     x = q if q is not None else k
     _need(x is not None, "tq_norm_rope_apply: no rows")
-    n, args = x.shape[0], []
+    n, dtype, dev, args = x.shape[0], x.dtype, x.get_device(), []
     for rows, out in ((q, q_out), (k, k_out)):
         if rows is None or out is None:
             if rows is not None or out is not None:
                 raise ValueError("tq_norm_rope_apply: rows and their output come together")
             args.append((None, 0, 0, 0, None, 0, 0))
             continue
-        m, heads, st, sh = _heads(rows, what)
-        mo, oheads, ot, oh = _heads(out, what)
-        if m != n or mo != n or oheads != heads or rows.dtype != x.dtype or out.dtype != x.dtype:
+        shape, stride, to = rows.shape, rows.stride(), out.stride()
+        if len(shape) != 3 or shape[2] != 128 or stride[2] != 1:
+            raise ValueError("tq_norm_rope_apply: [tokens, heads, 128] expected")
+        if shape[0] != n or out.shape != shape or to[2] != 1 or rows.dtype is not dtype or out.dtype is not dtype:
             raise ValueError("tq_norm_rope_apply: rows of one length and dtype, outputs of their shapes expected")
-        args.append((rows.data_ptr(), heads, st, sh, out.data_ptr(), ot, oh))
-    wd = None
+        if rows.get_device() != dev or out.get_device() != dev:
+            raise ValueError("tq_norm_rope_apply: tensors on different devices")
+        args.append((rows.data_ptr(), shape[1], stride[0], stride[1], out.data_ptr(), to[0], to[1]))
+    wd, weights = None, []
     for w in (q_weight, k_weight):
-        if w is not None:
-            if w.shape != (128,) or not w.is_contiguous() or (wd is not None and w.dtype != wd):
-                raise ValueError("tq_norm_rope_apply: weights [128] of one dtype expected")
-            wd = w.dtype
-    w = q_weight if q_weight is not None else k_weight
-    turn = rope is not None
-    pa = _axis_stride(pos, rope, n, what) if turn else 0
+        if w is None:
+            weights.append(None)
+            continue
+        if (w.shape != (128,) or not w.is_contiguous() or w.get_device() != dev or
+                (wd is not None and w.dtype is not wd)):
+            raise ValueError("tq_norm_rope_apply: weights [128] of one dtype, on the rows' device, expected")
+        wd = w.dtype
+        weights.append(w.data_ptr())
+    pp = pa = None
+    if rope is not None:
+        pp, pa = pos.data_ptr(), _axis_stride(pos, rope, n, what)
+        if pos.get_device() != dev:
+            raise ValueError("tq_norm_rope_apply: tensors on different devices")
+    if dev < 0:
+        raise ValueError("tq_norm_rope_apply: CUDA tensors expected")
+    if dtype not in _DT or (wd is not None and wd not in _DT):
+        raise TypeError("unsupported dtype %s" % (wd if dtype in _DT else dtype))
     (qp, qh, qt, qs, qo, qot, qoh), (kp, kh, kt, ks, ko, kot, koh) = args
-    with _on(what, q, k, q_out, k_out, q_weight, k_weight, pos if turn else None):
-        _check(lib().tq_norm_rope_apply(qp, qh, qt, qs, kp, kh, kt, ks, _dtype(x), n, _ptr(q_weight), _ptr(k_weight),
-                                        TQ_F32 if w is None else _dtype(w), eps, pos.data_ptr() if turn else None, pa,
-                                        rope if turn else None, qo, qot, qoh, ko, kot, koh, _stream(stream)), what)
+    _launch(what, dev, stream, (qp, qh, qt, qs, kp, kh, kt, ks, _DT[dtype], n, weights[0], weights[1],
+                                TQ_F32 if wd is None else _DT[wd], eps, pp, pa or 0, rope, qo, qot, qoh, ko, kot, koh))
 
 
 def tq_attn_shared_workspace_bytes(B, Hq, Hkv, P, T):
@@ -793,12 +815,15 @@ def tq_attn_decode_shared(q, k_prefix, v_prefix, k_blocks, kcb, v_blocks, vcb, o
         _lens(seq_lens, B, what)
     if prefix_len is not None:
         _lens(prefix_len, 1, what)
-    with _on(what, q, k_prefix, v_prefix, k_blocks, v_blocks, out, workspace, prefix_len, prefix_table, seq_lens,
-             block_table):
-        _check(lib().tq_attn_decode_shared(q.data_ptr(), _dtype(q), k_prefix.data_ptr(), v_prefix.data_ptr(),
-                                           _ptr(prefix_table), P_cap, P, _ptr(prefix_len), k_blocks.data_ptr(), kcb,
-                                           v_blocks.data_ptr(), vcb, _ptr(block_table), row, pages, unit,
-                                           _ptr(seq_lens), B, Hq, Hkv, unit, T, scale, signs, out.data_ptr(),
-                                           _dtype(out), workspace.data_ptr(),
-                                           workspace.numel() * workspace.element_size(), _stream(stream)), what)
+    dev = q.get_device()
+    for t in (k_prefix, v_prefix, k_blocks, v_blocks, out, workspace, prefix_len, prefix_table, seq_lens, block_table):
+        if t is not None and t.get_device() != dev:
+            raise ValueError("%s: tensors on different devices" % what)
+    if dev < 0:
+        raise ValueError("%s: CUDA tensors expected" % what)
+    _launch(what, dev, stream, (q.data_ptr(), _dtype(q), k_prefix.data_ptr(), v_prefix.data_ptr(), _ptr(prefix_table),
+                                P_cap, P, _ptr(prefix_len), k_blocks.data_ptr(), kcb, v_blocks.data_ptr(), vcb,
+                                _ptr(block_table), row, pages, unit, _ptr(seq_lens), B, Hq, Hkv, unit, T, scale, signs,
+                                out.data_ptr(), _dtype(out), workspace.data_ptr(),
+                                workspace.numel() * workspace.element_size()))
     return out
