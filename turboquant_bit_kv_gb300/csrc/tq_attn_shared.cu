@@ -15,7 +15,11 @@
 // values of its softmax, and those join exactly.
 //
 // Four launches, chained as programmatic dependents: query prep (rotated once,
-// as operand tiles and as fragments), prefix, own tokens, merge.
+// as operand tiles and as fragments), own tokens, prefix, merge.  The prefix
+// comes second because its start (tensor memory, the first blocks and their
+// levels) needs nothing of the others and goes on while the own tokens end; the
+// other way round 17 sequences behind 10007 tokens take 44.0 us, so 42.2 (64 behind
+// 32769: 81.9 and 81.3).
 //
 // The prefix kernel.  A CTA takes 256 query rows (two tiles of 128, one
 // stream each) or, where a KV head has an odd tile, 128 (both streams take that
@@ -51,10 +55,12 @@
 // Every wait is bounded; one that gives up is recorded (tq_device_status).
 //
 // What bounds it: 256 rows x 128 keys are 4096 cycles of products and take some
-// 6400, because the exponentials and splits of 32768 probabilities (two thirds
-// of the instructions) and the levels of 256 blocks fill the issue slots of four
-// schedulers, and shared memory serves the products and the levels' stores at
-// once.  MEASURED
+// 6400: a stream's scores, softmax and values follow one another, a row's 128
+// keys take its thread 2300 to 3000 cycles (two thirds of all instructions; the
+// levels of 256 blocks are the rest), and shared memory serves the products and
+// the levels' stores at once.  64 sequences of 28/4 heads behind 32769 tokens of
+// 3 bits: 63 us of the call's 81, the tensor pipe active for 51 % of them, 40 %
+// of the issue slots used.
 #include <cmath>
 
 #include "tq_attn.cuh"
@@ -535,7 +541,8 @@ __global__ void __launch_bounds__(kShThreads, 1) attn_shared_kernel(const __grid
     if (warp == kShProducer) {
         // ---- copies: lane l takes piece l of a tile (one, or one for each page it meets: 17 at most)
         bool ok = true;
-        // the query tiles come from the prep kernel; the blocks do not, and the first go ahead
+        // the query tiles come from the prep kernel (which the own tokens' has waited for); the blocks do not,
+        // and the first go ahead
         auto queries = [&]() {
             asm volatile("griddepcontrol.wait;" ::: "memory");
             if (nt > 0 && lane == 0) {
@@ -546,7 +553,7 @@ __global__ void __launch_bounds__(kShThreads, 1) attn_shared_kernel(const __grid
                     sh_bulk(base_s + i * S::kTile, src + (int64_t)i * S::kTile, S::kTile, bar(kQFull));
             }
         };
-        if (nt == 0) queries();   // (waits, as every CTA does: who waits for this grid counts on the prep kernel's end)
+        if (nt == 0) queries();   // (waits, as every CTA does: who waits for this grid counts on the end of those before)
         for (int i = 0; i < nt && ok; ++i) {
             const int t0 = (tile0 + i) * kShKeys;
             const int end = min(t0 + kShKeys, (len + 7) & ~7);
@@ -1136,12 +1143,12 @@ extern "C" int tq_attn_decode_shared(const void *q, int q_dtype, const uint8_t *
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     int r = launch_attn_prep_mma(a, plan, 0, st);
     if (r != TQ_OK) return r;
-    r = kb == 2 ? launch_shared_v<2>(s, vb, st) : kb == 3 ? launch_shared_v<3>(s, vb, st) : launch_shared_v<4>(s, vb, st);
-    if (r != TQ_OK) return r;
     const int nt = G <= 4 ? 1 : 2;
     r = kb == 2 ? launch_attn_mma_scores_k2(a, plan, vb, nt, paged, st)
                 : kb == 3 ? launch_attn_mma_scores_k3(a, plan, vb, nt, paged, st)
                           : launch_attn_mma_scores_k4(a, plan, vb, nt, paged, st);
+    if (r != TQ_OK) return r;
+    r = kb == 2 ? launch_shared_v<2>(s, vb, st) : kb == 3 ? launch_shared_v<3>(s, vb, st) : launch_shared_v<4>(s, vb, st);
     if (r != TQ_OK) return r;
 
     MergeArgs m = {};
