@@ -50,7 +50,9 @@ def test_plan_refusals(lib, want, kw):  # noqa: F811
 
 def test_plan_launches(lib):  # noqa: F811
     L = _typed(lib)
-    for kw, n in ((dict(), 1), (dict(n=0, dst=None, pos=None), 1), (dict(nfree=0, free=None), 1), (dict(n=100000), 2),
+    for kw, n in ((dict(), 1), (dict(n=0, dst=None, pos=None), 1), (dict(nfree=0, free=None), 1), (dict(n=100000), 2), (dict(n=100000, nheld=P(11 << 20)), 2),
+                  (dict(n=100000, ncount=P(11 << 20)), 2),
+                  (dict(n=100000, nheld=P(11 << 20), ncount=P(12 << 20)), 1),
                   (dict(B=1, row=0), 1), (dict(nheld=I, dst=D_, held=J, pos=C, table=A, cached=H, tok=E, free=G, seq=B,
                                                fresh=F, count=P(11 << 20), ncount=P(12 << 20)), 1)):
         L.fake_reset()
