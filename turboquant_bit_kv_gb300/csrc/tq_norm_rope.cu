@@ -11,13 +11,18 @@
 // Eight threads hold a head's row (16 elements each): three shuffles add its
 // squares up.  A group of eight takes up to eight heads of one token, queries or
 // keys, so that the sines of a thread's 8 pairs are worked out once for all of
-// them.  All its heads are requested at once, each thread's elements into a place
-// of its own in shared memory: 192 KB an SM on their way, and no registers held
-// for them.  HBM bounds it: 16411 tokens x 40 heads (336 MB) in 53.3 us, 0.93 of
-// the measured copy rate (requested into registers 63.8 us at 16 warps an SM;
+// them.  All its heads are requested at once into shared memory: 192 KB an SM on
+// their way, and no registers held for them.  A row is requested as it lies, 128
+// bytes by the eight threads at a time, whichever of them needs which (a thread's
+// own elements are 32 bytes apart or more where they are float32 or adjacent
+// pairs: half of each sector, twice; 16411 tokens x 40 heads 71 us in bf16 and
+// 141 in float32).  float32 rows leave the same way (101 us, as the threads hold
+// them 102 to 108; bf16 54, through shared memory 55.5).
+// HBM bounds it: bf16 (336 MB) in 53.6 us, 0.93 of the measured copy rate,
+// float32 in 101, 0.98 (requested into registers 63.8 us at 16 warps an SM;
 // sixteen threads a row, which need fewer, 78).  Blocks are small and take the
 // memory that their heads need, so that a few thousand tokens are one even wave:
-// 2049 tokens x 32 heads 8.8 us, with blocks of 256 threads 11.0, of 64 9.0.
+// 2049 tokens x 32 heads 7.6 us (with blocks of 256 threads 2 us more).
 #include <cmath>
 #include <type_traits>
 
@@ -125,18 +130,21 @@ __global__ void __launch_bounds__(kThreads, 6) norm_rope_kernel(const __grid_con
     const int64_t head = a.head[which], o_head = a.o_head[which];
     const uint8_t *x = a.x[which] + n * a.tok[which];
     uint8_t *o = a.out[which] + n * a.o_tok[which];
-    // the group's heads: vector i of the thread's elements of head u at [u][i][thread]
+    // the group's heads: vector v of head u's row at [u][group of threads][place(v)], where eight threads
+    // meet all banks whether they read v apart by 1, 2 or 4
     extern __shared__ uint4 held[];
-    constexpr int kWalk = heads_walked<DT>();
+    constexpr int kWalk = heads_walked<DT>(), kRow = 16 * NV;
+    auto row_of = [&](int u) { return held + (u * (kThreads / 8) + (threadIdx.x >> 3)) * kRow; };
+    auto place = [](int v) { return v ^ (v >> 3); };
 #pragma unroll
     for (int u = 0; u < kWalk; ++u) {
         if (first + u < end) {
             const uint8_t *xr = x + (first + u) * head;
 #pragma unroll
             for (int i = 0; i < 2 * NV; ++i) {
-                const uint8_t *src = xr + (i < NV ? e0 : e1) * ES + 16 * (i % NV);
-                const uint32_t dst = (uint32_t)__cvta_generic_to_shared(held + (u * 2 * NV + i) * kThreads + threadIdx.x);
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+                const int v = 8 * i + c;
+                const uint32_t dst = (uint32_t)__cvta_generic_to_shared(row_of(u) + place(v));
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(xr + 16 * v) : "memory");
             }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
@@ -158,11 +166,13 @@ __global__ void __launch_bounds__(kThreads, 6) norm_rope_kernel(const __grid_con
         constexpr int u = decltype(at)::value;
         asm volatile("cp.async.wait_group %0;" ::"n"(kWalk - 1 - u) : "memory");
         if (first + u >= end) return;
+        __syncwarp(lanes);
+        uint4 *row = row_of(u);
         uint4 va[NV], vb[NV];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            va[i] = held[(u * 2 * NV + i) * kThreads + threadIdx.x];
-            vb[i] = held[(u * 2 * NV + NV + i) * kThreads + threadIdx.x];
+            va[i] = row[place(e0 * ES / 16 + i)];
+            vb[i] = row[place(e1 * ES / 16 + i)];
         }
         float f[8], g[8];
         unpack8<DT>(va, f);
@@ -211,10 +221,19 @@ __global__ void __launch_bounds__(kThreads, 6) norm_rope_kernel(const __grid_con
         pack8<DT>(f, ra);
         pack8<DT>(g, rb);
         uint8_t *orow = o + (first + u) * o_head;
+        if constexpr (NV == 2) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            __stcs(reinterpret_cast<uint4 *>(orow + e0 * ES) + i, ra[i]);
-            __stcs(reinterpret_cast<uint4 *>(orow + e1 * ES) + i, rb[i]);
+            for (int i = 0; i < NV; ++i) {
+                row[place(e0 * ES / 16 + i)] = ra[i];
+                row[place(e1 * ES / 16 + i)] = rb[i];
+            }
+            __syncwarp(lanes);
+#pragma unroll
+            for (int i = 0; i < 2 * NV; ++i)
+                __stcs(reinterpret_cast<uint4 *>(orow) + 8 * i + c, row[place(8 * i + c)]);
+        } else {
+            __stcs(reinterpret_cast<uint4 *>(orow + e0 * ES), ra[0]);
+            __stcs(reinterpret_cast<uint4 *>(orow + e1 * ES), rb[0]);
         }
     });
 }
@@ -288,7 +307,7 @@ extern "C" int tq_norm_rope_apply(const void *q, int q_heads, int64_t q_tok_stri
     a.weight_dtype = weight_dtype;
     a.eps = eps;
     // heads of a group: with few tokens every head has threads of its own; once the groups fill the
-    // GPU (128 per SM; on 2049 tokens x 32 heads 8.8 us, with 256 10.6, with 64 10.5) they walk as many
+    // GPU (128 per SM; on 2049 tokens x 32 heads 7.6 us, with 256 10.2, with 64 8.4) they walk as many
     // heads as a block holds
     int walk = 1;
     const int most = dtype == TQ_F32 ? heads_walked<TQ_F32>() : heads_walked<TQ_BF16>();
